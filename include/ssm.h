@@ -14,8 +14,15 @@
  *   ssm_scan_fwd_tuned                the forward with its form and split chosen by the caller
  *   ssm_scan_fwd_noalloc              the forward for callers that cannot allocate device memory
  *   ssm_ssd_fwd                       the scan with a scalar transition per head
+ *   ssm_linattn_fwd, ssm_linattn_bwd, ssm_linattn_update
+ *                                     linear attention with a decay for each head: whole
+ *                                     sequences, the gradients, one token
+ *   ssm_layernorm_fwd, ssm_layernorm_bwd
+ *                                     layer norm over the model's width or each head's
+ *                                     channels, and its gradients
  *   ssm_conv_fwd, ssm_conv_update     the causal depthwise convolution + SiLU before
  *                                     the scan, and its token step
+ *   ssm_linattn_workspace, ssm_layernorm_workspace,
  *   ssm_scan_plan, ssm_profile_*, ssm_status_string, ssm_last_hip_error, ssm_version
  *                                     host-side queries
  *
@@ -39,8 +46,11 @@
  * backward and the per-head scan take a temporary workspace from the
  * stream-ordered allocator (hipMallocAsync / hipFreeAsync on `stream`), so
  * concurrent calls on different streams do not share memory.
- * ssm_state_update and ssm_conv_update take none and issue no memset: a
- * caller can capture them in a HIP graph.
+ * ssm_state_update, ssm_conv_update, ssm_linattn_update and
+ * ssm_layernorm_fwd take none and issue no memset: a caller can capture them
+ * in a HIP graph.  ssm_linattn_fwd, ssm_linattn_bwd and ssm_layernorm_bwd take
+ * a workspace of the caller's where one is given (then they allocate nothing
+ * and can be captured too), else from the stream-ordered allocator.
  *
  * Data types.  `dtype` (ssm_dtype) is the element type of the streamed
  * tensors u/x, delta, B, C, z and y: SSM_F32 (float) or SSM_BF16 (bfloat16,
@@ -49,7 +59,8 @@
  *
  * Sizes.  b (batch), L (sequence length), E (expanded channels) and
  * N (state size per channel).  Supported: 1 <= N <= 16 (ssm_ssd_fwd: N a
- * multiple of 16 up to 128); 0 <= b, L, E <= 2^48.  b == 0 or E == 0 is a no-op.
+ * multiple of 16 up to 128); 0 <= b, L, E <= 2^48.  Linear attention: head widths
+ * Dk and Dv of 1..128, H a multiple of G.  b == 0 or E == 0 is a no-op.
  * L == 0 writes a zero last_state (or the incoming state, where one is given).
  *
  * Alignment.  Every array must be aligned to its element size; float arrays
@@ -92,7 +103,8 @@ typedef enum {
   SSM_ERR_ALIGN = -5,         /* an array is not aligned to its element size */
   SSM_ERR_HIP = -6,           /* HIP launch / allocation failure */
   SSM_ERR_PLAN = -7,          /* an ssm_scan_tuning value is invalid or does not apply to the call */
-  SSM_ERR_SCRATCH = -8        /* ssm_scan_fwd_noalloc: the call needs more than SSM_NOALLOC_SCRATCH_BYTES */
+  SSM_ERR_SCRATCH = -8        /* ssm_scan_fwd_noalloc: the call needs more than SSM_NOALLOC_SCRATCH_BYTES;
+                                 elsewhere: the given workspace is smaller than the call needs */
 } ssm_status;
 
 /*
@@ -395,6 +407,109 @@ SSM_API int ssm_conv_update(void* conv_state, const void* v, const float* q, con
                             int64_t b, int64_t E, int64_t K, int dtype, void* stream);
 
 /*
+ * Linear attention with a decay for each head.  For every batch row b and
+ * head h, starting from S = initial_state (or zero), a [Dk, Dv] state:
+ *   r        = exp(A[h] + g[b,t,h])
+ *   S        = r * S + k[b,t,h'] v[b,t,h]^T
+ *   y[b,t,h] = scale * S^T q[b,t,h']            (read after the write)
+ *   last_state[b,h] = S after the row's last token
+ * with h' = h / (H / G): consecutive heads of a group share a row of q and k.
+ * ssm_ssd_fwd is the case of one group with g = delta * A and delta * x in the
+ * place of v.  The whole sequence is computed in chunks of matrix products.
+ *
+ * Arguments (device pointers):
+ *   q, k           [b, L, G, Dk]      dtype
+ *   v, y           [b, L, H, Dv]      dtype
+ *   g              [b, L, H]          dtype   log decay of each token (nullable: zero)
+ *   A              [H]                float   fixed log decay of each head (nullable: zero)
+ *   lengths        [b]                int32   (nullable: L) tokens of each batch row; values are
+ *                                             clamped to 0..L.  The tokens behind are not read: a
+ *                                             row's last_state is the one after its own last token, and
+ *                                             its y rows behind are zero.
+ *   scale                             factor of y, on the host
+ *   initial_state, last_state [b, H, Dk, Dv] float (nullable)
+ *   workspace, workspace_bytes        at least ssm_linattn_workspace() bytes, 256-byte aligned, used by
+ *                                     this call's work until it has run; NULL: from the stream-ordered
+ *                                     allocator on `stream`
+ * 1 <= Dk, Dv <= 128 (else SSM_ERR_DIM); G divides H; H <= 65535.  bf16: matrix products
+ * take bf16 operands and accumulate in fp32 (the state's two bf16 parts, high and low, where it
+ * is written); f32: fp32 matrix products.  Log decays are usually negative; one below -10^4, minus infinity
+ * included, counts as -10^4: a factor of zero, which drops the state (where a new
+ * document starts).  A value of v that is not finite may reach the outputs of up to
+ * 63 tokens before its own, through products with zero.
+ * L == 0 copies initial_state (or zeros) to last_state; b == 0 or H == 0 is a no-op.
+ */
+SSM_API int ssm_linattn_fwd(const void* q, const void* k, const void* v, const void* g, const float* A,
+                            const int32_t* lengths, float scale, const float* initial_state, void* y,
+                            float* last_state, int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
+                            int dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of  sum dy * y + sum d_last_state * last_state  with respect to
+ * the inputs of ssm_linattn_fwd (A is fixed: it has none).
+ *   inputs   the forward's; dy [b, L, H, Dv] dtype; d_last_state [b, H, Dk, Dv] float (nullable: zero)
+ *   outputs  (fully overwritten; zero rows behind a row's length)
+ *     dq, dk [b, L, G, Dk] dtype   (sums over a group's heads)
+ *     dv     [b, L, H, Dv] dtype
+ *     dg     [b, L, H]     dtype   (written when g is given and dg is not NULL)
+ *     d_initial_state [b, H, Dk, Dv] float (nullable; also when initial_state is NULL)
+ * Nothing of the forward is kept: the states are recomputed.  Results are
+ * deterministic.  Workspace as in ssm_linattn_fwd, of the backward's size.
+ */
+SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const void* g, const float* A,
+                            const int32_t* lengths, float scale, const float* initial_state, const void* dy,
+                            const float* d_last_state, void* dq, void* dk, void* dv, void* dg,
+                            float* d_initial_state, int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk,
+                            int64_t Dv, int dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * One token of ssm_linattn_fwd on a persistent state (generation):
+ *   state [b, H, Dk, Dv] float, in place;  q, k [b, G, Dk], v, y [b, H, Dv], g [b, H] dtype.
+ * A batch row whose lengths[b] is zero or less takes no step: its state stays as it is and its
+ * row of y is zero (rows behind the live sequences of a padded batch).
+ */
+SSM_API int ssm_linattn_update(float* state, const void* q, const void* k, const void* v, const void* g,
+                               const float* A, const int32_t* lengths, float scale, void* y, int64_t b, int64_t H,
+                               int64_t G, int64_t Dk, int64_t Dv, int dtype, void* stream);
+
+/*
+ * Bytes of workspace that ssm_linattn_fwd (backward == 0) or ssm_linattn_bwd
+ * (backward != 0) needs at these sizes, whatever its nullable arguments; a
+ * negative ssm_status for sizes those calls refuse.  Host-only.
+ */
+SSM_API int64_t ssm_linattn_workspace(int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype,
+                                      int backward);
+
+/*
+ * Layer norm over the last axis, for every row i and head h (H = 1: over the
+ * model's width; H > 1: over each head's channels, with the head's parameters):
+ *   mean = sum_j x[i,h,j] / W,  rstd = 1 / sqrt(sum_j (x[i,h,j] - mean)^2 / W + eps)
+ *   y[i,h,j] = (x[i,h,j] - mean) * rstd * weight[h,j] + bias[h,j]
+ * Arguments (device pointers):
+ *   x, y          [rows, H, W]  dtype
+ *   weight, bias  [H, W]        float  (nullable: one, zero)
+ *   mean, rstd    [rows, H]     float  (nullable; what the backward needs)
+ * 1 <= W <= 16384; eps >= 0 (else SSM_ERR_DIM).
+ */
+SSM_API int ssm_layernorm_fwd(const void* x, const float* weight, const float* bias, float eps, void* y, float* mean,
+                              float* rstd, int64_t rows, int64_t H, int64_t W, int dtype, void* stream);
+
+/*
+ * Gradients of sum dy * y of ssm_layernorm_fwd, from its x, mean and rstd:
+ *   dx              [rows, H, W]  dtype
+ *   dweight, dbias  [H, W]        float  (both, or both NULL; rows == 0 writes zeros)
+ * Sums over the rows are added in a fixed order (deterministic).  The partial sums take a
+ * workspace: at least ssm_layernorm_workspace() bytes at `workspace`, or NULL for the
+ * stream-ordered allocator; none without dweight and dbias.
+ */
+SSM_API int ssm_layernorm_bwd(const void* x, const float* weight, const float* mean, const float* rstd,
+                              const void* dy, void* dx, float* dweight, float* dbias, int64_t rows, int64_t H,
+                              int64_t W, int dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of ssm_layernorm_bwd; a negative ssm_status for sizes it refuses.  Host-only. */
+SSM_API int64_t ssm_layernorm_workspace(int64_t rows, int64_t H, int64_t W, int dtype);
+
+/*
  * How a forward scan of this size runs (tuning NULL: as ssm_scan_fwd): *path
  * receives SSM_PATH_CHUNKED or SSM_PATH_SINGLE_PASS, *chunk_len and *n_chunks
  * the chunks (single pass: chunks of 8 steps; chunked form: one chunk means a
@@ -418,7 +533,10 @@ SSM_API int ssm_scan_plan(int64_t b, int64_t L, int64_t E, int64_t N, int dtype,
  * forward and the reverse ones from one walk, whose forward chain is timed as
  * chunk_carry), 9 bwd_carry, 10 bwd_main, 11 bwd_reduce, 12 ssd_state,
  * 13 ssd_carry, 14 ssd_scan, 15 scan_fused (the single-pass forward),
- * 16 widen_rows (float copies of the bf16 B / C rows of a cut forward); names
+ * 16 widen_rows (float copies of the bf16 B / C rows of a cut forward),
+ * 17 linattn_sweep, 18 linattn_state, 19 linattn_chain, 20 linattn_gate,
+ * 21 linattn_reduce, 22 linattn_update, 23 layernorm, 24 layernorm_bwd,
+ * 25 layernorm_reduce; names
  * from ssm_profile_kind_name().  Off by default; the events add a few
  * microseconds per launch.  Process-wide, thread-safe.
  */

@@ -32,6 +32,14 @@ Functions (same names as the C entry points):
   return_last_state=True)`` -> ``(y, last_state)``: the scan with a scalar
   transition per head (x [b, L, H*64], delta [b, L, H], A, D, delta_bias [H]),
   bf16 only
+* ``ssm_linattn_fwd(q, k, v, g=None, A=None, scale=None, lengths=None,
+  initial_state=None, y=None, last_state=None, return_last_state=True)`` ->
+  ``(y, last_state)``: linear attention with a decay for each head over whole
+  sequences; ``ssm_linattn_bwd`` its gradients, ``ssm_linattn_update`` its step
+  for one token
+* ``ssm_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None)`` ->
+  ``(y, mean, rstd)``: layer norm over the last axis; ``ssm_layernorm_bwd`` its
+  gradients
 * ``ssm_conv_fwd(v, weight, conv_bias=None, state_in=None, x=None,
   state_out=None, return_state=True)`` -> ``(x, state_out)``: causal depthwise
   convolution + SiLU over the sequence
@@ -40,6 +48,9 @@ Functions (same names as the C entry points):
 
 Shapes: u, delta, z, y [b, L, E]; A [E, N] (float32); B, C [b, L, N];
 D, delta_bias [E] (float32); state / last_state [b, E, N] (float32).
+Linear attention: q, k [b, L, G, Dk]; v, y [b, L, H, Dv]; g [b, L, H]; A [H]
+float32; lengths [b] int32; states [b, H, Dk, Dv] float32 (G divides H;
+Dk, Dv <= 128).
 Convolution: v, x [b, L, E]; weight [E, K] float32 (1 <= K <= 8); conv_bias
 [E] float32; convolution state [b, E, K] in the streamed dtype, oldest sample
 first.  Streamed tensors are all float32 or all bfloat16.
@@ -49,7 +60,9 @@ import ctypes
 import os
 
 __all__ = [
-    "ssm_scan_fwd", "ssm_scan_fwd_from", "ssm_scan_fwd_noalloc", "ssm_scan_bwd", "ssm_ssd_fwd", "ssm_state_update", "ssm_conv_fwd", "ssm_conv_update", "ssm_scan_plan", "ssm_profile_enable", "ssm_profile_read",
+    "ssm_scan_fwd", "ssm_scan_fwd_from", "ssm_scan_fwd_noalloc", "ssm_scan_bwd", "ssm_ssd_fwd", "ssm_state_update", "ssm_conv_fwd", "ssm_conv_update",
+    "ssm_linattn_fwd", "ssm_linattn_bwd", "ssm_linattn_update", "ssm_linattn_workspace",
+    "ssm_layernorm_fwd", "ssm_layernorm_bwd", "ssm_layernorm_workspace", "ssm_scan_plan", "ssm_profile_enable", "ssm_profile_read",
     "ssm_status_string", "library_path", "SSMError", "ScanTuning", "SCAN_PATHS",
     "SSM_F32", "SSM_BF16", "load_library",
 ]
@@ -64,6 +77,7 @@ SSM_BF16 = 1
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 
 
 # ssm_scan_path values
@@ -136,6 +150,20 @@ def load_library():
     lib.ssm_conv_fwd.argtypes = [_vp] * 6 + [_i64] * 4 + [_int, _vp]
     lib.ssm_conv_update.restype = _int
     lib.ssm_conv_update.argtypes = [_vp] * 5 + [_i64] * 3 + [_int, _vp]
+    lib.ssm_linattn_fwd.restype = _int
+    lib.ssm_linattn_fwd.argtypes = [_vp] * 6 + [_f32] + [_vp] * 3 + [_i64] * 6 + [_int, _vp, _i64, _vp]
+    lib.ssm_linattn_bwd.restype = _int
+    lib.ssm_linattn_bwd.argtypes = [_vp] * 6 + [_f32] + [_vp] * 8 + [_i64] * 6 + [_int, _vp, _i64, _vp]
+    lib.ssm_linattn_update.restype = _int
+    lib.ssm_linattn_update.argtypes = [_vp] * 7 + [_f32, _vp] + [_i64] * 5 + [_int, _vp]
+    lib.ssm_linattn_workspace.restype = _i64
+    lib.ssm_linattn_workspace.argtypes = [_i64] * 6 + [_int, _int]
+    lib.ssm_layernorm_fwd.restype = _int
+    lib.ssm_layernorm_fwd.argtypes = [_vp] * 3 + [_f32] + [_vp] * 3 + [_i64] * 3 + [_int, _vp]
+    lib.ssm_layernorm_bwd.restype = _int
+    lib.ssm_layernorm_bwd.argtypes = [_vp] * 8 + [_i64] * 3 + [_int, _vp, _i64, _vp]
+    lib.ssm_layernorm_workspace.restype = _i64
+    lib.ssm_layernorm_workspace.argtypes = [_i64] * 3 + [_int]
     lib.ssm_status_string.restype = ctypes.c_char_p
     lib.ssm_status_string.argtypes = [_int]
     lib.ssm_last_hip_error.restype = ctypes.c_char_p
@@ -174,7 +202,8 @@ def ssm_scan_plan(b, L, E, N, dtype="bf16", tuning=None):
     return _PATH_NAMES[path.value], cl.value, nc.value
 
 
-PROFILE_KINDS = 17
+PROFILE_KINDS = 26
+_SCAN_KINDS = 17  # the kinds of the scans and the convolution, always in the answer
 
 
 def ssm_profile_enable(on=True):
@@ -183,12 +212,16 @@ def ssm_profile_enable(on=True):
 
 
 def ssm_profile_read():
-    """Wait for the recorded events; return {kind name: (total ms, launches)} and clear the record."""
+    """Wait for the recorded events; return {kind name: (total ms, launches)} and clear the record.
+
+    The kinds of linear attention and layer norm are there where they ran.
+    """
     lib = load_library()
     ms = (ctypes.c_double * PROFILE_KINDS)()
     cnt = (_i64 * PROFILE_KINDS)()
     _raise_on("ssm_profile_read", lib.ssm_profile_read(ms, cnt, PROFILE_KINDS))
-    return {lib.ssm_profile_kind_name(k).decode(): (ms[k], cnt[k]) for k in range(PROFILE_KINDS)}
+    return {lib.ssm_profile_kind_name(k).decode(): (ms[k], cnt[k]) for k in range(PROFILE_KINDS)
+            if k < _SCAN_KINDS or cnt[k]}
 
 
 def _ptr(t):
@@ -608,3 +641,225 @@ def ssm_conv_update(conv_state, v, weight, conv_bias=None, x=None):
                                      _stream_of(torch, device))
     _raise_on("ssm_conv_update", status)
     return x
+
+
+# ---------------------------------------------------------------------------
+# linear attention with a decay for each head
+# ---------------------------------------------------------------------------
+def ssm_linattn_workspace(b, L, H, G, Dk, Dv, dtype="bf16", backward=False):
+    """Bytes of workspace of ``ssm_linattn_fwd`` or ``ssm_linattn_bwd`` at these sizes (host-only query)."""
+    code = {"f32": SSM_F32, "bf16": SSM_BF16}.get(dtype, dtype)
+    n = load_library().ssm_linattn_workspace(int(b), int(L), int(H), int(G), int(Dk), int(Dv), int(code),
+                                             int(bool(backward)))
+    _raise_on("ssm_linattn_workspace", min(n, 0))
+    return n
+
+
+def _workspace(torch, n, device):
+    """A workspace of n bytes from the allocator of PyTorch, on its current stream of ``device`` (None for 0)."""
+    return torch.empty((n,), dtype=torch.uint8, device=device) if n else None
+
+
+def _linattn_sizes(torch, q, k, v, g, A, lengths, tokens):
+    """Checks the inputs of linear attention over ``tokens`` leading axes (2: [b, L], 1: [b]);
+    returns (b, L, H, G, Dk, Dv, io dtype, code, device)."""
+    shape = "[b, L, G, Dk]" if tokens == 2 else "[b, G, Dk]"
+    if not isinstance(q, torch.Tensor) or q.dim() != tokens + 2:
+        raise ValueError(f"q must be a {shape} tensor")
+    if not isinstance(v, torch.Tensor) or v.dim() != tokens + 2:
+        raise ValueError(f"v must be a {shape.replace('G, Dk', 'H, Dv')} tensor")
+    device = q.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU device, got {device}")
+    lead = tuple(q.shape[:tokens])
+    G, Dk = q.shape[tokens:]
+    H, Dv = v.shape[tokens:]
+    if G == 0 and H > 0 or G > 0 and H % G:
+        raise ValueError(f"the {H} heads of v must be a multiple of the {G} of q and k")
+    io = q.dtype
+    code = _dtype_code(torch, io)
+    _check(torch, "q", q, (*lead, G, Dk), io, device)
+    _check(torch, "k", k, (*lead, G, Dk), io, device)
+    _check(torch, "v", v, (*lead, H, Dv), io, device)
+    _check(torch, "g", g, (*lead, H), io, device, optional=True)
+    _check(torch, "A", A, (H,), torch.float32, device, optional=True)
+    _check(torch, "lengths", lengths, lead[:1], torch.int32, device, optional=True)
+    return lead[0], lead[1] if tokens == 2 else 1, H, G, Dk, Dv, io, code, device
+
+
+def _scale(scale, Dk):
+    return Dk ** -0.5 if scale is None else float(scale)
+
+
+def ssm_linattn_fwd(q, k, v, g=None, A=None, scale=None, lengths=None, initial_state=None, y=None, last_state=None,
+                    return_last_state=True):
+    """Linear attention with a decay for each head: ``(y, last_state)`` (None if not requested).
+
+    ``S = exp(A[h] + g[b, t, h]) S + k v^T``, ``y = scale S^T q`` for every token, from
+    ``initial_state`` (None: zero).  q, k [b, L, G, Dk]; v, y [b, L, H, Dv], each group of
+    H / G heads sharing a row of q and k; g [b, L, H] in the streamed dtype, A [H] float32 (None:
+    zero); ``scale`` None is Dk ** -0.5; ``lengths`` [b] int32 are the tokens of each batch row
+    (None: all L): the others are not read, and their rows of y are zero.
+    """
+    import torch
+
+    lib = load_library()
+    b, L, H, G, Dk, Dv, io, code, device = _linattn_sizes(torch, q, k, v, g, A, lengths, 2)
+    f32 = torch.float32
+    _check(torch, "initial_state", initial_state, (b, H, Dk, Dv), f32, device, optional=True)
+    if y is None:
+        y = torch.empty((b, L, H, Dv), dtype=io, device=device)
+    else:
+        _check(torch, "y", y, (b, L, H, Dv), io, device)
+    if last_state is None and return_last_state:
+        last_state = torch.empty((b, H, Dk, Dv), dtype=f32, device=device)
+    elif last_state is not None:
+        _check(torch, "last_state", last_state, (b, H, Dk, Dv), f32, device)
+    if b * H and initial_state is not None and last_state is not None and (
+            initial_state.data_ptr() == last_state.data_ptr()):
+        raise ValueError("initial_state must not be the last_state buffer")
+    n = lib.ssm_linattn_workspace(b, L, H, G, Dk, Dv, code, 0)
+    _raise_on("ssm_linattn_fwd", min(n, 0))
+    ws = _workspace(torch, n, device)
+    with _on(torch, device):
+        status = lib.ssm_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(A), _ptr(lengths), _scale(scale, Dk),
+                                     _ptr(initial_state), _ptr(y), _ptr(last_state), b, L, H, G, Dk, Dv, code,
+                                     _ptr(ws), n, _stream_of(torch, device))
+    _raise_on("ssm_linattn_fwd", status)
+    return y, last_state
+
+
+def ssm_linattn_bwd(q, k, v, dy, g=None, A=None, scale=None, lengths=None, initial_state=None, d_last_state=None):
+    """Gradients of sum(dy * y) + sum(d_last_state * last_state) for ``ssm_linattn_fwd``'s arguments.
+
+    Returns a dict: dq, dk [b, L, G, Dk], dv [b, L, H, Dv] and dg [b, L, H] (None without g) in the
+    streamed dtype, d_initial_state [b, H, Dk, Dv] float32 (None without initial_state).
+    """
+    import torch
+
+    lib = load_library()
+    b, L, H, G, Dk, Dv, io, code, device = _linattn_sizes(torch, q, k, v, g, A, lengths, 2)
+    f32 = torch.float32
+    _check(torch, "dy", dy, (b, L, H, Dv), io, device)
+    _check(torch, "initial_state", initial_state, (b, H, Dk, Dv), f32, device, optional=True)
+    _check(torch, "d_last_state", d_last_state, (b, H, Dk, Dv), f32, device, optional=True)
+    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+           "dg": None if g is None else torch.empty_like(g),
+           "d_initial_state": None if initial_state is None else torch.empty_like(initial_state)}
+    n = lib.ssm_linattn_workspace(b, L, H, G, Dk, Dv, code, 1)
+    _raise_on("ssm_linattn_bwd", min(n, 0))
+    ws = _workspace(torch, n, device)
+    with _on(torch, device):
+        status = lib.ssm_linattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(A), _ptr(lengths), _scale(scale, Dk),
+                                     _ptr(initial_state), _ptr(dy), _ptr(d_last_state), _ptr(out["dq"]),
+                                     _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["d_initial_state"]),
+                                     b, L, H, G, Dk, Dv, code, _ptr(ws), n, _stream_of(torch, device))
+    _raise_on("ssm_linattn_bwd", status)
+    return out
+
+
+def ssm_linattn_update(state, q, k, v, g=None, A=None, scale=None, lengths=None, y=None):
+    """One token of ``ssm_linattn_fwd``: ``state`` [b, H, Dk, Dv] float32 is updated in place; returns ``y``.
+
+    q, k [b, G, Dk]; v, y [b, H, Dv]; g [b, H].  A batch row whose ``lengths`` is zero takes no step:
+    its state stays and its row of y is zero.
+    """
+    import torch
+
+    lib = load_library()
+    b, _, H, G, Dk, Dv, io, code, device = _linattn_sizes(torch, q, k, v, g, A, lengths, 1)
+    _check(torch, "state", state, (b, H, Dk, Dv), torch.float32, device)
+    if y is None:
+        y = torch.empty((b, H, Dv), dtype=io, device=device)
+    else:
+        _check(torch, "y", y, (b, H, Dv), io, device)
+    with _on(torch, device):
+        status = lib.ssm_linattn_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(A), _ptr(lengths),
+                                        _scale(scale, Dk), _ptr(y), b, H, G, Dk, Dv, code, _stream_of(torch, device))
+    _raise_on("ssm_linattn_update", status)
+    return y
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+def ssm_layernorm_workspace(rows, H, W, dtype="bf16"):
+    """Bytes of workspace of ``ssm_layernorm_bwd`` at these sizes (host-only query)."""
+    code = {"f32": SSM_F32, "bf16": SSM_BF16}.get(dtype, dtype)
+    n = load_library().ssm_layernorm_workspace(int(rows), int(H), int(W), int(code))
+    _raise_on("ssm_layernorm_workspace", min(n, 0))
+    return n
+
+
+def _norm_sizes(torch, x, par):
+    """(parameter shape, rows, H, W, code, device) of a layer norm of x with parameters of that shape
+    ([W], or [H, W] for x [..., H, W])."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a [..., W] tensor")
+    if x.device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU device, got {x.device}")
+    par = tuple(x.shape[-1:]) if par is None else tuple(par)
+    if len(par) not in (1, 2) or len(par) > x.dim() or par != tuple(x.shape[x.dim() - len(par):]):
+        raise ValueError(f"parameters of shape {par} do not fit x of shape {tuple(x.shape)}: [W] or [H, W] of its last axes")
+    H, W = (1, par[0]) if len(par) == 1 else par
+    if W == 0:
+        raise ValueError("x has rows of no elements")
+    code = _dtype_code(torch, x.dtype)
+    _check(torch, "x", x, x.shape, x.dtype, x.device)
+    return par, x.numel() // (H * W) if H else 0, H, W, code, x.device
+
+
+def ssm_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None):
+    """Layer norm over the last axis of x [..., W]: ``(y, mean, rstd)``, mean and rstd [...] float32 for the backward.
+
+    weight and bias are float32, [W], or [H, W] for x [..., H, W] (each head's channels with the head's
+    own parameters); None is one and zero.
+    """
+    import torch
+
+    lib = load_library()
+    one = weight if weight is not None else bias
+    par, rows, H, W, code, device = _norm_sizes(torch, x, None if one is None else one.shape)
+    _check(torch, "weight", weight, par, torch.float32, device, optional=True)
+    _check(torch, "bias", bias, par, torch.float32, device, optional=True)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _check(torch, "y", y, x.shape, x.dtype, device)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+    rstd = torch.empty_like(mean)
+    with _on(torch, device):
+        status = lib.ssm_layernorm_fwd(_ptr(x), _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(mean), _ptr(rstd),
+                                       rows, H, W, code, _stream_of(torch, device))
+    _raise_on("ssm_layernorm_fwd", status)
+    return y, mean, rstd
+
+
+def ssm_layernorm_bwd(x, dy, mean, rstd, weight=None, heads=None, param_grads=True):
+    """Gradients of sum(dy * y) of ``ssm_layernorm_fwd``: a dict of dx (x's dtype) and dweight, dbias (float32).
+
+    mean and rstd are the forward's.  The parameters' shape is weight's; without a weight it is [W], or
+    [heads, W] where ``heads`` is given.  ``param_grads=False`` leaves dweight and dbias None.
+    """
+    import torch
+
+    lib = load_library()
+    shape = weight.shape if weight is not None else None if heads is None else (int(heads), *x.shape[-1:])
+    par, rows, H, W, code, device = _norm_sizes(torch, x, shape)
+    f32 = torch.float32
+    _check(torch, "dy", dy, x.shape, x.dtype, device)
+    _check(torch, "mean", mean, x.shape[:-1], f32, device)
+    _check(torch, "rstd", rstd, x.shape[:-1], f32, device)
+    _check(torch, "weight", weight, par, f32, device, optional=True)
+    out = {"dx": torch.empty_like(x),
+           "dweight": torch.empty(par, dtype=f32, device=device) if param_grads else None,
+           "dbias": torch.empty(par, dtype=f32, device=device) if param_grads else None}
+    n = lib.ssm_layernorm_workspace(rows, H, W, code) if param_grads else 0
+    _raise_on("ssm_layernorm_bwd", min(n, 0))
+    ws = _workspace(torch, n, device)
+    with _on(torch, device):
+        status = lib.ssm_layernorm_bwd(_ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(out["dx"]),
+                                       _ptr(out["dweight"]), _ptr(out["dbias"]), rows, H, W, code, _ptr(ws), n,
+                                       _stream_of(torch, device))
+    _raise_on("ssm_layernorm_bwd", status)
+    return out

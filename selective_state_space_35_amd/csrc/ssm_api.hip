@@ -411,6 +411,173 @@ int ssm_conv_update(void* conv_state, const void* v, const float* q, const float
   return hip_status(ssm::launch_conv_update(a));
 }
 
+}  // extern "C"
+
+namespace {
+
+// Sizes and dtype of a linear-attention call.
+int check_linattn(int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype) {
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
+  const int64_t max_dim = ssm::linattn_max_dim();
+  if (!size_ok(b) || !size_ok(L) || H < 0 || H > ssm::linattn_max_heads() || G < 0) return SSM_ERR_DIM;
+  if (Dk < 1 || Dk > max_dim || Dv < 1 || Dv > max_dim) return SSM_ERR_DIM;
+  if (H > 0 && (G < 1 || H % G != 0)) return SSM_ERR_DIM;
+  // every array and workspace in bytes, with room for the workspace's several copies
+  int64_t t = 0;
+  if (!mul_ok(b, L, &t) || !mul_ok(t, H, &t) || !mul_ok(t, max_dim * 64, &t)) return SSM_ERR_DIM;
+  if (!mul_ok(b, H, &t) || !mul_ok(t, max_dim * max_dim * 64, &t)) return SSM_ERR_DIM;
+  // grids: a workgroup per head (and segment) of a batch row; 256 tokens x 16 heads in the gate's sums;
+  // 256 elements of dq in the sums over a group
+  if (b * H > INT32_MAX / 2 || L > (int64_t(1) << 31) || !mul_ok(b * H, L / 256 + 1, &t) || t > INT32_MAX) return SSM_ERR_DIM;
+  if (!mul_ok(b * L, G * Dk, &t) || t / 256 > INT32_MAX - 1) return SSM_ERR_DIM;
+  return SSM_OK;
+}
+
+ssm::LinAttnArgs linattn_args(const void* q, const void* k, const void* v, const void* g, const float* A,
+                              const int32_t* lengths, float scale, int64_t b, int64_t L, int64_t H, int64_t G,
+                              int64_t Dk, int64_t Dv, int dtype, void* stream) {
+  ssm::LinAttnArgs a{};
+  a.q = q; a.k = k; a.v = v; a.g = g; a.A = A; a.lengths = lengths; a.scale = scale;
+  a.b = b; a.L = L; a.H = H; a.G = G; a.Dk = Dk; a.Dv = Dv; a.dtype = dtype;
+  a.stream = static_cast<hipStream_t>(stream);
+  return a;
+}
+
+bool all_aligned(const void* const* p, int n, size_t to) {
+  for (int i = 0; i < n; i++)
+    if (p[i] && !aligned(p[i], to)) return false;
+  return true;
+}
+
+// A workspace of `need` bytes: the caller's, or one of the stream-ordered allocator's that is
+// given back when `run` has enqueued its work.
+template <typename Run>
+int with_workspace(size_t need, void* workspace, int64_t bytes, hipStream_t stream, Run run) {
+  if (workspace) {
+    if (bytes < 0 || uint64_t(bytes) < need) return SSM_ERR_SCRATCH;
+    if (!aligned(workspace, 256)) return SSM_ERR_ALIGN;
+    return hip_status(run(workspace));
+  }
+  if (need == 0) return hip_status(run(nullptr));
+  void* ws = nullptr;
+  hipError_t err = hipMallocAsync(&ws, need, stream);
+  if (err != hipSuccess) return hip_status(err);
+  err = run(ws);
+  const hipError_t ferr = hipFreeAsync(ws, stream);
+  return hip_status(err != hipSuccess ? err : ferr);
+}
+
+int check_layernorm(int64_t rows, int64_t H, int64_t W, int dtype) {
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
+  if (!size_ok(rows) || H < 0 || H > (int64_t(1) << 24) || W < 1 || W > ssm::layernorm_max_width()) return SSM_ERR_DIM;
+  int64_t t = 0;
+  if (!mul_ok(rows, H, &t) || t > INT32_MAX || !mul_ok(t, W * 16, &t)) return SSM_ERR_DIM;  // a workgroup a row at most
+  return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssm_linattn_fwd(const void* q, const void* k, const void* v, const void* g, const float* A,
+                    const int32_t* lengths, float scale, const float* initial_state, void* y, float* last_state,
+                    int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+  const int st = check_linattn(b, L, H, G, Dk, Dv, dtype);
+  if (st != SSM_OK || b == 0 || H == 0) return st;
+  if (L > 0 && (!q || !k || !v || !y)) return SSM_ERR_NULL;
+  const void* streamed[] = {q, k, v, g, y};
+  const void* fl[] = {A, lengths, initial_state, last_state};
+  if (!all_aligned(streamed, 5, dtype == SSM_F32 ? 4 : 2) || !all_aligned(fl, 4, 4)) return SSM_ERR_ALIGN;
+  ssm::LinAttnArgs a = linattn_args(q, k, v, g, A, lengths, scale, b, L, H, G, Dk, Dv, dtype, stream);
+  a.h0 = initial_state; a.y = y; a.last = last_state;
+  return with_workspace(ssm::linattn_workspace_bytes(a, false), workspace, workspace_bytes, a.stream,
+                        [&](void* ws) { return ssm::launch_linattn_fwd(a, ws); });
+}
+
+int ssm_linattn_bwd(const void* q, const void* k, const void* v, const void* g, const float* A,
+                    const int32_t* lengths, float scale, const float* initial_state, const void* dy,
+                    const float* d_last_state, void* dq, void* dk, void* dv, void* dg, float* d_initial_state,
+                    int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+  const int st = check_linattn(b, L, H, G, Dk, Dv, dtype);
+  if (st != SSM_OK || b == 0 || H == 0) return st;
+  if (L > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv)) return SSM_ERR_NULL;
+  const void* streamed[] = {q, k, v, g, dy, dq, dk, dv, dg};
+  const void* fl[] = {A, lengths, initial_state, d_last_state, d_initial_state};
+  if (!all_aligned(streamed, 9, dtype == SSM_F32 ? 4 : 2) || !all_aligned(fl, 5, 4)) return SSM_ERR_ALIGN;
+  ssm::LinAttnArgs a = linattn_args(q, k, v, g, A, lengths, scale, b, L, H, G, Dk, Dv, dtype, stream);
+  a.h0 = initial_state; a.dy = dy; a.dlast = d_last_state; a.dq = dq; a.dk = dk; a.dv = dv;
+  a.dg = g ? dg : nullptr; a.dh0 = d_initial_state;
+  return with_workspace(ssm::linattn_workspace_bytes(a, true), workspace, workspace_bytes, a.stream,
+                        [&](void* ws) { return ssm::launch_linattn_bwd(a, ws); });
+}
+
+int ssm_linattn_update(float* state, const void* q, const void* k, const void* v, const void* g, const float* A,
+                       const int32_t* lengths, float scale, void* y, int64_t b, int64_t H, int64_t G, int64_t Dk,
+                       int64_t Dv, int dtype, void* stream) {
+  const int st = check_linattn(b, 1, H, G, Dk, Dv, dtype);
+  if (st != SSM_OK || b == 0 || H == 0) return st;
+  if (!state || !q || !k || !v || !y) return SSM_ERR_NULL;
+  const void* streamed[] = {q, k, v, g, y};
+  const void* fl[] = {state, A, lengths};
+  if (!all_aligned(streamed, 5, dtype == SSM_F32 ? 4 : 2) || !all_aligned(fl, 3, 4)) return SSM_ERR_ALIGN;
+  ssm::LinAttnArgs a = linattn_args(q, k, v, g, A, lengths, scale, b, 1, H, G, Dk, Dv, dtype, stream);
+  a.y = y; a.last = state;
+  return hip_status(ssm::launch_linattn_update(a));
+}
+
+int64_t ssm_linattn_workspace(int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype,
+                              int backward) {
+  const int st = check_linattn(b, L, H, G, Dk, Dv, dtype);
+  if (st != SSM_OK) return st;
+  const ssm::LinAttnArgs a = linattn_args(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 1.f, b, L, H, G, Dk, Dv,
+                                          dtype, nullptr);
+  return int64_t(ssm::linattn_workspace_bytes(a, backward != 0));
+}
+
+int ssm_layernorm_fwd(const void* x, const float* weight, const float* bias, float eps, void* y, float* mean,
+                      float* rstd, int64_t rows, int64_t H, int64_t W, int dtype, void* stream) {
+  const int st = check_layernorm(rows, H, W, dtype);
+  if (st != SSM_OK) return st;
+  if (!(eps >= 0.f)) return SSM_ERR_DIM;
+  if (rows == 0 || H == 0) return SSM_OK;
+  if (!x || !y) return SSM_ERR_NULL;
+  const void* streamed[] = {x, y};
+  const void* fl[] = {weight, bias, mean, rstd};
+  if (!all_aligned(streamed, 2, dtype == SSM_F32 ? 4 : 2) || !all_aligned(fl, 4, 4)) return SSM_ERR_ALIGN;
+  ssm::LayerNormArgs a{};
+  a.x = x; a.weight = weight; a.bias = bias; a.eps = eps; a.y = y; a.mean = mean; a.rstd = rstd;
+  a.rows = rows; a.H = H; a.W = W; a.dtype = dtype; a.stream = static_cast<hipStream_t>(stream);
+  return hip_status(ssm::launch_layernorm_fwd(a));
+}
+
+int ssm_layernorm_bwd(const void* x, const float* weight, const float* mean, const float* rstd, const void* dy,
+                      void* dx, float* dweight, float* dbias, int64_t rows, int64_t H, int64_t W, int dtype,
+                      void* workspace, int64_t workspace_bytes, void* stream) {
+  const int st = check_layernorm(rows, H, W, dtype);
+  if (st != SSM_OK || H == 0) return st;
+  if (!dweight != !dbias) return SSM_ERR_NULL;
+  if (rows > 0 && (!x || !mean || !rstd || !dy || !dx)) return SSM_ERR_NULL;
+  const void* streamed[] = {x, dy, dx};
+  const void* fl[] = {weight, mean, rstd, dweight, dbias};
+  if (!all_aligned(streamed, 3, dtype == SSM_F32 ? 4 : 2) || !all_aligned(fl, 5, 4)) return SSM_ERR_ALIGN;
+  ssm::LayerNormArgs a{};
+  a.x = x; a.weight = weight; a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+  a.dy = dy; a.dx = dx; a.dweight = dweight; a.dbias = dbias;
+  a.rows = rows; a.H = H; a.W = W; a.dtype = dtype; a.stream = static_cast<hipStream_t>(stream);
+  return with_workspace(dweight ? ssm::layernorm_workspace_bytes(a) : 0, workspace, workspace_bytes, a.stream,
+                        [&](void* ws) { return ssm::launch_layernorm_bwd(a, ws); });
+}
+
+int64_t ssm_layernorm_workspace(int64_t rows, int64_t H, int64_t W, int dtype) {
+  const int st = check_layernorm(rows, H, W, dtype);
+  if (st != SSM_OK) return st;
+  ssm::LayerNormArgs a{};
+  a.rows = rows; a.H = H; a.W = W; a.dtype = dtype;
+  return int64_t(ssm::layernorm_workspace_bytes(a));
+}
+
 const char* ssm_status_string(int status) {
   switch (status) {
     case SSM_OK: return "ok";
@@ -422,7 +589,7 @@ const char* ssm_status_string(int status) {
     case SSM_ERR_PLAN: return "the requested scan form or tuning does not apply to this call";
     case SSM_ERR_SCRATCH:
       return "the call needs more workspace than the fixed buffer of ssm_scan_fwd_noalloc holds "
-             "(SSM_NOALLOC_SCRATCH_BYTES)";
+             "(SSM_NOALLOC_SCRATCH_BYTES), or than the given workspace has";
     case SSM_ERR_ALIGN: return "array not aligned to its element size";
     case SSM_ERR_HIP: return "HIP launch or allocation failed";
     default: return "unknown status";

@@ -79,14 +79,18 @@ __device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, int voff, in
 // Every launch goes through here.  With profiling on, it is bracketed by two
 // HIP events on the launch stream (see ssm_profile_enable in ssm.h).
 template <typename Kern, typename... Args>
-hipError_t launch_kind(int kind, Kern k, int64_t blocks, int threads, hipStream_t s, Args... args) {
-  if (blocks <= 0) return hipSuccess;
+hipError_t launch_kind_3d(int kind, Kern k, dim3 grid, int threads, hipStream_t s, Args... args) {
   hipEvent_t ev0 = nullptr, ev1 = nullptr;
   const bool prof = profile_begin(s, &ev0, &ev1);
-  hipLaunchKernelGGL(k, dim3(unsigned(blocks)), dim3(threads), 0, s, args...);
+  hipLaunchKernelGGL(k, grid, dim3(threads), 0, s, args...);
   hipError_t err = hipGetLastError();
   if (prof) profile_end(kind, s, ev0, ev1);
   return err;
+}
+template <typename Kern, typename... Args>
+hipError_t launch_kind(int kind, Kern k, int64_t blocks, int threads, hipStream_t s, Args... args) {
+  if (blocks <= 0) return hipSuccess;
+  return launch_kind_3d(kind, k, dim3(unsigned(blocks)), threads, s, args...);
 }
 
 }  // namespace ssm

@@ -1,0 +1,420 @@
+// ssm_layernorm.hip -- layer norm over the last axis, forward and backward, with the
+// reduction of the parameters' gradients.
+//
+// A row is one [W] slice of x [rows, H, W]; the parameters are [H, W] (H = 1: the norm over
+// the model's width; H > 1: each head's channels, with the head's own weight).
+//   m = mean(x),  v = mean((x - m)^2),  r = 1 / sqrt(v + eps),  xh = (x - m) r
+//   y = xh w + b
+//   t = dy w,  dx = r (t - mean(t) - xh mean(t xh)),  dw = sum over rows of dy xh,  db = sum of dy
+// Both directions are bound by HBM: every streamed value is read once, held in registers for
+// the two sums of its row (the variance is taken around the mean, in a second pass over the
+// registers), and written once.  All sums are float.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ssm_device.h"
+#include "ssm_internal.h"
+#include "ssm_profile.h"
+
+namespace ssm {
+namespace {
+
+// VEC consecutive elements, as floats
+template <int VEC>
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  } else {
+    static_assert(VEC == 1, "");
+    v[0] = *p;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_vec(const bf16_bits* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  } else {
+    static_assert(VEC == 1, "");
+    v[0] = load_elem(p);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else *p = v[0];
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(bf16_bits* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const bf16_bits lo = __builtin_bit_cast(bf16_bits, static_cast<__bf16>(v[2 * j]));
+      const bf16_bits hi = __builtin_bit_cast(bf16_bits, static_cast<__bf16>(v[2 * j + 1]));
+      w[j] = uint32_t(lo) | (uint32_t(hi) << 16);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    store_elem(p, v[0]);
+  }
+}
+// VEC floats of a parameter row (only 4-byte aligned: W need not be a multiple of 4)
+template <int VEC>
+__device__ __forceinline__ void load_par(const float* p, float (&v)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; j++) v[j] = p[j];
+}
+
+// Sums of N values over the TPR threads of a row, the same in every one of them.  Rows of at
+// most a wave's lanes are summed with shuffles; wider ones through LDS, each call with its own
+// `buf` half so that one barrier a call is enough.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sum(float (&s)[N], float* buf) {
+#pragma unroll
+  for (int off = (TPR < kWave ? TPR : kWave) / 2; off > 0; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; i++) s[i] += __shfl_xor(s[i], off);
+  if constexpr (TPR > kWave) {
+    constexpr int kWaves = TPR / kWave;
+    if (threadIdx.x % kWave == 0)
+#pragma unroll
+      for (int i = 0; i < N; i++) buf[i * kWaves + threadIdx.x / kWave] = s[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; w++) t += buf[i * kWaves + w];
+      s[i] = t;
+    }
+  }
+}
+
+constexpr int block_threads(int tpr) { return tpr > 256 ? tpr : 256; }
+
+// TPR threads a row, each with NV vectors of VEC elements at columns (j TPR + lane) VEC.
+template <typename T, int VEC, int NV, int TPR>
+__global__ __launch_bounds__(block_threads(TPR)) void ln_fwd_kernel(
+    const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias, float eps,
+    T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int64_t n_rows, int H, int W) {
+  constexpr int kGroups = block_threads(TPR) / TPR;
+  __shared__ float buf[2][TPR > kWave ? TPR / kWave : 1];
+  const int64_t row = int64_t(blockIdx.x) * kGroups + threadIdx.x / TPR;
+  const int lane = threadIdx.x % TPR;
+  if (row >= n_rows) return;  // whole rows leave; a row of several waves is a whole workgroup
+  const T* xr = x + row * W;
+  float v[NV][VEC];
+  float s[1] = {0.f};
+#pragma unroll
+  for (int j = 0; j < NV; j++) {
+    const int c = (j * TPR + lane) * VEC;
+    if (c < W) {
+      load_vec<VEC>(xr + c, v[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; i++) v[j][i] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NV; j++)
+#pragma unroll
+    for (int i = 0; i < VEC; i++) s[0] += v[j][i];
+  row_sum<TPR>(s, buf[0]);
+  const float m = s[0] / float(W);
+  float q[1] = {0.f};
+#pragma unroll
+  for (int j = 0; j < NV; j++) {
+    if ((j * TPR + lane) * VEC < W) {
+#pragma unroll
+      for (int i = 0; i < VEC; i++) {
+        v[j][i] -= m;
+        q[0] = fmaf(v[j][i], v[j][i], q[0]);
+      }
+    }
+  }
+  row_sum<TPR>(q, buf[1]);
+  const float r = 1.f / sqrtf(q[0] / float(W) + eps);
+  const int h = H == 1 ? 0 : int(row % H);
+  const float* wr = weight ? weight + int64_t(h) * W : nullptr;
+  const float* br = bias ? bias + int64_t(h) * W : nullptr;
+  T* yr = y + row * W;
+#pragma unroll
+  for (int j = 0; j < NV; j++) {
+    const int c = (j * TPR + lane) * VEC;
+    if (c < W) {
+      float wv[VEC], bv[VEC], o[VEC];
+      if (wr) load_par<VEC>(wr + c, wv);
+      if (br) load_par<VEC>(br + c, bv);
+#pragma unroll
+      for (int i = 0; i < VEC; i++) {
+        const float xh = v[j][i] * r;
+        o[i] = fmaf(xh, wr ? wv[i] : 1.f, br ? bv[i] : 0.f);
+      }
+      store_vec<VEC>(yr + c, o);
+    }
+  }
+  if (lane == 0) {
+    if (mean) mean[row] = m;
+    if (rstd) rstd[row] = r;
+  }
+}
+
+// One group of TPR threads walks the rows slice, slice + n_slices, ... of head h and keeps the
+// head's parameter gradients in registers; each group writes its own row of the partial sums
+// [n_slices][H W], which ln_reduce_kernel adds in a fixed order.
+template <typename T, int VEC, int NV, int TPR>
+__global__ __launch_bounds__(block_threads(TPR)) void ln_bwd_kernel(
+    const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx, float* __restrict__ part_w,
+    float* __restrict__ part_b, int64_t rows, int64_t n_slices, int H, int W) {
+  constexpr int kGroups = block_threads(TPR) / TPR;
+  __shared__ float buf[2][TPR > kWave ? 2 * (TPR / kWave) : 1];
+  const int64_t gid = int64_t(blockIdx.x) * kGroups + threadIdx.x / TPR;
+  const int lane = threadIdx.x % TPR;
+  if (gid >= n_slices * H) return;
+  const int h = int(gid % H);
+  const int64_t slice = gid / H;
+  float wv[NV][VEC], dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; j++) {
+    const int c = (j * TPR + lane) * VEC;
+#pragma unroll
+    for (int i = 0; i < VEC; i++) {
+      wv[j][i] = 1.f;
+      dw[j][i] = 0.f;
+      db[j][i] = 0.f;
+    }
+    if (weight && c < W) load_par<VEC>(weight + int64_t(h) * W + c, wv[j]);
+  }
+  const float inv_w = 1.f / float(W);
+  int phase = 0;
+  for (int64_t i0 = slice; i0 < rows; i0 += n_slices) {
+    const int64_t row = i0 * H + h;
+    const float m = mean[row], r = rstd[row];
+    float xh[NV][VEC], g[NV][VEC];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      const int c = (j * TPR + lane) * VEC;
+      if (c < W) {
+        load_vec<VEC>(x + row * W + c, xh[j]);
+        load_vec<VEC>(dy + row * W + c, g[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i++) {
+          xh[j][i] = m;
+          g[j][i] = 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+      for (int i = 0; i < VEC; i++) {
+        xh[j][i] = (xh[j][i] - m) * r;
+        dw[j][i] = fmaf(g[j][i], xh[j][i], dw[j][i]);
+        db[j][i] += g[j][i];
+        g[j][i] *= wv[j][i];
+        s[0] += g[j][i];
+        s[1] = fmaf(g[j][i], xh[j][i], s[1]);
+      }
+    row_sum<TPR>(s, buf[phase]);
+    phase ^= 1;  // a row's sums are read before the barrier of the next one, which frees this half
+    const float c1 = s[0] * inv_w, c2 = s[1] * inv_w;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      const int c = (j * TPR + lane) * VEC;
+      if (c < W) {
+        float o[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; i++) o[i] = r * (g[j][i] - fmaf(xh[j][i], c2, c1));
+        store_vec<VEC>(dx + row * W + c, o);
+      }
+    }
+  }
+  if (!part_w) return;
+  const int64_t at = (slice * H + h) * int64_t(W);
+#pragma unroll
+  for (int j = 0; j < NV; j++) {
+    const int c = (j * TPR + lane) * VEC;
+    if (c < W) {
+#pragma unroll
+      for (int i = 0; i < VEC; i++) {
+        part_w[at + c + i] = dw[j][i];
+        part_b[at + c + i] = db[j][i];
+      }
+    }
+  }
+}
+
+// out[k][c] = sum of in[k per .. k per + per - 1][c] over its rows below n, in order: 64 columns
+// and 4 row strides a workgroup; blockIdx.z chooses the weight's or the bias's sums.
+__global__ __launch_bounds__(256) void ln_reduce_kernel(const float* __restrict__ in_w, const float* __restrict__ in_b,
+                                                        float* __restrict__ out_w, float* __restrict__ out_b,
+                                                        int64_t n, int64_t per, int64_t cols) {
+  __shared__ float sh[4][64];
+  const float* in = blockIdx.z ? in_b : in_w;
+  float* out = blockIdx.z ? out_b : out_w;
+  const int l = threadIdx.x % 64, g = threadIdx.x / 64;
+  const int64_t c = int64_t(blockIdx.x) * 64 + l;
+  const int64_t r0 = int64_t(blockIdx.y) * per, r1 = r0 + per < n ? r0 + per : n;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < cols) {
+    int64_t r = r0 + g;
+    for (; r + 12 < r1; r += 16) {
+#pragma unroll
+      for (int u = 0; u < 4; u++) s[u] += in[(r + 4 * u) * cols + c];
+    }
+    for (; r < r1; r += 4) s[0] += in[r * cols + c];
+  }
+  sh[g][l] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (g == 0 && c < cols) out[blockIdx.y * cols + c] = (sh[0][l] + sh[1][l]) + (sh[2][l] + sh[3][l]);
+}
+
+constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <typename T, int VEC, int NV, int TPR>
+hipError_t fwd_one(const LayerNormArgs& a) {
+  constexpr int threads = block_threads(TPR), groups = threads / TPR;
+  const int64_t n = a.rows * a.H;
+  return launch_kind(kKindNormFwd, ln_fwd_kernel<T, VEC, NV, TPR>, ceil_div(n, groups), threads, a.stream,
+                     static_cast<const T*>(a.x), a.weight, a.bias, a.eps, static_cast<T*>(a.y), a.mean, a.rstd, n,
+                     int(a.H), int(a.W));
+}
+template <typename T, int VEC, int NV, int TPR>
+hipError_t bwd_one(const LayerNormArgs& a, int64_t n_slices, float* pw, float* pb) {
+  constexpr int threads = block_threads(TPR), groups = threads / TPR;
+  return launch_kind(kKindNormBwd, ln_bwd_kernel<T, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream,
+                     static_cast<const T*>(a.x), a.weight, a.mean, a.rstd, static_cast<const T*>(a.dy),
+                     static_cast<T*>(a.dx), pw, pb, a.rows, n_slices, int(a.H), int(a.W));
+}
+
+// rows read and written in 16-byte vectors: whole vectors a row, aligned tensors
+template <typename T>
+bool whole_vectors(const LayerNormArgs& a) {
+  constexpr int VEC = 16 / sizeof(T);
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
+                      reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.dx);
+  return a.W % VEC == 0 && p % 16 == 0;
+}
+
+// Threads a row of W elements takes in the backward, for the number of groups.
+template <typename T>
+int bwd_threads_a_row(bool vec, int64_t W) {
+  constexpr int VEC = 16 / sizeof(T);
+  const int64_t n = vec ? W / VEC : W;  // accesses a row
+  if (!vec) return n <= 64 ? 8 : n <= 512 ? 64 : n <= 2048 ? 256 : 1024;
+  return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 128 ? 64 : n <= 1024 ? 256 : 1024;
+}
+
+template <typename T>
+hipError_t launch_fwd(const LayerNormArgs& a) {
+  constexpr int V = 16 / sizeof(T);
+  if (!whole_vectors<T>(a)) {
+    if (a.W <= 64) return fwd_one<T, 1, 8, 8>(a);
+    if (a.W <= 1024) return fwd_one<T, 1, 16, 64>(a);
+    if (a.W <= 4096) return fwd_one<T, 1, 16, 256>(a);
+    return fwd_one<T, 1, 16, 1024>(a);
+  }
+  const int64_t n = a.W / V;
+  if (n <= 8) return fwd_one<T, V, 1, 8>(a);
+  if (n <= 16) return fwd_one<T, V, 1, 16>(a);
+  if (n <= 32) return fwd_one<T, V, 1, 32>(a);
+  if (n <= 64) return fwd_one<T, V, 1, 64>(a);
+  if (n <= 128) return fwd_one<T, V, 2, 64>(a);
+  if (n <= 256) return fwd_one<T, V, 1, 256>(a);
+  if (n <= 512) return fwd_one<T, V, 2, 256>(a);
+  if (n <= 1024) return fwd_one<T, V, 4, 256>(a);
+  return fwd_one<T, V, 4, 1024>(a);
+}
+
+template <typename T>
+hipError_t launch_bwd(const LayerNormArgs& a, int64_t n_slices, float* pw, float* pb) {
+  constexpr int V = 16 / sizeof(T);
+  if (!whole_vectors<T>(a)) {
+    if (a.W <= 64) return bwd_one<T, 1, 8, 8>(a, n_slices, pw, pb);
+    if (a.W <= 512) return bwd_one<T, 1, 8, 64>(a, n_slices, pw, pb);
+    if (a.W <= 2048) return bwd_one<T, 1, 8, 256>(a, n_slices, pw, pb);
+    return bwd_one<T, 1, 16, 1024>(a, n_slices, pw, pb);
+  }
+  const int64_t n = a.W / V;
+  if (n <= 8) return bwd_one<T, V, 1, 8>(a, n_slices, pw, pb);
+  if (n <= 16) return bwd_one<T, V, 1, 16>(a, n_slices, pw, pb);
+  if (n <= 32) return bwd_one<T, V, 1, 32>(a, n_slices, pw, pb);
+  if (n <= 64) return bwd_one<T, V, 1, 64>(a, n_slices, pw, pb);
+  if (n <= 128) return bwd_one<T, V, 2, 64>(a, n_slices, pw, pb);
+  if (n <= 256) return bwd_one<T, V, 1, 256>(a, n_slices, pw, pb);
+  if (n <= 512) return bwd_one<T, V, 2, 256>(a, n_slices, pw, pb);
+  if (n <= 1024) return bwd_one<T, V, 4, 256>(a, n_slices, pw, pb);
+  return bwd_one<T, V, 4, 1024>(a, n_slices, pw, pb);
+}
+
+// How the backward's parameter sums are cut: n_slices partial rows [H W], added in n_parts parts of
+// `per` rows and then together.
+struct NormPlan {
+  int64_t n_slices, n_parts, per;
+};
+NormPlan plan_bwd(const LayerNormArgs& a, bool vec) {
+  NormPlan p;
+  const int tpr = a.dtype == 0 ? bwd_threads_a_row<float>(vec, a.W) : bwd_threads_a_row<bf16_bits>(vec, a.W);
+  const int64_t groups = 1024 * (block_threads(tpr) / tpr);  // 1024 workgroups: four a CU
+  p.n_slices = std::max<int64_t>(1, std::min<int64_t>(a.rows, ceil_div(groups, a.H)));
+  const int64_t blocks = 2 * ceil_div(a.H * a.W, 64);
+  p.n_parts = std::max<int64_t>(1, std::min<int64_t>(ceil_div(512, blocks), p.n_slices / 32));
+  p.per = ceil_div(p.n_slices, p.n_parts);
+  p.n_parts = ceil_div(p.n_slices, p.per);
+  return p;
+}
+int64_t plan_floats(const LayerNormArgs& a, const NormPlan& p) {
+  return 2 * (p.n_slices + (p.n_parts > 1 ? p.n_parts : 0)) * a.H * a.W;
+}
+
+}  // namespace
+
+int64_t layernorm_max_width() { return 16384; }
+
+size_t layernorm_workspace_bytes(const LayerNormArgs& a) {
+  if (a.rows == 0 || a.H == 0 || a.W == 0) return 0;
+  // tensors of any alignment: the larger of the two forms
+  const int64_t n = std::max(plan_floats(a, plan_bwd(a, true)), plan_floats(a, plan_bwd(a, false)));
+  return size_t(n) * sizeof(float);
+}
+
+hipError_t launch_layernorm_fwd(const LayerNormArgs& a) {
+  return a.dtype == 0 ? launch_fwd<float>(a) : launch_fwd<bf16_bits>(a);
+}
+
+hipError_t launch_layernorm_bwd(const LayerNormArgs& a, void* workspace) {
+  const int64_t cols = a.H * a.W, blocks = ceil_div(cols, 64);
+  const bool params = a.dweight != nullptr;
+  auto reduce = [&](const float* iw, const float* ib, float* ow, float* ob, int64_t n, int64_t per, int64_t parts) {
+    return launch_kind_3d(kKindNormReduce, ln_reduce_kernel, dim3(unsigned(blocks), unsigned(parts), 2), 256, a.stream,
+                          iw, ib, ow, ob, n, per, cols);
+  };
+  if (a.rows == 0)  // sums over no rows
+    return params ? reduce(nullptr, nullptr, a.dweight, a.dbias, 0, 0, 1) : hipSuccess;
+  const bool vec = a.dtype == 0 ? whole_vectors<float>(a) : whole_vectors<bf16_bits>(a);
+  const NormPlan p = plan_bwd(a, vec);
+  float* pw = params ? static_cast<float*>(workspace) : nullptr;
+  float* pb = params ? pw + p.n_slices * cols : nullptr;
+  hipError_t err = a.dtype == 0 ? launch_bwd<float>(a, p.n_slices, pw, pb) : launch_bwd<bf16_bits>(a, p.n_slices, pw, pb);
+  if (err != hipSuccess || !params) return err;
+  if (p.n_parts == 1) return reduce(pw, pb, a.dweight, a.dbias, p.n_slices, p.n_slices, 1);
+  float* qw = pb + p.n_slices * cols;
+  float* qb = qw + p.n_parts * cols;
+  err = reduce(pw, pb, qw, qb, p.n_slices, p.per, p.n_parts);
+  if (err != hipSuccess) return err;
+  return reduce(qw, qb, a.dweight, a.dbias, p.n_parts, p.n_parts, 1);
+}
+
+}  // namespace ssm

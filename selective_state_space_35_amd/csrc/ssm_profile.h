@@ -24,7 +24,16 @@ enum : int {
   kKindSsdScan = 14,    // scalar-per-head scan: chunk outputs (matrix products)
   kKindFused = 15,      // single-pass scan: chunks of a block joined through LDS
   kKindWiden = 16,      // bf16 -> f32 copy of the B / C rows of a cut scan
-  kNumKinds = 17
+  kKindLinSweep = 17,   // linear attention: a sweep over the sequence (outputs, or a gradient)
+  kKindLinState = 18,   // linear attention: states of the segments of a cut sequence
+  kKindLinChain = 19,   // linear attention: chain of the segments' states
+  kKindLinGate = 20,    // linear attention backward: gradient of the gates
+  kKindLinReduce = 21,  // linear attention backward: sums over the heads of a group
+  kKindLinUpdate = 22,  // linear attention: single-token state update
+  kKindNormFwd = 23,    // layer norm
+  kKindNormBwd = 24,    // layer norm backward: input gradient, partial parameter gradients
+  kKindNormReduce = 25, // layer norm backward: sums of the partial parameter gradients
+  kNumKinds = 26
 };
 
 // When profiling is on, creates and records the start event on `s` and returns true.

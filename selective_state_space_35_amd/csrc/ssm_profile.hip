@@ -27,7 +27,9 @@ const char* const kNames[kNumKinds] = {"chunk_aggregate", "chunk_carry",   "scan
                                        "state_update",    "conv",          "conv_update",   "bwd_rows",
                                        "bwd_aggregate",   "bwd_carry",     "bwd_main",      "bwd_reduce",
                                        "ssd_state",       "ssd_carry",     "ssd_scan",      "scan_fused",
-                                       "widen_rows"};
+                                       "widen_rows",      "linattn_sweep", "linattn_state", "linattn_chain",
+                                       "linattn_gate",    "linattn_reduce", "linattn_update", "layernorm",
+                                       "layernorm_bwd",   "layernorm_reduce"};
 
 }  // namespace
 
