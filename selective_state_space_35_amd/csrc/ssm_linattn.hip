@@ -20,6 +20,7 @@
 
 #include <algorithm>
 
+#include "ssm_chain.h"
 #include "ssm_device.h"
 #include "ssm_internal.h"
 #include "ssm_profile.h"
@@ -52,8 +53,14 @@ struct Sweep {
   float* dots;
   const float* dstate;     // [b, H, VD, KD] (transposed); dstate_dot[b, H] = its product with the last state
   float* dstate_dot;
+  bool reverse;            // from the last token to the first
   int64_t b, L;
   int H, KD, VD;
+  // the cut: n_segs segments of seg_chunks chunks; with more than one, the state leaving segment s is in
+  // seg_state[b][s][H] (in the place of `init`, stored as `init` is) and the log decays' sums in seg_decay
+  int n_chunks, n_segs, seg_chunks;
+  float* seg_state;
+  float* seg_decay;
   hipStream_t stream;
 };
 
@@ -68,99 +75,605 @@ __device__ __forceinline__ float log_decay(const Sweep& p, int64_t bi, int64_t t
   return clamp_log(x);
 }
 
-__device__ __forceinline__ int64_t live_length(const int32_t* lengths, int64_t bi, int64_t L) {
-  if (!lengths) return L;
-  const int64_t n = lengths[bi];
-  return n < 0 ? 0 : n > L ? L : n;
+__device__ __forceinline__ int live_length(const int32_t* lengths, int64_t bi, int64_t L) {
+  const int n = lengths ? lengths[bi] : int(L);
+  return __builtin_amdgcn_readfirstlane(n < 0 ? 0 : n > L ? int(L) : n);
 }
 
-// sum of v over the 128 threads of the workgroup, in every thread
-__device__ __forceinline__ float block_sum(float v, float* sh) {
+// ---------------------------------------------------------------------------
+// Matrix products.  A fragment is one lane's 8 elements of an operand of 16 rows (or columns) by
+// 32: lane l holds row l % 16 and the contraction indices 8 (l / 16) .. + 7.  bf16 takes one
+// v_mfma_f32_16x16x32_bf16; float takes eight v_mfma_f32_16x16x4_f32, the j-th with every lane's
+// j-th element (the order of the contraction index is free, as long as both operands share it).
+// The result of 16 x 16 has, in lane l, rows 4 (l / 16) .. + 3 of column l % 16.
+// ---------------------------------------------------------------------------
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+struct f32x8 {
+  float v[8];
+};
+template <typename T>
+struct FragOf;
+template <>
+struct FragOf<bf16_bits> {
+  typedef bf16x8 type;
+};
+template <>
+struct FragOf<float> {
+  typedef f32x8 type;
+};
+template <typename T>
+using Frag = typename FragOf<T>::type;
+
+__device__ __forceinline__ f32x4 mma(const bf16x8& a, const bf16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(const f32x8& a, const f32x8& b, f32x4 c) {
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  __syncthreads();
-  if (threadIdx.x % kWave == 0) sh[threadIdx.x / kWave] = v;
-  __syncthreads();
-  return sh[0] + sh[1];
+  for (int j = 0; j < 8; j++) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
+  return c;
 }
 
-// The recurrence token by token: a workgroup holds a head's state, thread j its column j.
-template <typename T, bool REVERSE>
-__global__ __launch_bounds__(128) void lin_sweep_kernel(Sweep p) {
-  __shared__ float ks[kMaxDim], qs[kMaxDim], sh[2];
-  const int h = blockIdx.x % p.H;
-  const int64_t bi = blockIdx.x / p.H;
-  const int j = threadIdx.x;
-  const bool live = j < p.VD;
-  const int Hq = p.H / p.gq, Hk = p.H / p.gk, Hv = p.H / p.gv;
-  const int64_t n = live_length(p.lengths, bi, p.L);
-  float S[kMaxDim];
+__device__ __forceinline__ bf16x8 row_frag(const bf16_bits* p) { return *reinterpret_cast<const bf16x8*>(p); }
+__device__ __forceinline__ f32x8 row_frag(const float* p) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  return f32x8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+// Column c0 + step (i / 4) + i % 4 (i = lane % 16) of rows r .. r + 7 of a row-major LDS tile; r may
+// differ between the groups of 16 lanes.  bf16 goes through the transposing LDS read of gfx950: in a group of 16
+// lanes, lane m names 8 bytes and lane i receives element i % 4 of the bytes named by lanes
+// i / 4 + 4 j, j = 0..3.
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bf16x8 col_frag(const bf16_bits* t, int ld, int r, int c0, int step) {
+  const int m = threadIdx.x % 16;
+  const bf16_bits* p = t + (r + m / 4) * ld + c0 + step * (m % 4);
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)p);
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(p + 4 * ld));
+  const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+  return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
+}
+__device__ __forceinline__ f32x8 col_frag(const float* t, int ld, int r, int c0, int step) {
+  const int i = threadIdx.x % 16;
+  const float* p = t + r * ld + c0 + step * (i / 4) + i % 4;
+  f32x8 f;
 #pragma unroll
-  for (int i = 0; i < kMaxDim; i++) {
-    S[i] = 0.f;
-    if (p.init && live && i < p.KD) {
-      const int64_t at = (bi * p.H + h) * p.KD * p.VD;
-      S[i] = p.init_t ? p.init[at + int64_t(j) * p.KD + i] : p.init[at + int64_t(i) * p.VD + j];
-    }
-  }
-  for (int64_t i = 0; i < p.L; i++) {
-    const int64_t t = REVERSE ? p.L - 1 - i : i, row = bi * p.L + t;
-    const int64_t oat = (row * p.H + h) * p.VD + j;
-    if (t >= n) {
-      if (p.out && live) {
-        if (p.out_f32) static_cast<float*>(p.out)[oat] = 0.f;
-        else store_elem(static_cast<T*>(p.out) + oat, 0.f);
+  for (int j = 0; j < 8; j++) f.v[j] = p[j * ld];
+  return f;
+}
+
+// x as one rounded fragment, and (bf16) what the rounding left, rounded again
+__device__ __forceinline__ void make_frag(const float (&x)[8], bf16x8& hi) {
+#pragma unroll
+  for (int j = 0; j < 8; j++) hi[j] = static_cast<__bf16>(x[j]);
+}
+__device__ __forceinline__ void make_frag(const float (&x)[8], f32x8& hi) {
+#pragma unroll
+  for (int j = 0; j < 8; j++) hi.v[j] = x[j];
+}
+__device__ __forceinline__ bf16x8 rest_frag(const float (&x)[8], const bf16x8& hi) {
+  bf16x8 lo;
+#pragma unroll
+  for (int j = 0; j < 8; j++) lo[j] = static_cast<__bf16>(x[j] - static_cast<float>(hi[j]));
+  return lo;
+}
+__device__ __forceinline__ void frag_floats(const bf16x8& f, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j++) x[j] = static_cast<float>(f[j]);
+}
+__device__ __forceinline__ void frag_floats(const f32x8& f, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j++) x[j] = f.v[j];
+}
+
+// ---------------------------------------------------------------------------
+// Chunks of kC tokens.  A sweep counts positions from its own start: position i is token i, or in
+// reversed time token n - 1 - i of the row's n.  Rows of an LDS tile are positions.
+// ---------------------------------------------------------------------------
+constexpr int kC = 64;
+constexpr int kThreads = 256;  // four waves; wave w holds a quarter of the state's columns
+
+template <typename T, int DP>
+struct Tile {
+  static constexpr int kVec = 16 / sizeof(T);                  // elements of a 16-byte piece
+  static constexpr int kRow = DP / kVec;                       // pieces a row
+  static constexpr int kPieces = kC * kRow / kThreads;         // pieces a thread
+  static constexpr int ld = DP + kVec;                         // elements a row of the LDS tile (padded by one piece)
+  static constexpr int kElems = kC * ld;
+};
+
+// A chunk's rows of one tensor, on their way from memory to LDS: rows of D <= DP elements, `stride`
+// elements apart, the rest zero.  VEC: rows are whole 16-byte pieces, 16-byte aligned.
+template <typename T, int DP, bool VEC>
+struct Stage {
+  typedef Tile<T, DP> L;
+  uint4 r[L::kPieces];
+  // row0: the chunk's row of the lowest token; nv live rows
+  __device__ __forceinline__ void load(const T* row0, int stride, int D, int nv, bool reverse) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(row0);
+#pragma unroll
+    for (int j = 0; j < L::kPieces; j++) {
+      const int pc = threadIdx.x + j * kThreads;
+      const int i = pc / L::kRow, c = (pc % L::kRow) * L::kVec;
+      const int off = ((reverse ? nv - 1 - i : i) * stride + c) * int(sizeof(T));
+      if constexpr (VEC) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, i < nv && c < D ? off : 0x7fffffff, 0, 0);
+        r[j] = make_uint4(v[0], v[1], v[2], v[3]);
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < L::kVec; e++) {
+          const int o = i < nv && c + e < D ? off + e * int(sizeof(T)) : 0x7fffffff;
+          if constexpr (sizeof(T) == 4) w[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
+          else w[e / 2] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0)) << (16 * (e % 2));
+        }
+        r[j] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (p.dots && j == 0) p.dots[row * p.H + h] = 0.f;
-      continue;
     }
-    __syncthreads();
-    if (j < p.KD) {
-      ks[j] = load_elem(static_cast<const T*>(p.xk) + (row * Hk + h / p.gk) * p.KD + j);
-      qs[j] = load_elem(static_cast<const T*>(p.xq) + (row * Hq + h / p.gq) * p.KD + j);
+  }
+  __device__ __forceinline__ void store(T* tile) const {
+#pragma unroll
+    for (int j = 0; j < L::kPieces; j++) {
+      const int pc = threadIdx.x + j * kThreads;
+      *reinterpret_cast<uint4*>(tile + (pc / L::kRow) * L::ld + (pc % L::kRow) * L::kVec) = r[j];
+    }
+  }
+};
+
+// N consecutive elements of row[c ..] (c + j < D), as floats
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void load_part(const T* row, int c, int D, bool live, float (&x)[N]) {
+  if constexpr (VEC) {
+    static_assert(N == 4 || N == 8, "");
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int k = 0; k < N; k += 4) {
+        const float4 v = live && c + k < D ? *reinterpret_cast<const float4*>(row + c + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[k] = v.x; x[k + 1] = v.y; x[k + 2] = v.z; x[k + 3] = v.w;
+      }
     } else {
-      ks[j] = 0.f;
-      qs[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < N; k += 4) {
+        const uint2 v = live && c + k < D ? *reinterpret_cast<const uint2*>(row + c + k) : make_uint2(0, 0);
+        x[k] = __uint_as_float(v.x << 16); x[k + 1] = __uint_as_float(v.x & 0xffff0000u);
+        x[k + 2] = __uint_as_float(v.y << 16); x[k + 3] = __uint_as_float(v.y & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; k++) x[k] = live && c + k < D ? load_elem(row + c + k) : 0.f;
+  }
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return uint32_t(__builtin_bit_cast(bf16_bits, static_cast<__bf16>(lo))) |
+         (uint32_t(__builtin_bit_cast(bf16_bits, static_cast<__bf16>(hi))) << 16);
+}
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void store_part(T* row, int c, int D, const float (&x)[N]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+      if (c + k < D) {
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(row + c + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        else *reinterpret_cast<uint2*>(row + c + k) = make_uint2(pack_bf16(x[k], x[k + 1]), pack_bf16(x[k + 2], x[k + 3]));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; k++)
+      if (c + k < D) store_elem(row + c + k, x[k]);
+  }
+}
+
+// Decays of a chunk, for its kC positions, in LDS.  The running sum is kept in double, in units of
+// log 2, and handed on in two floats: differences of it are exact to fp32 even where a reset
+// put it at -10^4.
+struct Decays {
+  float hi[kC], lo[kC];  // running sum up to and with the position
+  float in[kC];          // exp of it: what the state entering the chunk has kept
+  float out[kC];         // exp(last - own) wscale: what a product written here keeps to the chunk's end
+  float all;             // exp of the last
+};
+// log decay of position i (one lane each): a token's own, or in reversed time the token's after it
+template <typename T>
+__device__ __forceinline__ float gate_of(const Sweep& p, int64_t bi, int h, int i, int n) {
+  const int t = p.reverse ? n - i : i;
+  if (i >= n || (p.reverse && i == 0)) return 0.f;
+  return log_decay<T>(p, bi, t, h);
+}
+// by one wave; returns the chunk's sum in natural units
+__device__ __forceinline__ double fill_decays(Decays& d, float gate, float wscale) {
+  const int l = threadIdx.x % kWave;
+  double run = double(gate) * 1.4426950408889634;
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const double o = __shfl_up(run, off);
+    if (l >= off) run += o;
+  }
+  const double last = __shfl(run, kWave - 1);
+  const float hi = float(run);
+  d.hi[l] = hi;
+  d.lo[l] = float(run - double(hi));
+  d.in[l] = exp2_fast(hi);
+  d.out[l] = exp2_fast(float(last - run)) * wscale;
+  if (l == 0) d.all = exp2_fast(float(last));
+  return last * 0.6931471805599453;
+}
+
+// The state in registers: wave w holds its VDP / 4 columns, as 16 x 16 results whose rows run along
+// the KDP index in the order that makes two neighbouring results an operand fragment: result m has, at
+// row i, index 32 (m / 2) + 4 (m % 2) + 8 (i / 4) + i % 4, so results 2 kk and 2 kk + 1 of a lane are
+// the 8 indices 32 kk + 8 (l / 16) .. + 7.  Columns likewise, where a wave has two results of them.
+template <int KDP, int VDP>
+struct Layout {
+  static constexpr int MT = KDP / 16, NT = VDP / 64, KS = KDP / 32;
+  static constexpr int vstep = NT == 2 ? 8 : 4;
+  static __device__ __forceinline__ int v0(int nt) { return int(threadIdx.x / kWave) * (VDP / 4) + 4 * nt; }
+  // column of lane index i of result nt
+  static __device__ __forceinline__ int col(int nt) {
+    const int i = threadIdx.x % 16;
+    return v0(nt) + vstep * (i / 4) + i % 4;
+  }
+  // first of the 4 rows that this lane holds of result m
+  static __device__ __forceinline__ int row(int m) {
+    return 32 * (m / 2) + 4 * (m % 2) + 8 * int((threadIdx.x % kWave) / 16);
+  }
+  typedef f32x4 State[MT][NT];
+  static __device__ __forceinline__ void zero(State& S) {
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+      for (int n = 0; n < NT; n++) S[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  static __device__ __forceinline__ void load(State& S, const float* src, bool transposed, int KD, int VD) {
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const int k = row(m) + r, v = col(n);
+          S[m][n][r] = k < KD && v < VD ? src[transposed ? v * KD + k : k * VD + v] : 0.f;
+        }
+  }
+  static __device__ __forceinline__ void store(const State& S, float* dst, int KD, int VD, float f) {
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const int k = row(m) + r, v = col(n);
+          if (k < KD && v < VD) dst[k * VD + v] = S[m][n][r] * f;
+        }
+  }
+};
+
+// S = all S + K^T (out o V) over a chunk.  The weighted values are split into two bf16 parts (2^-17 of
+// a product is lost; one part would lose 2^-9 and the state is a float result).
+template <typename T, int KDP, int VDP>
+__device__ __forceinline__ void write_state(typename Layout<KDP, VDP>::State& S, const T* Ks, const Frag<T> (&vf)[2][VDP / 64],
+                                            const Decays& d) {
+  typedef Layout<KDP, VDP> Y;
+  const int g8 = 8 * int((threadIdx.x % kWave) / 16);
+  Frag<T> hi[2][Y::NT], lo[2][Y::NT];
+#pragma unroll
+  for (int ks = 0; ks < 2; ks++) {
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) w[j] = d.out[32 * ks + g8 + j];
+#pragma unroll
+    for (int n = 0; n < Y::NT; n++) {
+      float x[8];
+      frag_floats(vf[ks][n], x);
+#pragma unroll
+      for (int j = 0; j < 8; j++) x[j] *= w[j];
+      make_frag(x, hi[ks][n]);
+      if constexpr (sizeof(T) == 2) lo[ks][n] = rest_frag(x, hi[ks][n]);
+    }
+  }
+  const float all = d.all;
+#pragma unroll
+  for (int m = 0; m < Y::MT; m++) {
+#pragma unroll
+    for (int n = 0; n < Y::NT; n++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) S[m][n][r] *= all;
+#pragma unroll
+    for (int ks = 0; ks < 2; ks++) {
+      const Frag<T> kf = col_frag(Ks, Tile<T, KDP>::ld, 32 * ks + g8, 32 * (m / 2) + 4 * (m % 2), 8);
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++) {
+        S[m][n] = mma(kf, hi[ks][n], S[m][n]);
+        if constexpr (sizeof(T) == 2) S[m][n] = mma(kf, lo[ks][n], S[m][n]);
+      }
+    }
+  }
+}
+
+// Where a workgroup is: its head, batch row, segment and the chunks of it.
+struct Place {
+  int h, seg, c0, c1, n;
+  int64_t bi, bh;
+};
+__device__ __forceinline__ Place place_of(const Sweep& p, int n_segs) {
+  Place w;
+  w.h = blockIdx.x % p.H;
+  const int rest = blockIdx.x / p.H;
+  w.seg = rest % n_segs;
+  w.bi = rest / n_segs;
+  w.bh = w.bi * p.H + w.h;
+  w.n = live_length(p.lengths, w.bi, p.L);
+  w.c0 = w.seg * p.seg_chunks;
+  w.c1 = min(w.c0 + p.seg_chunks, p.n_chunks);
+  return w;
+}
+
+// The row of a tensor of `heads` heads of D elements that token t of a batch row has for head h
+template <typename T>
+__device__ __forceinline__ const T* row_of(const void* x, const Sweep& p, const Place& w, int share, int64_t t, int D) {
+  return static_cast<const T*>(x) + ((w.bi * p.L + t) * (p.H / share) + w.h / share) * int64_t(D);
+}
+
+// ---------------------------------------------------------------------------
+// States of the segments of a cut sequence, each from zero, and the sums of their log decays.
+// ---------------------------------------------------------------------------
+template <typename T, int KDP, int VDP, bool VEC>
+__global__ __launch_bounds__(kThreads) void lin_state_kernel(Sweep p) {
+  typedef Layout<KDP, VDP> Y;
+  __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP>::kElems];
+  __shared__ __attribute__((aligned(16))) T Vs[Tile<T, VDP>::kElems];
+  __shared__ Decays d;
+  const Place w = place_of(p, p.n_segs - 1);
+  const int g8 = 8 * int((threadIdx.x % kWave) / 16);
+  Stage<T, KDP, VEC> sk;
+  Stage<T, VDP, VEC> sv;
+  float gate = 0.f;
+  auto fetch = [&](int c) {
+    const int p0 = c * kC, nv = max(0, min(kC, w.n - p0));
+    const int t0 = p.reverse ? w.n - p0 - nv : p0;
+    const int t = nv > 0 ? t0 : 0;
+    sk.load(row_of<T>(p.xk, p, w, p.gk, t, p.KD), p.H / p.gk * p.KD, p.KD, nv, p.reverse);
+    sv.load(row_of<T>(p.xv, p, w, p.gv, t, p.VD), p.H / p.gv * p.VD, p.VD, nv, p.reverse);
+    if (threadIdx.x < kWave) gate = gate_of<T>(p, w.bi, w.h, p0 + int(threadIdx.x), w.n);
+  };
+  typename Y::State S;
+  Y::zero(S);
+  double total = 0.0;
+  fetch(w.c0);
+  for (int c = w.c0; c < w.c1; c++) {
+    sk.store(Ks);
+    sv.store(Vs);
+    if (threadIdx.x < kWave) total += fill_decays(d, gate, p.wscale);
+    __syncthreads();
+    if (c + 1 < w.c1) fetch(c + 1);
+    Frag<T> vf[2][Y::NT];
+#pragma unroll
+    for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++) vf[ks][n] = col_frag(Vs, Tile<T, VDP>::ld, 32 * ks + g8, Y::v0(n), Y::vstep);
+    write_state<T, KDP, VDP>(S, Ks, vf, d);
+    __syncthreads();
+  }
+  const int64_t at = (w.bi * (p.n_segs - 1) + w.seg) * p.H + w.h;
+  Y::store(S, p.seg_state + at * p.KD * p.VD, p.KD, p.VD, 1.f);
+  if (threadIdx.x == 0) p.seg_decay[at] = float(total);
+}
+
+// ---------------------------------------------------------------------------
+// The sweep.  Per chunk:
+//   P[t][s] = (q_t . k_s) exp(G_t - G_s) for s <= t, computed as K Q^T (a lane then has four
+//             consecutive s of its t), 10 blocks of 16 x 16 shared out over the waves, to LDS
+//   out     = exp(G_t) S^T q_t + P V, as its transpose: a lane has consecutive columns of its own t
+//   S       = exp(G) S + K^T (out o V)
+// With DOTS the output without the token's own product is multiplied with the rows of xd, which
+// has to be right to fp32 over long sums: P and S go into the products as two bf16 parts.
+// ---------------------------------------------------------------------------
+template <typename T, int KDP, int VDP, bool DOTS, bool VEC>
+__global__ __launch_bounds__(kThreads) void lin_sweep_kernel(Sweep p) {
+  typedef Layout<KDP, VDP> Y;
+  constexpr bool kTwo = DOTS && sizeof(T) == 2;
+  constexpr int ldp = kC + 16 / int(sizeof(T)), kN = 4 * Y::NT;
+  constexpr int ldk = Tile<T, KDP>::ld, ldv = Tile<T, VDP>::ld;
+  __shared__ __attribute__((aligned(16))) T Qs[Tile<T, KDP>::kElems];
+  __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP>::kElems];
+  __shared__ __attribute__((aligned(16))) T Vs[Tile<T, VDP>::kElems];
+  __shared__ __attribute__((aligned(16))) T Ps[kTwo ? 2 : 1][kC * ldp];
+  __shared__ Decays d;
+  __shared__ float diag[DOTS ? kC : 1], dot_part[DOTS ? 4 : 1][kC], red[4];
+  const Place w = place_of(p, p.n_segs);
+  const int wv = threadIdx.x / kWave, l = threadIdx.x % kWave;
+  const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
+  const int vc = wv * (VDP / 4) + (l / 16) * kN;  // first of the kN columns that this lane has of an output row
+  const float sscale = p.wscale * p.rscale;
+  Stage<T, KDP, VEC> sq, sk;
+  Stage<T, VDP, VEC> sv;
+  float gate = 0.f;
+  auto fetch = [&](int c) {
+    const int p0 = c * kC, nv = max(0, min(kC, w.n - p0));
+    const int t = nv > 0 ? (p.reverse ? w.n - p0 - nv : p0) : 0;
+    sq.load(row_of<T>(p.xq, p, w, p.gq, t, p.KD), p.H / p.gq * p.KD, p.KD, nv, p.reverse);
+    sk.load(row_of<T>(p.xk, p, w, p.gk, t, p.KD), p.H / p.gk * p.KD, p.KD, nv, p.reverse);
+    sv.load(row_of<T>(p.xv, p, w, p.gv, t, p.VD), p.H / p.gv * p.VD, p.VD, nv, p.reverse);
+    if (threadIdx.x < kWave) gate = gate_of<T>(p, w.bi, w.h, p0 + int(threadIdx.x), w.n);
+  };
+  // the two blocks above the diagonal that the products read stay zero
+  for (int i = threadIdx.x; i < 2 * 16 * 16; i += kThreads) {
+    const int b = i / 256, t = 32 * b + (i / 16) % 16, s = 32 * b + 16 + i % 16;
+#pragma unroll
+    for (int k = 0; k < (kTwo ? 2 : 1); k++) Ps[k][t * ldp + s] = T(0);
+  }
+  typename Y::State S;
+  const float* from = w.seg > 0 ? p.seg_state + ((w.bi * (p.n_segs - 1) + w.seg - 1) * p.H + w.h) * p.KD * p.VD
+                                : p.init ? p.init + w.bh * p.KD * p.VD : nullptr;
+  if (from) Y::load(S, from, p.init_t, p.KD, p.VD);
+  else Y::zero(S);
+  if (w.c0 < w.c1) fetch(w.c0);
+  for (int c = w.c0; c < w.c1; c++) {
+    const int p0 = c * kC, nv = max(0, min(kC, w.n - p0));
+    sq.store(Qs);
+    sk.store(Ks);
+    sv.store(Vs);
+    if (threadIdx.x < kWave) fill_decays(d, gate, p.wscale);
+    __syncthreads();
+    if (c + 1 < w.c1) fetch(c + 1);
+    // the rows of xd for the lane's outputs
+    float xd[DOTS ? 4 : 1][DOTS ? kN : 1];
+    if constexpr (DOTS) {
+#pragma unroll
+      for (int tt = 0; tt < 4; tt++) {
+        const int i = 16 * tt + lr, t = p.reverse ? w.n - 1 - p0 - i : p0 + i;
+        load_part<T, kN, VEC>(row_of<T>(p.xd, p, w, p.gd, i < nv ? t : 0, p.VD), vc, p.VD, i < nv, xd[tt]);
+      }
+    }
+    // ---- P: blocks b = wv, wv + 4, wv + 8 of the ten (t block, s block) with s <= t ----
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+      const int b = wv + 4 * i;
+      if (b < 10) {
+        const int tb = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, sb = b - tb * (tb + 1) / 2;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kk = 0; kk < Y::KS; kk++)
+          acc = mma(row_frag(Ks + (16 * sb + lr) * ldk + 32 * kk + g8), row_frag(Qs + (16 * tb + lr) * ldk + 32 * kk + g8), acc);
+        const int t = 16 * tb + lr;
+        const float th = d.hi[t], tl = d.lo[t];
+        float x[4];
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const int s = 16 * sb + g4 + r;
+          const float e = exp2_fast((th - d.hi[s]) + (tl - d.lo[s])) * sscale;
+          x[r] = (DOTS ? s < t : s <= t) ? acc[r] * e : 0.f;
+          if (DOTS && s == t) diag[t] = acc[r] * sscale;
+        }
+        T* pr = Ps[0] + t * ldp + 16 * sb + g4;
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<float4*>(pr) = make_float4(x[0], x[1], x[2], x[3]);
+        } else {
+          const uint2 hi = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+          *reinterpret_cast<uint2*>(pr) = hi;
+          if constexpr (kTwo) {
+            const float y[4] = {x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xffff0000u),
+                                x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xffff0000u)};
+            *reinterpret_cast<uint2*>(Ps[1] + t * ldp + 16 * sb + g4) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+          }
+        }
+      }
+    }
+    // ---- the entering state's part of the outputs ----
+    f32x4 o[4][Y::NT];
+#pragma unroll
+    for (int tt = 0; tt < 4; tt++)
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++) o[tt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kk = 0; kk < Y::KS; kk++) {
+      Frag<T> sh[Y::NT], sl[Y::NT];
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++) {
+        float x[8];
+#pragma unroll
+        for (int r = 0; r < 8; r++) x[r] = S[2 * kk + r / 4][n][r % 4];
+        make_frag(x, sh[n]);
+        if constexpr (kTwo) sl[n] = rest_frag(x, sh[n]);
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; tt++) {
+        const Frag<T> qf = row_frag(Qs + (16 * tt + lr) * ldk + 32 * kk + g8);
+#pragma unroll
+        for (int n = 0; n < Y::NT; n++) {
+          o[tt][n] = mma(sh[n], qf, o[tt][n]);
+          if constexpr (kTwo) o[tt][n] = mma(sl[n], qf, o[tt][n]);
+        }
+      }
+    }
+#pragma unroll
+    for (int tt = 0; tt < 4; tt++) {
+      const float f = d.in[16 * tt + lr] * p.rscale;
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) o[tt][n][r] *= f;
     }
     __syncthreads();
-    const float v = live ? load_elem(static_cast<const T*>(p.xv) + (row * Hv + h / p.gv) * p.VD + j) * p.wscale : 0.f;
-    float dec;
-    if (REVERSE) dec = t + 1 < n ? expf(log_decay<T>(p, bi, t + 1, h)) : 1.f;
-    else dec = expf(log_decay<T>(p, bi, t, h));
-    float o = 0.f, qk = 0.f;
+    // ---- the chunk's own part ----
+    Frag<T> vf[2][Y::NT];
 #pragma unroll
-    for (int i2 = 0; i2 < kMaxDim; i2++) {
-      S[i2] *= dec;
-      o = fmaf(qs[i2], S[i2], o);
-      qk = fmaf(qs[i2], ks[i2], qk);
-      S[i2] = fmaf(ks[i2], v, S[i2]);
+    for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++) vf[ks][n] = col_frag(Vs, ldv, 32 * ks + g8, Y::v0(n), Y::vstep);
+#pragma unroll
+    for (int tt = 0; tt < 4; tt++)
+#pragma unroll
+      for (int ks = 0; ks <= tt / 2; ks++)
+#pragma unroll
+        for (int k = 0; k < (kTwo ? 2 : 1); k++) {
+          const Frag<T> pf = row_frag(Ps[k] + (16 * tt + lr) * ldp + 32 * ks + g8);
+#pragma unroll
+          for (int n = 0; n < Y::NT; n++) o[tt][n] = mma(vf[ks][n], pf, o[tt][n]);
+        }
+    // ---- outputs ----
+#pragma unroll
+    for (int tt = 0; tt < 4; tt++) {
+      const int i = 16 * tt + lr;
+      float y[kN];
+#pragma unroll
+      for (int j = 0; j < kN; j++) y[j] = o[tt][j / 4][j % 4];
+      if constexpr (DOTS) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < kN; j++) s = fmaf(y[j], xd[tt][j], s);
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (l < 16) dot_part[wv][i] = s;
+        const float dg = diag[i];
+#pragma unroll
+        for (int j = 0; j < kN; j++) y[j] = fmaf(dg, load_elem(Vs + i * ldv + vc + j), y[j]);
+      }
+      if (p.out && p0 + i < p.L) {
+        if (i >= nv) {
+#pragma unroll
+          for (int j = 0; j < kN; j++) y[j] = 0.f;
+        }
+        const int64_t t = i >= nv ? p0 + i : p.reverse ? w.n - 1 - p0 - i : p0 + i;
+        const int64_t at = ((w.bi * p.L + t) * p.H + w.h) * p.VD;
+        if (p.out_f32) store_part<float, kN, VEC>(static_cast<float*>(p.out) + at, vc, p.VD, y);
+        else store_part<T, kN, VEC>(static_cast<T*>(p.out) + at, vc, p.VD, y);
+      }
     }
-    o *= p.rscale;
-    if (p.dots) {
-      const int Hd = p.H / p.gd;
-      const float x = live ? load_elem(static_cast<const T*>(p.xd) + (row * Hd + h / p.gd) * p.VD + j) : 0.f;
-      const float d = block_sum(o * x, sh);
-      if (j == 0) p.dots[row * p.H + h] = d;
-    }
-    o = fmaf(qk * p.rscale, v, o);
-    if (p.out && live) {
-      if (p.out_f32) static_cast<float*>(p.out)[oat] = o;
-      else store_elem(static_cast<T*>(p.out) + oat, o);
+    write_state<T, KDP, VDP>(S, Ks, vf, d);
+    __syncthreads();
+    if constexpr (DOTS) {
+      const int i = threadIdx.x;
+      if (i < kC && p0 + i < p.L) {
+        const int64_t t = i >= nv ? p0 + i : p.reverse ? w.n - 1 - p0 - i : p0 + i;
+        p.dots[(w.bi * p.L + t) * p.H + w.h] =
+            i < nv ? (dot_part[0][i] + dot_part[1][i]) + (dot_part[2][i] + dot_part[3][i]) : 0.f;
+      }
     }
   }
-  if (p.dstate_dot) {
-    float d = 0.f;
+  if (w.seg != p.n_segs - 1) return;
+  if (DOTS && p.dstate_dot) {
+    const float* src = p.dstate + w.bh * p.KD * p.VD;  // [VD][KD]
+    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMaxDim; i++)
-      if (p.dstate && live && i < p.KD) d += S[i] * p.dstate[((bi * p.H + h) * p.VD + j) * p.KD + i];
-    d = block_sum(d, sh);
-    if (j == 0) p.dstate_dot[bi * p.H + h] = d;
+    for (int m = 0; m < Y::MT; m++)
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const int k = Y::row(m) + r, v = Y::col(n);
+          if (k < p.KD && v < p.VD) s = fmaf(S[m][n][r], src[v * p.KD + k], s);
+        }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+    if (l == 0) red[wv] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) p.dstate_dot[w.bh] = (red[0] + red[1]) + (red[2] + red[3]);
   }
-  if (p.last && live) {
-    const float f = p.final_decay && n > 0 ? expf(log_decay<T>(p, bi, 0, h)) : 1.f;
-#pragma unroll
-    for (int i = 0; i < kMaxDim; i++)
-      if (i < p.KD) p.last[((bi * p.H + h) * p.KD + i) * p.VD + j] = S[i] * f;
+  if (p.last) {
+    const float f = p.final_decay && w.n > 0 ? exp2_fast(log_decay<T>(p, w.bi, 0, w.h) * kLog2e) : 1.f;
+    Y::store(S, p.last + w.bh * p.KD * p.VD, p.KD, p.VD, f);
   }
 }
 
@@ -319,10 +832,67 @@ __global__ __launch_bounds__(256) void lin_update_kernel(float* __restrict__ sta
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// rows of whole 16-byte pieces, 16-byte aligned
 template <typename T>
-hipError_t run_sweep(const Sweep& p, bool reverse) {
-  if (reverse) return launch_kind(kKindLinSweep, lin_sweep_kernel<T, true>, p.b * p.H, 128, p.stream, p);
-  return launch_kind(kKindLinSweep, lin_sweep_kernel<T, false>, p.b * p.H, 128, p.stream, p);
+bool pieces(const void* x, int D) {
+  return D % (16 / int(sizeof(T))) == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+}
+
+template <typename T, int KDP, int VDP, bool DOTS>
+hipError_t sweep_kernel(const Sweep& p, bool vec) {
+  const int64_t blocks = p.b * p.H * p.n_segs;
+  return vec ? launch_kind(kKindLinSweep, lin_sweep_kernel<T, KDP, VDP, DOTS, true>, blocks, kThreads, p.stream, p)
+             : launch_kind(kKindLinSweep, lin_sweep_kernel<T, KDP, VDP, DOTS, false>, blocks, kThreads, p.stream, p);
+}
+template <typename T, bool DOTS>
+hipError_t sweep_sizes(const Sweep& p, bool vec) {
+  if (p.KD <= 64) return p.VD <= 64 ? sweep_kernel<T, 64, 64, DOTS>(p, vec) : sweep_kernel<T, 64, 128, DOTS>(p, vec);
+  return p.VD <= 64 ? sweep_kernel<T, 128, 64, DOTS>(p, vec) : sweep_kernel<T, 128, 128, DOTS>(p, vec);
+}
+template <typename T>
+hipError_t run_sweep(const Sweep& p) {
+  const bool vec = pieces<T>(p.xq, p.KD) && pieces<T>(p.xk, p.KD) && pieces<T>(p.xv, p.VD) &&
+                   (!p.out || pieces<T>(p.out, p.VD)) && (!p.xd || pieces<T>(p.xd, p.VD));
+  return p.dots ? sweep_sizes<T, true>(p, vec) : sweep_sizes<T, false>(p, vec);
+}
+
+template <typename T, int KDP, int VDP>
+hipError_t state_kernel(const Sweep& p, bool vec) {
+  const int64_t blocks = p.b * p.H * (p.n_segs - 1);
+  return vec ? launch_kind(kKindLinState, lin_state_kernel<T, KDP, VDP, true>, blocks, kThreads, p.stream, p)
+             : launch_kind(kKindLinState, lin_state_kernel<T, KDP, VDP, false>, blocks, kThreads, p.stream, p);
+}
+// States leaving the segments of a cut sequence: every segment's own, then the chain over them.
+template <typename T>
+hipError_t run_states(const Sweep& p) {
+  if (p.n_segs <= 1) return hipSuccess;
+  const bool vec = pieces<T>(p.xk, p.KD) && pieces<T>(p.xv, p.VD);
+  hipError_t err = p.KD <= 64 ? (p.VD <= 64 ? state_kernel<T, 64, 64>(p, vec) : state_kernel<T, 64, 128>(p, vec))
+                              : (p.VD <= 64 ? state_kernel<T, 128, 64>(p, vec) : state_kernel<T, 128, 128>(p, vec));
+  if (err != hipSuccess) return err;
+  ChainArgs c{};
+  c.agg = p.seg_state; c.sums = p.seg_decay;
+  c.init = p.init;
+  c.outer = p.b; c.mid = p.H; c.inner = p.KD * p.VD; c.N = c.inner;
+  c.n_chunks = c.K = p.n_segs - 1;
+  return launch_chain<false, false, false>(kKindLinChain, c, p.stream);
+}
+
+// The cut of a sequence: segments so that the workgroups fill the chip twice, of at least kMinSeg chunks.
+constexpr int kMinSeg = 4;
+struct Cut {
+  int n_chunks, n_segs, seg_chunks;
+};
+Cut cut_of(const LinAttnArgs& a) {
+  Cut c;
+  c.n_chunks = int(ceil_div(a.L, kC));
+  const int64_t heads = a.b * a.H;
+  const int64_t want = std::max<int64_t>(1, ceil_div(512, std::max<int64_t>(heads, 1)));
+  const int64_t most = std::max<int64_t>(1, c.n_chunks / kMinSeg);
+  c.n_segs = int(std::min(want, most));
+  c.seg_chunks = int(std::max<int64_t>(1, ceil_div(c.n_chunks, c.n_segs)));
+  c.n_segs = int(std::max<int64_t>(1, ceil_div(c.n_chunks, c.seg_chunks)));
+  return c;
 }
 
 Sweep common(const LinAttnArgs& a) {
@@ -331,48 +901,93 @@ Sweep common(const LinAttnArgs& a) {
   p.wscale = p.rscale = 1.f;
   p.gq = p.gk = p.gv = p.gd = 1;
   p.b = a.b; p.L = a.L; p.H = int(a.H);
+  const Cut c = cut_of(a);
+  p.n_chunks = c.n_chunks; p.n_segs = c.n_segs; p.seg_chunks = c.seg_chunks;
   p.stream = a.stream;
   return p;
 }
 
-// The backward's workspace, in bytes from its start.
-struct BwdWork {
+// Bytes from the workspace's start of its parts.
+struct Work {
+  size_t seg_f, dec_f, seg_r, dec_r;  // segment states and decays, forwards and (backward) in reversed time
   size_t dot_q, dot_k, end, sums, dq, dk, total;
   int n_tiles;
 };
-BwdWork plan_bwd(const LinAttnArgs& a) {
-  BwdWork w{};
+Work plan_work(const LinAttnArgs& a, bool backward) {
+  Work w{};
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t r = at;
     at += up256(bytes);
     return r;
   };
-  const size_t rows = size_t(a.b) * a.L * a.H;
-  w.n_tiles = int(ceil_div(a.L, kGateTile));
-  w.dot_q = take(rows * 4);
-  w.dot_k = take(rows * 4);
-  w.end = take(size_t(a.b) * a.H * 4);
-  w.sums = take(size_t(a.b) * w.n_tiles * a.H * 8);
-  if (a.G != a.H) {
-    w.dq = take(rows * a.Dk * 4);
-    w.dk = take(rows * a.Dk * 4);
+  const size_t heads = size_t(a.b) * a.H, segs = heads * (cut_of(a).n_segs - 1);
+  w.seg_f = take(segs * a.Dk * a.Dv * 4);
+  w.dec_f = take(segs * 4);
+  if (backward) {
+    const size_t rows = heads * a.L;
+    w.n_tiles = int(ceil_div(a.L, kGateTile));
+    w.seg_r = take(segs * a.Dk * a.Dv * 4);
+    w.dec_r = take(segs * 4);
+    w.dot_q = take(rows * 4);
+    w.dot_k = take(rows * 4);
+    w.end = take(heads * 4);
+    w.sums = take(heads * w.n_tiles * 8);
+    if (a.G != a.H) {
+      w.dq = take(rows * a.Dk * 4);
+      w.dk = take(rows * a.Dk * 4);
+    }
   }
   w.total = at;
   return w;
 }
 
 template <typename T>
+hipError_t fwd_impl(const LinAttnArgs& a, char* ws) {
+  const Work w = plan_work(a, false);
+  const int share = int(a.H / a.G);
+  Sweep p = common(a);
+  p.xq = a.q; p.xk = a.k; p.xv = a.v; p.gq = p.gk = share;
+  p.KD = int(a.Dk); p.VD = int(a.Dv);
+  p.rscale = a.scale;
+  p.init = a.h0;
+  p.seg_state = reinterpret_cast<float*>(ws + w.seg_f); p.seg_decay = reinterpret_cast<float*>(ws + w.dec_f);
+  const hipError_t err = run_states<T>(p);
+  if (err != hipSuccess) return err;
+  p.out = a.y;
+  p.last = a.last;
+  return run_sweep<T>(p);
+}
+
+template <typename T>
 hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
-  const BwdWork w = plan_bwd(a);
+  const Work w = plan_work(a, true);
   const int share = int(a.H / a.G);
   const bool gate = a.dg != nullptr;
   float* end = gate && a.dlast ? reinterpret_cast<float*>(ws + w.end) : nullptr;
+  float* seg_f = reinterpret_cast<float*>(ws + w.seg_f);
+  float* dec_f = reinterpret_cast<float*>(ws + w.dec_f);
+  float* seg_r = reinterpret_cast<float*>(ws + w.seg_r);
+  float* dec_r = reinterpret_cast<float*>(ws + w.dec_r);
+  hipError_t err = hipSuccess;
+  if (common(a).n_segs > 1) {  // the segments' S and D, [Dk, Dv]; dq and dk read them transposed
+    Sweep p = common(a);
+    p.xk = a.k; p.gk = share; p.xv = a.v;
+    p.KD = int(a.Dk); p.VD = int(a.Dv);
+    p.init = a.h0; p.seg_state = seg_f; p.seg_decay = dec_f;
+    err = run_states<T>(p);
+    if (err != hipSuccess) return err;
+    p.xk = a.q; p.xv = a.dy;
+    p.wscale = a.scale; p.reverse = true;
+    p.init = a.dlast; p.seg_state = seg_r; p.seg_decay = dec_r;
+    err = run_states<T>(p);
+    if (err != hipSuccess) return err;
+  }
   Sweep p = common(a);  // dq: forwards, the state is S^T [Dv, Dk]
   p.xq = a.dy; p.xk = a.v; p.xv = a.k; p.gv = share;
   p.KD = int(a.Dv); p.VD = int(a.Dk);
   p.rscale = a.scale;
-  p.init = a.h0; p.init_t = true;
+  p.init = a.h0; p.init_t = true; p.seg_state = seg_f;
   p.out = share > 1 ? static_cast<void*>(ws + w.dq) : a.dq; p.out_f32 = share > 1;
   if (gate) {
     p.xd = a.q; p.gd = share;
@@ -380,28 +995,28 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
     p.dstate = a.dlast;
     p.dstate_dot = end;
   }
-  hipError_t err = run_sweep<T>(p, false);
+  err = run_sweep<T>(p);
   if (err != hipSuccess) return err;
   p = common(a);  // dk: backwards, the state is D^T [Dv, Dk]
   p.xq = a.v; p.xk = a.dy; p.xv = a.q; p.gv = share;
   p.KD = int(a.Dv); p.VD = int(a.Dk);
-  p.wscale = a.scale;
-  p.init = a.dlast; p.init_t = true;
+  p.wscale = a.scale; p.reverse = true;
+  p.init = a.dlast; p.init_t = true; p.seg_state = seg_r;
   p.out = share > 1 ? static_cast<void*>(ws + w.dk) : a.dk; p.out_f32 = share > 1;
   if (gate) {
     p.xd = a.k; p.gd = share;
     p.dots = reinterpret_cast<float*>(ws + w.dot_k);
   }
-  err = run_sweep<T>(p, true);
+  err = run_sweep<T>(p);
   if (err != hipSuccess) return err;
   p = common(a);  // dv: backwards, the state is D [Dk, Dv]
   p.xq = a.k; p.gq = share; p.xk = a.q; p.gk = share; p.xv = a.dy;
   p.KD = int(a.Dk); p.VD = int(a.Dv);
-  p.wscale = a.scale;
-  p.init = a.dlast;
+  p.wscale = a.scale; p.reverse = true;
+  p.init = a.dlast; p.seg_state = seg_r;
   p.out = a.dv;
   p.last = a.dh0; p.final_decay = true;
-  err = run_sweep<T>(p, true);
+  err = run_sweep<T>(p);
   if (err != hipSuccess || a.L == 0) return err;
   if (share > 1) {
     const int64_t n = a.b * a.L * a.G * a.Dk;
@@ -447,20 +1062,13 @@ int64_t linattn_max_dim() { return kMaxDim; }
 int64_t linattn_max_heads() { return 65535; }
 
 size_t linattn_workspace_bytes(const LinAttnArgs& a, bool backward) {
-  if (a.b == 0 || a.H == 0 || !backward) return 0;
-  return plan_bwd(a).total;
+  if (a.b == 0 || a.H == 0) return 0;
+  return plan_work(a, backward).total;
 }
 
-hipError_t launch_linattn_fwd(const LinAttnArgs& a, void*) {
-  const int share = int(a.H / a.G);
-  Sweep p = common(a);
-  p.xq = a.q; p.xk = a.k; p.xv = a.v; p.gq = p.gk = share;
-  p.KD = int(a.Dk); p.VD = int(a.Dv);
-  p.rscale = a.scale;
-  p.init = a.h0;
-  p.out = a.y;
-  p.last = a.last;
-  return a.dtype == 0 ? run_sweep<float>(p, false) : run_sweep<bf16_bits>(p, false);
+hipError_t launch_linattn_fwd(const LinAttnArgs& a, void* workspace) {
+  char* ws = static_cast<char*>(workspace);
+  return a.dtype == 0 ? fwd_impl<float>(a, ws) : fwd_impl<bf16_bits>(a, ws);
 }
 
 hipError_t launch_linattn_bwd(const LinAttnArgs& a, void* workspace) {
