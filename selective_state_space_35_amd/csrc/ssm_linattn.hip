@@ -167,6 +167,17 @@ __device__ __forceinline__ void frag_floats(const f32x8& f, float (&x)[8]) {
 }
 
 // ---------------------------------------------------------------------------
+// Workgroups of a CU (= waves of a SIMD) that the registers are held to; the LDS has room for as many.
+#define SSM_LIN_WAVES(n) __attribute__((amdgpu_waves_per_eu(n, n)))
+template <typename T>
+constexpr int sweep_waves(int kd, int vd, bool dots) {
+  return sizeof(T) == 4 ? (kd + vd > 128 ? 1 : 2) : kd + vd > 128 ? 2 : 3;
+}
+template <typename T>
+constexpr int state_waves(int kd, int vd) {
+  return sizeof(T) == 4 ? 2 : kd + vd > 128 ? 2 : 4;
+}
+
 // Chunks of kC tokens.  A sweep counts positions from its own start: position i is token i, or in
 // reversed time token n - 1 - i of the row's n.  Rows of an LDS tile are positions.
 // ---------------------------------------------------------------------------
@@ -183,40 +194,61 @@ struct Tile {
 };
 
 // A chunk's rows of one tensor, on their way from memory to LDS: rows of D <= DP elements, `stride`
-// elements apart, the rest zero.  VEC: rows are whole 16-byte pieces, 16-byte aligned.
+// elements apart, the rest zero.  VEC: rows are whole 16-byte pieces, 16-byte aligned.  A thread's
+// pieces are kStep rows apart, so one lane offset serves them all, the steps and the chunks being
+// wave-uniform.  In reversed time the descriptor starts at the chunk's last position: position i is
+// row 63 - i of it, and rows below a short last chunk's, which are not read, may lie before the tensor.
 template <typename T, int DP, bool VEC>
 struct Stage {
   typedef Tile<T, DP> L;
+  static constexpr int kStep = kThreads / L::kRow;  // rows between a thread's pieces
   uint4 r[L::kPieces];
-  // row0: the chunk's row of the lowest token; nv live rows
-  __device__ __forceinline__ void load(const T* row0, int stride, int D, int nv, bool reverse) {
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(row0);
+  const T* base;     // row of the chunk's first position, or (reversed) of position 63
+  int voff, soff, sstep, chunk, live_cols;
+  // first: row of position p0 of the sweep (reversed: of position p0 + 63, maybe before the tensor)
+  __device__ __forceinline__ void init(const T* first, int stride, int D, bool reverse) {
+    const int i = threadIdx.x / L::kRow, c = (threadIdx.x % L::kRow) * L::kVec;
+    base = first;
+    chunk = reverse ? -kC * stride : kC * stride;
+    sstep = kStep * stride * int(sizeof(T));
+    soff = 0;
+    if (reverse) {
+      voff = ((kStep - 1 - i) * stride + c) * int(sizeof(T));
+      soff = (L::kPieces - 1) * sstep;
+      sstep = -sstep;
+    } else {
+      voff = (i * stride + c) * int(sizeof(T));
+    }
+    live_cols = D - c;
+    if (live_cols <= 0) voff = 0x7fffffff;
+  }
+  // the next chunk, of nv live positions
+  __device__ __forceinline__ void load(int nv) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base);
+    base += chunk;
+    const int i = threadIdx.x / L::kRow;
 #pragma unroll
     for (int j = 0; j < L::kPieces; j++) {
-      const int pc = threadIdx.x + j * kThreads;
-      const int i = pc / L::kRow, c = (pc % L::kRow) * L::kVec;
-      const int off = ((reverse ? nv - 1 - i : i) * stride + c) * int(sizeof(T));
+      const int o = i + j * kStep < nv ? voff : 0x7fffffff;
       if constexpr (VEC) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, i < nv && c < D ? off : 0x7fffffff, 0, 0);
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, o, soff + j * sstep, 0);
         r[j] = make_uint4(v[0], v[1], v[2], v[3]);
       } else {
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < L::kVec; e++) {
-          const int o = i < nv && c + e < D ? off + e * int(sizeof(T)) : 0x7fffffff;
-          if constexpr (sizeof(T) == 4) w[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
-          else w[e / 2] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0)) << (16 * (e % 2));
+          const int oe = i + j * kStep < nv && e < live_cols ? voff + e * int(sizeof(T)) : 0x7fffffff;
+          if constexpr (sizeof(T) == 4) w[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, oe, soff + j * sstep, 0);
+          else w[e / 2] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b16(rs, oe, soff + j * sstep, 0)) << (16 * (e % 2));
         }
         r[j] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
   __device__ __forceinline__ void store(T* tile) const {
+    T* to = tile + (threadIdx.x / L::kRow) * L::ld + (threadIdx.x % L::kRow) * L::kVec;
 #pragma unroll
-    for (int j = 0; j < L::kPieces; j++) {
-      const int pc = threadIdx.x + j * kThreads;
-      *reinterpret_cast<uint4*>(tile + (pc / L::kRow) * L::ld + (pc % L::kRow) * L::kVec) = r[j];
-    }
+    for (int j = 0; j < L::kPieces; j++) *reinterpret_cast<uint4*>(to + j * kStep * L::ld) = r[j];
   }
 };
 
@@ -415,36 +447,44 @@ __device__ __forceinline__ const T* row_of(const void* x, const Sweep& p, const 
   return static_cast<const T*>(x) + ((w.bi * p.L + t) * (p.H / share) + w.h / share) * int64_t(D);
 }
 
+// Where a Stage of the tensor starts: the row of the sweep's position 64 c0, or in reversed time of position 64 c0 + 63
+template <typename T>
+__device__ __forceinline__ const T* start_of(const void* x, const Sweep& p, const Place& w, int share, int D) {
+  const int64_t t = p.reverse ? int64_t(w.n) - int64_t(w.c0) * kC - kC : int64_t(w.c0) * kC;
+  return row_of<T>(x, p, w, share, t, D);
+}
+
 // ---------------------------------------------------------------------------
 // States of the segments of a cut sequence, each from zero, and the sums of their log decays.
 // ---------------------------------------------------------------------------
 template <typename T, int KDP, int VDP, bool VEC>
-__global__ __launch_bounds__(kThreads) void lin_state_kernel(Sweep p) {
+__global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) void lin_state_kernel(Sweep p) {
   typedef Layout<KDP, VDP> Y;
   __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP>::kElems];
   __shared__ __attribute__((aligned(16))) T Vs[Tile<T, VDP>::kElems];
-  __shared__ Decays d;
+  __shared__ Decays ds[2];
   const Place w = place_of(p, p.n_segs - 1);
   const int g8 = 8 * int((threadIdx.x % kWave) / 16);
   Stage<T, KDP, VEC> sk;
   Stage<T, VDP, VEC> sv;
+  sk.init(start_of<T>(p.xk, p, w, p.gk, p.KD), p.H / p.gk * p.KD, p.KD, p.reverse);
+  sv.init(start_of<T>(p.xv, p, w, p.gv, p.VD), p.H / p.gv * p.VD, p.VD, p.reverse);
   float gate = 0.f;
   auto fetch = [&](int c) {
-    const int p0 = c * kC, nv = max(0, min(kC, w.n - p0));
-    const int t0 = p.reverse ? w.n - p0 - nv : p0;
-    const int t = nv > 0 ? t0 : 0;
-    sk.load(row_of<T>(p.xk, p, w, p.gk, t, p.KD), p.H / p.gk * p.KD, p.KD, nv, p.reverse);
-    sv.load(row_of<T>(p.xv, p, w, p.gv, t, p.VD), p.H / p.gv * p.VD, p.VD, nv, p.reverse);
-    if (threadIdx.x < kWave) gate = gate_of<T>(p, w.bi, w.h, p0 + int(threadIdx.x), w.n);
+    const int nv = w.n - c * kC;
+    sk.load(nv);
+    sv.load(nv);
+    if (threadIdx.x < kWave) gate = gate_of<T>(p, w.bi, w.h, c * kC + int(threadIdx.x), w.n);
   };
   typename Y::State S;
   Y::zero(S);
   double total = 0.0;
   fetch(w.c0);
+  if (threadIdx.x < kWave) total += fill_decays(ds[0], gate, p.wscale);
   for (int c = w.c0; c < w.c1; c++) {
+    const Decays& d = ds[(c - w.c0) & 1];
     sk.store(Ks);
     sv.store(Vs);
-    if (threadIdx.x < kWave) total += fill_decays(d, gate, p.wscale);
     __syncthreads();
     if (c + 1 < w.c1) fetch(c + 1);
     Frag<T> vf[2][Y::NT];
@@ -453,6 +493,7 @@ __global__ __launch_bounds__(kThreads) void lin_state_kernel(Sweep p) {
 #pragma unroll
       for (int n = 0; n < Y::NT; n++) vf[ks][n] = col_frag(Vs, Tile<T, VDP>::ld, 32 * ks + g8, Y::v0(n), Y::vstep);
     write_state<T, KDP, VDP>(S, Ks, vf, d);
+    if (c + 1 < w.c1 && threadIdx.x < kWave) total += fill_decays(ds[(c + 1 - w.c0) & 1], gate, p.wscale);
     __syncthreads();
   }
   const int64_t at = (w.bi * (p.n_segs - 1) + w.seg) * p.H + w.h;
@@ -470,7 +511,7 @@ __global__ __launch_bounds__(kThreads) void lin_state_kernel(Sweep p) {
 // has to be right to fp32 over long sums: P and S go into the products as two bf16 parts.
 // ---------------------------------------------------------------------------
 template <typename T, int KDP, int VDP, bool DOTS, bool VEC>
-__global__ __launch_bounds__(kThreads) void lin_sweep_kernel(Sweep p) {
+__global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DOTS)) void lin_sweep_kernel(Sweep p) {
   typedef Layout<KDP, VDP> Y;
   constexpr bool kTwo = DOTS && sizeof(T) == 2;
   constexpr int ldp = kC + 16 / int(sizeof(T)), kN = 4 * Y::NT;
@@ -479,7 +520,7 @@ __global__ __launch_bounds__(kThreads) void lin_sweep_kernel(Sweep p) {
   __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP>::kElems];
   __shared__ __attribute__((aligned(16))) T Vs[Tile<T, VDP>::kElems];
   __shared__ __attribute__((aligned(16))) T Ps[kTwo ? 2 : 1][kC * ldp];
-  __shared__ Decays d;
+  __shared__ Decays ds[2];
   __shared__ float diag[DOTS ? kC : 1], dot_part[DOTS ? 4 : 1][kC], red[4];
   const Place w = place_of(p, p.n_segs);
   const int wv = threadIdx.x / kWave, l = threadIdx.x % kWave;
@@ -488,14 +529,16 @@ __global__ __launch_bounds__(kThreads) void lin_sweep_kernel(Sweep p) {
   const float sscale = p.wscale * p.rscale;
   Stage<T, KDP, VEC> sq, sk;
   Stage<T, VDP, VEC> sv;
+  sq.init(start_of<T>(p.xq, p, w, p.gq, p.KD), p.H / p.gq * p.KD, p.KD, p.reverse);
+  sk.init(start_of<T>(p.xk, p, w, p.gk, p.KD), p.H / p.gk * p.KD, p.KD, p.reverse);
+  sv.init(start_of<T>(p.xv, p, w, p.gv, p.VD), p.H / p.gv * p.VD, p.VD, p.reverse);
   float gate = 0.f;
   auto fetch = [&](int c) {
-    const int p0 = c * kC, nv = max(0, min(kC, w.n - p0));
-    const int t = nv > 0 ? (p.reverse ? w.n - p0 - nv : p0) : 0;
-    sq.load(row_of<T>(p.xq, p, w, p.gq, t, p.KD), p.H / p.gq * p.KD, p.KD, nv, p.reverse);
-    sk.load(row_of<T>(p.xk, p, w, p.gk, t, p.KD), p.H / p.gk * p.KD, p.KD, nv, p.reverse);
-    sv.load(row_of<T>(p.xv, p, w, p.gv, t, p.VD), p.H / p.gv * p.VD, p.VD, nv, p.reverse);
-    if (threadIdx.x < kWave) gate = gate_of<T>(p, w.bi, w.h, p0 + int(threadIdx.x), w.n);
+    const int nv = w.n - c * kC;
+    sq.load(nv);
+    sk.load(nv);
+    sv.load(nv);
+    if (threadIdx.x < kWave) gate = gate_of<T>(p, w.bi, w.h, c * kC + int(threadIdx.x), w.n);
   };
   // the two blocks above the diagonal that the products read stay zero
   for (int i = threadIdx.x; i < 2 * 16 * 16; i += kThreads) {
@@ -508,13 +551,16 @@ __global__ __launch_bounds__(kThreads) void lin_sweep_kernel(Sweep p) {
                                 : p.init ? p.init + w.bh * p.KD * p.VD : nullptr;
   if (from) Y::load(S, from, p.init_t, p.KD, p.VD);
   else Y::zero(S);
-  if (w.c0 < w.c1) fetch(w.c0);
+  if (w.c0 < w.c1) {
+    fetch(w.c0);
+    if (threadIdx.x < kWave) fill_decays(ds[0], gate, p.wscale);
+  }
   for (int c = w.c0; c < w.c1; c++) {
     const int p0 = c * kC, nv = max(0, min(kC, w.n - p0));
+    const Decays& d = ds[(c - w.c0) & 1];
     sq.store(Qs);
     sk.store(Ks);
     sv.store(Vs);
-    if (threadIdx.x < kWave) fill_decays(d, gate, p.wscale);
     __syncthreads();
     if (c + 1 < w.c1) fetch(c + 1);
     // the rows of xd for the lane's outputs
@@ -642,6 +688,7 @@ __global__ __launch_bounds__(kThreads) void lin_sweep_kernel(Sweep p) {
       }
     }
     write_state<T, KDP, VDP>(S, Ks, vf, d);
+    if (c + 1 < w.c1 && threadIdx.x < kWave) fill_decays(ds[(c + 1 - w.c0) & 1], gate, p.wscale);
     __syncthreads();
     if constexpr (DOTS) {
       const int i = threadIdx.x;
@@ -878,7 +925,8 @@ hipError_t run_states(const Sweep& p) {
   return launch_chain<false, false, false>(kKindLinChain, c, p.stream);
 }
 
-// The cut of a sequence: segments so that the workgroups fill the chip twice, of at least kMinSeg chunks.
+// The cut of a sequence: as many segments as fill the chip's 256 CUs with the workgroups that run at once, and
+// no second generation of them; of at least kMinSeg chunks.
 constexpr int kMinSeg = 4;
 struct Cut {
   int n_chunks, n_segs, seg_chunks;
@@ -887,7 +935,9 @@ Cut cut_of(const LinAttnArgs& a) {
   Cut c;
   c.n_chunks = int(ceil_div(a.L, kC));
   const int64_t heads = a.b * a.H;
-  const int64_t want = std::max<int64_t>(1, ceil_div(512, std::max<int64_t>(heads, 1)));
+  const int kd = a.Dk <= 64 ? 64 : 128, vd = a.Dv <= 64 ? 64 : 128;
+  const int64_t at_once = 256 * (a.dtype == 0 ? sweep_waves<float>(kd, vd, false) : sweep_waves<bf16_bits>(kd, vd, false));
+  const int64_t want = std::max<int64_t>(1, at_once / std::max<int64_t>(heads, 1));
   const int64_t most = std::max<int64_t>(1, c.n_chunks / kMinSeg);
   c.n_segs = int(std::min(want, most));
   c.seg_chunks = int(std::max<int64_t>(1, ceil_div(c.n_chunks, c.n_segs)));
