@@ -43,7 +43,7 @@ struct Sweep {
   float wscale, rscale;    // factors of the products written into the state, and of the readout
   const float* init;       // state before the first token of the sweep, or null
   bool init_t;             // it is stored [VD][KD]
-  void* out;               // [b, L, H, VD], of the streamed type or (out_f32) float; null: not written
+  void* out;               // [b, L, H, VD], of the streamed type or (out_f32) float
   bool out_f32;
   float* last;             // [b, H, KD, VD], or null
   bool final_decay;        // `last` takes the first token's decay too (gradient of the initial state)
@@ -252,55 +252,117 @@ struct Stage {
   }
 };
 
-// N consecutive elements of row[c ..] (c + j < D), as floats
-template <typename T, int N, bool VEC>
-__device__ __forceinline__ void load_part(const T* row, int c, int D, bool live, float (&x)[N]) {
-  if constexpr (VEC) {
-    static_assert(N == 4 || N == 8, "");
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        const float4 v = live && c + k < D ? *reinterpret_cast<const float4*>(row + c + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[k] = v.x; x[k + 1] = v.y; x[k + 2] = v.z; x[k + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        const uint2 v = live && c + k < D ? *reinterpret_cast<const uint2*>(row + c + k) : make_uint2(0, 0);
-        x[k] = __uint_as_float(v.x << 16); x[k + 1] = __uint_as_float(v.x & 0xffff0000u);
-        x[k + 2] = __uint_as_float(v.y << 16); x[k + 3] = __uint_as_float(v.y & 0xffff0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; k++) x[k] = live && c + k < D ? load_elem(row + c + k) : 0.f;
-  }
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return uint32_t(__builtin_bit_cast(bf16_bits, static_cast<__bf16>(lo))) |
          (uint32_t(__builtin_bit_cast(bf16_bits, static_cast<__bf16>(hi))) << 16);
 }
+// four consecutive elements of an LDS row, as floats
+__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 lds4(const bf16_bits* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
+
+// A lane's part of a chunk's rows of one tensor in memory: N consecutive elements at column c of position
+// 16 tt + lane % 16, tt = 0..3.  As in Stage, one lane offset and wave-uniform steps; what is not live is
+// read as zero and not written.
 template <typename T, int N, bool VEC>
-__device__ __forceinline__ void store_part(T* row, int c, int D, const float (&x)[N]) {
-  if constexpr (VEC) {
+struct Rows {
+  static constexpr int kBytes = int(sizeof(T));
+  const T* base;
+  int voff, soff, sstep, chunk, cols;
+  __device__ __forceinline__ void init(const T* first, int stride, int c, int D, bool reverse) {
+    const int i = threadIdx.x % 16;
+    base = first;
+    chunk = reverse ? -kC * stride : kC * stride;
+    sstep = 16 * stride * kBytes;
+    soff = 0;
+    if (reverse) {
+      voff = ((15 - i) * stride + c) * kBytes;
+      soff = 3 * sstep;
+      sstep = -sstep;
+    } else {
+      voff = (i * stride + c) * kBytes;
+    }
+    cols = D - c;
+  }
+  __device__ __forceinline__ void next() { base += chunk; }
+  struct Raw {
+    uint32_t w[N * kBytes / 4];
+  };
+  __device__ __forceinline__ Raw load(int tt, int nv) const {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base);
+    const bool row = 16 * tt + int(threadIdx.x % 16) < nv;
+    const int so = soff + tt * sstep;
+    Raw x;
+    if constexpr (VEC) {
+      if constexpr (N * kBytes == 8) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, row && cols > 0 ? voff : 0x7fffffff, so, 0);
+        x.w[0] = v[0]; x.w[1] = v[1];
+      } else {
 #pragma unroll
-    for (int k = 0; k < N; k += 4) {
-      if (c + k < D) {
-        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(row + c + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-        else *reinterpret_cast<uint2*>(row + c + k) = make_uint2(pack_bf16(x[k], x[k + 1]), pack_bf16(x[k + 2], x[k + 3]));
+        for (int k = 0; k < N * kBytes / 16; k++) {
+          const int at = row && cols > k * 16 / kBytes ? voff + 16 * k : 0x7fffffff;
+          const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, at, so, 0);
+#pragma unroll
+          for (int j = 0; j < 4; j++) x.w[4 * k + j] = v[j];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N * kBytes / 4; k++) x.w[k] = 0;
+#pragma unroll
+      for (int e = 0; e < N; e++) {
+        const int at = row && e < cols ? voff + e * kBytes : 0x7fffffff;
+        if constexpr (kBytes == 4) x.w[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, so, 0);
+        else x.w[e / 2] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b16(rs, at, so, 0)) << (16 * (e % 2));
       }
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; k++)
-      if (c + k < D) store_elem(row + c + k, x[k]);
+    return x;
   }
-}
+  static __device__ __forceinline__ float element(const Raw& x, int j) {
+    if constexpr (kBytes == 4) return __uint_as_float(x.w[j]);
+    else return __uint_as_float(j % 2 ? x.w[j / 2] & 0xffff0000u : x.w[j / 2] << 16);
+  }
+  __device__ __forceinline__ void store(int tt, int nv, const float (&y)[N]) const {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base);
+    const bool row = 16 * tt + int(threadIdx.x % 16) < nv;
+    const int so = soff + tt * sstep;
+    if constexpr (VEC) {
+      uint32_t w[N * kBytes / 4];
+      if constexpr (kBytes == 4) {
+#pragma unroll
+        for (int j = 0; j < N; j++) w[j] = __float_as_uint(y[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N / 2; j++) w[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+      }
+      if constexpr (N * kBytes == 8) {
+        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+        __builtin_amdgcn_raw_buffer_store_b64(u2{w[0], w[1]}, rs, row && cols > 0 ? voff : 0x7fffffff, so, 0);
+      } else {
+        typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int k = 0; k < N * kBytes / 16; k++)
+          __builtin_amdgcn_raw_buffer_store_b128(u4{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]}, rs,
+                                                 row && cols > k * 16 / kBytes ? voff + 16 * k : 0x7fffffff, so, 0);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; e++) {
+        const int at = row && e < cols ? voff + e * kBytes : 0x7fffffff;
+        if constexpr (kBytes == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[e]), rs, at, so, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(bf16_bits, static_cast<__bf16>(y[e])), rs, at, so, 0);
+      }
+    }
+  }
+};
 
 // Decays of a chunk, for its kC positions, in LDS.  The running sum is kept in double, in units of
 // log 2, and handed on in two floats: differences of it are exact to fp32 even where a reset
 // put it at -10^4.
-struct Decays {
+struct __attribute__((aligned(16))) Decays {
   float hi[kC], lo[kC];  // running sum up to and with the position
   float in[kC];          // exp of it: what the state entering the chunk has kept
   float out[kC];         // exp(last - own) wscale: what a product written here keeps to the chunk's end
@@ -391,9 +453,8 @@ __device__ __forceinline__ void write_state(typename Layout<KDP, VDP>::State& S,
   Frag<T> hi[2][Y::NT], lo[2][Y::NT];
 #pragma unroll
   for (int ks = 0; ks < 2; ks++) {
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) w[j] = d.out[32 * ks + g8 + j];
+    const float4 w0 = lds4(d.out + 32 * ks + g8), w1 = lds4(d.out + 32 * ks + g8 + 4);
+    const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
     for (int n = 0; n < Y::NT; n++) {
       float x[8];
@@ -430,7 +491,10 @@ struct Place {
 };
 __device__ __forceinline__ Place place_of(const Sweep& p, int n_segs) {
   Place w;
-  w.h = blockIdx.x % p.H;
+  // Workgroups are dealt to the 8 XCDs in turn: with H a multiple of 8, each XCD takes H / 8 neighbouring
+  // heads, so that the heads of a group read their shared rows through one L2.
+  const int id = blockIdx.x;
+  w.h = p.H % 8 == 0 ? (id % 8) * (p.H / 8) + (id / 8) % (p.H / 8) : id % p.H;
   const int rest = blockIdx.x / p.H;
   w.seg = rest % n_segs;
   w.bi = rest / n_segs;
@@ -532,13 +596,19 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
   sq.init(start_of<T>(p.xq, p, w, p.gq, p.KD), p.H / p.gq * p.KD, p.KD, p.reverse);
   sk.init(start_of<T>(p.xk, p, w, p.gk, p.KD), p.H / p.gk * p.KD, p.KD, p.reverse);
   sv.init(start_of<T>(p.xv, p, w, p.gv, p.VD), p.H / p.gv * p.VD, p.VD, p.reverse);
+  Rows<T, kN, VEC> xr, yr;
+  Rows<float, kN, VEC> fr;
+  if constexpr (DOTS) xr.init(start_of<T>(p.xd, p, w, p.gd, p.VD), p.H / p.gd * p.VD, vc, p.VD, p.reverse);
+  if (p.out_f32) fr.init(start_of<float>(p.out, p, w, 1, p.VD), p.H * p.VD, vc, p.VD, p.reverse);
+  else yr.init(start_of<T>(p.out, p, w, 1, p.VD), p.H * p.VD, vc, p.VD, p.reverse);
   float gate = 0.f;
+  const bool gates = threadIdx.x >= 3 * kWave;  // the wave with the fewest blocks of P takes the decays
   auto fetch = [&](int c) {
     const int nv = w.n - c * kC;
     sq.load(nv);
     sk.load(nv);
     sv.load(nv);
-    if (threadIdx.x < kWave) gate = gate_of<T>(p, w.bi, w.h, c * kC + int(threadIdx.x), w.n);
+    if (gates) gate = gate_of<T>(p, w.bi, w.h, c * kC + l, w.n);
   };
   // the two blocks above the diagonal that the products read stay zero
   for (int i = threadIdx.x; i < 2 * 16 * 16; i += kThreads) {
@@ -553,7 +623,7 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
   else Y::zero(S);
   if (w.c0 < w.c1) {
     fetch(w.c0);
-    if (threadIdx.x < kWave) fill_decays(ds[0], gate, p.wscale);
+    if (gates) fill_decays(ds[0], gate, p.wscale);
   }
   for (int c = w.c0; c < w.c1; c++) {
     const int p0 = c * kC, nv = max(0, min(kC, w.n - p0));
@@ -563,15 +633,6 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
     sv.store(Vs);
     __syncthreads();
     if (c + 1 < w.c1) fetch(c + 1);
-    // the rows of xd for the lane's outputs
-    float xd[DOTS ? 4 : 1][DOTS ? kN : 1];
-    if constexpr (DOTS) {
-#pragma unroll
-      for (int tt = 0; tt < 4; tt++) {
-        const int i = 16 * tt + lr, t = p.reverse ? w.n - 1 - p0 - i : p0 + i;
-        load_part<T, kN, VEC>(row_of<T>(p.xd, p, w, p.gd, i < nv ? t : 0, p.VD), vc, p.VD, i < nv, xd[tt]);
-      }
-    }
     // ---- P: blocks b = wv, wv + 4, wv + 8 of the ten (t block, s block) with s <= t ----
 #pragma unroll
     for (int i = 0; i < 3; i++) {
@@ -584,11 +645,13 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
           acc = mma(row_frag(Ks + (16 * sb + lr) * ldk + 32 * kk + g8), row_frag(Qs + (16 * tb + lr) * ldk + 32 * kk + g8), acc);
         const int t = 16 * tb + lr;
         const float th = d.hi[t], tl = d.lo[t];
+        const float4 sh4 = lds4(d.hi + 16 * sb + g4), sl4 = lds4(d.lo + 16 * sb + g4);
+        const float shi[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, slo[4] = {sl4.x, sl4.y, sl4.z, sl4.w};
         float x[4];
 #pragma unroll
         for (int r = 0; r < 4; r++) {
           const int s = 16 * sb + g4 + r;
-          const float e = exp2_fast((th - d.hi[s]) + (tl - d.lo[s])) * sscale;
+          const float e = exp2_fast((th - shi[r]) + (tl - slo[r])) * sscale;
           x[r] = (DOTS ? s < t : s <= t) ? acc[r] * e : 0.f;
           if (DOTS && s == t) diag[t] = acc[r] * sscale;
         }
@@ -641,6 +704,12 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
 #pragma unroll
         for (int r = 0; r < 4; r++) o[tt][n][r] *= f;
     }
+    typename Rows<T, kN, VEC>::Raw xd[DOTS ? 4 : 1];  // the rows of xd for the lane's outputs
+    if constexpr (DOTS) {
+#pragma unroll
+      for (int tt = 0; tt < 4; tt++) xd[tt] = xr.load(tt, nv);
+      xr.next();
+    }
     __syncthreads();
     // ---- the chunk's own part ----
     Frag<T> vf[2][Y::NT];
@@ -668,27 +737,25 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
       if constexpr (DOTS) {
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < kN; j++) s = fmaf(y[j], xd[tt][j], s);
+        for (int j = 0; j < kN; j++) s = fmaf(y[j], Rows<T, kN, VEC>::element(xd[tt], j), s);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (l < 16) dot_part[wv][i] = s;
         const float dg = diag[i];
 #pragma unroll
-        for (int j = 0; j < kN; j++) y[j] = fmaf(dg, load_elem(Vs + i * ldv + vc + j), y[j]);
-      }
-      if (p.out && p0 + i < p.L) {
-        if (i >= nv) {
-#pragma unroll
-          for (int j = 0; j < kN; j++) y[j] = 0.f;
+        for (int j = 0; j < kN; j += 4) {
+          const float4 v = lds4(Vs + i * ldv + vc + j);
+          y[j] = fmaf(dg, v.x, y[j]); y[j + 1] = fmaf(dg, v.y, y[j + 1]);
+          y[j + 2] = fmaf(dg, v.z, y[j + 2]); y[j + 3] = fmaf(dg, v.w, y[j + 3]);
         }
-        const int64_t t = i >= nv ? p0 + i : p.reverse ? w.n - 1 - p0 - i : p0 + i;
-        const int64_t at = ((w.bi * p.L + t) * p.H + w.h) * p.VD;
-        if (p.out_f32) store_part<float, kN, VEC>(static_cast<float*>(p.out) + at, vc, p.VD, y);
-        else store_part<T, kN, VEC>(static_cast<T*>(p.out) + at, vc, p.VD, y);
       }
+      if (p.out_f32) fr.store(tt, nv, y);
+      else yr.store(tt, nv, y);
     }
+    fr.next();
+    yr.next();
     write_state<T, KDP, VDP>(S, Ks, vf, d);
-    if (c + 1 < w.c1 && threadIdx.x < kWave) fill_decays(ds[(c + 1 - w.c0) & 1], gate, p.wscale);
+    if (c + 1 < w.c1 && gates) fill_decays(ds[(c + 1 - w.c0) & 1], gate, p.wscale);
     __syncthreads();
     if constexpr (DOTS) {
       const int i = threadIdx.x;
@@ -696,6 +763,16 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
         const int64_t t = i >= nv ? p0 + i : p.reverse ? w.n - 1 - p0 - i : p0 + i;
         p.dots[(w.bi * p.L + t) * p.H + w.h] =
             i < nv ? (dot_part[0][i] + dot_part[1][i]) + (dot_part[2][i] + dot_part[3][i]) : 0.f;
+      }
+    }
+    if (nv < kC) {  // rows behind the sequence's length are zero
+      const int rows = min(kC, int(p.L) - p0);
+      for (int i = nv + threadIdx.x / kWave; i < rows; i += kThreads / kWave) {
+        const int64_t at = ((w.bi * p.L + p0 + i) * p.H + w.h) * p.VD;
+        for (int j = l; j < p.VD; j += kWave) {
+          if (p.out_f32) static_cast<float*>(p.out)[at + j] = 0.f;
+          else store_elem(static_cast<T*>(p.out) + at + j, 0.f);
+        }
       }
     }
   }
@@ -899,7 +976,7 @@ hipError_t sweep_sizes(const Sweep& p, bool vec) {
 template <typename T>
 hipError_t run_sweep(const Sweep& p) {
   const bool vec = pieces<T>(p.xq, p.KD) && pieces<T>(p.xk, p.KD) && pieces<T>(p.xv, p.VD) &&
-                   (!p.out || pieces<T>(p.out, p.VD)) && (!p.xd || pieces<T>(p.xd, p.VD));
+                   pieces<T>(p.out, p.VD) && (!p.xd || pieces<T>(p.xd, p.VD));
   return p.dots ? sweep_sizes<T, true>(p, vec) : sweep_sizes<T, false>(p, vec);
 }
 
