@@ -19,6 +19,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ssm_chain.h"
 #include "ssm_device.h"
@@ -120,6 +121,16 @@ __device__ __forceinline__ f32x8 row_frag(const float* p) {
   return f32x8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 
+// the same of two separate groups of four
+__device__ __forceinline__ bf16x8 pair_frag(const bf16_bits* a, const bf16_bits* b) {
+  const uint2 x = *reinterpret_cast<const uint2*>(a), y = *reinterpret_cast<const uint2*>(b);
+  return __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
+}
+__device__ __forceinline__ f32x8 pair_frag(const float* a, const float* b) {
+  const float4 x = *reinterpret_cast<const float4*>(a), y = *reinterpret_cast<const float4*>(b);
+  return f32x8{{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
+}
+
 // Column c0 + step (i / 4) + i % 4 (i = lane % 16) of rows r .. r + 7 of a row-major LDS tile; r may
 // differ between the groups of 16 lanes.  bf16 goes through the transposing LDS read of gfx950: in a group of 16
 // lanes, lane m names 8 bytes and lane i receives element i % 4 of the bytes named by lanes
@@ -167,49 +178,80 @@ __device__ __forceinline__ void frag_floats(const f32x8& f, float (&x)[8]) {
 }
 
 // ---------------------------------------------------------------------------
-// Workgroups of a CU (= waves of a SIMD) that the registers are held to; the LDS has room for as many.
+// Waves of a SIMD that the registers are held to.  A sweep's workgroup alone is two.
 #define SSM_LIN_WAVES(n) __attribute__((amdgpu_waves_per_eu(n, n)))
-template <typename T>
-constexpr int sweep_waves(int kd, int vd, bool dots) {
-  return sizeof(T) == 4 ? (kd + vd > 128 ? 1 : 2) : kd + vd > 128 ? 2 : 3;
-}
+constexpr int kSweepWaves = 2;
 template <typename T>
 constexpr int state_waves(int kd, int vd) {
   return sizeof(T) == 4 ? 2 : kd + vd > 128 ? 2 : 4;
 }
 
-// Chunks of kC tokens.  A sweep counts positions from its own start: position i is token i, or in
+// Chunks of kChunk tokens.  A sweep counts positions from its own start: position i is token i, or in
 // reversed time token n - 1 - i of the row's n.  Rows of an LDS tile are positions.
 // ---------------------------------------------------------------------------
-constexpr int kC = 64;
-constexpr int kThreads = 256;  // four waves; wave w holds a quarter of the state's columns
+template <typename T>
+constexpr int kChunk = sizeof(T) == 4 ? 32 : 64;  // float tiles are twice as wide, and two chunks of them have to fit in the LDS
+constexpr int kThreads = 256;  // four waves that hold a quarter of the state's columns each, or that stage and score
 
-template <typename T, int DP>
+// Tiles in LDS: their rows are padded so that the reads of their kind fall on different banks (64 of 4 bytes).
+// Row fragments (16 bytes a lane, 8 rows at once) and pairs of 8 bytes (16 rows at once) want rows 4 banks apart,
+// transposing reads (4 rows by 32 or, of every other 8 bytes, 64 bytes) want 8 or 16.  At 64 elements a row of
+// bf16 with one piece of padding is 36 banks on, which serves all of them.
+enum Role { kQuery, kKey, kValue };
+template <typename T, int DP, Role ROLE>
 struct Tile {
   static constexpr int kVec = 16 / sizeof(T);                  // elements of a 16-byte piece
   static constexpr int kRow = DP / kVec;                       // pieces a row
+  static constexpr int kC = kChunk<T>;
   static constexpr int kPieces = kC * kRow / kThreads;         // pieces a thread
-  static constexpr int ld = DP + kVec;                         // elements a row of the LDS tile (padded by one piece)
+  static constexpr int ld = DP + (sizeof(T) == 4 || DP == 64 ? 1 : ROLE == kQuery ? 1 : ROLE == kKey ? 2 : 4) * kVec;  // elements a row
   static constexpr int kElems = kC * ld;
 };
+
+// Where a workgroup is: its head, batch row, segment and the chunks of it.
+struct Place {
+  int h, seg, c0, c1, n;
+  int64_t bi, bh;
+};
+__device__ __forceinline__ Place place_of(const Sweep& p, int n_segs) {
+  Place w;
+  // Workgroups are dealt to the 8 XCDs in turn: with H a multiple of 8, each XCD takes H / 8 neighbouring
+  // heads, so that the heads of a group read their shared rows through one L2.
+  const int id = blockIdx.x;
+  w.h = p.H % 8 == 0 ? (id % 8) * (p.H / 8) + (id / 8) % (p.H / 8) : id % p.H;
+  const int rest = blockIdx.x / p.H;
+  w.seg = rest % n_segs;
+  w.bi = rest / n_segs;
+  w.bh = w.bi * p.H + w.h;
+  w.n = live_length(p.lengths, w.bi, p.L);
+  w.c0 = w.seg * p.seg_chunks;
+  w.c1 = min(w.c0 + p.seg_chunks, p.n_chunks);
+  return w;
+}
+
+// Descriptor at an address that is the same in every lane (said so: the compiler would loop over the lanes' values)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(int(uint32_t(u))), hi = __builtin_amdgcn_readfirstlane(int(uint32_t(u >> 32)));
+  return make_rsrc(reinterpret_cast<const void*>((uint64_t(hi) << 32) | lo));
+}
 
 // A chunk's rows of one tensor, on their way from memory to LDS: rows of D <= DP elements, `stride`
 // elements apart, the rest zero.  VEC: rows are whole 16-byte pieces, 16-byte aligned.  A thread's
 // pieces are kStep rows apart, so one lane offset serves them all, the steps and the chunks being
 // wave-uniform.  In reversed time the descriptor starts at the chunk's last position: position i is
-// row 63 - i of it, and rows below a short last chunk's, which are not read, may lie before the tensor.
-template <typename T, int DP, bool VEC>
+// row kC - 1 - i of it, and rows below a short last chunk's, which are not read, may lie before the tensor.
+template <typename T, int DP, Role ROLE, bool VEC>
 struct Stage {
-  typedef Tile<T, DP> L;
+  typedef Tile<T, DP, ROLE> L;
   static constexpr int kStep = kThreads / L::kRow;  // rows between a thread's pieces
-  uint4 r[L::kPieces];
-  const T* base;     // row of the chunk's first position, or (reversed) of position 63
+  const T* base;     // row of the chunk's first position, or (reversed) of its last
   int voff, soff, sstep, chunk, live_cols;
-  // first: row of position p0 of the sweep (reversed: of position p0 + 63, maybe before the tensor)
-  __device__ __forceinline__ void init(const T* first, int stride, int D, bool reverse) {
-    const int i = threadIdx.x / L::kRow, c = (threadIdx.x % L::kRow) * L::kVec;
+  // first: row of position p0 of the sweep (reversed: of position p0 + kC - 1, maybe before the tensor); tid: of 256
+  __device__ __forceinline__ void init(const T* first, int stride, int D, bool reverse, int tid) {
+    const int i = tid / L::kRow, c = (tid % L::kRow) * L::kVec;
     base = first;
-    chunk = reverse ? -kC * stride : kC * stride;
+    chunk = reverse ? -L::kC * stride : L::kC * stride;
     sstep = kStep * stride * int(sizeof(T));
     soff = 0;
     if (reverse) {
@@ -223,10 +265,10 @@ struct Stage {
     if (live_cols <= 0) voff = 0x7fffffff;
   }
   // the next chunk, of nv live positions
-  __device__ __forceinline__ void load(int nv) {
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base);
+  __device__ __forceinline__ void load(uint4 (&r)[L::kPieces], int nv, int tid) {
+    const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(base);
     base += chunk;
-    const int i = threadIdx.x / L::kRow;
+    const int i = tid / L::kRow;
 #pragma unroll
     for (int j = 0; j < L::kPieces; j++) {
       const int o = i + j * kStep < nv ? voff : 0x7fffffff;
@@ -245,8 +287,8 @@ struct Stage {
       }
     }
   }
-  __device__ __forceinline__ void store(T* tile) const {
-    T* to = tile + (threadIdx.x / L::kRow) * L::ld + (threadIdx.x % L::kRow) * L::kVec;
+  static __device__ __forceinline__ void store(T* tile, const uint4 (&r)[L::kPieces], int tid) {
+    T* to = tile + (tid / L::kRow) * L::ld + (tid % L::kRow) * L::kVec;
 #pragma unroll
     for (int j = 0; j < L::kPieces; j++) *reinterpret_cast<uint4*>(to + j * kStep * L::ld) = r[j];
   }
@@ -264,38 +306,35 @@ __device__ __forceinline__ float4 lds4(const bf16_bits* p) {
                      __uint_as_float(v.y & 0xffff0000u));
 }
 
-// A lane's part of a chunk's rows of one tensor in memory: N consecutive elements at column c of position
-// 16 tt + lane % 16, tt = 0..3.  As in Stage, one lane offset and wave-uniform steps; what is not live is
+// A lane's part of a chunk's rows of one tensor in memory, of elements of `es` bytes: N consecutive elements at
+// column c of position 16 tt + lane % 16.  As in Stage, one lane offset and wave-uniform steps; what is not live is
 // read as zero and not written.
-template <typename T, int N, bool VEC>
+template <int N, bool VEC, int kC>
 struct Rows {
-  static constexpr int kBytes = int(sizeof(T));
-  const T* base;
+  const char* base;
   int voff, soff, sstep, chunk, cols;
-  __device__ __forceinline__ void init(const T* first, int stride, int c, int D, bool reverse) {
-    const int i = threadIdx.x % 16;
-    base = first;
-    chunk = reverse ? -kC * stride : kC * stride;
-    sstep = 16 * stride * kBytes;
-    soff = 0;
-    if (reverse) {
-      voff = ((15 - i) * stride + c) * kBytes;
-      soff = 3 * sstep;
-      sstep = -sstep;
-    } else {
-      voff = (i * stride + c) * kBytes;
-    }
+  __device__ __forceinline__ void init(const Sweep& p, const Place& w, const void* x, int es, int share, int c) {
+    const int i = threadIdx.x % 16, D = p.VD, stride = p.H / share * D * es;
+    const int64_t t = p.reverse ? int64_t(w.n) - int64_t(w.c0) * kC - kC : int64_t(w.c0) * kC;
+    base = static_cast<const char*>(x) + ((w.bi * p.L + t) * (p.H / share) + w.h / share) * D * es;
+    chunk = p.reverse ? -kC * stride : kC * stride;
+    sstep = p.reverse ? -16 * stride : 16 * stride;
+    soff = p.reverse ? (kC - 16) * stride : 0;
+    voff = (p.reverse ? 15 - i : i) * stride + c * es;
     cols = D - c;
   }
   __device__ __forceinline__ void next() { base += chunk; }
+  template <typename T>
   struct Raw {
-    uint32_t w[N * kBytes / 4];
+    uint32_t w[N * int(sizeof(T)) / 4];
   };
-  __device__ __forceinline__ Raw load(int tt, int nv) const {
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base);
+  template <typename T>
+  __device__ __forceinline__ Raw<T> load(int tt, int nv) const {
+    constexpr int kBytes = int(sizeof(T));
+    const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(base);
     const bool row = 16 * tt + int(threadIdx.x % 16) < nv;
     const int so = soff + tt * sstep;
-    Raw x;
+    Raw<T> x;
     if constexpr (VEC) {
       if constexpr (N * kBytes == 8) {
         const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, row && cols > 0 ? voff : 0x7fffffff, so, 0);
@@ -321,12 +360,15 @@ struct Rows {
     }
     return x;
   }
-  static __device__ __forceinline__ float element(const Raw& x, int j) {
-    if constexpr (kBytes == 4) return __uint_as_float(x.w[j]);
+  template <typename T>
+  static __device__ __forceinline__ float element(const Raw<T>& x, int j) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(x.w[j]);
     else return __uint_as_float(j % 2 ? x.w[j / 2] & 0xffff0000u : x.w[j / 2] << 16);
   }
+  template <typename T>
   __device__ __forceinline__ void store(int tt, int nv, const float (&y)[N]) const {
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base);
+    constexpr int kBytes = int(sizeof(T));
+    const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(base);
     const bool row = 16 * tt + int(threadIdx.x % 16) < nv;
     const int so = soff + tt * sstep;
     if constexpr (VEC) {
@@ -362,56 +404,95 @@ struct Rows {
 // Decays of a chunk, for its kC positions, in LDS.  The running sum is kept in double, in units of
 // log 2, and handed on in two floats: differences of it are exact to fp32 even where a reset
 // put it at -10^4.
+template <int kC>
 struct __attribute__((aligned(16))) Decays {
   float hi[kC], lo[kC];  // running sum up to and with the position
   float in[kC];          // exp of it: what the state entering the chunk has kept
   float out[kC];         // exp(last - own) wscale: what a product written here keeps to the chunk's end
   float all;             // exp of the last
 };
-// log decay of position i (one lane each): a token's own, or in reversed time the token's after it
-template <typename T>
-__device__ __forceinline__ float gate_of(const Sweep& p, int64_t bi, int h, int i, int n) {
-  const int t = p.reverse ? n - i : i;
-  if (i >= n || (p.reverse && i == 0)) return 0.f;
-  return log_decay<T>(p, bi, t, h);
+// Log decays of a chunk's positions, lane i of a wave with position i's: a token's own, or in reversed time
+// the one of the token after it (the first position has none).
+template <typename T, int kC>
+struct Gates {
+  const T* base;
+  int voff, chunk;
+  float fixed;
+  bool given, reverse;
+  __device__ __forceinline__ void init(const Sweep& p, const Place& w, int c0) {
+    const int l = threadIdx.x % kWave;
+    given = p.g != nullptr;
+    reverse = p.reverse;
+    fixed = p.A ? p.A[w.h] : 0.f;
+    const int64_t t = reverse ? int64_t(w.n) - int64_t(c0) * kC - kC : int64_t(c0) * kC;
+    base = static_cast<const T*>(p.g) + ((w.bi * p.L + t) * p.H + w.h);
+    chunk = reverse ? -kC * p.H : kC * p.H;
+    voff = (reverse ? kC - l : l) * p.H * int(sizeof(T));
+  }
+  // the next chunk, from position p0, nv live; the raw value, to be turned into a log decay later
+  __device__ __forceinline__ float load(int p0, int nv) {
+    const int l = threadIdx.x % kWave;
+    const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(base);
+    base += chunk;
+    const int at = given && l < kC && l < nv && !(reverse && p0 + l == 0) ? voff : 0x7fffffff;
+    if constexpr (sizeof(T) == 4) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0));
+    else return __uint_as_float(uint32_t(__builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0)) << 16);
+  }
+  __device__ __forceinline__ float log_of(float raw, int p0, int nv) const {
+    const int l = threadIdx.x % kWave;
+    return l < kC && l < nv && !(reverse && p0 + l == 0) ? clamp_log(raw + fixed) : 0.f;
+  }
+};
+// x of the lane N below in the row of 16 (or, N = 16 and 32, of the last lane of the row or half below), else 0
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(u >> 32)), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
 }
-// by one wave; returns the chunk's sum in natural units
-__device__ __forceinline__ double fill_decays(Decays& d, float gate, float wscale) {
+// by one wave, lane i with position i's gate; returns the chunk's sum in natural units
+template <int kC>
+__device__ __forceinline__ double fill_decays(Decays<kC>& d, float gate, float wscale) {
   const int l = threadIdx.x % kWave;
   double run = double(gate) * 1.4426950408889634;
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const double o = __shfl_up(run, off);
-    if (l >= off) run += o;
+  run += dpp_or_zero<0x111, 0xF>(run);  // row_shr:1
+  run += dpp_or_zero<0x112, 0xF>(run);  // row_shr:2
+  run += dpp_or_zero<0x114, 0xF>(run);  // row_shr:4
+  run += dpp_or_zero<0x118, 0xF>(run);  // row_shr:8
+  run += dpp_or_zero<0x142, 0xA>(run);  // row_bcast:15 into rows 1 and 3
+  run += dpp_or_zero<0x143, 0xC>(run);  // row_bcast:31 into rows 2 and 3
+  const uint64_t u = __builtin_bit_cast(uint64_t, run);
+  const uint64_t ul = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(u)), kC - 1));
+  const uint64_t uh = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(u >> 32)), kC - 1));
+  const double last = __builtin_bit_cast(double, (uh << 32) | ul);
+  if (l < kC) {
+    const float hi = float(run);
+    d.hi[l] = hi;
+    d.lo[l] = float(run - double(hi));
+    d.in[l] = exp2_fast(hi);
+    d.out[l] = exp2_fast(float(last - run)) * wscale;
+    if (l == 0) d.all = exp2_fast(float(last));
   }
-  const double last = __shfl(run, kWave - 1);
-  const float hi = float(run);
-  d.hi[l] = hi;
-  d.lo[l] = float(run - double(hi));
-  d.in[l] = exp2_fast(hi);
-  d.out[l] = exp2_fast(float(last - run)) * wscale;
-  if (l == 0) d.all = exp2_fast(float(last));
   return last * 0.6931471805599453;
 }
 
 // The state in registers: wave w holds its VDP / 4 columns, as 16 x 16 results whose rows run along
-// the KDP index in the order that makes two neighbouring results an operand fragment: result m has, at
-// row i, index 32 (m / 2) + 4 (m % 2) + 8 (i / 4) + i % 4, so results 2 kk and 2 kk + 1 of a lane are
-// the 8 indices 32 kk + 8 (l / 16) .. + 7.  Columns likewise, where a wave has two results of them.
+// the KDP index.  Two neighbouring results are an operand fragment as they are: a lane then has indices
+// 32 kk + 4 (l / 16) .. + 3 and 16 more, and the other operand is read in that order (pair_frag).  Where a wave has two
+// results side by side, their columns interleave by fours, so that a lane has 8 consecutive outputs.
 template <int KDP, int VDP>
 struct Layout {
   static constexpr int MT = KDP / 16, NT = VDP / 64, KS = KDP / 32;
   static constexpr int vstep = NT == 2 ? 8 : 4;
-  static __device__ __forceinline__ int v0(int nt) { return int(threadIdx.x / kWave) * (VDP / 4) + 4 * nt; }
+  static __device__ __forceinline__ int v0(int nt) { return int(threadIdx.x / kWave) * (VDP / 4) + 4 * nt; }  // waves 0..3
   // column of lane index i of result nt
   static __device__ __forceinline__ int col(int nt) {
     const int i = threadIdx.x % 16;
     return v0(nt) + vstep * (i / 4) + i % 4;
   }
   // first of the 4 rows that this lane holds of result m
-  static __device__ __forceinline__ int row(int m) {
-    return 32 * (m / 2) + 4 * (m % 2) + 8 * int((threadIdx.x % kWave) / 16);
-  }
+  static __device__ __forceinline__ int row(int m) { return 16 * m + 4 * int((threadIdx.x % kWave) / 16); }
   typedef f32x4 State[MT][NT];
   static __device__ __forceinline__ void zero(State& S) {
 #pragma unroll
@@ -446,13 +527,15 @@ struct Layout {
 // S = all S + K^T (out o V) over a chunk.  The weighted values are split into two bf16 parts (2^-17 of
 // a product is lost; one part would lose 2^-9 and the state is a float result).
 template <typename T, int KDP, int VDP>
-__device__ __forceinline__ void write_state(typename Layout<KDP, VDP>::State& S, const T* Ks, const Frag<T> (&vf)[2][VDP / 64],
-                                            const Decays& d) {
+__device__ __forceinline__ void write_state(typename Layout<KDP, VDP>::State& S, const T* Ks,
+                                            const Frag<T> (&vf)[kChunk<T> / 32][VDP / 64],
+                                            const Decays<kChunk<T>>& d) {
   typedef Layout<KDP, VDP> Y;
+  constexpr int kSteps = kChunk<T> / 32;
   const int g8 = 8 * int((threadIdx.x % kWave) / 16);
-  Frag<T> hi[2][Y::NT], lo[2][Y::NT];
+  Frag<T> hi[kSteps][Y::NT], lo[kSteps][Y::NT];
 #pragma unroll
-  for (int ks = 0; ks < 2; ks++) {
+  for (int ks = 0; ks < kSteps; ks++) {
     const float4 w0 = lds4(d.out + 32 * ks + g8), w1 = lds4(d.out + 32 * ks + g8 + 4);
     const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
@@ -466,43 +549,38 @@ __device__ __forceinline__ void write_state(typename Layout<KDP, VDP>::State& S,
     }
   }
   const float all = d.all;
+  constexpr int kHalf = Y::MT / 2;  // the keys' fragments are read half a round ahead of their products
+  Frag<T> kf[2][kHalf][kSteps];
+  auto read = [&](int half) {
 #pragma unroll
-  for (int m = 0; m < Y::MT; m++) {
+    for (int m = 0; m < kHalf; m++)
 #pragma unroll
-    for (int n = 0; n < Y::NT; n++)
+      for (int ks = 0; ks < kSteps; ks++)
+        kf[half][m][ks] = col_frag(Ks, Tile<T, KDP, kKey>::ld, 32 * ks + g8, 16 * (half * kHalf + m), 4);
+  };
+  auto multiply = [&](int half) {
 #pragma unroll
-      for (int r = 0; r < 4; r++) S[m][n][r] *= all;
+    for (int i = 0; i < kHalf; i++) {
+      const int m = half * kHalf + i;
 #pragma unroll
-    for (int ks = 0; ks < 2; ks++) {
-      const Frag<T> kf = col_frag(Ks, Tile<T, KDP>::ld, 32 * ks + g8, 32 * (m / 2) + 4 * (m % 2), 8);
+      for (int n = 0; n < Y::NT; n++)
 #pragma unroll
-      for (int n = 0; n < Y::NT; n++) {
-        S[m][n] = mma(kf, hi[ks][n], S[m][n]);
-        if constexpr (sizeof(T) == 2) S[m][n] = mma(kf, lo[ks][n], S[m][n]);
-      }
+        for (int r = 0; r < 4; r++) S[m][n][r] *= all;
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ks++)
+#pragma unroll
+        for (int n = 0; n < Y::NT; n++) {
+          S[m][n] = mma(kf[half][i][ks], hi[ks][n], S[m][n]);
+          if constexpr (sizeof(T) == 2) S[m][n] = mma(kf[half][i][ks], lo[ks][n], S[m][n]);
+        }
     }
-  }
-}
-
-// Where a workgroup is: its head, batch row, segment and the chunks of it.
-struct Place {
-  int h, seg, c0, c1, n;
-  int64_t bi, bh;
-};
-__device__ __forceinline__ Place place_of(const Sweep& p, int n_segs) {
-  Place w;
-  // Workgroups are dealt to the 8 XCDs in turn: with H a multiple of 8, each XCD takes H / 8 neighbouring
-  // heads, so that the heads of a group read their shared rows through one L2.
-  const int id = blockIdx.x;
-  w.h = p.H % 8 == 0 ? (id % 8) * (p.H / 8) + (id / 8) % (p.H / 8) : id % p.H;
-  const int rest = blockIdx.x / p.H;
-  w.seg = rest % n_segs;
-  w.bi = rest / n_segs;
-  w.bh = w.bi * p.H + w.h;
-  w.n = live_length(p.lengths, w.bi, p.L);
-  w.c0 = w.seg * p.seg_chunks;
-  w.c1 = min(w.c0 + p.seg_chunks, p.n_chunks);
-  return w;
+  };
+  read(0);
+  __builtin_amdgcn_sched_barrier(0);
+  read(1);
+  multiply(0);
+  __builtin_amdgcn_sched_barrier(0);
+  multiply(1);
 }
 
 // The row of a tensor of `heads` heads of D elements that token t of a batch row has for head h
@@ -511,8 +589,8 @@ __device__ __forceinline__ const T* row_of(const void* x, const Sweep& p, const 
   return static_cast<const T*>(x) + ((w.bi * p.L + t) * (p.H / share) + w.h / share) * int64_t(D);
 }
 
-// Where a Stage of the tensor starts: the row of the sweep's position 64 c0, or in reversed time of position 64 c0 + 63
-template <typename T>
+// Where the chunks of a tensor start: the row of the first chunk's first position, or in reversed time of its last
+template <typename T, int kC>
 __device__ __forceinline__ const T* start_of(const void* x, const Sweep& p, const Place& w, int share, int D) {
   const int64_t t = p.reverse ? int64_t(w.n) - int64_t(w.c0) * kC - kC : int64_t(w.c0) * kC;
   return row_of<T>(x, p, w, share, t, D);
@@ -524,138 +602,183 @@ __device__ __forceinline__ const T* start_of(const void* x, const Sweep& p, cons
 template <typename T, int KDP, int VDP, bool VEC>
 __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) void lin_state_kernel(Sweep p) {
   typedef Layout<KDP, VDP> Y;
-  __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP>::kElems];
-  __shared__ __attribute__((aligned(16))) T Vs[Tile<T, VDP>::kElems];
-  __shared__ Decays ds[2];
+  constexpr int kC = kChunk<T>;
+  __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP, kKey>::kElems];
+  __shared__ __attribute__((aligned(16))) T Vs[Tile<T, VDP, kValue>::kElems];
+  __shared__ Decays<kC> ds[2];
   const Place w = place_of(p, p.n_segs - 1);
-  const int g8 = 8 * int((threadIdx.x % kWave) / 16);
-  Stage<T, KDP, VEC> sk;
-  Stage<T, VDP, VEC> sv;
-  sk.init(start_of<T>(p.xk, p, w, p.gk, p.KD), p.H / p.gk * p.KD, p.KD, p.reverse);
-  sv.init(start_of<T>(p.xv, p, w, p.gv, p.VD), p.H / p.gv * p.VD, p.VD, p.reverse);
+  const int tid = threadIdx.x, g8 = 8 * ((tid % kWave) / 16);
+  Stage<T, KDP, kKey, VEC> sk;
+  Stage<T, VDP, kValue, VEC> sv;
+  uint4 rk[Tile<T, KDP, kKey>::kPieces], rv[Tile<T, VDP, kValue>::kPieces];
+  sk.init(start_of<T, kC>(p.xk, p, w, p.gk, p.KD), p.H / p.gk * p.KD, p.KD, p.reverse, tid);
+  sv.init(start_of<T, kC>(p.xv, p, w, p.gv, p.VD), p.H / p.gv * p.VD, p.VD, p.reverse, tid);
+  Gates<T, kC> gates;
+  gates.init(p, w, w.c0);
   float gate = 0.f;
   auto fetch = [&](int c) {
-    const int nv = w.n - c * kC;
-    sk.load(nv);
-    sv.load(nv);
-    if (threadIdx.x < kWave) gate = gate_of<T>(p, w.bi, w.h, c * kC + int(threadIdx.x), w.n);
+    const int nv = c < w.c1 ? w.n - c * kC : 0;  // behind the segment nothing is read
+    sk.load(rk, nv, tid);
+    sv.load(rv, nv, tid);
+    gate = gates.load(c * kC, nv);
   };
   typename Y::State S;
   Y::zero(S);
   double total = 0.0;
   fetch(w.c0);
-  if (threadIdx.x < kWave) total += fill_decays(ds[0], gate, p.wscale);
+  if (tid < kWave) total += fill_decays(ds[0], gates.log_of(gate, w.c0 * kC, w.n - w.c0 * kC), p.wscale);
   for (int c = w.c0; c < w.c1; c++) {
-    const Decays& d = ds[(c - w.c0) & 1];
-    sk.store(Ks);
-    sv.store(Vs);
+    const Decays<kC>& d = ds[(c - w.c0) & 1];
+    sk.store(Ks, rk, tid);
+    sv.store(Vs, rv, tid);
     __syncthreads();
-    if (c + 1 < w.c1) fetch(c + 1);
-    Frag<T> vf[2][Y::NT];
+    fetch(c + 1);
+    Frag<T> vf[kC / 32][Y::NT];
 #pragma unroll
-    for (int ks = 0; ks < 2; ks++)
+    for (int ks = 0; ks < kC / 32; ks++)
 #pragma unroll
-      for (int n = 0; n < Y::NT; n++) vf[ks][n] = col_frag(Vs, Tile<T, VDP>::ld, 32 * ks + g8, Y::v0(n), Y::vstep);
+      for (int n = 0; n < Y::NT; n++) vf[ks][n] = col_frag(Vs, Tile<T, VDP, kValue>::ld, 32 * ks + g8, Y::v0(n), Y::vstep);
     write_state<T, KDP, VDP>(S, Ks, vf, d);
-    if (c + 1 < w.c1 && threadIdx.x < kWave) total += fill_decays(ds[(c + 1 - w.c0) & 1], gate, p.wscale);
+    if (c + 1 < w.c1 && tid < kWave)
+      total += fill_decays(ds[(c + 1 - w.c0) & 1], gates.log_of(gate, (c + 1) * kC, w.n - (c + 1) * kC), p.wscale);
     __syncthreads();
   }
   const int64_t at = (w.bi * (p.n_segs - 1) + w.seg) * p.H + w.h;
   Y::store(S, p.seg_state + at * p.KD * p.VD, p.KD, p.VD, 1.f);
-  if (threadIdx.x == 0) p.seg_decay[at] = float(total);
+  if (tid == 0) p.seg_decay[at] = float(total);
 }
 
 // ---------------------------------------------------------------------------
 // The sweep.  Per chunk:
 //   P[t][s] = (q_t . k_s) exp(G_t - G_s) for s <= t, computed as K Q^T (a lane then has four
-//             consecutive s of its t), 10 blocks of 16 x 16 shared out over the waves, to LDS
+//             consecutive s of its t), to LDS
 //   out     = exp(G_t) S^T q_t + P V, as its transpose: a lane has consecutive columns of its own t
 //   S       = exp(G) S + K^T (out o V)
 // With DOTS the output without the token's own product is multiplied with the rows of xd, which
 // has to be right to fp32 over long sums: P and S go into the products as two bf16 parts.
+//
+// Only the state runs from chunk to chunk, so it has waves of its own: waves 0..3 take the outputs and
+// the state's update, while waves 4..7 bring the next chunk's rows to the other half of the LDS tiles
+// and then compute its P, in the other half of P; two barriers a chunk.  One SIMD has a wave of each kind.  The rows of the
+// two chunks after are on their way into registers meanwhile.
 // ---------------------------------------------------------------------------
+template <typename T, int KDP, int VDP, bool DOTS>
+struct SweepLds {
+  static constexpr int kC = kChunk<T>;
+  static constexpr bool kTwo = DOTS && sizeof(T) == 2;
+  static constexpr int ldp = kC + 16 / int(sizeof(T));
+  __attribute__((aligned(16))) T q[2][Tile<T, KDP, kQuery>::kElems];
+  __attribute__((aligned(16))) T k[2][Tile<T, KDP, kKey>::kElems];
+  __attribute__((aligned(16))) T v[2][Tile<T, VDP, kValue>::kElems];
+  __attribute__((aligned(16))) T P[2][kTwo ? 2 : 1][kC * ldp];
+  Decays<kC> d[2];
+  float diag[2][DOTS ? kC : 1], dot_part[DOTS ? 4 : 1][kC], red[4];
+};
+
 template <typename T, int KDP, int VDP, bool DOTS, bool VEC>
-__global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DOTS)) void lin_sweep_kernel(Sweep p) {
+__global__ __launch_bounds__(2 * kThreads) SSM_LIN_WAVES(kSweepWaves) void lin_sweep_kernel(Sweep p) {
   typedef Layout<KDP, VDP> Y;
-  constexpr bool kTwo = DOTS && sizeof(T) == 2;
-  constexpr int ldp = kC + 16 / int(sizeof(T)), kN = 4 * Y::NT;
-  constexpr int ldk = Tile<T, KDP>::ld, ldv = Tile<T, VDP>::ld;
-  __shared__ __attribute__((aligned(16))) T Qs[Tile<T, KDP>::kElems];
-  __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP>::kElems];
-  __shared__ __attribute__((aligned(16))) T Vs[Tile<T, VDP>::kElems];
-  __shared__ __attribute__((aligned(16))) T Ps[kTwo ? 2 : 1][kC * ldp];
-  __shared__ Decays ds[2];
-  __shared__ float diag[DOTS ? kC : 1], dot_part[DOTS ? 4 : 1][kC], red[4];
+  typedef SweepLds<T, KDP, VDP, DOTS> Lds;
+  constexpr int kC = Lds::kC, ldp = Lds::ldp, kN = 4 * Y::NT, TB = kC / 16, kSteps = kC / 32;
+  constexpr bool kTwo = Lds::kTwo;
+  constexpr int ldq = Tile<T, KDP, kQuery>::ld, ldk = Tile<T, KDP, kKey>::ld, ldv = Tile<T, VDP, kValue>::ld;
+  __shared__ Lds sh;
   const Place w = place_of(p, p.n_segs);
-  const int wv = threadIdx.x / kWave, l = threadIdx.x % kWave;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = threadIdx.x % kWave;
   const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
-  const int vc = wv * (VDP / 4) + (l / 16) * kN;  // first of the kN columns that this lane has of an output row
-  const float sscale = p.wscale * p.rscale;
-  Stage<T, KDP, VEC> sq, sk;
-  Stage<T, VDP, VEC> sv;
-  sq.init(start_of<T>(p.xq, p, w, p.gq, p.KD), p.H / p.gq * p.KD, p.KD, p.reverse);
-  sk.init(start_of<T>(p.xk, p, w, p.gk, p.KD), p.H / p.gk * p.KD, p.KD, p.reverse);
-  sv.init(start_of<T>(p.xv, p, w, p.gv, p.VD), p.H / p.gv * p.VD, p.VD, p.reverse);
-  Rows<T, kN, VEC> xr, yr;
-  Rows<float, kN, VEC> fr;
-  if constexpr (DOTS) xr.init(start_of<T>(p.xd, p, w, p.gd, p.VD), p.H / p.gd * p.VD, vc, p.VD, p.reverse);
-  if (p.out_f32) fr.init(start_of<float>(p.out, p, w, 1, p.VD), p.H * p.VD, vc, p.VD, p.reverse);
-  else yr.init(start_of<T>(p.out, p, w, 1, p.VD), p.H * p.VD, vc, p.VD, p.reverse);
-  float gate = 0.f;
-  const bool gates = threadIdx.x >= 3 * kWave;  // the wave with the fewest blocks of P takes the decays
-  auto fetch = [&](int c) {
-    const int nv = w.n - c * kC;
-    sq.load(nv);
-    sk.load(nv);
-    sv.load(nv);
-    if (gates) gate = gate_of<T>(p, w.bi, w.h, c * kC + l, w.n);
-  };
-  // the two blocks above the diagonal that the products read stay zero
-  for (int i = threadIdx.x; i < 2 * 16 * 16; i += kThreads) {
+  const int chunks = w.c1 - w.c0;
+  // the blocks above the diagonal that the products read stay zero
+  for (int i = threadIdx.x; i < (TB / 2) * 256; i += 2 * kThreads) {
     const int b = i / 256, t = 32 * b + (i / 16) % 16, s = 32 * b + 16 + i % 16;
 #pragma unroll
-    for (int k = 0; k < (kTwo ? 2 : 1); k++) Ps[k][t * ldp + s] = T(0);
+    for (int k = 0; k < 2 * (kTwo ? 2 : 1); k++) sh.P[0][k][t * ldp + s] = T(0);
   }
-  typename Y::State S;
-  const float* from = w.seg > 0 ? p.seg_state + ((w.bi * (p.n_segs - 1) + w.seg - 1) * p.H + w.h) * p.KD * p.VD
-                                : p.init ? p.init + w.bh * p.KD * p.VD : nullptr;
-  if (from) Y::load(S, from, p.init_t, p.KD, p.VD);
-  else Y::zero(S);
-  if (w.c0 < w.c1) {
-    fetch(w.c0);
-    if (gates) fill_decays(ds[0], gate, p.wscale);
-  }
-  for (int c = w.c0; c < w.c1; c++) {
-    const int p0 = c * kC, nv = max(0, min(kC, w.n - p0));
-    const Decays& d = ds[(c - w.c0) & 1];
-    sq.store(Qs);
-    sk.store(Ks);
-    sv.store(Vs);
-    __syncthreads();
-    if (c + 1 < w.c1) fetch(c + 1);
-    // ---- P: blocks b = wv, wv + 4, wv + 8 of the ten (t block, s block) with s <= t ----
+
+  if (wv >= 4) {
+    // ------------------------------------------------------------------ staging and scores
+    const int pw = wv - 4, tid = threadIdx.x - kThreads;
+    const float sscale = p.wscale * p.rscale;
+    Stage<T, KDP, kQuery, VEC> sq;
+    Stage<T, KDP, kKey, VEC> sk;
+    Stage<T, VDP, kValue, VEC> sv;
+    sq.init(start_of<T, kC>(p.xq, p, w, p.gq, p.KD), p.H / p.gq * p.KD, p.KD, p.reverse, tid);
+    sk.init(start_of<T, kC>(p.xk, p, w, p.gk, p.KD), p.H / p.gk * p.KD, p.KD, p.reverse, tid);
+    sv.init(start_of<T, kC>(p.xv, p, w, p.gv, p.VD), p.H / p.gv * p.VD, p.VD, p.reverse, tid);
+    struct Regs {
+      uint4 q[Tile<T, KDP, kQuery>::kPieces], k[Tile<T, KDP, kKey>::kPieces], v[Tile<T, VDP, kValue>::kPieces];
+      float gate;
+    };
+    Regs r0, r1;
+    Gates<T, kC> gates;
+    gates.init(p, w, w.c0);
+    // behind the segment (i >= chunks) nothing is read and the rows are zero
+    auto live = [&](int i) { return i < chunks ? w.n - (w.c0 + i) * kC : 0; };
+    auto fetch = [&](Regs& r, int i) {  // the i-th chunk of the segment
+      const int nv = live(i);
+      sq.load(r.q, nv, tid);
+      sk.load(r.k, nv, tid);
+      sv.load(r.v, nv, tid);
+      r.gate = gates.load((w.c0 + i) * kC, nv);
+    };
+    auto place = [&](const Regs& r, int i) {
+      const int b = i & 1;
+      sq.store(sh.q[b], r.q, tid);
+      sk.store(sh.k[b], r.k, tid);
+      sv.store(sh.v[b], r.v, tid);
+      const float g = gates.log_of(r.gate, (w.c0 + i) * kC, live(i));
+      if (pw == 3) fill_decays(sh.d[b], g, p.wscale);
+    };
+    // P of the i-th chunk: its blocks (t block, s block) with s <= t, mostly of one t block a wave, so that the rows of Q
+    // are read once; the wave that takes the decays has the fewest.  All reads come first, all products next.
+    auto score_blocks = [&](int i, auto count, int t0, int s0, int t1, int s1, int t2, int s2) {
+      constexpr int N = decltype(count)::value;
+      const int tbs[3] = {t0, t1, t2}, sbs[3] = {s0, s1, s2};
+      const T* Qs = sh.q[i & 1];
+      const T* Ks = sh.k[i & 1];
+      const Decays<kC>& d = sh.d[i & 1];
+      const int pb = i & 1;
+      Frag<T> qf[N][Y::KS], kf[N][Y::KS];
+      float th[N], tl[N];
+      float4 h4[N], l4[N];
 #pragma unroll
-    for (int i = 0; i < 3; i++) {
-      const int b = wv + 4 * i;
-      if (b < 10) {
-        const int tb = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, sb = b - tb * (tb + 1) / 2;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < N; j++) {
 #pragma unroll
-        for (int kk = 0; kk < Y::KS; kk++)
-          acc = mma(row_frag(Ks + (16 * sb + lr) * ldk + 32 * kk + g8), row_frag(Qs + (16 * tb + lr) * ldk + 32 * kk + g8), acc);
-        const int t = 16 * tb + lr;
-        const float th = d.hi[t], tl = d.lo[t];
-        const float4 sh4 = lds4(d.hi + 16 * sb + g4), sl4 = lds4(d.lo + 16 * sb + g4);
-        const float shi[4] = {sh4.x, sh4.y, sh4.z, sh4.w}, slo[4] = {sl4.x, sl4.y, sl4.z, sl4.w};
+        for (int kk = 0; kk < Y::KS; kk++) {
+          qf[j][kk] = row_frag(Qs + (16 * tbs[j] + lr) * ldq + 32 * kk + g8);
+          kf[j][kk] = row_frag(Ks + (16 * sbs[j] + lr) * ldk + 32 * kk + g8);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        th[j] = d.hi[16 * tbs[j] + lr];
+        tl[j] = d.lo[16 * tbs[j] + lr];
+        h4[j] = lds4(d.hi + 16 * sbs[j] + g4);
+        l4[j] = lds4(d.lo + 16 * sbs[j] + g4);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 acc[N];
+#pragma unroll
+      for (int j = 0; j < N; j++) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < Y::KS; kk++)
+#pragma unroll
+        for (int j = 0; j < N; j++) acc[j] = mma(kf[j][kk], qf[j][kk], acc[j]);
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        const int tb = tbs[j], sb = sbs[j], t = 16 * tb + lr;
+        const float shi[4] = {h4[j].x, h4[j].y, h4[j].z, h4[j].w}, slo[4] = {l4[j].x, l4[j].y, l4[j].z, l4[j].w};
         float x[4];
 #pragma unroll
         for (int r = 0; r < 4; r++) {
           const int s = 16 * sb + g4 + r;
-          const float e = exp2_fast((th - shi[r]) + (tl - slo[r])) * sscale;
-          x[r] = (DOTS ? s < t : s <= t) ? acc[r] * e : 0.f;
-          if (DOTS && s == t) diag[t] = acc[r] * sscale;
+          const float e = acc[j][r] * exp2_fast((th[j] - shi[r]) + (tl[j] - slo[r])) * sscale;
+          x[r] = (DOTS ? s < t : s <= t) ? e : 0.f;
         }
-        T* pr = Ps[0] + t * ldp + 16 * sb + g4;
+        if (DOTS && tb == sb && lr / 4 == l / 16) {  // the lane with s == t among its four
+          const float a01 = lr % 2 ? acc[j][1] : acc[j][0], a23 = lr % 2 ? acc[j][3] : acc[j][2];
+          sh.diag[pb][t] = (lr % 4 < 2 ? a01 : a23) * sscale;
+        }
+        T* pr = sh.P[pb][0] + t * ldp + 16 * sb + g4;
         if constexpr (sizeof(T) == 4) {
           *reinterpret_cast<float4*>(pr) = make_float4(x[0], x[1], x[2], x[3]);
         } else {
@@ -664,72 +787,179 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
           if constexpr (kTwo) {
             const float y[4] = {x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xffff0000u),
                                 x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xffff0000u)};
-            *reinterpret_cast<uint2*>(Ps[1] + t * ldp + 16 * sb + g4) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+            *reinterpret_cast<uint2*>(sh.P[pb][1] + t * ldp + 16 * sb + g4) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
           }
         }
       }
-    }
-    // ---- the entering state's part of the outputs ----
-    f32x4 o[4][Y::NT];
-#pragma unroll
-    for (int tt = 0; tt < 4; tt++)
-#pragma unroll
-      for (int n = 0; n < Y::NT; n++) o[tt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int kk = 0; kk < Y::KS; kk++) {
-      Frag<T> sh[Y::NT], sl[Y::NT];
-#pragma unroll
-      for (int n = 0; n < Y::NT; n++) {
-        float x[8];
-#pragma unroll
-        for (int r = 0; r < 8; r++) x[r] = S[2 * kk + r / 4][n][r % 4];
-        make_frag(x, sh[n]);
-        if constexpr (kTwo) sl[n] = rest_frag(x, sh[n]);
+    };
+    auto score = [&](int i) {
+      using std::integral_constant;
+      if constexpr (TB == 4) {
+        if (pw < 3) {
+          if constexpr (KDP == 64) {
+            score_blocks(i, integral_constant<int, 3>{}, 3 - pw, 0, 3 - pw, 1, pw == 2 ? 0 : 3 - pw, pw == 2 ? 0 : 2);
+          } else {  // three at once would not fit in the registers
+            score_blocks(i, integral_constant<int, 1>{}, 3 - pw, 0, 0, 0, 0, 0);
+            score_blocks(i, integral_constant<int, 1>{}, 3 - pw, 1, 0, 0, 0, 0);
+            score_blocks(i, integral_constant<int, 1>{}, pw == 2 ? 0 : 3 - pw, pw == 2 ? 0 : 2, 0, 0, 0, 0);
+          }
+        } else score_blocks(i, integral_constant<int, 1>{}, 3, 3, 0, 0, 0, 0);
+      } else {
+        if (pw < 3) score_blocks(i, integral_constant<int, 1>{}, pw > 0, pw > 1, 0, 0, 0, 0);
       }
-#pragma unroll
-      for (int tt = 0; tt < 4; tt++) {
-        const Frag<T> qf = row_frag(Qs + (16 * tt + lr) * ldk + 32 * kk + g8);
-#pragma unroll
-        for (int n = 0; n < Y::NT; n++) {
-          o[tt][n] = mma(sh[n], qf, o[tt][n]);
-          if constexpr (kTwo) o[tt][n] = mma(sl[n], qf, o[tt][n]);
+    };
+    // what follows the outputs of the i-th chunk: the dots' sums over the waves, and zero rows behind the length
+    auto finish = [&](int i) {
+      if (i < 0 || i >= chunks) return;
+      const int p0 = (w.c0 + i) * kC, nv = max(0, min(kC, w.n - p0)), rows = min(kC, int(p.L) - p0);
+      if constexpr (DOTS) {
+        if (tid < rows) {
+          const int64_t t = tid >= nv ? p0 + tid : p.reverse ? w.n - 1 - p0 - tid : p0 + tid;
+          p.dots[(w.bi * p.L + t) * p.H + w.h] =
+              tid < nv ? (sh.dot_part[0][tid] + sh.dot_part[1][tid]) + (sh.dot_part[2][tid] + sh.dot_part[3][tid]) : 0.f;
         }
       }
+      for (int r = nv + pw; r < rows; r += 4) {
+        const int64_t at = ((w.bi * p.L + p0 + r) * p.H + w.h) * p.VD;
+        for (int j = l; j < p.VD; j += kWave) {
+          if (p.out_f32) static_cast<float*>(p.out)[at + j] = 0.f;
+          else store_elem(static_cast<T*>(p.out) + at + j, 0.f);
+        }
+      }
+    };
+    fetch(r0, 0);
+    fetch(r1, 1);
+    place(r0, 0);
+    fetch(r0, 2);
+    __syncthreads();
+    score(0);
+    __syncthreads();
+    // at the top of step i: chunk i is in the tiles and in P, chunks i + 1 (in r) and i + 2 in registers or under
+    // way.  Steps go by twos, each with its set of registers, so that a wait is for the older loads only.
+    auto step = [&](Regs& r, int i) {
+      place(r, i + 1);
+      fetch(r, i + 3);
+      finish(i - 1);
+      __syncthreads();
+      score(i + 1);
+      __syncthreads();
+    };
+    for (int i = 0; i < chunks; i += 2) {
+      step(r1, i);
+      step(r0, i + 1);
     }
-#pragma unroll
-    for (int tt = 0; tt < 4; tt++) {
-      const float f = d.in[16 * tt + lr] * p.rscale;
-#pragma unroll
-      for (int n = 0; n < Y::NT; n++)
-#pragma unroll
-        for (int r = 0; r < 4; r++) o[tt][n][r] *= f;
-    }
-    typename Rows<T, kN, VEC>::Raw xd[DOTS ? 4 : 1];  // the rows of xd for the lane's outputs
+    if (chunks % 2 == 0) finish(chunks - 1);
+    if (DOTS && p.dstate_dot && w.seg == p.n_segs - 1) __syncthreads();  // the state waves' sum
+    return;
+  }
+
+  // -------------------------------------------------------------------- outputs and state
+  const int vc = wv * (VDP / 4) + (l / 16) * kN;  // first of the kN columns that this lane has of an output row
+  typedef Rows<kN, VEC, kC> R;
+  R xr, yr;
+  if constexpr (DOTS) xr.init(p, w, p.xd, int(sizeof(T)), p.gd, vc);
+  yr.init(p, w, p.out, p.out_f32 ? 4 : int(sizeof(T)), 1, vc);
+  typename R::template Raw<T> xd[DOTS ? TB : 1];  // the rows of xd for the lane's outputs
+  auto fetch_xd = [&](int i) {
     if constexpr (DOTS) {
+      const int nv = i < chunks ? w.n - (w.c0 + i) * kC : 0;
 #pragma unroll
-      for (int tt = 0; tt < 4; tt++) xd[tt] = xr.load(tt, nv);
+      for (int tt = 0; tt < TB; tt++) xd[tt] = xr.template load<T>(tt, nv);
       xr.next();
     }
-    __syncthreads();
-    // ---- the chunk's own part ----
-    Frag<T> vf[2][Y::NT];
+  };
+  typename Y::State S;
+  const float* from = w.seg > 0 ? p.seg_state + ((w.bi * (p.n_segs - 1) + w.seg - 1) * p.H + w.h) * p.KD * p.VD
+                                : p.init ? p.init + w.bh * p.KD * p.VD : nullptr;
+  if (from) Y::load(S, from, p.init_t, p.KD, p.VD);
+  else Y::zero(S);
+  fetch_xd(0);
+  __syncthreads();
+  __syncthreads();
+  for (int c = 0; c < chunks; c++) {
+    const int nv = max(0, min(kC, w.n - (w.c0 + c) * kC));
+    const Decays<kC>& d = sh.d[c & 1];
+    const T* Qs = sh.q[c & 1];
+    const T* Ks = sh.k[c & 1];
+    const T* Vs = sh.v[c & 1];
+    // ---- the entering state's part of the outputs, and the chunk's own: reads a step ahead of their products ----
+    f32x4 o[TB][Y::NT];
 #pragma unroll
-    for (int ks = 0; ks < 2; ks++)
+    for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++) o[tt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int kHalf = Y::KS / 2;
+    Frag<T> qf[2][kHalf][TB];
+    auto read_q = [&](int half) {
+#pragma unroll
+      for (int k = 0; k < kHalf; k++)
+#pragma unroll
+        for (int tt = 0; tt < TB; tt++) {
+          const T* q = Qs + (16 * tt + lr) * ldq + 32 * (half * kHalf + k) + g4;
+          qf[half][k][tt] = pair_frag(q, q + 16);
+        }
+    };
+    auto times_state = [&](int half) {
+#pragma unroll
+      for (int k = 0; k < kHalf; k++) {
+        const int kk = half * kHalf + k;
+        Frag<T> shi[Y::NT], slo[Y::NT];
+#pragma unroll
+        for (int n = 0; n < Y::NT; n++) {
+          float x[8];
+#pragma unroll
+          for (int r = 0; r < 8; r++) x[r] = S[2 * kk + r / 4][n][r % 4];
+          make_frag(x, shi[n]);
+          if constexpr (kTwo) slo[n] = rest_frag(x, shi[n]);
+        }
+#pragma unroll
+        for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+          for (int n = 0; n < Y::NT; n++) {
+            o[tt][n] = mma(shi[n], qf[half][k][tt], o[tt][n]);
+            if constexpr (kTwo) o[tt][n] = mma(slo[n], qf[half][k][tt], o[tt][n]);
+          }
+      }
+    };
+    Frag<T> vf[kSteps][Y::NT], pf[kTwo ? 2 : 1][TB][kSteps];
+    read_q(0);
+    __builtin_amdgcn_sched_barrier(0);
+    read_q(1);
+    times_state(0);
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+    float in[TB];
+#pragma unroll
+    for (int tt = 0; tt < TB; tt++) in[tt] = d.in[16 * tt + lr] * p.rscale;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ks++)
 #pragma unroll
       for (int n = 0; n < Y::NT; n++) vf[ks][n] = col_frag(Vs, ldv, 32 * ks + g8, Y::v0(n), Y::vstep);
 #pragma unroll
-    for (int tt = 0; tt < 4; tt++)
+    for (int k = 0; k < (kTwo ? 2 : 1); k++)
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+        for (int ks = 0; ks <= tt / 2; ks++) pf[k][tt][ks] = row_frag(sh.P[c & 1][k] + (16 * tt + lr) * ldp + 32 * ks + g8);
+    times_state(1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) o[tt][n][r] *= in[tt];
+#pragma unroll
+    for (int tt = 0; tt < TB; tt++)
 #pragma unroll
       for (int ks = 0; ks <= tt / 2; ks++)
 #pragma unroll
-        for (int k = 0; k < (kTwo ? 2 : 1); k++) {
-          const Frag<T> pf = row_frag(Ps[k] + (16 * tt + lr) * ldp + 32 * ks + g8);
+        for (int k = 0; k < (kTwo ? 2 : 1); k++)
 #pragma unroll
-          for (int n = 0; n < Y::NT; n++) o[tt][n] = mma(vf[ks][n], pf, o[tt][n]);
-        }
+          for (int n = 0; n < Y::NT; n++) o[tt][n] = mma(vf[ks][n], pf[k][tt][ks], o[tt][n]);
     // ---- outputs ----
 #pragma unroll
-    for (int tt = 0; tt < 4; tt++) {
+    for (int tt = 0; tt < TB; tt++) {
       const int i = 16 * tt + lr;
       float y[kN];
 #pragma unroll
@@ -737,11 +967,11 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
       if constexpr (DOTS) {
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < kN; j++) s = fmaf(y[j], Rows<T, kN, VEC>::element(xd[tt], j), s);
+        for (int j = 0; j < kN; j++) s = fmaf(y[j], R::template element<T>(xd[tt], j), s);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
-        if (l < 16) dot_part[wv][i] = s;
-        const float dg = diag[i];
+        if (l < 16) sh.dot_part[wv][i] = s;
+        const float dg = sh.diag[c & 1][i];
 #pragma unroll
         for (int j = 0; j < kN; j += 4) {
           const float4 v = lds4(Vs + i * ldv + vc + j);
@@ -749,32 +979,17 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
           y[j + 2] = fmaf(dg, v.z, y[j + 2]); y[j + 3] = fmaf(dg, v.w, y[j + 3]);
         }
       }
-      if (p.out_f32) fr.store(tt, nv, y);
-      else yr.store(tt, nv, y);
+      if (sizeof(T) == 2 && p.out_f32) yr.template store<float>(tt, nv, y);
+      else yr.template store<T>(tt, nv, y);
     }
-    fr.next();
     yr.next();
+    fetch_xd(c + 1);
     write_state<T, KDP, VDP>(S, Ks, vf, d);
-    if (c + 1 < w.c1 && gates) fill_decays(ds[(c + 1 - w.c0) & 1], gate, p.wscale);
     __syncthreads();
-    if constexpr (DOTS) {
-      const int i = threadIdx.x;
-      if (i < kC && p0 + i < p.L) {
-        const int64_t t = i >= nv ? p0 + i : p.reverse ? w.n - 1 - p0 - i : p0 + i;
-        p.dots[(w.bi * p.L + t) * p.H + w.h] =
-            i < nv ? (dot_part[0][i] + dot_part[1][i]) + (dot_part[2][i] + dot_part[3][i]) : 0.f;
-      }
-    }
-    if (nv < kC) {  // rows behind the sequence's length are zero
-      const int rows = min(kC, int(p.L) - p0);
-      for (int i = nv + threadIdx.x / kWave; i < rows; i += kThreads / kWave) {
-        const int64_t at = ((w.bi * p.L + p0 + i) * p.H + w.h) * p.VD;
-        for (int j = l; j < p.VD; j += kWave) {
-          if (p.out_f32) static_cast<float*>(p.out)[at + j] = 0.f;
-          else store_elem(static_cast<T*>(p.out) + at + j, 0.f);
-        }
-      }
-    }
+  }
+  if (chunks % 2) {  // the staging waves' steps go by twos
+    __syncthreads();
+    __syncthreads();
   }
   if (w.seg != p.n_segs - 1) return;
   if (DOTS && p.dstate_dot) {
@@ -791,9 +1006,9 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(sweep_waves<T>(KDP, VDP, DO
         }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-    if (l == 0) red[wv] = s;
+    if (l == 0) sh.red[wv] = s;
     __syncthreads();
-    if (threadIdx.x == 0) p.dstate_dot[w.bh] = (red[0] + red[1]) + (red[2] + red[3]);
+    if (threadIdx.x == 0) p.dstate_dot[w.bh] = (sh.red[0] + sh.red[1]) + (sh.red[2] + sh.red[3]);
   }
   if (p.last) {
     const float f = p.final_decay && w.n > 0 ? exp2_fast(log_decay<T>(p, w.bi, 0, w.h) * kLog2e) : 1.f;
@@ -965,8 +1180,8 @@ bool pieces(const void* x, int D) {
 template <typename T, int KDP, int VDP, bool DOTS>
 hipError_t sweep_kernel(const Sweep& p, bool vec) {
   const int64_t blocks = p.b * p.H * p.n_segs;
-  return vec ? launch_kind(kKindLinSweep, lin_sweep_kernel<T, KDP, VDP, DOTS, true>, blocks, kThreads, p.stream, p)
-             : launch_kind(kKindLinSweep, lin_sweep_kernel<T, KDP, VDP, DOTS, false>, blocks, kThreads, p.stream, p);
+  return vec ? launch_kind(kKindLinSweep, lin_sweep_kernel<T, KDP, VDP, DOTS, true>, blocks, 2 * kThreads, p.stream, p)
+             : launch_kind(kKindLinSweep, lin_sweep_kernel<T, KDP, VDP, DOTS, false>, blocks, 2 * kThreads, p.stream, p);
 }
 template <typename T, bool DOTS>
 hipError_t sweep_sizes(const Sweep& p, bool vec) {
@@ -1002,19 +1217,19 @@ hipError_t run_states(const Sweep& p) {
   return launch_chain<false, false, false>(kKindLinChain, c, p.stream);
 }
 
-// The cut of a sequence: as many segments as fill the chip's 256 CUs with the workgroups that run at once, and
-// no second generation of them; of at least kMinSeg chunks.
+// The cut of a sequence: as many segments as give every CU a workgroup, and no second generation of them
+// (a cut costs another reading of keys and values); of at least kMinSeg chunks.  Measured, bf16, b8 L2048 H24 D64:
+// 66 us in one piece, 96 us in two; b2 L8192 H32 D128: 422, 345, 246, 208 and 257 us in 1 to 5.
 constexpr int kMinSeg = 4;
+constexpr int64_t kAtOnce = 256;
 struct Cut {
   int n_chunks, n_segs, seg_chunks;
 };
 Cut cut_of(const LinAttnArgs& a) {
   Cut c;
-  c.n_chunks = int(ceil_div(a.L, kC));
+  c.n_chunks = int(ceil_div(a.L, a.dtype == 0 ? kChunk<float> : kChunk<bf16_bits>));
   const int64_t heads = a.b * a.H;
-  const int kd = a.Dk <= 64 ? 64 : 128, vd = a.Dv <= 64 ? 64 : 128;
-  const int64_t at_once = 256 * (a.dtype == 0 ? sweep_waves<float>(kd, vd, false) : sweep_waves<bf16_bits>(kd, vd, false));
-  const int64_t want = std::max<int64_t>(1, at_once / std::max<int64_t>(heads, 1));
+  const int64_t want = std::max<int64_t>(1, kAtOnce / std::max<int64_t>(heads, 1));
   const int64_t most = std::max<int64_t>(1, c.n_chunks / kMinSeg);
   c.n_segs = int(std::min(want, most));
   c.seg_chunks = int(std::max<int64_t>(1, ceil_div(c.n_chunks, c.n_segs)));
