@@ -213,13 +213,12 @@ struct Place {
   int h, seg, c0, c1, n;
   int64_t bi, bh;
 };
-__device__ __forceinline__ Place place_of(const Sweep& p, int n_segs) {
+__device__ __forceinline__ Place place_of(const Sweep& p, int n_segs, int id) {
   Place w;
   // Workgroups are dealt to the 8 XCDs in turn: with H a multiple of 8, each XCD takes H / 8 neighbouring
   // heads, so that the heads of a group read their shared rows through one L2.
-  const int id = blockIdx.x;
   w.h = p.H % 8 == 0 ? (id % 8) * (p.H / 8) + (id / 8) % (p.H / 8) : id % p.H;
-  const int rest = blockIdx.x / p.H;
+  const int rest = id / p.H;
   w.seg = rest % n_segs;
   w.bi = rest / n_segs;
   w.bh = w.bi * p.H + w.h;
@@ -606,7 +605,7 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) v
   __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP, kKey>::kElems];
   __shared__ __attribute__((aligned(16))) T Vs[Tile<T, VDP, kValue>::kElems];
   __shared__ Decays<kC> ds[2];
-  const Place w = place_of(p, p.n_segs - 1);
+  const Place w = place_of(p, p.n_segs - 1, blockIdx.x);
   const int tid = threadIdx.x, g8 = 8 * ((tid % kWave) / 16);
   Stage<T, KDP, kKey, VEC> sk;
   Stage<T, VDP, kValue, VEC> sv;
@@ -676,14 +675,13 @@ struct SweepLds {
 };
 
 template <typename T, int KDP, int VDP, bool DOTS, bool VEC>
-__global__ __launch_bounds__(2 * kThreads) SSM_LIN_WAVES(kSweepWaves) void lin_sweep_kernel(Sweep p) {
+__device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS>& sh, int id) {
   typedef Layout<KDP, VDP> Y;
   typedef SweepLds<T, KDP, VDP, DOTS> Lds;
   constexpr int kC = Lds::kC, ldp = Lds::ldp, kN = 4 * Y::NT, TB = kC / 16, kSteps = kC / 32;
   constexpr bool kTwo = Lds::kTwo;
   constexpr int ldq = Tile<T, KDP, kQuery>::ld, ldk = Tile<T, KDP, kKey>::ld, ldv = Tile<T, VDP, kValue>::ld;
-  __shared__ Lds sh;
-  const Place w = place_of(p, p.n_segs);
+  const Place w = place_of(p, p.n_segs, id);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = threadIdx.x % kWave;
   const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
   const int chunks = w.c1 - w.c0;
@@ -1016,6 +1014,36 @@ __global__ __launch_bounds__(2 * kThreads) SSM_LIN_WAVES(kSweepWaves) void lin_s
   }
 }
 
+template <typename T, int KDP, int VDP, bool VEC>
+__global__ __launch_bounds__(2 * kThreads) SSM_LIN_WAVES(kSweepWaves) void lin_fwd_kernel(Sweep p) {
+  __shared__ SweepLds<T, KDP, VDP, false> sh;
+  sweep<T, KDP, VDP, false, VEC>(p, sh, blockIdx.x);
+}
+
+// The three sweeps of the backward in one launch, n workgroups each: dq first, then dk and dv of the same heads on the
+// same XCD side by side (both run backwards over the same rows, which the second to come finds in the L2).
+template <typename T, int DKP, int DVP, bool GATE, bool VEC>
+__global__ __launch_bounds__(2 * kThreads) SSM_LIN_WAVES(kSweepWaves) void lin_bwd_kernel(Sweep dq, Sweep dk, Sweep dv, int n) {
+  typedef SweepLds<T, DVP, DKP, GATE> LdsK;
+  typedef SweepLds<T, DKP, DVP, false> LdsV;
+  __shared__ __attribute__((aligned(16))) char pool[sizeof(LdsK) > sizeof(LdsV) ? sizeof(LdsK) : sizeof(LdsV)];
+  const int id = blockIdx.x, j = id - n, even = n / 8 * 16;  // pairs of 8 workgroups, and what is left over
+  bool values;
+  int at;
+  if (id < n) {
+    at = id;
+    values = false;
+  } else if (j < even) {
+    at = j / 16 * 8 + j % 8;
+    values = j % 16 >= 8;
+  } else {
+    at = n / 8 * 8 + (j - even) % (n % 8);
+    values = j - even >= n % 8;
+  }
+  if (values) sweep<T, DKP, DVP, false, VEC>(dv, *reinterpret_cast<LdsV*>(pool), at);
+  else sweep<T, DVP, DKP, GATE, VEC>(id < n ? dq : dk, *reinterpret_cast<LdsK*>(pool), at);
+}
+
 // ---------------------------------------------------------------------------
 // Gradient of the gates: dg_t = end + sum over i >= t of (a_i - c_i), per batch row and head, where
 // end = <d_last, S_last>.  a and c are [b, L, H].  Tiles of kGateTile tokens: first each tile's
@@ -1089,17 +1117,33 @@ __global__ __launch_bounds__(256) void lin_gate_kernel(const float* __restrict__
   }
 }
 
-// out[row, g, :] = sum over the group's heads of in[row, h, :] (float), rounded once
-template <typename T>
+// out[row, g, :] = sum over the group's heads of in[row, h, :] (float), rounded once; VEC elements a thread
+template <typename T, int VEC>
 __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* __restrict__ in, T* __restrict__ out,
                                                             int64_t n, int share, int D) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * VEC;
   if (i >= n) return;
   const int64_t rg = i / D;
-  const int d = int(i % D);
-  float s = 0.f;
-  for (int k = 0; k < share; k++) s += in[(rg * share + k) * D + d];
-  store_elem(out + i, s);
+  const float* p = in + rg * share * D + i % D;
+  float s[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; j++) s[j] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < share; k++) {
+    if constexpr (VEC == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + int64_t(k) * D);
+      s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+    } else {
+      s[0] += p[int64_t(k) * D];
+    }
+  }
+  if constexpr (VEC == 4 && sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(out + i) = make_float4(s[0], s[1], s[2], s[3]);
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
+  } else {
+    store_elem(out + i, s[0]);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1177,22 +1221,35 @@ bool pieces(const void* x, int D) {
   return D % (16 / int(sizeof(T))) == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
 }
 
-template <typename T, int KDP, int VDP, bool DOTS>
-hipError_t sweep_kernel(const Sweep& p, bool vec) {
-  const int64_t blocks = p.b * p.H * p.n_segs;
-  return vec ? launch_kind(kKindLinSweep, lin_sweep_kernel<T, KDP, VDP, DOTS, true>, blocks, 2 * kThreads, p.stream, p)
-             : launch_kind(kKindLinSweep, lin_sweep_kernel<T, KDP, VDP, DOTS, false>, blocks, 2 * kThreads, p.stream, p);
+template <typename T>
+bool sweep_pieces(const Sweep& p) {
+  return pieces<T>(p.xq, p.KD) && pieces<T>(p.xk, p.KD) && pieces<T>(p.xv, p.VD) && pieces<T>(p.out, p.VD) &&
+         (!p.xd || pieces<T>(p.xd, p.VD));
 }
-template <typename T, bool DOTS>
-hipError_t sweep_sizes(const Sweep& p, bool vec) {
-  if (p.KD <= 64) return p.VD <= 64 ? sweep_kernel<T, 64, 64, DOTS>(p, vec) : sweep_kernel<T, 64, 128, DOTS>(p, vec);
-  return p.VD <= 64 ? sweep_kernel<T, 128, 64, DOTS>(p, vec) : sweep_kernel<T, 128, 128, DOTS>(p, vec);
+
+template <typename T, int KDP, int VDP>
+hipError_t fwd_kernel(const Sweep& p) {
+  const int64_t blocks = p.b * p.H * p.n_segs;
+  return sweep_pieces<T>(p) ? launch_kind(kKindLinSweep, lin_fwd_kernel<T, KDP, VDP, true>, blocks, 2 * kThreads, p.stream, p)
+                            : launch_kind(kKindLinSweep, lin_fwd_kernel<T, KDP, VDP, false>, blocks, 2 * kThreads, p.stream, p);
 }
 template <typename T>
-hipError_t run_sweep(const Sweep& p) {
-  const bool vec = pieces<T>(p.xq, p.KD) && pieces<T>(p.xk, p.KD) && pieces<T>(p.xv, p.VD) &&
-                   pieces<T>(p.out, p.VD) && (!p.xd || pieces<T>(p.xd, p.VD));
-  return p.dots ? sweep_sizes<T, true>(p, vec) : sweep_sizes<T, false>(p, vec);
+hipError_t run_fwd(const Sweep& p) {
+  if (p.KD <= 64) return p.VD <= 64 ? fwd_kernel<T, 64, 64>(p) : fwd_kernel<T, 64, 128>(p);
+  return p.VD <= 64 ? fwd_kernel<T, 128, 64>(p) : fwd_kernel<T, 128, 128>(p);
+}
+
+template <typename T, int DKP, int DVP, bool GATE>
+hipError_t bwd_kernel(const Sweep& dq, const Sweep& dk, const Sweep& dv) {
+  const int64_t n = dq.b * dq.H * dq.n_segs;
+  const bool vec = sweep_pieces<T>(dq) && sweep_pieces<T>(dk) && sweep_pieces<T>(dv);
+  return vec ? launch_kind(kKindLinSweep, lin_bwd_kernel<T, DKP, DVP, GATE, true>, 3 * n, 2 * kThreads, dq.stream, dq, dk, dv, int(n))
+             : launch_kind(kKindLinSweep, lin_bwd_kernel<T, DKP, DVP, GATE, false>, 3 * n, 2 * kThreads, dq.stream, dq, dk, dv, int(n));
+}
+template <typename T, bool GATE>
+hipError_t bwd_sizes(const Sweep& dq, const Sweep& dk, const Sweep& dv) {
+  if (dv.KD <= 64) return dv.VD <= 64 ? bwd_kernel<T, 64, 64, GATE>(dq, dk, dv) : bwd_kernel<T, 64, 128, GATE>(dq, dk, dv);
+  return dv.VD <= 64 ? bwd_kernel<T, 128, 64, GATE>(dq, dk, dv) : bwd_kernel<T, 128, 128, GATE>(dq, dk, dv);
 }
 
 template <typename T, int KDP, int VDP>
@@ -1298,7 +1355,7 @@ hipError_t fwd_impl(const LinAttnArgs& a, char* ws) {
   if (err != hipSuccess) return err;
   p.out = a.y;
   p.last = a.last;
-  return run_sweep<T>(p);
+  return run_fwd<T>(p);
 }
 
 template <typename T>
@@ -1325,60 +1382,56 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
     err = run_states<T>(p);
     if (err != hipSuccess) return err;
   }
-  Sweep p = common(a);  // dq: forwards, the state is S^T [Dv, Dk]
-  p.xq = a.dy; p.xk = a.v; p.xv = a.k; p.gv = share;
-  p.KD = int(a.Dv); p.VD = int(a.Dk);
-  p.rscale = a.scale;
-  p.init = a.h0; p.init_t = true; p.seg_state = seg_f;
-  p.out = share > 1 ? static_cast<void*>(ws + w.dq) : a.dq; p.out_f32 = share > 1;
+  Sweep dq = common(a);  // forwards, the state is S^T [Dv, Dk]
+  dq.xq = a.dy; dq.xk = a.v; dq.xv = a.k; dq.gv = share;
+  dq.KD = int(a.Dv); dq.VD = int(a.Dk);
+  dq.rscale = a.scale;
+  dq.init = a.h0; dq.init_t = true; dq.seg_state = seg_f;
+  dq.out = share > 1 ? static_cast<void*>(ws + w.dq) : a.dq; dq.out_f32 = share > 1;
+  Sweep dk = common(a);  // backwards, the state is D^T [Dv, Dk]
+  dk.xq = a.v; dk.xk = a.dy; dk.xv = a.q; dk.gv = share;
+  dk.KD = int(a.Dv); dk.VD = int(a.Dk);
+  dk.wscale = a.scale; dk.reverse = true;
+  dk.init = a.dlast; dk.init_t = true; dk.seg_state = seg_r;
+  dk.out = share > 1 ? static_cast<void*>(ws + w.dk) : a.dk; dk.out_f32 = share > 1;
+  Sweep dv = common(a);  // backwards, the state is D [Dk, Dv]
+  dv.xq = a.k; dv.gq = share; dv.xk = a.q; dv.gk = share; dv.xv = a.dy;
+  dv.KD = int(a.Dk); dv.VD = int(a.Dv);
+  dv.wscale = a.scale; dv.reverse = true;
+  dv.init = a.dlast; dv.seg_state = seg_r;
+  dv.out = a.dv;
+  dv.last = a.dh0; dv.final_decay = true;
   if (gate) {
-    p.xd = a.q; p.gd = share;
-    p.dots = reinterpret_cast<float*>(ws + w.dot_q);
-    p.dstate = a.dlast;
-    p.dstate_dot = end;
+    dq.xd = a.q; dk.xd = a.k;
+    dq.gd = dk.gd = share;
+    dq.dots = reinterpret_cast<float*>(ws + w.dot_q);
+    dk.dots = reinterpret_cast<float*>(ws + w.dot_k);
+    dq.dstate = a.dlast;
+    dq.dstate_dot = end;
   }
-  err = run_sweep<T>(p);
-  if (err != hipSuccess) return err;
-  p = common(a);  // dk: backwards, the state is D^T [Dv, Dk]
-  p.xq = a.v; p.xk = a.dy; p.xv = a.q; p.gv = share;
-  p.KD = int(a.Dv); p.VD = int(a.Dk);
-  p.wscale = a.scale; p.reverse = true;
-  p.init = a.dlast; p.init_t = true; p.seg_state = seg_r;
-  p.out = share > 1 ? static_cast<void*>(ws + w.dk) : a.dk; p.out_f32 = share > 1;
-  if (gate) {
-    p.xd = a.k; p.gd = share;
-    p.dots = reinterpret_cast<float*>(ws + w.dot_k);
-  }
-  err = run_sweep<T>(p);
-  if (err != hipSuccess) return err;
-  p = common(a);  // dv: backwards, the state is D [Dk, Dv]
-  p.xq = a.k; p.gq = share; p.xk = a.q; p.gk = share; p.xv = a.dy;
-  p.KD = int(a.Dk); p.VD = int(a.Dv);
-  p.wscale = a.scale; p.reverse = true;
-  p.init = a.dlast; p.seg_state = seg_r;
-  p.out = a.dv;
-  p.last = a.dh0; p.final_decay = true;
-  err = run_sweep<T>(p);
+  err = gate ? bwd_sizes<T, true>(dq, dk, dv) : bwd_sizes<T, false>(dq, dk, dv);
   if (err != hipSuccess || a.L == 0) return err;
   if (share > 1) {
     const int64_t n = a.b * a.L * a.G * a.Dk;
     for (int k = 0; k < 2; k++) {
-      err = launch_kind(kKindLinReduce, lin_group_sum_kernel<T>, ceil_div(n, 256), 256, a.stream,
-                        reinterpret_cast<const float*>(ws + (k ? w.dk : w.dq)), static_cast<T*>(k ? a.dk : a.dq), n,
-                        share, int(a.Dk));
+      const float* in = reinterpret_cast<const float*>(ws + (k ? w.dk : w.dq));
+      T* out = static_cast<T*>(k ? a.dk : a.dq);
+      const bool vec = a.Dk % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
+      err = vec ? launch_kind(kKindLinReduce, lin_group_sum_kernel<T, 4>, ceil_div(n, 1024), 256, a.stream, in, out, n, share, int(a.Dk))
+                : launch_kind(kKindLinReduce, lin_group_sum_kernel<T, 1>, ceil_div(n, 256), 256, a.stream, in, out, n, share, int(a.Dk));
       if (err != hipSuccess) return err;
     }
   }
   if (gate) {
     const int h_blocks = int(ceil_div(a.H, kGateHeads));
-    const float* dq = reinterpret_cast<const float*>(ws + w.dot_q);
-    const float* dk = reinterpret_cast<const float*>(ws + w.dot_k);
+    const float* dots_q = reinterpret_cast<const float*>(ws + w.dot_q);
+    const float* dots_k = reinterpret_cast<const float*>(ws + w.dot_k);
     double* sums = reinterpret_cast<double*>(ws + w.sums);
     const int64_t blocks = a.b * w.n_tiles * h_blocks;
-    err = launch_kind(kKindLinGate, lin_gate_tiles_kernel, blocks, 256, a.stream, dq, dk, sums, a.L, int(a.H),
+    err = launch_kind(kKindLinGate, lin_gate_tiles_kernel, blocks, 256, a.stream, dots_q, dots_k, sums, a.L, int(a.H),
                       w.n_tiles, h_blocks);
     if (err != hipSuccess) return err;
-    err = launch_kind(kKindLinGate, lin_gate_kernel<T>, blocks, 256, a.stream, dq, dk, sums, end, a.lengths,
+    err = launch_kind(kKindLinGate, lin_gate_kernel<T>, blocks, 256, a.stream, dots_q, dots_k, sums, end, a.lengths,
                       static_cast<T*>(a.dg), a.L, int(a.H), w.n_tiles, h_blocks);
   }
   return err;
