@@ -670,8 +670,8 @@ struct SweepLds {
   __attribute__((aligned(16))) T k[2][Tile<T, KDP, kKey>::kElems];
   __attribute__((aligned(16))) T v[2][Tile<T, VDP, kValue>::kElems];
   __attribute__((aligned(16))) T P[2][kTwo ? 2 : 1][kC * ldp];
-  Decays<kC> d[2];
-  float diag[2][DOTS ? kC : 1], dot_part[DOTS ? 4 : 1][kC], red[4];
+  Decays<kC> d[4];  // written two chunks ahead
+  float diag[2][DOTS ? kC : 1], dot_part[DOTS ? 16 : 1][kC], red[4];
 };
 
 template <typename T, int KDP, int VDP, bool DOTS, bool VEC>
@@ -723,8 +723,10 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
       sq.store(sh.q[b], r.q, tid);
       sk.store(sh.k[b], r.k, tid);
       sv.store(sh.v[b], r.v, tid);
+    };
+    auto decays = [&](const Regs& r, int i) {  // by the wave with the fewest blocks of P
       const float g = gates.log_of(r.gate, (w.c0 + i) * kC, live(i));
-      if (pw == 3) fill_decays(sh.d[b], g, p.wscale);
+      if (pw == 3) fill_decays(sh.d[i & 3], g, p.wscale);
     };
     // P of the i-th chunk: its blocks (t block, s block) with s <= t, mostly of one t block a wave, so that the rows of Q
     // are read once; the wave that takes the decays has the fewest.  All reads come first, all products next.
@@ -733,7 +735,7 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
       const int tbs[3] = {t0, t1, t2}, sbs[3] = {s0, s1, s2};
       const T* Qs = sh.q[i & 1];
       const T* Ks = sh.k[i & 1];
-      const Decays<kC>& d = sh.d[i & 1];
+      const Decays<kC>& d = sh.d[i & 3];
       const int pb = i & 1;
       Frag<T> qf[N][Y::KS], kf[N][Y::KS];
       float th[N], tl[N];
@@ -813,8 +815,10 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
       if constexpr (DOTS) {
         if (tid < rows) {
           const int64_t t = tid >= nv ? p0 + tid : p.reverse ? w.n - 1 - p0 - tid : p0 + tid;
-          p.dots[(w.bi * p.L + t) * p.H + w.h] =
-              tid < nv ? (sh.dot_part[0][tid] + sh.dot_part[1][tid]) + (sh.dot_part[2][tid] + sh.dot_part[3][tid]) : 0.f;
+          float s = 0.f;
+#pragma unroll
+          for (int k = 0; k < 16; k++) s += sh.dot_part[k][tid];
+          p.dots[(w.bi * p.L + t) * p.H + w.h] = tid < nv ? s : 0.f;
         }
       }
       for (int r = nv + pw; r < rows; r += 4) {
@@ -828,23 +832,26 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
     fetch(r0, 0);
     fetch(r1, 1);
     place(r0, 0);
+    decays(r0, 0);
     fetch(r0, 2);
+    decays(r1, 1);
     __syncthreads();
     score(0);
     __syncthreads();
-    // at the top of step i: chunk i is in the tiles and in P, chunks i + 1 (in r) and i + 2 in registers or under
-    // way.  Steps go by twos, each with its set of registers, so that a wait is for the older loads only.
-    auto step = [&](Regs& r, int i) {
+    // at the top of step i: chunk i is in the tiles and in P; chunks i + 1 (in r) and i + 2 (in the other set) are in
+    // registers or under way.  Steps go by twos, each with its set, so that a wait is for the older loads only.
+    auto step = [&](Regs& r, const Regs& other, int i) {
       place(r, i + 1);
       fetch(r, i + 3);
       finish(i - 1);
       __syncthreads();
       score(i + 1);
+      decays(other, i + 2);
       __syncthreads();
     };
     for (int i = 0; i < chunks; i += 2) {
-      step(r1, i);
-      step(r0, i + 1);
+      step(r1, r0, i);
+      step(r0, r1, i + 1);
     }
     if (chunks % 2 == 0) finish(chunks - 1);
     if (DOTS && p.dstate_dot && w.seg == p.n_segs - 1) __syncthreads();  // the state waves' sum
@@ -876,7 +883,7 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
   __syncthreads();
   for (int c = 0; c < chunks; c++) {
     const int nv = max(0, min(kC, w.n - (w.c0 + c) * kC));
-    const Decays<kC>& d = sh.d[c & 1];
+    const Decays<kC>& d = sh.d[c & 3];
     const T* Qs = sh.q[c & 1];
     const T* Ks = sh.k[c & 1];
     const T* Vs = sh.v[c & 1];
@@ -925,7 +932,7 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
     read_q(1);
     times_state(0);
     __builtin_amdgcn_sched_barrier(0);
-    __syncthreads();
+    if (!kTwo) __syncthreads();  // the half of the step: here, or with more products after them
     float in[TB];
 #pragma unroll
     for (int tt = 0; tt < TB; tt++) in[tt] = d.in[16 * tt + lr] * p.rscale;
@@ -955,6 +962,7 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
         for (int k = 0; k < (kTwo ? 2 : 1); k++)
 #pragma unroll
           for (int n = 0; n < Y::NT; n++) o[tt][n] = mma(vf[ks][n], pf[k][tt][ks], o[tt][n]);
+    if (kTwo) __syncthreads();
     // ---- outputs ----
 #pragma unroll
     for (int tt = 0; tt < TB; tt++) {
@@ -966,9 +974,7 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
         float s = 0.f;
 #pragma unroll
         for (int j = 0; j < kN; j++) s = fmaf(y[j], R::template element<T>(xd[tt], j), s);
-        s += __shfl_xor(s, 16);
-        s += __shfl_xor(s, 32);
-        if (l < 16) sh.dot_part[wv][i] = s;
+        sh.dot_part[4 * wv + l / 16][i] = s;
         const float dg = sh.diag[c & 1][i];
 #pragma unroll
         for (int j = 0; j < kN; j += 4) {
