@@ -671,7 +671,7 @@ struct SweepLds {
   __attribute__((aligned(16))) T v[2][Tile<T, VDP, kValue>::kElems];
   __attribute__((aligned(16))) T P[2][kTwo ? 2 : 1][kC * ldp];
   Decays<kC> d[4];  // written two chunks ahead
-  float diag[2][DOTS ? kC : 1], dot_part[DOTS ? 16 : 1][kC], red[4];
+  float diag[2][DOTS ? kC : 1], dot_part[2][DOTS ? 16 : 1][kC], red[4];
 };
 
 template <typename T, int KDP, int VDP, bool DOTS, bool VEC>
@@ -808,18 +808,16 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
         if (pw < 3) score_blocks(i, integral_constant<int, 1>{}, pw > 0, pw > 1, 0, 0, 0, 0);
       }
     };
-    // what follows the outputs of the i-th chunk: the dots' sums over the waves, and zero rows behind the length
+    // what follows the outputs of the i-th chunk: the dots' sums (by one wave), and zero rows behind the length
     auto finish = [&](int i) {
       if (i < 0 || i >= chunks) return;
       const int p0 = (w.c0 + i) * kC, nv = max(0, min(kC, w.n - p0)), rows = min(kC, int(p.L) - p0);
-      if constexpr (DOTS) {
-        if (tid < rows) {
-          const int64_t t = tid >= nv ? p0 + tid : p.reverse ? w.n - 1 - p0 - tid : p0 + tid;
-          float s = 0.f;
+      if (DOTS && pw == 3 && l < rows) {
+        const int64_t t = l >= nv ? p0 + l : p.reverse ? w.n - 1 - p0 - l : p0 + l;
+        float s = 0.f;
 #pragma unroll
-          for (int k = 0; k < 16; k++) s += sh.dot_part[k][tid];
-          p.dots[(w.bi * p.L + t) * p.H + w.h] = tid < nv ? s : 0.f;
-        }
+        for (int k = 0; k < 16; k++) s += sh.dot_part[i & 1][DOTS ? k : 0][l];
+        p.dots[(w.bi * p.L + t) * p.H + w.h] = l < nv ? s : 0.f;
       }
       for (int r = nv + pw; r < rows; r += 4) {
         const int64_t at = ((w.bi * p.L + p0 + r) * p.H + w.h) * p.VD;
@@ -843,10 +841,10 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
     auto step = [&](Regs& r, const Regs& other, int i) {
       place(r, i + 1);
       fetch(r, i + 3);
-      finish(i - 1);
       __syncthreads();
       score(i + 1);
       decays(other, i + 2);
+      finish(i - 1);
       __syncthreads();
     };
     for (int i = 0; i < chunks; i += 2) {
@@ -974,7 +972,7 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
         float s = 0.f;
 #pragma unroll
         for (int j = 0; j < kN; j++) s = fmaf(y[j], R::template element<T>(xd[tt], j), s);
-        sh.dot_part[4 * wv + l / 16][i] = s;
+        sh.dot_part[c & 1][4 * wv + l / 16][i] = s;
         const float dg = sh.diag[c & 1][i];
 #pragma unroll
         for (int j = 0; j < kN; j += 4) {
@@ -1288,10 +1286,10 @@ constexpr int64_t kAtOnce = 256;
 struct Cut {
   int n_chunks, n_segs, seg_chunks;
 };
-Cut cut_of(const LinAttnArgs& a) {
+Cut cut_of(const LinAttnArgs& a, bool backward) {
   Cut c;
   c.n_chunks = int(ceil_div(a.L, a.dtype == 0 ? kChunk<float> : kChunk<bf16_bits>));
-  const int64_t heads = a.b * a.H;
+  const int64_t heads = a.b * a.H * (backward ? 3 : 1);  // workgroups of an uncut call
   const int64_t want = std::max<int64_t>(1, kAtOnce / std::max<int64_t>(heads, 1));
   const int64_t most = std::max<int64_t>(1, c.n_chunks / kMinSeg);
   c.n_segs = int(std::min(want, most));
@@ -1300,13 +1298,13 @@ Cut cut_of(const LinAttnArgs& a) {
   return c;
 }
 
-Sweep common(const LinAttnArgs& a) {
+Sweep common(const LinAttnArgs& a, bool backward) {
   Sweep p{};
   p.g = a.g; p.A = a.A; p.lengths = a.lengths;
   p.wscale = p.rscale = 1.f;
   p.gq = p.gk = p.gv = p.gd = 1;
   p.b = a.b; p.L = a.L; p.H = int(a.H);
-  const Cut c = cut_of(a);
+  const Cut c = cut_of(a, backward);
   p.n_chunks = c.n_chunks; p.n_segs = c.n_segs; p.seg_chunks = c.seg_chunks;
   p.stream = a.stream;
   return p;
@@ -1326,7 +1324,7 @@ Work plan_work(const LinAttnArgs& a, bool backward) {
     at += up256(bytes);
     return r;
   };
-  const size_t heads = size_t(a.b) * a.H, segs = heads * (cut_of(a).n_segs - 1);
+  const size_t heads = size_t(a.b) * a.H, segs = heads * (cut_of(a, backward).n_segs - 1);
   w.seg_f = take(segs * a.Dk * a.Dv * 4);
   w.dec_f = take(segs * 4);
   if (backward) {
@@ -1351,7 +1349,7 @@ template <typename T>
 hipError_t fwd_impl(const LinAttnArgs& a, char* ws) {
   const Work w = plan_work(a, false);
   const int share = int(a.H / a.G);
-  Sweep p = common(a);
+  Sweep p = common(a, false);
   p.xq = a.q; p.xk = a.k; p.xv = a.v; p.gq = p.gk = share;
   p.KD = int(a.Dk); p.VD = int(a.Dv);
   p.rscale = a.scale;
@@ -1375,8 +1373,8 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
   float* seg_r = reinterpret_cast<float*>(ws + w.seg_r);
   float* dec_r = reinterpret_cast<float*>(ws + w.dec_r);
   hipError_t err = hipSuccess;
-  if (common(a).n_segs > 1) {  // the segments' S and D, [Dk, Dv]; dq and dk read them transposed
-    Sweep p = common(a);
+  if (common(a, true).n_segs > 1) {  // the segments' S and D, [Dk, Dv]; dq and dk read them transposed
+    Sweep p = common(a, true);
     p.xk = a.k; p.gk = share; p.xv = a.v;
     p.KD = int(a.Dk); p.VD = int(a.Dv);
     p.init = a.h0; p.seg_state = seg_f; p.seg_decay = dec_f;
@@ -1388,19 +1386,19 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
     err = run_states<T>(p);
     if (err != hipSuccess) return err;
   }
-  Sweep dq = common(a);  // forwards, the state is S^T [Dv, Dk]
+  Sweep dq = common(a, true);  // forwards, the state is S^T [Dv, Dk]
   dq.xq = a.dy; dq.xk = a.v; dq.xv = a.k; dq.gv = share;
   dq.KD = int(a.Dv); dq.VD = int(a.Dk);
   dq.rscale = a.scale;
   dq.init = a.h0; dq.init_t = true; dq.seg_state = seg_f;
   dq.out = share > 1 ? static_cast<void*>(ws + w.dq) : a.dq; dq.out_f32 = share > 1;
-  Sweep dk = common(a);  // backwards, the state is D^T [Dv, Dk]
+  Sweep dk = common(a, true);  // backwards, the state is D^T [Dv, Dk]
   dk.xq = a.v; dk.xk = a.dy; dk.xv = a.q; dk.gv = share;
   dk.KD = int(a.Dv); dk.VD = int(a.Dk);
   dk.wscale = a.scale; dk.reverse = true;
   dk.init = a.dlast; dk.init_t = true; dk.seg_state = seg_r;
   dk.out = share > 1 ? static_cast<void*>(ws + w.dk) : a.dk; dk.out_f32 = share > 1;
-  Sweep dv = common(a);  // backwards, the state is D [Dk, Dv]
+  Sweep dv = common(a, true);  // backwards, the state is D [Dk, Dv]
   dv.xq = a.k; dv.gq = share; dv.xk = a.q; dv.gk = share; dv.xv = a.dy;
   dv.KD = int(a.Dk); dv.VD = int(a.Dv);
   dv.wscale = a.scale; dv.reverse = true;
