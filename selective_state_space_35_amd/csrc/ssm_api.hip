@@ -428,7 +428,7 @@ int check_linattn(int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_
   if (!mul_ok(b, H, &t) || !mul_ok(t, max_dim * max_dim * 64, &t)) return SSM_ERR_DIM;
   // grids: a workgroup per head (and segment) of a batch row; 256 tokens x 16 heads in the gate's sums;
   // 256 elements of dq in the sums over a group
-  if (b * H > INT32_MAX / 2 || L > INT32_MAX - 4096 || !mul_ok(b * H, L / 256 + 1, &t) || t > INT32_MAX) return SSM_ERR_DIM;
+  if (b * H > INT32_MAX / 4 || L > INT32_MAX - 4096 || !mul_ok(b * H, L / 256 + 1, &t) || t > INT32_MAX) return SSM_ERR_DIM;
   if (!mul_ok(b * L, G * Dk, &t) || t / 256 > INT32_MAX - 1) return SSM_ERR_DIM;
   return SSM_OK;
 }

@@ -57,9 +57,10 @@ struct Sweep {
   bool reverse;            // from the last token to the first
   int64_t b, L;
   int H, KD, VD;
-  // the cut: n_segs segments of seg_chunks chunks; with more than one, the state leaving segment s is in
-  // seg_state[b][s][H] (in the place of `init`, stored as `init` is) and the log decays' sums in seg_decay
-  int n_chunks, n_segs, seg_chunks;
+  // the cut: n_segs segments of `parts` parts of part_chunks chunks.  With more than one segment, the states leaving the
+  // n_parts parts of all but the last are in seg_state[b][n_parts][H], stored as `init` is, and the sums of the parts' log
+  // decays in seg_decay
+  int n_chunks, n_segs, parts, part_chunks, n_parts;
   float* seg_state;
   float* seg_decay;
   hipStream_t stream;
@@ -213,18 +214,19 @@ struct Place {
   int h, seg, c0, c1, n;
   int64_t bi, bh;
 };
-__device__ __forceinline__ Place place_of(const Sweep& p, int n_segs, int id) {
+// workgroup `id` of n pieces of `chunks` chunks a head
+__device__ __forceinline__ Place place_of(const Sweep& p, int n, int chunks, int id) {
   Place w;
   // Workgroups are dealt to the 8 XCDs in turn: with H a multiple of 8, each XCD takes H / 8 neighbouring
   // heads, so that the heads of a group read their shared rows through one L2.
   w.h = p.H % 8 == 0 ? (id % 8) * (p.H / 8) + (id / 8) % (p.H / 8) : id % p.H;
   const int rest = id / p.H;
-  w.seg = rest % n_segs;
-  w.bi = rest / n_segs;
+  w.seg = rest % n;
+  w.bi = rest / n;
   w.bh = w.bi * p.H + w.h;
   w.n = live_length(p.lengths, w.bi, p.L);
-  w.c0 = w.seg * p.seg_chunks;
-  w.c1 = min(w.c0 + p.seg_chunks, p.n_chunks);
+  w.c0 = w.seg * chunks;
+  w.c1 = min(w.c0 + chunks, p.n_chunks);
   return w;
 }
 
@@ -596,16 +598,19 @@ __device__ __forceinline__ const T* start_of(const void* x, const Sweep& p, cons
 }
 
 // ---------------------------------------------------------------------------
-// States of the segments of a cut sequence, each from zero, and the sums of their log decays.
+// States of the parts of a cut sequence, each from zero, and the sums of their log decays; the workgroups from n on
+// take the second sweep's.  The parts are shorter than the segments, so that a few heads fill the chip here too.
 // ---------------------------------------------------------------------------
 template <typename T, int KDP, int VDP, bool VEC>
-__global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) void lin_state_kernel(Sweep p) {
+__global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) void lin_state_kernel(Sweep p0, Sweep p1, int n) {
+  const bool second = int(blockIdx.x) >= n;
+  const Sweep& p = second ? p1 : p0;
   typedef Layout<KDP, VDP> Y;
   constexpr int kC = kChunk<T>;
   __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP, kKey>::kElems];
   __shared__ __attribute__((aligned(16))) T Vs[Tile<T, VDP, kValue>::kElems];
   __shared__ Decays<kC> ds[2];
-  const Place w = place_of(p, p.n_segs - 1, blockIdx.x);
+  const Place w = place_of(p, p.n_parts, p.part_chunks, int(blockIdx.x) - (second ? n : 0));
   const int tid = threadIdx.x, g8 = 8 * ((tid % kWave) / 16);
   Stage<T, KDP, kKey, VEC> sk;
   Stage<T, VDP, kValue, VEC> sv;
@@ -642,7 +647,7 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) v
       total += fill_decays(ds[(c + 1 - w.c0) & 1], gates.log_of(gate, (c + 1) * kC, w.n - (c + 1) * kC), p.wscale);
     __syncthreads();
   }
-  const int64_t at = (w.bi * (p.n_segs - 1) + w.seg) * p.H + w.h;
+  const int64_t at = (w.bi * p.n_parts + w.seg) * p.H + w.h;
   Y::store(S, p.seg_state + at * p.KD * p.VD, p.KD, p.VD, 1.f);
   if (tid == 0) p.seg_decay[at] = float(total);
 }
@@ -681,7 +686,7 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
   constexpr int kC = Lds::kC, ldp = Lds::ldp, kN = 4 * Y::NT, TB = kC / 16, kSteps = kC / 32;
   constexpr bool kTwo = Lds::kTwo;
   constexpr int ldq = Tile<T, KDP, kQuery>::ld, ldk = Tile<T, KDP, kKey>::ld, ldv = Tile<T, VDP, kValue>::ld;
-  const Place w = place_of(p, p.n_segs, id);
+  const Place w = place_of(p, p.n_segs, p.parts * p.part_chunks, id);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = threadIdx.x % kWave;
   const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
   const int chunks = w.c1 - w.c0;
@@ -872,7 +877,7 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
     }
   };
   typename Y::State S;
-  const float* from = w.seg > 0 ? p.seg_state + ((w.bi * (p.n_segs - 1) + w.seg - 1) * p.H + w.h) * p.KD * p.VD
+  const float* from = w.seg > 0 ? p.seg_state + ((w.bi * p.n_parts + w.seg * p.parts - 1) * p.H + w.h) * p.KD * p.VD
                                 : p.init ? p.init + w.bh * p.KD * p.VD : nullptr;
   if (from) Y::load(S, from, p.init_t, p.KD, p.VD);
   else Y::zero(S);
@@ -1257,25 +1262,30 @@ hipError_t bwd_sizes(const Sweep& dq, const Sweep& dk, const Sweep& dv) {
 }
 
 template <typename T, int KDP, int VDP>
-hipError_t state_kernel(const Sweep& p, bool vec) {
-  const int64_t blocks = p.b * p.H * (p.n_segs - 1);
-  return vec ? launch_kind(kKindLinState, lin_state_kernel<T, KDP, VDP, true>, blocks, kThreads, p.stream, p)
-             : launch_kind(kKindLinState, lin_state_kernel<T, KDP, VDP, false>, blocks, kThreads, p.stream, p);
+hipError_t state_kernel(const Sweep& p, const Sweep& q, int sweeps, bool vec) {
+  const int64_t n = p.b * p.H * p.n_parts;
+  return vec ? launch_kind(kKindLinState, lin_state_kernel<T, KDP, VDP, true>, sweeps * n, kThreads, p.stream, p, q, int(n))
+             : launch_kind(kKindLinState, lin_state_kernel<T, KDP, VDP, false>, sweeps * n, kThreads, p.stream, p, q, int(n));
 }
-// States leaving the segments of a cut sequence: every segment's own, then the chain over them.
+// States leaving the parts of a cut sequence, for one sweep or two of the same sizes: every part's own, then the chain
+// over them.
 template <typename T>
-hipError_t run_states(const Sweep& p) {
+hipError_t run_states(const Sweep& p, const Sweep& q, int sweeps) {
   if (p.n_segs <= 1) return hipSuccess;
-  const bool vec = pieces<T>(p.xk, p.KD) && pieces<T>(p.xv, p.VD);
-  hipError_t err = p.KD <= 64 ? (p.VD <= 64 ? state_kernel<T, 64, 64>(p, vec) : state_kernel<T, 64, 128>(p, vec))
-                              : (p.VD <= 64 ? state_kernel<T, 128, 64>(p, vec) : state_kernel<T, 128, 128>(p, vec));
-  if (err != hipSuccess) return err;
-  ChainArgs c{};
-  c.agg = p.seg_state; c.sums = p.seg_decay;
-  c.init = p.init;
-  c.outer = p.b; c.mid = p.H; c.inner = p.KD * p.VD; c.N = c.inner;
-  c.n_chunks = c.K = p.n_segs - 1;
-  return launch_chain<false, false, false>(kKindLinChain, c, p.stream);
+  const bool vec = pieces<T>(p.xk, p.KD) && pieces<T>(p.xv, p.VD) && pieces<T>(q.xk, q.KD) && pieces<T>(q.xv, q.VD);
+  hipError_t err = p.KD <= 64 ? (p.VD <= 64 ? state_kernel<T, 64, 64>(p, q, sweeps, vec) : state_kernel<T, 64, 128>(p, q, sweeps, vec))
+                              : (p.VD <= 64 ? state_kernel<T, 128, 64>(p, q, sweeps, vec) : state_kernel<T, 128, 128>(p, q, sweeps, vec));
+  for (int k = 0; k < sweeps && err == hipSuccess; k++) {
+    const Sweep& s = k ? q : p;
+    if (s.n_parts == 1 && !s.init) continue;  // the one part's own state is the one that leaves it
+    ChainArgs c{};
+    c.agg = s.seg_state; c.sums = s.seg_decay;
+    c.init = s.init;
+    c.outer = s.b; c.mid = s.H; c.inner = s.KD * s.VD; c.N = c.inner;
+    c.n_chunks = c.K = s.n_parts;
+    err = launch_chain<false, false, false>(kKindLinChain, c, s.stream);
+  }
+  return err;
 }
 
 // The cut of a sequence: as many segments as give every CU a workgroup, and no second generation of them
@@ -1284,17 +1294,24 @@ hipError_t run_states(const Sweep& p) {
 constexpr int kMinSeg = 4;
 constexpr int64_t kAtOnce = 256;
 struct Cut {
-  int n_chunks, n_segs, seg_chunks;
+  int n_chunks, n_segs, parts, part_chunks, n_parts;
 };
 Cut cut_of(const LinAttnArgs& a, bool backward) {
   Cut c;
   c.n_chunks = int(ceil_div(a.L, a.dtype == 0 ? kChunk<float> : kChunk<bf16_bits>));
-  const int64_t heads = a.b * a.H * (backward ? 3 : 1);  // workgroups of an uncut call
-  const int64_t want = std::max<int64_t>(1, kAtOnce / std::max<int64_t>(heads, 1));
-  const int64_t most = std::max<int64_t>(1, c.n_chunks / kMinSeg);
-  c.n_segs = int(std::min(want, most));
-  c.seg_chunks = int(std::max<int64_t>(1, ceil_div(c.n_chunks, c.n_segs)));
-  c.n_segs = int(std::max<int64_t>(1, ceil_div(c.n_chunks, c.seg_chunks)));
+  const int64_t heads = a.b * a.H, sweeps = backward ? 3 : 1;
+  const int64_t want = std::max<int64_t>(1, kAtOnce / std::max<int64_t>(heads * sweeps, 1));
+  const int64_t segs = std::min(want, std::max<int64_t>(1, c.n_chunks / kMinSeg));
+  int64_t seg = std::max<int64_t>(1, ceil_div(c.n_chunks, segs));
+  c.parts = 1;
+  if (segs > 1) {  // parts for two generations of the smaller workgroups of the states' pass
+    const int64_t more = 2 * kAtOnce / std::max<int64_t>(heads * (segs - 1) * (backward ? 2 : 1), 1);
+    c.parts = int(std::max<int64_t>(1, std::min(more, seg / kMinSeg)));
+  }
+  c.part_chunks = int(ceil_div(seg, c.parts));
+  seg = int64_t(c.part_chunks) * c.parts;
+  c.n_segs = int(std::max<int64_t>(1, ceil_div(c.n_chunks, seg)));
+  c.n_parts = (c.n_segs - 1) * c.parts;
   return c;
 }
 
@@ -1305,7 +1322,7 @@ Sweep common(const LinAttnArgs& a, bool backward) {
   p.gq = p.gk = p.gv = p.gd = 1;
   p.b = a.b; p.L = a.L; p.H = int(a.H);
   const Cut c = cut_of(a, backward);
-  p.n_chunks = c.n_chunks; p.n_segs = c.n_segs; p.seg_chunks = c.seg_chunks;
+  p.n_chunks = c.n_chunks; p.n_segs = c.n_segs; p.parts = c.parts; p.part_chunks = c.part_chunks; p.n_parts = c.n_parts;
   p.stream = a.stream;
   return p;
 }
@@ -1324,7 +1341,7 @@ Work plan_work(const LinAttnArgs& a, bool backward) {
     at += up256(bytes);
     return r;
   };
-  const size_t heads = size_t(a.b) * a.H, segs = heads * (cut_of(a, backward).n_segs - 1);
+  const size_t heads = size_t(a.b) * a.H, segs = heads * cut_of(a, backward).n_parts;
   w.seg_f = take(segs * a.Dk * a.Dv * 4);
   w.dec_f = take(segs * 4);
   if (backward) {
@@ -1355,7 +1372,7 @@ hipError_t fwd_impl(const LinAttnArgs& a, char* ws) {
   p.rscale = a.scale;
   p.init = a.h0;
   p.seg_state = reinterpret_cast<float*>(ws + w.seg_f); p.seg_decay = reinterpret_cast<float*>(ws + w.dec_f);
-  const hipError_t err = run_states<T>(p);
+  const hipError_t err = run_states<T>(p, p, 1);
   if (err != hipSuccess) return err;
   p.out = a.y;
   p.last = a.last;
@@ -1374,16 +1391,14 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
   float* dec_r = reinterpret_cast<float*>(ws + w.dec_r);
   hipError_t err = hipSuccess;
   if (common(a, true).n_segs > 1) {  // the segments' S and D, [Dk, Dv]; dq and dk read them transposed
-    Sweep p = common(a, true);
-    p.xk = a.k; p.gk = share; p.xv = a.v;
-    p.KD = int(a.Dk); p.VD = int(a.Dv);
-    p.init = a.h0; p.seg_state = seg_f; p.seg_decay = dec_f;
-    err = run_states<T>(p);
-    if (err != hipSuccess) return err;
-    p.xk = a.q; p.xv = a.dy;
-    p.wscale = a.scale; p.reverse = true;
-    p.init = a.dlast; p.seg_state = seg_r; p.seg_decay = dec_r;
-    err = run_states<T>(p);
+    Sweep f = common(a, true), r = common(a, true);
+    f.xk = a.k; f.gk = share; f.xv = a.v;
+    f.init = a.h0; f.seg_state = seg_f; f.seg_decay = dec_f;
+    r.xk = a.q; r.gk = share; r.xv = a.dy;
+    r.wscale = a.scale; r.reverse = true;
+    r.init = a.dlast; r.seg_state = seg_r; r.seg_decay = dec_r;
+    f.KD = r.KD = int(a.Dk); f.VD = r.VD = int(a.Dv);
+    err = run_states<T>(f, r, 2);
     if (err != hipSuccess) return err;
   }
   Sweep dq = common(a, true);  // forwards, the state is S^T [Dv, Dk]
