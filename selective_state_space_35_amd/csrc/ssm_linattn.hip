@@ -501,27 +501,43 @@ struct Layout {
 #pragma unroll
       for (int n = 0; n < NT; n++) S[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
+  // a state in memory, [KD][VD] or transposed, through a descriptor: what lies outside is read as zero and not written
   static __device__ __forceinline__ void load(State& S, const float* src, bool transposed, int KD, int VD) {
+    const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(src);
+    const int dk = transposed ? 4 : 4 * VD;  // bytes from row to row
 #pragma unroll
-    for (int m = 0; m < MT; m++)
+    for (int n = 0; n < NT; n++) {
+      const int v = col(n);
+      int at = row(0) * dk + (transposed ? 4 * v * KD : 4 * v);
 #pragma unroll
-      for (int n = 0; n < NT; n++)
+      for (int m = 0; m < MT; m++) {
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-          const int k = row(m) + r, v = col(n);
-          S[m][n][r] = k < KD && v < VD ? src[transposed ? v * KD + k : k * VD + v] : 0.f;
+          S[m][n][r] = __uint_as_float(
+              __builtin_amdgcn_raw_buffer_load_b32(rs, row(m) + r < KD && v < VD ? at : 0x7fffffff, 0, 0));
+          at += dk;
         }
+        at += 12 * dk;
+      }
+    }
   }
   static __device__ __forceinline__ void store(const State& S, float* dst, int KD, int VD, float f) {
+    const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(dst);
 #pragma unroll
-    for (int m = 0; m < MT; m++)
+    for (int n = 0; n < NT; n++) {
+      const int v = col(n);
+      int at = 4 * (row(0) * VD + v);
 #pragma unroll
-      for (int n = 0; n < NT; n++)
+      for (int m = 0; m < MT; m++) {
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-          const int k = row(m) + r, v = col(n);
-          if (k < KD && v < VD) dst[k * VD + v] = S[m][n][r] * f;
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[m][n][r] * f), rs,
+                                                row(m) + r < KD && v < VD ? at : 0x7fffffff, 0, 0);
+          at += 4 * VD;
         }
+        at += 48 * VD;
+      }
+    }
   }
 };
 
@@ -1000,17 +1016,15 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
   }
   if (w.seg != p.n_segs - 1) return;
   if (DOTS && p.dstate_dot) {
-    const float* src = p.dstate + w.bh * p.KD * p.VD;  // [VD][KD]
+    typename Y::State D;
+    Y::load(D, p.dstate + w.bh * p.KD * p.VD, true, p.KD, p.VD);
     float s = 0.f;
 #pragma unroll
     for (int m = 0; m < Y::MT; m++)
 #pragma unroll
       for (int n = 0; n < Y::NT; n++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
-          const int k = Y::row(m) + r, v = Y::col(n);
-          if (k < p.KD && v < p.VD) s = fmaf(S[m][n][r], src[v * p.KD + k], s);
-        }
+        for (int r = 0; r < 4; r++) s = fmaf(S[m][n][r], D[m][n][r], s);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
     if (l == 0) sh.red[wv] = s;
