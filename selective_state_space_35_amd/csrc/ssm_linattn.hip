@@ -51,9 +51,10 @@ struct Sweep {
   // with dots: dots[b, L, H] = (output without the token's own product) . xd
   const void* xd;
   int gd;
-  float* dots;
+  void* dots;              // Dot<T>
   const float* dstate;     // [b, H, VD, KD] (transposed); dstate_dot[b, H] = its product with the last state
   float* dstate_dot;
+  bool exact;              // the state is an output: its products keep all bits of a float
   bool reverse;            // from the last token to the first
   int64_t b, L;
   int H, KD, VD;
@@ -65,6 +66,10 @@ struct Sweep {
   float* seg_decay;
   hipStream_t stream;
 };
+
+// The dots of one token, float or (float tensors, whose gate gradient has to be right to their last bits) double
+template <typename T>
+using Dot = typename std::conditional<sizeof(T) == 4, double, float>::type;
 
 // A log decay below -10^4 counts as -10^4 (its factor is zero in float either way), so that
 // minus infinity is a reset and differences of running sums stay numbers.
@@ -541,16 +546,17 @@ struct Layout {
   }
 };
 
-// S = all S + K^T (out o V) over a chunk.  The weighted values are split into two bf16 parts (2^-17 of
-// a product is lost; one part would lose 2^-9 and the state is a float result).
+// S = all S + K^T (out o V) over a chunk.  The weighted values are split into two bf16 parts (half a step of 2^-8
+// twice: 2^-16 of a product at most, 2 10^-6 of the state measured), and where the state itself is an output
+// (exact) into three, which hold all 24 bits of a float.
 template <typename T, int KDP, int VDP>
 __device__ __forceinline__ void write_state(typename Layout<KDP, VDP>::State& S, const T* Ks,
                                             const Frag<T> (&vf)[kChunk<T> / 32][VDP / 64],
-                                            const Decays<kChunk<T>>& d) {
+                                            const Decays<kChunk<T>>& d, bool exact) {
   typedef Layout<KDP, VDP> Y;
   constexpr int kSteps = kChunk<T> / 32;
   const int g8 = 8 * int((threadIdx.x % kWave) / 16);
-  Frag<T> hi[kSteps][Y::NT], lo[kSteps][Y::NT];
+  Frag<T> hi[kSteps][Y::NT], lo[kSteps][Y::NT], rest[kSteps][Y::NT];
 #pragma unroll
   for (int ks = 0; ks < kSteps; ks++) {
     const float4 w0 = lds4(d.out + 32 * ks + g8), w1 = lds4(d.out + 32 * ks + g8 + 4);
@@ -562,7 +568,14 @@ __device__ __forceinline__ void write_state(typename Layout<KDP, VDP>::State& S,
 #pragma unroll
       for (int j = 0; j < 8; j++) x[j] *= w[j];
       make_frag(x, hi[ks][n]);
-      if constexpr (sizeof(T) == 2) lo[ks][n] = rest_frag(x, hi[ks][n]);
+      if constexpr (sizeof(T) == 2) {
+        lo[ks][n] = rest_frag(x, hi[ks][n]);
+        if (exact) {
+#pragma unroll
+          for (int j = 0; j < 8; j++) x[j] -= static_cast<float>(hi[ks][n][j]);
+          rest[ks][n] = rest_frag(x, lo[ks][n]);
+        }
+      }
     }
   }
   const float all = d.all;
@@ -590,6 +603,17 @@ __device__ __forceinline__ void write_state(typename Layout<KDP, VDP>::State& S,
           S[m][n] = mma(kf[half][i][ks], hi[ks][n], S[m][n]);
           if constexpr (sizeof(T) == 2) S[m][n] = mma(kf[half][i][ks], lo[ks][n], S[m][n]);
         }
+    }
+    if constexpr (sizeof(T) == 2) {
+      if (exact) {
+#pragma unroll
+        for (int i = 0; i < kHalf; i++)
+#pragma unroll
+          for (int ks = 0; ks < kSteps; ks++)
+#pragma unroll
+            for (int n = 0; n < Y::NT; n++)
+              S[half * kHalf + i][n] = mma(kf[half][i][ks], rest[ks][n], S[half * kHalf + i][n]);
+      }
     }
   };
   read(0);
@@ -658,7 +682,7 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) v
     for (int ks = 0; ks < kC / 32; ks++)
 #pragma unroll
       for (int n = 0; n < Y::NT; n++) vf[ks][n] = col_frag(Vs, Tile<T, VDP, kValue>::ld, 32 * ks + g8, Y::v0(n), Y::vstep);
-    write_state<T, KDP, VDP>(S, Ks, vf, d);
+    write_state<T, KDP, VDP>(S, Ks, vf, d, p.exact);
     if (c + 1 < w.c1 && tid < kWave)
       total += fill_decays(ds[(c + 1 - w.c0) & 1], gates.log_of(gate, (c + 1) * kC, w.n - (c + 1) * kC), p.wscale);
     __syncthreads();
@@ -692,7 +716,8 @@ struct SweepLds {
   __attribute__((aligned(16))) T v[2][Tile<T, VDP, kValue>::kElems];
   __attribute__((aligned(16))) T P[2][kTwo ? 2 : 1][kC * ldp];
   Decays<kC> d[4];  // written two chunks ahead
-  float diag[2][DOTS ? kC : 1], dot_part[2][DOTS ? 16 : 1][kC], red[4];
+  Dot<T> dot_part[2][DOTS ? 16 : 1][kC];
+  float diag[2][DOTS ? kC : 1], red[4];
 };
 
 template <typename T, int KDP, int VDP, bool DOTS, bool VEC>
@@ -835,10 +860,10 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
       const int p0 = (w.c0 + i) * kC, nv = max(0, min(kC, w.n - p0)), rows = min(kC, int(p.L) - p0);
       if (DOTS && pw == 3 && l < rows) {
         const int64_t t = l >= nv ? p0 + l : p.reverse ? w.n - 1 - p0 - l : p0 + l;
-        float s = 0.f;
+        Dot<T> s = 0;
 #pragma unroll
         for (int k = 0; k < 16; k++) s += sh.dot_part[i & 1][DOTS ? k : 0][l];
-        p.dots[(w.bi * p.L + t) * p.H + w.h] = l < nv ? s : 0.f;
+        static_cast<Dot<T>*>(p.dots)[(w.bi * p.L + t) * p.H + w.h] = l < nv ? s : Dot<T>(0);
       }
       for (int r = nv + pw; r < rows; r += 4) {
         const int64_t at = ((w.bi * p.L + p0 + r) * p.H + w.h) * p.VD;
@@ -990,9 +1015,9 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
 #pragma unroll
       for (int j = 0; j < kN; j++) y[j] = o[tt][j / 4][j % 4];
       if constexpr (DOTS) {
-        float s = 0.f;
+        Dot<T> s = 0;
 #pragma unroll
-        for (int j = 0; j < kN; j++) s = fmaf(y[j], R::template element<T>(xd[tt], j), s);
+        for (int j = 0; j < kN; j++) s = fma(Dot<T>(y[j]), Dot<T>(R::template element<T>(xd[tt], j)), s);
         sh.dot_part[c & 1][4 * wv + l / 16][i] = s;
         const float dg = sh.diag[c & 1][i];
 #pragma unroll
@@ -1007,7 +1032,7 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
     }
     yr.next();
     fetch_xd(c + 1);
-    write_state<T, KDP, VDP>(S, Ks, vf, d);
+    write_state<T, KDP, VDP>(S, Ks, vf, d, !DOTS && p.exact);
     __syncthreads();
   }
   if (chunks % 2) {  // the staging waves' steps go by twos
@@ -1075,7 +1100,8 @@ __global__ __launch_bounds__(2 * kThreads) SSM_LIN_WAVES(kSweepWaves) void lin_b
 constexpr int kGateTile = 256;
 constexpr int kGateHeads = 16;  // heads of a workgroup: 16 consecutive floats of a row, times 16 tokens
 
-__global__ __launch_bounds__(256) void lin_gate_tiles_kernel(const float* __restrict__ a, const float* __restrict__ c,
+template <typename D>
+__global__ __launch_bounds__(256) void lin_gate_tiles_kernel(const D* __restrict__ a, const D* __restrict__ c,
                                                              double* __restrict__ sums, int64_t L, int H, int n_tiles,
                                                              int h_blocks) {
   __shared__ double sh[16][kGateHeads];
@@ -1102,7 +1128,7 @@ __global__ __launch_bounds__(256) void lin_gate_tiles_kernel(const float* __rest
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void lin_gate_kernel(const float* __restrict__ a, const float* __restrict__ c,
+__global__ __launch_bounds__(256) void lin_gate_kernel(const Dot<T>* __restrict__ a, const Dot<T>* __restrict__ c,
                                                        const double* __restrict__ sums, const float* __restrict__ end,
                                                        const int32_t* __restrict__ lengths, T* __restrict__ dg,
                                                        int64_t L, int H, int n_tiles, int h_blocks) {
@@ -1363,8 +1389,8 @@ Work plan_work(const LinAttnArgs& a, bool backward) {
     w.n_tiles = int(ceil_div(a.L, kGateTile));
     w.seg_r = take(segs * a.Dk * a.Dv * 4);
     w.dec_r = take(segs * 4);
-    w.dot_q = take(rows * 4);
-    w.dot_k = take(rows * 4);
+    w.dot_q = take(rows * (a.dtype == 0 ? sizeof(Dot<float>) : sizeof(Dot<bf16_bits>)));
+    w.dot_k = take(rows * (a.dtype == 0 ? sizeof(Dot<float>) : sizeof(Dot<bf16_bits>)));
     w.end = take(heads * 4);
     w.sums = take(heads * w.n_tiles * 8);
     if (a.G != a.H) {
@@ -1386,6 +1412,7 @@ hipError_t fwd_impl(const LinAttnArgs& a, char* ws) {
   p.rscale = a.scale;
   p.init = a.h0;
   p.seg_state = reinterpret_cast<float*>(ws + w.seg_f); p.seg_decay = reinterpret_cast<float*>(ws + w.dec_f);
+  p.exact = a.last != nullptr;
   const hipError_t err = run_states<T>(p, p, 1);
   if (err != hipSuccess) return err;
   p.out = a.y;
@@ -1411,6 +1438,7 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
     r.xk = a.q; r.gk = share; r.xv = a.dy;
     r.wscale = a.scale; r.reverse = true;
     r.init = a.dlast; r.seg_state = seg_r; r.seg_decay = dec_r;
+    r.exact = a.dh0 != nullptr;
     f.KD = r.KD = int(a.Dk); f.VD = r.VD = int(a.Dv);
     err = run_states<T>(f, r, 2);
     if (err != hipSuccess) return err;
@@ -1434,11 +1462,12 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
   dv.init = a.dlast; dv.seg_state = seg_r;
   dv.out = a.dv;
   dv.last = a.dh0; dv.final_decay = true;
+  dv.exact = a.dh0 != nullptr;
   if (gate) {
     dq.xd = a.q; dk.xd = a.k;
     dq.gd = dk.gd = share;
-    dq.dots = reinterpret_cast<float*>(ws + w.dot_q);
-    dk.dots = reinterpret_cast<float*>(ws + w.dot_k);
+    dq.dots = ws + w.dot_q;
+    dk.dots = ws + w.dot_k;
     dq.dstate = a.dlast;
     dq.dstate_dot = end;
   }
@@ -1457,11 +1486,11 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
   }
   if (gate) {
     const int h_blocks = int(ceil_div(a.H, kGateHeads));
-    const float* dots_q = reinterpret_cast<const float*>(ws + w.dot_q);
-    const float* dots_k = reinterpret_cast<const float*>(ws + w.dot_k);
+    const Dot<T>* dots_q = reinterpret_cast<const Dot<T>*>(ws + w.dot_q);
+    const Dot<T>* dots_k = reinterpret_cast<const Dot<T>*>(ws + w.dot_k);
     double* sums = reinterpret_cast<double*>(ws + w.sums);
     const int64_t blocks = a.b * w.n_tiles * h_blocks;
-    err = launch_kind(kKindLinGate, lin_gate_tiles_kernel, blocks, 256, a.stream, dots_q, dots_k, sums, a.L, int(a.H),
+    err = launch_kind(kKindLinGate, lin_gate_tiles_kernel<Dot<T>>, blocks, 256, a.stream, dots_q, dots_k, sums, a.L, int(a.H),
                       w.n_tiles, h_blocks);
     if (err != hipSuccess) return err;
     err = launch_kind(kKindLinGate, lin_gate_kernel<T>, blocks, 256, a.stream, dots_q, dots_k, sums, end, a.lengths,
