@@ -242,6 +242,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* p) {
   return make_rsrc(reinterpret_cast<const void*>((uint64_t(hi) << 32) | lo));
 }
 
+// Any bytes at any address: the compiler reads and writes them at once (unaligned access is on for global memory)
+__device__ __forceinline__ uint4 load_16(const char* p) {
+  uint4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+// v moved down by n bytes, 0 < n < 16, zeros above
+__device__ __forceinline__ uint4 down_bytes(const uint4& v, int n) {
+  const uint64_t lo = uint64_t(v.x) | (uint64_t(v.y) << 32), hi = uint64_t(v.z) | (uint64_t(v.w) << 32);
+  const int b = 8 * n;
+  const uint64_t a = b >= 64 ? hi >> (b - 64) : (lo >> b) | (hi << (64 - b)), c = b >= 64 ? 0 : hi >> b;
+  return make_uint4(uint32_t(a), uint32_t(a >> 32), uint32_t(c), uint32_t(c >> 32));
+}
+
 // A chunk's rows of one tensor, on their way from memory to LDS: rows of D <= DP elements, `stride`
 // elements apart, the rest zero.  VEC: rows are whole 16-byte pieces, 16-byte aligned.  A thread's
 // pieces are kStep rows apart, so one lane offset serves them all, the steps and the chunks being
@@ -253,6 +267,7 @@ struct Stage {
   static constexpr int kStep = kThreads / L::kRow;  // rows between a thread's pieces
   const T* base;     // row of the chunk's first position, or (reversed) of its last
   int voff, soff, sstep, chunk, live_cols;
+  bool wide;
   // first: row of position p0 of the sweep (reversed: of position p0 + kC - 1, maybe before the tensor); tid: of 256
   __device__ __forceinline__ void init(const T* first, int stride, int D, bool reverse, int tid) {
     const int i = tid / L::kRow, c = (tid % L::kRow) * L::kVec;
@@ -268,12 +283,12 @@ struct Stage {
       voff = (i * stride + c) * int(sizeof(T));
     }
     live_cols = D - c;
-    if (live_cols <= 0) voff = 0x7fffffff;
+    wide = D >= L::kVec;
+    if (VEC && live_cols <= 0) voff = 0x7fffffff;
   }
   // the next chunk, of nv live positions
   __device__ __forceinline__ void load(uint4 (&r)[L::kPieces], int nv, int tid) {
     const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(base);
-    base += chunk;
     const int i = tid / L::kRow;
 #pragma unroll
     for (int j = 0; j < L::kPieces; j++) {
@@ -281,6 +296,15 @@ struct Stage {
       if constexpr (VEC) {
         const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, o, soff + j * sstep, 0);
         r[j] = make_uint4(v[0], v[1], v[2], v[3]);
+      } else if (sizeof(T) == 2 && wide) {  // 16 bytes from any address; a row's last piece is moved to its place from a
+                                            // read that ends with the row (b4 L2048 H24 D100: 322 us by elements, 205 so)
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i + j * kStep < nv && live_cols > 0) {
+          const int over = live_cols < L::kVec ? (L::kVec - live_cols) * int(sizeof(T)) : 0;
+          v = load_16(reinterpret_cast<const char*>(base) + (int64_t(voff) + soff + j * sstep - over));
+          if (over) v = down_bytes(v, over);
+        }
+        r[j] = v;
       } else {
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -292,6 +316,7 @@ struct Stage {
         r[j] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
+    base += chunk;
   }
   static __device__ __forceinline__ void store(T* tile, const uint4 (&r)[L::kPieces], int tid) {
     T* to = tile + (tid / L::kRow) * L::ld + (tid % L::kRow) * L::kVec;
@@ -357,6 +382,10 @@ struct Rows {
     } else {
 #pragma unroll
       for (int k = 0; k < N * kBytes / 4; k++) x.w[k] = 0;
+      if (kBytes == 2 && row && cols >= N) {
+        __builtin_memcpy(x.w, base + (int64_t(voff) + so), N * kBytes);
+        return x;
+      }
 #pragma unroll
       for (int e = 0; e < N; e++) {
         const int at = row && e < cols ? voff + e * kBytes : 0x7fffffff;
@@ -377,15 +406,15 @@ struct Rows {
     const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(base);
     const bool row = 16 * tt + int(threadIdx.x % 16) < nv;
     const int so = soff + tt * sstep;
+    uint32_t w[N * kBytes / 4];
+    if constexpr (kBytes == 4) {
+#pragma unroll
+      for (int j = 0; j < N; j++) w[j] = __float_as_uint(y[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N / 2; j++) w[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+    }
     if constexpr (VEC) {
-      uint32_t w[N * kBytes / 4];
-      if constexpr (kBytes == 4) {
-#pragma unroll
-        for (int j = 0; j < N; j++) w[j] = __float_as_uint(y[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < N / 2; j++) w[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
-      }
       if constexpr (N * kBytes == 8) {
         typedef uint32_t u2 __attribute__((ext_vector_type(2)));
         __builtin_amdgcn_raw_buffer_store_b64(u2{w[0], w[1]}, rs, row && cols > 0 ? voff : 0x7fffffff, so, 0);
@@ -396,12 +425,14 @@ struct Rows {
           __builtin_amdgcn_raw_buffer_store_b128(u4{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]}, rs,
                                                  row && cols > k * 16 / kBytes ? voff + 16 * k : 0x7fffffff, so, 0);
       }
+    } else if (kBytes == 2 && row && cols >= N) {
+      __builtin_memcpy(const_cast<char*>(base) + (int64_t(voff) + so), w, N * kBytes);
     } else {
 #pragma unroll
       for (int e = 0; e < N; e++) {
         const int at = row && e < cols ? voff + e * kBytes : 0x7fffffff;
-        if constexpr (kBytes == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[e]), rs, at, so, 0);
-        else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(bf16_bits, static_cast<__bf16>(y[e])), rs, at, so, 0);
+        if constexpr (kBytes == 4) __builtin_amdgcn_raw_buffer_store_b32(w[e], rs, at, so, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(w[e / 2] >> (16 * (e % 2))), rs, at, so, 0);
       }
     }
   }
