@@ -707,7 +707,9 @@ LIB_KERNELS = ("scan_main_kernel", "scan_chunk_agg_kernel", "chain_kernel", "sca
                "fill_state_kernel", "state_update_kernel", "bwd_main_kernel", "bwd_chunk_maps_kernel",
                "bwd_chunk_agg_kernel", "bwd_rows_kernel", "bwd_reduce_bc_kernel", "bwd_reduce_chan_kernel",
                "bwd_fill_kernel", "ssd_state_kernel", "ssd_scan_kernel", "ssd_fill_kernel", "conv_fwd_kernel",
-               "conv_fwd_vec_kernel", "conv_update_kernel", "conv_state_copy_kernel")
+               "conv_fwd_vec_kernel", "conv_update_kernel", "conv_state_copy_kernel",
+               "lin_fwd_kernel", "lin_bwd_kernel", "lin_state_kernel", "lin_gate_tiles_kernel", "lin_gate_kernel",
+               "lin_group_sum_kernel", "lin_update_kernel", "ln_fwd_kernel", "ln_bwd_kernel", "ln_reduce_kernel")
 
 
 def summarize(run_root, prefix, title, commands, profiled_hash=None):

@@ -377,8 +377,9 @@ bool whole_vectors(const LayerNormArgs& a) {
 
 // The form of rows of W elements: as few threads as hold a row in at most 4 vectors each (one element at a time, 8 or
 // 16), in whole waves above one.  Measured, 65536 rows of 2560 in bf16, forward / backward: 3 vectors of 128 threads
-// 157 / 212 us where 2 of 256 took 191 / 253 us and 1 of 512 242 / 254 us.
-template <typename T, typename Go>
+// 157 / 212 us where 2 of 256 took 191 / 253 us and 1 of 512 242 / 254 us.  Between 129 and 256 vectors the forward has
+// one wave a row (1536: 77 us, 94 us with two) and the backward, which keeps twice as much, two (114 us, 126 us with one).
+template <typename T, bool FWD, typename Go>
 auto with_form(bool vec, int64_t W, Go go) {
   constexpr int V = 16 / sizeof(T);
   if (!vec) {
@@ -393,6 +394,8 @@ auto with_form(bool vec, int64_t W, Go go) {
   if (n <= 32) return go(Form<T, V, 1, 32>{});
   if (n <= 64) return go(Form<T, V, 1, 64>{});
   if (n <= 128) return go(Form<T, V, 2, 64>{});
+  if (FWD && n <= 192) return go(Form<T, V, 3, 64>{});
+  if (FWD && n <= 256) return go(Form<T, V, 4, 64>{});
   if (n <= 256) return go(Form<T, V, 2, 128>{});
   if (n <= 384) return go(Form<T, V, 3, 128>{});
   if (n <= 512) return go(Form<T, V, 4, 128>{});
@@ -408,11 +411,11 @@ int64_t slices_of(const LayerNormArgs& a, int tpr, int64_t blocks) {
 
 template <typename T>
 hipError_t launch_fwd(const LayerNormArgs& a) {
-  return with_form<T>(whole_vectors<T>(a), a.W, [&](auto f) { return f.fwd(a, slices_of(a, f.tpr, kFwdBlocks)); });
+  return with_form<T, true>(whole_vectors<T>(a), a.W, [&](auto f) { return f.fwd(a, slices_of(a, f.tpr, kFwdBlocks)); });
 }
 template <typename T>
 hipError_t launch_bwd(const LayerNormArgs& a, int64_t n_slices, float* pw, float* pb) {
-  return with_form<T>(whole_vectors<T>(a), a.W, [&](auto f) { return f.bwd(a, n_slices, pw, pb); });
+  return with_form<T, false>(whole_vectors<T>(a), a.W, [&](auto f) { return f.bwd(a, n_slices, pw, pb); });
 }
 
 // How the backward's parameter sums are cut: n_slices partial rows [H W], added in n_parts parts of
@@ -423,7 +426,7 @@ struct NormPlan {
 NormPlan plan_bwd(const LayerNormArgs& a, bool vec) {
   NormPlan p;
   auto tpr_of = [](auto f) { return int(f.tpr); };
-  const int tpr = a.dtype == 0 ? with_form<float>(vec, a.W, tpr_of) : with_form<bf16_bits>(vec, a.W, tpr_of);
+  const int tpr = a.dtype == 0 ? with_form<float, false>(vec, a.W, tpr_of) : with_form<bf16_bits, false>(vec, a.W, tpr_of);
   p.n_slices = slices_of(a, tpr, kBwdBlocks);
   const int64_t blocks = 2 * ceil_div(a.H * a.W, 64);
   p.n_parts = std::max<int64_t>(1, std::min<int64_t>(ceil_div(512, blocks), p.n_slices / 32));

@@ -363,6 +363,38 @@ def test_graphs_replay_exactly():
             assert all(torch.equal(s, t) for s, t in zip(a, b)), f"replay {rep}"
 
 
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: with decays of e^-1 a token, the first and the last tokens see only their
+    neighbours, so short calls on those alone give the same values (up to e^-100, and the order of their chunks)."""
+    import torch
+
+    import selective_state_space_35_amd as ssm
+
+    L, H, D, n = (1 << 18) + 77, 65, 128, 300
+    say(f"linattn L={L} H={H} D={D}: {L * H * D / 2 ** 31:.2f} x 2^31 elements")
+    if torch.cuda.mem_get_info()[0] < (80 << 30):
+        pytest.skip("needs 80 GB of device memory")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v, dy = (torch.randn((1, L, H, D), generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    A = torch.full((H,), -1.0, device="cuda")
+    y, last = ssm.ssm_linattn_fwd(q, k, v, A=A)
+    d = ssm.ssm_linattn_bwd(q, k, v, dy, A=A)
+    torch.cuda.synchronize()
+    for part, keep in ((slice(0, n), slice(0, n - 100)), (slice(L - n, L), slice(100, n))):
+        t = [z[:, part].contiguous() for z in (q, k, v, dy)]
+        y2, last2 = ssm.ssm_linattn_fwd(*t[:3], A=A)
+        d2 = ssm.ssm_linattn_bwd(*t, A=A)
+        torch.cuda.synchronize()
+        for name, a, b in (("y", y, y2), *((m, d[m], d2[m]) for m in ("dq", "dk", "dv"))):
+            a, b = a[:, part][:, keep].float(), b[:, keep].float()
+            # two results of one definition: each within the documented bound, of which sums of about 1 / (1 - e^-1)
+            # products make the magnitude; the state's and the mixing matrix's rounding to bf16 dominate
+            e = (a - b).norm() / b.norm()
+            assert e <= 4 * 2.0 ** -8, (name, part, float(e))
+    e = (last - last2).norm() / last2.norm()
+    assert e <= 1e-6, float(e)
+
+
 def test_agrees_with_the_scalar_per_head_scan():
     """ssm_ssd_fwd is the case of one group: q = C, k = B, v = delta x, log decay delta A."""
     import torch
