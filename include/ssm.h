@@ -436,7 +436,7 @@ SSM_API int ssm_conv_update(void* conv_state, const void* v, const float* q, con
  * is written); f32: fp32 matrix products.  Log decays are usually negative; one below -10^4, minus infinity
  * included, counts as -10^4: a factor of zero, which drops the state (where a new
  * document starts).  A value of v that is not finite may reach the outputs of up to
- * 63 tokens before its own, through products with zero.
+ * 63 tokens (f32: 31) before its own, through products with zero.
  * L == 0 copies initial_state (or zeros) to last_state; b == 0 or H == 0 is a no-op.
  */
 SSM_API int ssm_linattn_fwd(const void* q, const void* k, const void* v, const void* g, const float* A,

@@ -670,7 +670,8 @@ __device__ __forceinline__ const T* start_of(const void* x, const Sweep& p, cons
 
 // ---------------------------------------------------------------------------
 // States of the parts of a cut sequence, each from zero, and the sums of their log decays; the workgroups from n on
-// take the second sweep's.  The parts are shorter than the segments, so that a few heads fill the chip here too.
+// take the second sweep's.  The parts are shorter than the segments, so that a few heads fill the chip here too
+// (b1 L65536 H40 D128: 300 us, 3.7 TB/s; with a part a segment 345 us).  Bound by HBM.
 // ---------------------------------------------------------------------------
 template <typename T, int KDP, int VDP, bool VEC>
 __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) void lin_state_kernel(Sweep p0, Sweep p1, int n) {
@@ -736,6 +737,12 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) v
 // the state's update, while waves 4..7 bring the next chunk's rows to the other half of the LDS tiles
 // and then compute its P, in the other half of P; two barriers a chunk.  One SIMD has a wave of each kind.  The rows of the
 // two chunks after are on their way into registers meanwhile.
+//
+// Measured (bf16): b8 L2048 H24 D64 forward 64 us (HBM floor 43 us; all eight waves doing all the work in turn 84 us in
+// segments, 105 us uncut); a chunk is 3700 cycles, of which the LDS is busy 1800 and each SIMD's VALU 1600, partly
+// one after the other.  b1 L65536 H40 D128: 990 us (floor 562 us) of which 300 us are the pass over k and v that the cut needs.
+// Backward, three sweeps: b8 L2048 H24 D64 235 us, b4 L4096 H32 G8 D128 640 us (floors 74, 113 us), bound by VALU and
+// MFMA issue of the sweeps with dots (8100 cycles a chunk at D128: 760 VALU and 150 MFMA instructions a state wave).
 // ---------------------------------------------------------------------------
 template <typename T, int KDP, int VDP, bool DOTS>
 struct SweepLds {
@@ -1130,7 +1137,7 @@ __global__ __launch_bounds__(2 * kThreads) SSM_LIN_WAVES(kSweepWaves) void lin_b
 // Gradient of the gates: dg_t = end + sum over i >= t of (a_i - c_i), per batch row and head, where
 // end = <d_last, S_last>.  a and c are [b, L, H].  Tiles of kGateTile tokens: first each tile's
 // sum, then each tile adds the sums of the later ones to its own running sum (double: the terms
-// cancel over the sequence).
+// cancel over the sequence).  b8 L2048 H24: 9 and 7 us, by the latency of a row's 64-byte pieces.
 constexpr int kGateTile = 256;
 constexpr int kGateHeads = 16;  // heads of a workgroup: 16 consecutive floats of a row, times 16 tokens
 
@@ -1200,7 +1207,8 @@ __global__ __launch_bounds__(256) void lin_gate_kernel(const Dot<T>* __restrict_
   }
 }
 
-// out[row, g, :] = sum over the group's heads of in[row, h, :] (float), rounded once; VEC elements a thread
+// out[row, g, :] = sum over the group's heads of in[row, h, :] (float), rounded once; VEC elements a thread.  Bound by HBM
+// (b4 L4096, 32 heads in 8 groups, D128: 57 us, 5.3 TB/s; one element a thread 91 us).
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* __restrict__ in, T* __restrict__ out,
                                                             int64_t n, int share, int D) {
@@ -1231,7 +1239,8 @@ __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* __restr
 
 // ---------------------------------------------------------------------------
 // One token: a workgroup holds one head of one batch row.  Lanes run along the columns of the
-// state, the workgroup's row groups along its rows; the readout is summed over the row groups in LDS.
+// state, the workgroup's row groups along its rows; the readout is summed over the row groups in LDS.  Bound by HBM, the
+// state read and written once: b256 H40 D128 260 us, 5.2 TB/s.
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void lin_update_kernel(float* __restrict__ state, const T* __restrict__ q,
                                                          const T* __restrict__ k, const T* __restrict__ v,
