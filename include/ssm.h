@@ -455,6 +455,8 @@ SSM_API int ssm_linattn_fwd(const void* q, const void* k, const void* v, const v
  *     d_initial_state [b, H, Dk, Dv] float (nullable; also when initial_state is NULL)
  * Nothing of the forward is kept: the states are recomputed.  Results are
  * deterministic.  Workspace as in ssm_linattn_fwd, of the backward's size.
+ * As there, what is not finite may reach up to 63 tokens (f32: 31) through
+ * products with zero: of dy the dv after its own, of k the dq before, of q the dk after.
  */
 SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const void* g, const float* A,
                             const int32_t* lengths, float scale, const float* initial_state, const void* dy,

@@ -160,6 +160,47 @@ def test_many_segments(dtype):
     check(make(b=1, L=1500, H=2, G=1, Dk=64, Dv=48, dtype=dtype, rate=0.01, seed=2), f"linattn segments {dtype}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_what_is_not_finite_does_not_reach_back(name, bad, dtype):
+    """A token's value that is no number reaches its own output and later ones, bit for bit no earlier token's; in the
+    backward (through dy) no later token's dq and dk.  What stands in v's place (v in y, dy in dv) may reach the other
+    tokens of its step, 63 (f32: 31) at most, in its own column, as documented: beyond them it is equality too."""
+    import torch
+
+    x = make(b=1, L=230, H=4, G=4, Dk=40, Dv=72, dtype=dtype, seed=21, rate=0.05)
+    say(f"linattn {name} = {bad} {dtype}")
+    step = 31 if dtype == "f32" else 63
+    y0, _ = fwd(x)
+    d0 = bwd(x)
+    others = [0, 2, 3]
+    col = [j for j in range(72) if j != 5]
+    for t in (0, 70, 127, 229):
+        z = dict(x, **{name: x[name].clone()})
+        z[name][0, t, 1, 5] = bad
+        y, last = fwd(z)
+        torch.cuda.synchronize()
+        before = max(t - step, 0) if name == "v" else t
+        assert torch.equal(y[0, :before], y0[0, :before]), t
+        assert torch.equal(y[0, :, others], y0[0, :, others])
+        if name == "v":
+            assert torch.equal(y[0, :t, 1][:, col], y0[0, :t, 1][:, col])
+            assert not torch.isfinite(y[0, t:, 1, 5]).any() and torch.isfinite(y[0, :, 1, col]).all()
+        if name == "q":
+            assert torch.equal(y[0, t + 1:], y0[0, t + 1:]) and not torch.isfinite(y[0, t, 1]).any()
+        if name != "q":
+            assert not torch.isfinite(last[0, 1]).all() and torch.isfinite(last[0, others]).all()
+        z = dict(x, dy=x["dy"].clone())
+        z["dy"][0, t, 1, 5] = bad
+        d = bwd(z)
+        torch.cuda.synchronize()
+        assert torch.equal(d["dk"][0, t + 1:], d0["dk"][0, t + 1:]), t
+        assert torch.equal(d["dv"][0, t + 1 + step:], d0["dv"][0, t + 1 + step:]), t
+        assert torch.equal(d["dv"][0, t + 1:, 1][:, col], d0["dv"][0, t + 1:, 1][:, col]), t
+        assert torch.equal(d["dq"][0, :t], d0["dq"][0, :t]) and torch.equal(d["dq"][0, t + 1:], d0["dq"][0, t + 1:])
+
+
 def test_unaligned_rows():
     """Tensors that start in the middle of a 16-byte unit."""
     import torch
