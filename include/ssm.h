@@ -431,7 +431,7 @@ SSM_API int ssm_conv_update(void* conv_state, const void* v, const float* q, con
  *   workspace, workspace_bytes        at least ssm_linattn_workspace() bytes, 256-byte aligned, used by
  *                                     this call's work until it has run; NULL: from the stream-ordered
  *                                     allocator on `stream`
- * 1 <= Dk, Dv <= 128 (else SSM_ERR_DIM); G divides H; H <= 65535.  bf16: matrix products
+ * 1 <= Dk, Dv <= 128 (else SSM_ERR_DIM); G divides H; H <= 65535; b H <= 2^21.  bf16: matrix products
  * take bf16 operands and accumulate in fp32 (the state's two bf16 parts, high and low, where it
  * is written); f32: fp32 matrix products.  Log decays are usually negative; one below -10^4, minus infinity
  * included, counts as -10^4: a factor of zero, which drops the state (where a new
@@ -491,7 +491,7 @@ SSM_API int64_t ssm_linattn_workspace(int64_t b, int64_t L, int64_t H, int64_t G
  *   x, y          [rows, H, W]  dtype
  *   weight, bias  [H, W]        float  (nullable: one, zero)
  *   mean, rstd    [rows, H]     float  (nullable; what the backward needs)
- * 1 <= W <= 16384; eps >= 0 (else SSM_ERR_DIM).
+ * 1 <= W <= 16384; H <= 2^21; H W < 2^30 - 64; eps >= 0 (else SSM_ERR_DIM).
  */
 SSM_API int ssm_layernorm_fwd(const void* x, const float* weight, const float* bias, float eps, void* y, float* mean,
                               float* rstd, int64_t rows, int64_t H, int64_t W, int dtype, void* stream);

@@ -426,10 +426,10 @@ int check_linattn(int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_
   int64_t t = 0;
   if (!mul_ok(b, L, &t) || !mul_ok(t, H, &t) || !mul_ok(t, max_dim * 64, &t)) return SSM_ERR_DIM;
   if (!mul_ok(b, H, &t) || !mul_ok(t, max_dim * max_dim * 64, &t)) return SSM_ERR_DIM;
-  // grids: a workgroup per head (and segment) of a batch row; 256 tokens x 16 heads in the gate's sums;
-  // 256 elements of dq in the sums over a group
-  if (b * H > INT32_MAX / 4 || L > INT32_MAX - 4096 || !mul_ok(b * H, L / 256 + 1, &t) || t > INT32_MAX) return SSM_ERR_DIM;
-  if (!mul_ok(b * L, G * Dk, &t) || t / 256 > INT32_MAX - 1) return SSM_ERR_DIM;
+  // grids hold less than 2^32 threads: three sweeps of 512 threads a head of a batch row (fewer heads than workgroups
+  // at once where a sequence is cut into segments); 256 threads for 256 tokens x 16 heads in the gate's sums
+  if (b * H > (int64_t(1) << 21) || L > INT32_MAX - 4096) return SSM_ERR_DIM;
+  if (!mul_ok(b * (L / 256 + 1), H / 16 + 1, &t) || t > UINT32_MAX / 256) return SSM_ERR_DIM;
   return SSM_OK;
 }
 
@@ -469,9 +469,11 @@ int with_workspace(size_t need, void* workspace, int64_t bytes, hipStream_t stre
 
 int check_layernorm(int64_t rows, int64_t H, int64_t W, int dtype) {
   if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
-  if (!size_ok(rows) || H < 0 || H > (int64_t(1) << 24) || W < 1 || W > ssm::layernorm_max_width()) return SSM_ERR_DIM;
+  if (!size_ok(rows) || H < 0 || H > (int64_t(1) << 21) || W < 1 || W > ssm::layernorm_max_width()) return SSM_ERR_DIM;
   int64_t t = 0;
-  if (!mul_ok(rows, H, &t) || t > INT32_MAX || !mul_ok(t, W * 16, &t)) return SSM_ERR_DIM;  // a workgroup a row at most
+  if (!mul_ok(rows, H, &t) || t > INT32_MAX || !mul_ok(t, W * 16, &t)) return SSM_ERR_DIM;
+  // grids hold less than 2^32 threads: up to 1024 for each head, and 256 for 64 columns of the parameters' sums
+  if (H * W >= (int64_t(1) << 30) - 64) return SSM_ERR_DIM;
   return SSM_OK;
 }
 

@@ -1212,28 +1212,28 @@ __global__ __launch_bounds__(256) void lin_gate_kernel(const Dot<T>* __restrict_
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* __restrict__ in, T* __restrict__ out,
                                                             int64_t n, int share, int D) {
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * VEC;
-  if (i >= n) return;
-  const int64_t rg = i / D;
-  const float* p = in + rg * share * D + i % D;
-  float s[VEC];
+  for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * VEC; i < n; i += int64_t(gridDim.x) * 256 * VEC) {
+    const int64_t rg = i / D;
+    const float* p = in + rg * share * D + i % D;
+    float s[VEC];
 #pragma unroll
-  for (int j = 0; j < VEC; j++) s[j] = 0.f;
+    for (int j = 0; j < VEC; j++) s[j] = 0.f;
 #pragma unroll 4
-  for (int k = 0; k < share; k++) {
-    if constexpr (VEC == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + int64_t(k) * D);
-      s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
-    } else {
-      s[0] += p[int64_t(k) * D];
+    for (int k = 0; k < share; k++) {
+      if constexpr (VEC == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + int64_t(k) * D);
+        s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+      } else {
+        s[0] += p[int64_t(k) * D];
+      }
     }
-  }
-  if constexpr (VEC == 4 && sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(out + i) = make_float4(s[0], s[1], s[2], s[3]);
-  } else if constexpr (VEC == 4) {
-    *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
-  } else {
-    store_elem(out + i, s[0]);
+    if constexpr (VEC == 4 && sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(out + i) = make_float4(s[0], s[1], s[2], s[3]);
+    } else if constexpr (VEC == 4) {
+      *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
+    } else {
+      store_elem(out + i, s[0]);
+    }
   }
 }
 
@@ -1305,6 +1305,7 @@ __global__ __launch_bounds__(256) void lin_update_kernel(float* __restrict__ sta
 // host side
 // ---------------------------------------------------------------------------
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr int64_t kSumBlocks = int64_t(1) << 22;  // a grid holds less than 2^32 threads: beyond, a thread has several sums
 constexpr size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // rows of whole 16-byte pieces, 16-byte aligned
@@ -1522,8 +1523,8 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
       const float* in = reinterpret_cast<const float*>(ws + (k ? w.dk : w.dq));
       T* out = static_cast<T*>(k ? a.dk : a.dq);
       const bool vec = a.Dk % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
-      err = vec ? launch_kind(kKindLinReduce, lin_group_sum_kernel<T, 4>, ceil_div(n, 1024), 256, a.stream, in, out, n, share, int(a.Dk))
-                : launch_kind(kKindLinReduce, lin_group_sum_kernel<T, 1>, ceil_div(n, 256), 256, a.stream, in, out, n, share, int(a.Dk));
+      err = vec ? launch_kind(kKindLinReduce, lin_group_sum_kernel<T, 4>, std::min(ceil_div(n, 1024), kSumBlocks), 256, a.stream, in, out, n, share, int(a.Dk))
+                : launch_kind(kKindLinReduce, lin_group_sum_kernel<T, 1>, std::min(ceil_div(n, 256), kSumBlocks), 256, a.stream, in, out, n, share, int(a.Dk));
       if (err != hipSuccess) return err;
     }
   }

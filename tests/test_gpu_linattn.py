@@ -436,6 +436,23 @@ def test_offsets_past_32_bits():
     assert e <= 1e-6, float(e)
 
 
+def test_group_sums_of_more_elements_than_a_grid():
+    """dq and dk of shared heads beyond 2^30 elements one at a time (Dk 33): equal batch rows, equal gradients."""
+    import torch
+
+    b, L, H, Dk = 512, 65536, 2, 33
+    say(f"linattn bwd b={b} L={L} H={H} Dk={Dk}")
+    if torch.cuda.mem_get_info()[0] < (80 << 30):
+        pytest.skip("needs 80 GB of free memory")
+    x = make(b=1, L=L, H=H, G=1, Dk=Dk, Dv=1, dtype="bf16", seed=5)
+    d = bwd({n: t.expand(b, *t.shape[1:]).contiguous() if isinstance(t, torch.Tensor) else t for n, t in x.items()})
+    torch.cuda.synchronize()
+    for n in ("dq", "dk"):
+        assert d[n].numel() > 1 << 30 and torch.isfinite(d[n][0]).all() and d[n][0].abs().max() > 0
+        for i in range(0, b, 64):
+            assert torch.equal(d[n][i:i + 64], d[n][:1].expand(64, L, 1, Dk)), (n, i)
+
+
 def test_agrees_with_the_scalar_per_head_scan():
     """ssm_ssd_fwd is the case of one group: q = C, k = B, v = delta x, log decay delta A."""
     import torch

@@ -153,3 +153,20 @@ def test_binding_refuses_what_does_not_fit():
         ssm.ssm_linattn_fwd(z(4, 2, 8), z(4, 2, 8), z(4, 2, 8))
     with pytest.raises(ValueError, match="v must be"):
         ssm.ssm_linattn_update(z(1, 2, 8, 8), z(1, 2, 8), z(1, 2, 8), z(1, 2, 8, 1))
+
+
+def test_grids_of_more_threads_than_a_launch_holds(lib):
+    """b H beyond 2^21, too many tiles of the gate's sums, and H or H W beyond the layer norm's: refused, and just
+    below only the missing pointer is."""
+    for call, first in ((fwd, "q"), (bwd, "q"), (update, "state")):
+        a = dict(H=16, G=16, Dk=1, Dv=1)
+        assert call(lib, b=(1 << 17) + 1, **a) == DIM
+        assert call(lib, b=1 << 17, **a, **{first: None}) == NULL
+    for call in (fwd, bwd):
+        assert call(lib, b=1 << 17, L=1 << 16, H=1, G=1, Dk=1, Dv=1) == DIM
+        assert call(lib, b=1 << 15, L=1 << 16, H=1, G=1, Dk=1, Dv=1, q=None) == NULL
+    for call in (norm, norm_bwd):
+        assert call(lib, rows=1, H=(1 << 21) + 1, W=1) == DIM
+        assert call(lib, rows=1, H=1 << 21, W=1, x=None) == NULL
+        assert call(lib, rows=1, H=1 << 17, W=1 << 13) == DIM
+        assert call(lib, rows=1, H=1 << 16, W=1 << 13, x=None) == NULL
