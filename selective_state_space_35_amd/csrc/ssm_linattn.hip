@@ -730,8 +730,10 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) v
 //             consecutive s of its t), to LDS
 //   out     = exp(G_t) S^T q_t + P V, as its transpose: a lane has consecutive columns of its own t
 //   S       = exp(G) S + K^T (out o V)
-// With DOTS the output without the token's own product is multiplied with the rows of xd, which
-// has to be right to fp32 over long sums: P and S go into the products as two bf16 parts.
+// bf16: P and S go into the products as two bf16 parts (2^-16 of a product at most), so that an output's error is its
+// own rounding: against float64 1.7 10^-3 of y in the norm, with one part 2.3 10^-3; b8 L2048 H24 D64 forward 62 us, with
+// one part 59 us.  With DOTS the output without the token's own product is multiplied with the rows of xd, for sums over
+// the whole sequence that one part would not be right enough for at all.
 //
 // Only the state runs from chunk to chunk, so it has waves of its own: waves 0..3 take the outputs and
 // the state's update, while waves 4..7 bring the next chunk's rows to the other half of the LDS tiles
@@ -747,7 +749,7 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) v
 template <typename T, int KDP, int VDP, bool DOTS>
 struct SweepLds {
   static constexpr int kC = kChunk<T>;
-  static constexpr bool kTwo = DOTS && sizeof(T) == 2;
+  static constexpr bool kTwo = sizeof(T) == 2;  // operands that are not given in bf16 are taken in two parts
   static constexpr int ldp = kC + 16 / int(sizeof(T));
   __attribute__((aligned(16))) T q[2][Tile<T, KDP, kQuery>::kElems];
   __attribute__((aligned(16))) T k[2][Tile<T, KDP, kKey>::kElems];
@@ -773,7 +775,10 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
   for (int i = threadIdx.x; i < (TB / 2) * 256; i += 2 * kThreads) {
     const int b = i / 256, t = 32 * b + (i / 16) % 16, s = 32 * b + 16 + i % 16;
 #pragma unroll
-    for (int k = 0; k < 2 * (kTwo ? 2 : 1); k++) sh.P[0][k][t * ldp + s] = T(0);
+    for (int k = 0; k < 2; k++) {
+      sh.P[k][0][t * ldp + s] = T(0);
+      if constexpr (kTwo) sh.P[k][1][t * ldp + s] = T(0);
+    }
   }
 
   if (wv >= 4) {
@@ -941,9 +946,6 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
   }
 
   // -------------------------------------------------------------------- outputs and state
-  // Where the state's waves come to the middle of a step, so that neither half waits long: before the products with P,
-  // or after them (float, b32 L512 H8 D128, backward: 340 and 330 us; bf16, b8 L2048 H24 D128, forward: 144 and 148 us).
-  constexpr bool kLateHalf = kTwo || sizeof(T) == 4;
   const int vc = wv * (VDP / 4) + (l / 16) * kN;  // first of the kN columns that this lane has of an output row
   typedef Rows<kN, VEC, kC> R;
   R xr, yr;
@@ -1017,7 +1019,6 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
     read_q(1);
     times_state(0);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (!kLateHalf) __syncthreads();
     float in[TB];
 #pragma unroll
     for (int tt = 0; tt < TB; tt++) in[tt] = d.in[16 * tt + lr] * p.rscale;
@@ -1047,7 +1048,9 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
         for (int k = 0; k < (kTwo ? 2 : 1); k++)
 #pragma unroll
           for (int n = 0; n < Y::NT; n++) o[tt][n] = mma(vf[ks][n], pf[k][tt][ks], o[tt][n]);
-    if constexpr (kLateHalf) __syncthreads();
+    // The middle of a step, after the products with P, so that neither half waits long (before them: float, b32 L512 H8
+    // D128, backward, 340 us and here 330; bf16, b8 L2048 H24 D64, forward, 65 and 62 us)
+    __syncthreads();
     // ---- outputs ----
 #pragma unroll
     for (int tt = 0; tt < TB; tt++) {

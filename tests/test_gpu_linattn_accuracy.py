@@ -1,0 +1,49 @@
+"""How near linear attention's outputs are to float64, in bounds that one lost rounding breaks.
+
+Beside those of tests/linattn_ref.py, whose magnitudes and counts of roundings are used here:
+
+* y, dq, dk, dv of bf16 tensors: an operand that is not given in bf16 (the mixing matrix, the state that is read, the
+  values that are written into a state) is taken in two bf16 parts at least.  The first is off by 2^-8 of it at most, the
+  second by 2^-8 of that: 2^-16.  A product goes through one such operand inside its chunk, through two (written and
+  read) beyond it: 2^-15 of the magnitude.  Then the output's own rounding, 2^-8 of the value.
+"""
+import pytest
+
+from tests import linattn_ref as ref
+from tests.gpu_common import say
+from tests.test_gpu_linattn import bwd, fwd, make
+
+pytestmark = pytest.mark.gpu
+PARTS = 2.0 ** -15
+
+
+def near(got, want, mag, name, x, what):
+    """The elementwise bound above (bf16), of an output in the streamed type."""
+    tol = mag * (PARTS + 2 * ref.terms(x) * 2.0 ** -24) + want.abs() * 2.0 ** -8
+    over = ((got.detach().cpu().to(ref.F64) - want).abs() / (tol * 1.01 + 1e-37)).max().item()
+    print(f"[accuracy] {what}: {name} at {over:.3f} of its bound", flush=True)
+    assert over <= 1.0, f"{what}: {name} is {over:.3f} times its bound"
+
+
+SIZES = [dict(L=200, H=4, G=2, Dk=64, Dv=64), dict(L=150, H=2, G=2, Dk=64, Dv=128), dict(L=150, H=2, G=1, Dk=128, Dv=64),
+         dict(L=130, H=2, G=2, Dk=128, Dv=128), dict(L=140, H=3, G=3, Dk=40, Dv=24), dict(L=97, H=2, G=2, Dk=33, Dv=70),
+         dict(L=130, H=2, G=2, Dk=100, Dv=127), dict(L=1500, H=2, G=1, Dk=64, Dv=48, rate=0.01)]
+
+
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()))
+def test_outputs_are_rounded_once(size, gate):
+    """Without a gate too: the sweeps that need no dots are other kernels."""
+    import torch
+
+    x = make(b=1, seed=31, gate=gate, fixed=not gate, **size)
+    what = f"linattn {size} gate={gate}"
+    say(what)
+    y, _ = fwd(x)
+    torch.cuda.synchronize()
+    near(y, ref.forward(x)["y"], ref.forward(x, absolute=True)["y"], "y", x, what)
+    d = bwd(x)
+    torch.cuda.synchronize()
+    want, mag = ref.backward(x), ref.backward(x, absolute=True)
+    for name in ("dq", "dk", "dv"):
+        near(d[name], want[name], mag[name], name, x, what)
