@@ -433,8 +433,8 @@ SSM_API int ssm_conv_update(void* conv_state, const void* v, const float* q, con
  *                                     allocator on `stream`
  * 1 <= Dk, Dv <= 128 (else SSM_ERR_DIM); G divides H; H <= 65535; b H <= 2^21.  bf16: matrix products
  * take bf16 operands and accumulate in fp32; what is not given in bf16 (the mixing weights, the state) is
- * taken in two bf16 parts, high and low (written into a state that is an output: in three), so that an
- * output is right to its own rounding; f32: fp32 matrix products.  Log decays are usually negative; one below -10^4, minus infinity
+ * taken in two bf16 parts, high and low (written into a state that can be an output: in three), so that
+ * an output is right to its own rounding; f32: fp32 matrix products.  NULL outputs change no bit of the others.  Log decays are usually negative; one below -10^4, minus infinity
  * included, counts as -10^4: a factor of zero, which drops the state (where a new
  * document starts).  A value of v that is not finite may reach the outputs of up to
  * 63 tokens (f32: 31) before its own, through products with zero.

@@ -54,7 +54,7 @@ struct Sweep {
   void* dots;              // Dot<T>
   const float* dstate;     // [b, H, VD, KD] (transposed); dstate_dot[b, H] = its product with the last state
   float* dstate_dot;
-  bool exact;              // the state is an output: its products keep all bits of a float
+  bool exact;              // a sweep whose last state can be asked for: its products keep all bits of a float, asked for or not
   bool reverse;            // from the last token to the first
   int64_t b, L;
   int H, KD, VD;
@@ -578,8 +578,9 @@ struct Layout {
 };
 
 // S = all S + K^T (out o V) over a chunk.  The weighted values are split into two bf16 parts (half a step of 2^-8
-// twice: 2^-16 of a product at most, 2 10^-6 of the state measured), and where the state itself is an output
-// (exact) into three, which hold all 24 bits of a float.
+// twice: 2^-16 of a product at most, 2 10^-6 of the state measured), and in the sweeps whose state can be an output
+// (exact) into three, which hold all 24 bits of a float: whether it is asked for does not change the other outputs' bits
+// (b1 L65536 H40 D128 forward 1030 us, with two parts 920 us).
 template <typename T, int KDP, int VDP>
 __device__ __forceinline__ void write_state(typename Layout<KDP, VDP>::State& S, const T* Ks,
                                             const Frag<T> (&vf)[kChunk<T> / 32][VDP / 64],
@@ -1459,7 +1460,7 @@ hipError_t fwd_impl(const LinAttnArgs& a, char* ws) {
   p.rscale = a.scale;
   p.init = a.h0;
   p.seg_state = reinterpret_cast<float*>(ws + w.seg_f); p.seg_decay = reinterpret_cast<float*>(ws + w.dec_f);
-  p.exact = a.last != nullptr;
+  p.exact = true;
   const hipError_t err = run_states<T>(p, p, 1);
   if (err != hipSuccess) return err;
   p.out = a.y;
@@ -1485,7 +1486,7 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
     r.xk = a.q; r.gk = share; r.xv = a.dy;
     r.wscale = a.scale; r.reverse = true;
     r.init = a.dlast; r.seg_state = seg_r; r.seg_decay = dec_r;
-    r.exact = a.dh0 != nullptr;
+    r.exact = true;
     f.KD = r.KD = int(a.Dk); f.VD = r.VD = int(a.Dv);
     err = run_states<T>(f, r, 2);
     if (err != hipSuccess) return err;
@@ -1509,7 +1510,7 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
   dv.init = a.dlast; dv.seg_state = seg_r;
   dv.out = a.dv;
   dv.last = a.dh0; dv.final_decay = true;
-  dv.exact = a.dh0 != nullptr;
+  dv.exact = true;
   if (gate) {
     dq.xd = a.q; dk.xd = a.k;
     dq.gd = dk.gd = share;

@@ -47,3 +47,22 @@ def test_outputs_are_rounded_once(size, gate):
     want, mag = ref.backward(x), ref.backward(x, absolute=True)
     for name in ("dq", "dk", "dv"):
         near(d[name], want[name], mag[name], name, x, what)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [200, 1500])
+def test_what_else_is_asked_for_changes_no_bit(L, dtype):
+    """y is the same with and without last_state, dv with and without the gradient of an initial state of zero."""
+    import torch
+
+    x = make(b=1, L=L, H=2, G=1, Dk=64, Dv=48, dtype=dtype, rate=0.01, seed=32)
+    x["d_last_state"] = None
+    say(f"linattn optional outputs L={L} {dtype}")
+    y, _ = fwd(x)
+    alone, none = fwd(x, return_last_state=False)
+    assert none is None and torch.equal(y, alone)
+    zero = torch.zeros_like(x["initial_state"])
+    d0, d = bwd(dict(x, initial_state=zero)), bwd(dict(x, initial_state=None))
+    torch.cuda.synchronize()
+    for name in ("dq", "dk", "dv", "dg"):
+        assert torch.equal(d0[name], d[name]), name
