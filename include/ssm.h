@@ -436,8 +436,9 @@ SSM_API int ssm_conv_update(void* conv_state, const void* v, const float* q, con
  * taken in two bf16 parts, high and low (written into a state that can be an output: in three), so that
  * an output is right to its own rounding; f32: fp32 matrix products.  NULL outputs change no bit of the others.  Log decays are usually negative; one below -10^4, minus infinity
  * included, counts as -10^4: a factor of zero, which drops the state (where a new
- * document starts).  A value of v that is not finite may reach the outputs of up to
- * 63 tokens (f32: 31) before its own, through products with zero.
+ * document starts; zero times a state that is not finite is NaN).  What is not finite reaches the
+ * outputs that read it and no others; a value of v makes its column of y from its token on, and of the
+ * state, NaN.
  * L == 0 copies initial_state (or zeros) to last_state; b == 0 or H == 0 is a no-op.
  */
 SSM_API int ssm_linattn_fwd(const void* q, const void* k, const void* v, const void* g, const float* A,
@@ -456,8 +457,8 @@ SSM_API int ssm_linattn_fwd(const void* q, const void* k, const void* v, const v
  *     d_initial_state [b, H, Dk, Dv] float (nullable; also when initial_state is NULL)
  * Nothing of the forward is kept: the states are recomputed.  Results are
  * deterministic.  Workspace as in ssm_linattn_fwd, of the backward's size.
- * As there, what is not finite may reach up to 63 tokens (f32: 31) through
- * products with zero: of dy the dv after its own, of k the dq before, of q the dk after.
+ * As there, what is not finite reaches the outputs that read it and no others, but for dg, a sum over the tokens
+ * from its own on: a k or v that is not finite makes the dg of all tokens before it NaN too.
  */
 SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const void* g, const float* A,
                             const int32_t* lengths, float scale, const float* initial_state, const void* dy,

@@ -514,6 +514,57 @@ __device__ __forceinline__ double fill_decays(Decays<kC>& d, float gate, float w
   return last * 0.6931471805599453;
 }
 
+// Whether a lane's fragments (or, bf16, those of lanes that share a row of 16 with it) hold what is not finite: its
+// products with zero are no numbers.  bf16: one matrix product a fragment (b8 L2048 H24 D64 forward 63 us with and without
+// it, b4 L4096 H32 G8 D128 backward 647 and 638 us).
+template <int KS, int N>
+__device__ __forceinline__ bool not_finite(const bf16x8 (&f)[KS][N]) {
+  const bf16x8 zero = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
+  f32x4 z{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < KS; k++)
+#pragma unroll
+    for (int n = 0; n < N; n++) z = mma(f[k][n], zero, z);
+  return !((z[0] + z[1]) + (z[2] + z[3]) == 0.f);
+}
+template <int KS, int N>
+__device__ __forceinline__ bool not_finite(const f32x8 (&f)[KS][N]) {
+  float z = 0.f;
+#pragma unroll
+  for (int k = 0; k < KS; k++)
+#pragma unroll
+    for (int n = 0; n < N; n++)
+#pragma unroll
+      for (int j = 0; j < 8; j++) z = fmaf(f[k][n].v[j], 0.f, z);
+  return !(z == 0.f);
+}
+// Zero in the place of what is not finite; the first such element, 8 if there is none
+__device__ __forceinline__ int drop_not_finite(bf16x8& f) {
+  uint4 u = __builtin_bit_cast(uint4, f);
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  int first = 8;
+#pragma unroll
+  for (int j = 7; j >= 0; j--) {
+    const uint32_t exponent = 0x7f80u << (16 * (j % 2));
+    if ((w[j / 2] & exponent) == exponent) {
+      first = j;
+      w[j / 2] &= j % 2 ? 0x0000ffffu : 0xffff0000u;
+    }
+  }
+  f = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+  return first;
+}
+__device__ __forceinline__ int drop_not_finite(f32x8& f) {
+  int first = 8;
+#pragma unroll
+  for (int j = 7; j >= 0; j--)
+    if ((__float_as_uint(f.v[j]) & 0x7f800000u) == 0x7f800000u) {
+      first = j;
+      f.v[j] = 0.f;
+    }
+  return first;
+}
+
 // The state in registers: wave w holds its VDP / 4 columns, as 16 x 16 results whose rows run along
 // the KDP index.  Two neighbouring results are an operand fragment as they are: a lane then has indices
 // 32 kk + 4 (l / 16) .. + 3 and 16 more, and the other operand is read in that order (pair_frag).  Where a wave has two
@@ -1041,6 +1092,33 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
       for (int n = 0; n < Y::NT; n++)
 #pragma unroll
         for (int r = 0; r < 4; r++) o[tt][n][r] *= in[tt];
+    // A value that is not finite must not meet P's zeros: the outputs before it would be no numbers.  It is taken out, and
+    // its column of the outputs from its own position on, and of the state, is set to NaN.  (With DOTS the own product is
+    // added below, from the tile.)
+    if (__builtin_expect(__ballot(not_finite(vf)) != 0, 0)) {
+      const float nan = __builtin_nanf("");
+#pragma unroll
+      for (int n = 0; n < Y::NT; n++) {
+        int first = kC;
+#pragma unroll
+        for (int ks = kSteps - 1; ks >= 0; ks--) {
+          const int j = drop_not_finite(vf[ks][n]);
+          if (j < 8) first = 32 * ks + g8 + j;
+        }
+        first = min(first, __shfl_xor(first, 16));
+        first = min(first, __shfl_xor(first, 32));
+#pragma unroll
+        for (int m = 0; m < Y::MT; m++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) S[m][n][r] = first < kC ? nan : S[m][n][r];
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const int at = __shfl(first, g4 + r);
+#pragma unroll
+          for (int tt = 0; tt < TB; tt++) o[tt][n][r] = 16 * tt + lr >= at + (DOTS ? 1 : 0) ? nan : o[tt][n][r];
+        }
+      }
+    }
 #pragma unroll
     for (int tt = 0; tt < TB; tt++)
 #pragma unroll

@@ -66,3 +66,65 @@ def test_what_else_is_asked_for_changes_no_bit(L, dtype):
     torch.cuda.synchronize()
     for name in ("dq", "dk", "dv", "dg"):
         assert torch.equal(d0[name], d[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("size", [dict(Dk=40, Dv=72), dict(Dk=64, Dv=64), dict(Dk=128, Dv=128), dict(L=1500, H=2, G=2, Dk=64, Dv=64)],
+                         ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()))
+def test_what_is_not_finite_reaches_what_reads_it(size, bad, dtype):
+    """One value that is not finite changes no bit of the outputs that do not read it by the definition: tokens before
+    it (in the backward, of q and dy, those after), the other columns of v, other heads."""
+    import torch
+
+    x = make(**dict(dict(b=1, L=200, H=2, G=2, dtype=dtype, seed=21, rate=0.05), **size))
+    x["d_last_state"] = None
+    say(f"linattn {size} {bad} {dtype}")
+    L = x["v"].shape[1]
+    y0, _ = fwd(x)
+    d0 = bwd(x)
+
+    def same(a, b, what):
+        assert torch.equal(a, b), what
+
+    for t in (0, 40, 63, 64, 127, L - 1):
+        for name in ("q", "k", "v", "dy"):
+            z = dict(x, **{name: x[name].clone()})
+            z[name][0, t, 1, 5] = bad
+            at = (name, t)
+            y, _ = fwd(z)
+            d = bwd(z)
+            torch.cuda.synchronize()
+            same(y[:, :, 0], y0[:, :, 0], at)
+            for n in d:
+                if n == "d_initial_state":
+                    same(d[n][:, 0], d0[n][:, 0], at)
+                else:
+                    same(d[n][:, :, 0], d0[n][:, :, 0], at)
+            if name == "dy":
+                same(y, y0, at)
+            else:
+                same(y[:, :t], y0[:, :t], at)
+                assert not torch.isfinite(y[0, t, 1, 5 if name == "v" else 0])
+            if name == "q":
+                same(y[:, t + 1:], y0[:, t + 1:], at)
+                same(d["dq"], d0["dq"], at)
+            if name == "v":
+                same(y[:, :, 1, :5], y0[:, :, 1, :5], at)
+                same(y[:, :, 1, 6:], y0[:, :, 1, 6:], at)
+                assert not torch.isfinite(y[0, t:, 1, 5]).any()
+            if name in ("k", "v"):
+                same(d["dq"][:, :t], d0["dq"][:, :t], at)
+                assert not torch.isfinite(d["dq"][0, t:, 1, 5]).any()
+                n, alone = ("dv", "dk") if name == "v" else ("dk", "dv")
+                same(d[n], d0[n], at)  # read by no dv (of v), by no dk (of k) ...
+                same(d[alone][:, :t], d0[alone][:, :t], at)  # ... and by its own token's dk, dv
+                same(d[alone][:, t + 1:], d0[alone][:, t + 1:], at)
+                same(d["d_initial_state"], d0["d_initial_state"], at)
+            if name in ("q", "dy"):
+                for n in ("dk", "dv", "dg"):
+                    same(d[n][:, t + 1:], d0[n][:, t + 1:], (n, *at))
+                assert not torch.isfinite(d["dk"][0, :t + 1, 1, 5]).any()
+            if name == "dy":
+                same(d["dq"][:, :t], d0["dq"][:, :t], at)
+                same(d["dq"][:, t + 1:], d0["dq"][:, t + 1:], at)
