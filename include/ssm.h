@@ -458,7 +458,9 @@ SSM_API int ssm_linattn_fwd(const void* q, const void* k, const void* v, const v
  * Nothing of the forward is kept: the states are recomputed.  Results are
  * deterministic.  Workspace as in ssm_linattn_fwd, of the backward's size.
  * As there, what is not finite reaches the outputs that read it and no others, but for dg, a sum over the tokens
- * from its own on: a k or v that is not finite makes the dg of all tokens before it NaN too.
+ * from its own on: a k or v that is not finite makes the dg of the tokens before it NaN too, back to the last
+ * reset.  A reset is a token whose log decay is below -104 (its factor is zero in float): its dg is zero, and nothing
+ * of the tokens from it on comes into the dg of those before.
  */
 SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const void* g, const float* A,
                             const int32_t* lengths, float scale, const float* initial_state, const void* dy,

@@ -14,7 +14,8 @@
 // and k_i . dk_i leaves it as it is written (counting backwards), so
 //   dg_t = <d_last, S_last> + sum over i >= t of (q_i . dq_i - k_i . dk_i),
 // where the product of token i with itself, in both terms, is left out of both: a difference of
-// rounded values would not cancel it, and with strong decays it is much larger than dg.
+// rounded values would not cancel it, and with strong decays it is much larger than dg.  Where r_t is
+// zero (a reset) dg_t is zero, and the sums of the tokens before end there.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -1217,75 +1218,138 @@ __global__ __launch_bounds__(2 * kThreads) SSM_LIN_WAVES(kSweepWaves) void lin_b
 
 // ---------------------------------------------------------------------------
 // Gradient of the gates: dg_t = end + sum over i >= t of (a_i - c_i), per batch row and head, where
-// end = <d_last, S_last>.  a and c are [b, L, H].  Tiles of kGateTile tokens: first each tile's
-// sum, then each tile adds the sums of the later ones to its own running sum (double: the terms
-// cancel over the sequence).  b8 L2048 H24: 9 and 7 us, by the latency of a row's 64-byte pieces.
+// end = <d_last, S_last>.  a and c are [b, L, H].  At a reset, a token whose factor r_t is zero in float, dg_t = <D_t, 0> is
+// zero, and so is the sum up to it: the sum starts again there, so that nothing of a document comes into the one before
+// it.  Tiles of kGateTile tokens: first each tile's sum up to its first reset (and whether it has one), then each tile adds
+// the later ones' up to the first reset to its own running sum (double: the terms cancel over the sequence).
+// b8 L2048 H24: 9 and 7 us, by the latency of a row's 64-byte pieces.
 constexpr int kGateTile = 256;
 constexpr int kGateHeads = 16;  // heads of a workgroup: 16 consecutive floats of a row, times 16 tokens
+// exp of a log decay below this is zero in float, denormal numbers included (2^-150)
+constexpr float kZeroLog = -104.f;
 
-template <typename D>
-__global__ __launch_bounds__(256) void lin_gate_tiles_kernel(const D* __restrict__ a, const D* __restrict__ c,
-                                                             double* __restrict__ sums, int64_t L, int H, int n_tiles,
-                                                             int h_blocks) {
+template <typename T>
+struct GateArgs {
+  const Dot<T>* a;
+  const Dot<T>* c;
+  double* sums;      // [b, n_tiles, H]
+  uint8_t* resets;   // [b, n_tiles, H]: whether the tile has a reset
+  const float* end;  // [b, H], nullable
+  const T* g;
+  const float* A;    // nullable
+  const int32_t* lengths;
+  T* dg;
+  int64_t L;
+  int H, n_tiles, h_blocks;
+};
+template <typename T>
+__device__ __forceinline__ bool is_reset(const T* g, float fixed) { return load_elem(g) + fixed < kZeroLog; }
+
+template <typename T>
+__global__ __launch_bounds__(256) void lin_gate_tiles_kernel(GateArgs<T> p) {
   __shared__ double sh[16][kGateHeads];
-  const int h = (blockIdx.x % h_blocks) * kGateHeads + threadIdx.x % kGateHeads;
-  const int64_t rest = blockIdx.x / h_blocks;
-  const int tile = int(rest % n_tiles);
-  const int64_t bi = rest / n_tiles;
+  __shared__ int first[kGateHeads];  // the tile's first reset of each head
+  const int hl = threadIdx.x % kGateHeads;
+  const int h = (blockIdx.x % p.h_blocks) * kGateHeads + hl;
+  const int64_t rest = blockIdx.x / p.h_blocks;
+  const int tile = int(rest % p.n_tiles);
+  const int64_t bi = rest / p.n_tiles;
   const int s = threadIdx.x / kGateHeads;
-  double d = 0.0;
+  const int64_t n = live_length(p.lengths, bi, p.L);
+  const float fixed = p.A && h < p.H ? p.A[h] : 0.f;
+  if (s == 0) first[hl] = kGateTile;
+  __syncthreads();
+  double d[kGateTile / 16];
+#pragma unroll
   for (int i = 0; i < kGateTile / 16; i++) {
     const int64_t t = int64_t(tile) * kGateTile + i * 16 + s;
-    if (t < L && h < H) {
-      const int64_t at = (bi * L + t) * H + h;
-      d += double(a[at]) - double(c[at]);
+    d[i] = 0.0;
+    if (t < n && h < p.H) {  // the dots behind the length are zero
+      const int64_t at = (bi * p.L + t) * p.H + h;
+      d[i] = double(p.a[at]) - double(p.c[at]);
+      if (is_reset(p.g + at, fixed)) atomicMin(&first[hl], i * 16 + s);
     }
   }
-  sh[s][threadIdx.x % kGateHeads] = d;
   __syncthreads();
-  if (s == 0 && h < H) {
+  const int stop = first[hl];
+  double own = 0.0;
+#pragma unroll
+  for (int i = 0; i < kGateTile / 16; i++)
+    if (i * 16 + s < stop) own += d[i];
+  sh[s][hl] = own;
+  __syncthreads();
+  if (s == 0 && h < p.H) {
     double tot = 0.0;
-    for (int i = 0; i < 16; i++) tot += sh[i][threadIdx.x];
-    sums[(bi * n_tiles + tile) * H + h] = tot;
+    for (int i = 0; i < 16; i++) tot += sh[i][hl];
+    const int64_t at = (bi * p.n_tiles + tile) * p.H + h;
+    p.sums[at] = tot;
+    p.resets[at] = stop < kGateTile;
   }
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void lin_gate_kernel(const Dot<T>* __restrict__ a, const Dot<T>* __restrict__ c,
-                                                       const double* __restrict__ sums, const float* __restrict__ end,
-                                                       const int32_t* __restrict__ lengths, T* __restrict__ dg,
-                                                       int64_t L, int H, int n_tiles, int h_blocks) {
-  __shared__ double sh[16][kGateHeads];
+__global__ __launch_bounds__(256) void lin_gate_kernel(GateArgs<T> p) {
+  __shared__ double sh[16][kGateHeads];     // sums of 16 tokens up to their first reset
   __shared__ double after[16][kGateHeads];
+  __shared__ int cut[16][kGateHeads];       // whether the 16 tokens have a reset
+  __shared__ int last[kGateHeads];          // the first later tile with a reset: its sum is the last to count
   const int hl = threadIdx.x % kGateHeads;
-  const int h = (blockIdx.x % h_blocks) * kGateHeads + hl;
-  const int64_t rest = blockIdx.x / h_blocks;
-  const int tile = int(rest % n_tiles);
-  const int64_t bi = rest / n_tiles;
+  const int h = (blockIdx.x % p.h_blocks) * kGateHeads + hl;
+  const int64_t rest = blockIdx.x / p.h_blocks;
+  const int tile = int(rest % p.n_tiles);
+  const int64_t bi = rest / p.n_tiles;
   const int s = threadIdx.x / kGateHeads;  // 16 consecutive tokens of the tile
-  const bool ok = h < H;
+  const bool ok = h < p.H;
   const int64_t t0 = int64_t(tile) * kGateTile + s * 16;
+  const int64_t n = live_length(p.lengths, bi, p.L);
+  const float fixed = p.A && ok ? p.A[h] : 0.f;
+  if (s == 0) last[hl] = p.n_tiles;
   double d[16], own = 0.0, later = 0.0;
+  uint32_t reset = 0;
 #pragma unroll
   for (int i = 0; i < 16; i++) {
-    const int64_t at = (bi * L + t0 + i) * H + h;
-    d[i] = ok && t0 + i < L ? double(a[at]) - double(c[at]) : 0.0;
-    own += d[i];
+    d[i] = 0.0;
+    if (ok && t0 + i < n) {
+      const int64_t at = (bi * p.L + t0 + i) * p.H + h;
+      d[i] = double(p.a[at]) - double(p.c[at]);
+      reset |= uint32_t(is_reset(p.g + at, fixed)) << i;
+    }
   }
-  for (int k = tile + 1 + s; k < n_tiles; k += 16)
-    if (ok) later += sums[(bi * n_tiles + k) * H + h];
+#pragma unroll
+  for (int i = 0; i < 16; i++)
+    if (!(reset & ((2u << i) - 1))) own += d[i];
   sh[s][hl] = own;
+  cut[s][hl] = reset != 0;
+  __syncthreads();
+  const int64_t col = bi * p.n_tiles * p.H + h;  // of sums and resets, H apart
+  if (ok)
+    for (int k = tile + 1 + s; k < p.n_tiles; k += 16)
+      if (p.resets[col + int64_t(k) * p.H]) {
+        atomicMin(&last[hl], k);
+        break;
+      }
+  __syncthreads();
+  const int stop = last[hl];
+  for (int k = tile + 1 + s; k < p.n_tiles && k <= stop; k += 16)
+    if (ok) later += p.sums[col + int64_t(k) * p.H];
   after[s][hl] = later;
   __syncthreads();
-  double run = ok && end ? double(end[bi * H + h]) : 0.0;
-  for (int i = 0; i < 16; i++) run += after[i][hl];
-  for (int i = s + 1; i < 16; i++) run += sh[i][hl];
-  const int64_t n = live_length(lengths, bi, L);
+  // what comes after this thread's tokens, up to the first reset
+  double run = 0.0;
+  bool open = true;
+  for (int i = s + 1; i < 16; i++) {
+    if (open) run += sh[i][hl];
+    open = open && !cut[i][hl];
+  }
+  if (open) {
+    for (int i = 0; i < 16; i++) run += after[i][hl];
+    if (ok && p.end && stop == p.n_tiles) run += double(p.end[bi * p.H + h]);
+  }
 #pragma unroll
   for (int i = 15; i >= 0; i--) {
-    run += d[i];
     const int64_t t = t0 + i;
-    if (ok && t < L) store_elem(dg + (bi * L + t) * H + h, t < n ? float(run) : 0.f);
+    run = reset >> i & 1 ? 0.0 : run + d[i];
+    if (ok && t < p.L) store_elem(p.dg + (bi * p.L + t) * p.H + h, t < n ? float(run) : 0.f);
   }
 }
 
@@ -1496,7 +1560,7 @@ Sweep common(const LinAttnArgs& a, bool backward) {
 // Bytes from the workspace's start of its parts.
 struct Work {
   size_t seg_f, dec_f, seg_r, dec_r;  // segment states and decays, forwards and (backward) in reversed time
-  size_t dot_q, dot_k, end, sums, dq, dk, total;
+  size_t dot_q, dot_k, end, sums, resets, dq, dk, total;
   int n_tiles;
 };
 Work plan_work(const LinAttnArgs& a, bool backward) {
@@ -1519,6 +1583,7 @@ Work plan_work(const LinAttnArgs& a, bool backward) {
     w.dot_k = take(rows * (a.dtype == 0 ? sizeof(Dot<float>) : sizeof(Dot<bf16_bits>)));
     w.end = take(heads * 4);
     w.sums = take(heads * w.n_tiles * 8);
+    w.resets = take(heads * w.n_tiles);
     if (a.G != a.H) {
       w.dq = take(rows * a.Dk * 4);
       w.dk = take(rows * a.Dk * 4);
@@ -1612,15 +1677,16 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
   }
   if (gate) {
     const int h_blocks = int(ceil_div(a.H, kGateHeads));
-    const Dot<T>* dots_q = reinterpret_cast<const Dot<T>*>(ws + w.dot_q);
-    const Dot<T>* dots_k = reinterpret_cast<const Dot<T>*>(ws + w.dot_k);
-    double* sums = reinterpret_cast<double*>(ws + w.sums);
+    GateArgs<T> p{};
+    p.a = reinterpret_cast<const Dot<T>*>(ws + w.dot_q); p.c = reinterpret_cast<const Dot<T>*>(ws + w.dot_k);
+    p.sums = reinterpret_cast<double*>(ws + w.sums); p.resets = reinterpret_cast<uint8_t*>(ws + w.resets);
+    p.end = end;
+    p.g = static_cast<const T*>(a.g); p.A = a.A; p.lengths = a.lengths; p.dg = static_cast<T*>(a.dg);
+    p.L = a.L; p.H = int(a.H); p.n_tiles = w.n_tiles; p.h_blocks = h_blocks;
     const int64_t blocks = a.b * w.n_tiles * h_blocks;
-    err = launch_kind(kKindLinGate, lin_gate_tiles_kernel<Dot<T>>, blocks, 256, a.stream, dots_q, dots_k, sums, a.L, int(a.H),
-                      w.n_tiles, h_blocks);
+    err = launch_kind(kKindLinGate, lin_gate_tiles_kernel<T>, blocks, 256, a.stream, p);
     if (err != hipSuccess) return err;
-    err = launch_kind(kKindLinGate, lin_gate_kernel<T>, blocks, 256, a.stream, dots_q, dots_k, sums, end, a.lengths,
-                      static_cast<T*>(a.dg), a.L, int(a.H), w.n_tiles, h_blocks);
+    err = launch_kind(kKindLinGate, lin_gate_kernel<T>, blocks, 256, a.stream, p);
   }
   return err;
 }
