@@ -54,7 +54,7 @@ struct Sweep {
   int gd;
   void* dots;              // Dot<T>
   const float* dstate;     // [b, H, VD, KD] (transposed); dstate_dot[b, H] = its product with the last state
-  float* dstate_dot;
+  void* dstate_dot;        // Dot<T>
   bool exact;              // a sweep whose last state can be asked for: its products keep all bits of a float, asked for or not
   bool reverse;            // from the last token to the first
   int64_t b, L;
@@ -810,7 +810,8 @@ struct SweepLds {
   __attribute__((aligned(16))) T P[2][kTwo ? 2 : 1][kC * ldp];
   Decays<kC> d[4];  // written two chunks ahead
   Dot<T> dot_part[2][DOTS ? 16 : 1][kC];
-  float diag[2][DOTS ? kC : 1], red[4];
+  float diag[2][DOTS ? kC : 1];
+  Dot<T> red[4];
 };
 
 template <typename T, int KDP, int VDP, bool DOTS, bool VEC>
@@ -1167,18 +1168,18 @@ __device__ __forceinline__ void sweep(const Sweep& p, SweepLds<T, KDP, VDP, DOTS
   if (DOTS && p.dstate_dot) {
     typename Y::State D;
     Y::load(D, p.dstate + w.bh * p.KD * p.VD, true, p.KD, p.VD);
-    float s = 0.f;
+    Dot<T> s = 0;
 #pragma unroll
     for (int m = 0; m < Y::MT; m++)
 #pragma unroll
       for (int n = 0; n < Y::NT; n++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) s = fmaf(S[m][n][r], D[m][n][r], s);
+        for (int r = 0; r < 4; r++) s = fma(Dot<T>(S[m][n][r]), Dot<T>(D[m][n][r]), s);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
     if (l == 0) sh.red[wv] = s;
     __syncthreads();
-    if (threadIdx.x == 0) p.dstate_dot[w.bh] = (sh.red[0] + sh.red[1]) + (sh.red[2] + sh.red[3]);
+    if (threadIdx.x == 0) static_cast<Dot<T>*>(p.dstate_dot)[w.bh] = (sh.red[0] + sh.red[1]) + (sh.red[2] + sh.red[3]);
   }
   if (p.last) {
     const float f = p.final_decay && w.n > 0 ? exp2_fast(log_decay<T>(p, w.bi, 0, w.h) * kLog2e) : 1.f;
@@ -1234,7 +1235,7 @@ struct GateArgs {
   const Dot<T>* c;
   double* sums;      // [b, n_tiles, H]
   uint8_t* resets;   // [b, n_tiles, H]: whether the tile has a reset
-  const float* end;  // [b, H], nullable
+  const Dot<T>* end; // [b, H], nullable
   const T* g;
   const float* A;    // nullable
   const int32_t* lengths;
@@ -1581,7 +1582,7 @@ Work plan_work(const LinAttnArgs& a, bool backward) {
     w.dec_r = take(segs * 4);
     w.dot_q = take(rows * (a.dtype == 0 ? sizeof(Dot<float>) : sizeof(Dot<bf16_bits>)));
     w.dot_k = take(rows * (a.dtype == 0 ? sizeof(Dot<float>) : sizeof(Dot<bf16_bits>)));
-    w.end = take(heads * 4);
+    w.end = take(heads * sizeof(double));
     w.sums = take(heads * w.n_tiles * 8);
     w.resets = take(heads * w.n_tiles);
     if (a.G != a.H) {
@@ -1616,7 +1617,7 @@ hipError_t bwd_impl(const LinAttnArgs& a, char* ws) {
   const Work w = plan_work(a, true);
   const int share = int(a.H / a.G);
   const bool gate = a.dg != nullptr;
-  float* end = gate && a.dlast ? reinterpret_cast<float*>(ws + w.end) : nullptr;
+  Dot<T>* end = gate && a.dlast ? reinterpret_cast<Dot<T>*>(ws + w.end) : nullptr;
   float* seg_f = reinterpret_cast<float*>(ws + w.seg_f);
   float* dec_f = reinterpret_cast<float*>(ws + w.dec_f);
   float* seg_r = reinterpret_cast<float*>(ws + w.seg_r);

@@ -69,3 +69,22 @@ def test_resets_by_both_decays_and_behind_the_length(dtype):
     d = bwd(x)
     torch.cuda.synchronize()
     assert torch.equal(d["dg"], d0["dg"])
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (33, 70)])
+def test_the_last_states_part_of_float_gates(Dk, Dv):
+    """Without decays, keys and dy every dg is <d_last_state, initial_state>, a sum of up to 16384 products that is part
+    of the dg of every token: the products are exact in float64 and the sum is off by 2^-52 of its terms' sizes, so
+    dg is off by its own rounding."""
+    import torch
+
+    x = make(b=2, L=70, H=3, G=3, Dk=Dk, Dv=Dv, dtype="f32", seed=Dk)
+    for k in ("k", "dy", "g"):
+        x[k].zero_()
+    say(f"linattn end of the gates Dk={Dk} Dv={Dv}")
+    d = bwd(x)
+    torch.cuda.synchronize()
+    terms = x["d_last_state"].double() * x["initial_state"].double()
+    want = terms.sum((-1, -2))[:, None].expand(2, 70, 3)
+    tol = want.abs() * 2.0 ** -24 + terms.abs().sum((-1, -2))[:, None] * Dk * Dv * 2.0 ** -52
+    assert ((d["dg"].double() - want).abs() <= tol * 1.01).all(), ((d["dg"].double() - want).abs() / tol).max()
