@@ -688,7 +688,7 @@ def _linattn_sizes(torch, q, k, v, g, A, lengths, tokens):
 
 
 def _scale(scale, Dk):
-    return Dk ** -0.5 if scale is None else float(scale)
+    return (Dk or 1) ** -0.5 if scale is None else float(scale)  # a width of zero is refused by the library
 
 
 def ssm_linattn_fwd(q, k, v, g=None, A=None, scale=None, lengths=None, initial_state=None, y=None, last_state=None,
@@ -792,13 +792,20 @@ def ssm_layernorm_workspace(rows, H, W, dtype="bf16"):
 
 
 def _norm_sizes(torch, x, par):
-    """(parameter shape, rows, H, W, code, device) of a layer norm of x with parameters of that shape
-    ([W], or [H, W] for x [..., H, W])."""
+    """(parameter shape, rows, H, W, code, device) of a layer norm of x with parameters like ``par``: a tensor [W], or
+    [H, W] for x [..., H, W]; a number of heads H; or None for [W]."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be a [..., W] tensor")
     if x.device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU device, got {x.device}")
-    par = tuple(x.shape[-1:]) if par is None else tuple(par)
+    if isinstance(par, int):
+        par = (par, *x.shape[-1:])
+    elif par is not None:
+        if not isinstance(par, torch.Tensor):
+            raise TypeError("weight and bias must be a torch.Tensor each")
+        par = tuple(par.shape)
+    else:
+        par = tuple(x.shape[-1:])
     if len(par) not in (1, 2) or len(par) > x.dim() or par != tuple(x.shape[x.dim() - len(par):]):
         raise ValueError(f"parameters of shape {par} do not fit x of shape {tuple(x.shape)}: [W] or [H, W] of its last axes")
     H, W = (1, par[0]) if len(par) == 1 else par
@@ -818,8 +825,7 @@ def ssm_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None):
     import torch
 
     lib = load_library()
-    one = weight if weight is not None else bias
-    par, rows, H, W, code, device = _norm_sizes(torch, x, None if one is None else one.shape)
+    par, rows, H, W, code, device = _norm_sizes(torch, x, weight if weight is not None else bias)
     _check(torch, "weight", weight, par, torch.float32, device, optional=True)
     _check(torch, "bias", bias, par, torch.float32, device, optional=True)
     if y is None:
@@ -844,8 +850,7 @@ def ssm_layernorm_bwd(x, dy, mean, rstd, weight=None, heads=None, param_grads=Tr
     import torch
 
     lib = load_library()
-    shape = weight.shape if weight is not None else None if heads is None else (int(heads), *x.shape[-1:])
-    par, rows, H, W, code, device = _norm_sizes(torch, x, shape)
+    par, rows, H, W, code, device = _norm_sizes(torch, x, weight if weight is not None else None if heads is None else int(heads))
     f32 = torch.float32
     _check(torch, "dy", dy, x.shape, x.dtype, device)
     _check(torch, "mean", mean, x.shape[:-1], f32, device)
