@@ -130,12 +130,13 @@ def conv_update_bytes(b, E, K, s, bias=True):
     return 2 * b * E * K * s + 2 * b * E * s + E * K * 4 + (E * 4 if bias else 0)
 
 
-HASH_EXCLUDES = ("ssm_api.hip",)  # the C ABI's argument checks: no kernel, no launch shape
+# what no kernel of the scans is built from: the C ABI's argument checks, the event timing, linear attention and layer norm
+HASH_EXCLUDES = ("ssm_api.hip", "ssm_profile.hip", "ssm_linattn.hip", "ssm_linattn.h", "ssm_layernorm.hip", "ssm_layernorm.h")
 
 
 def source_hash():
-    """sha256[:16] of every library source that builds a kernel or plans a launch (all of csrc/ but the argument
-    checks): a profile taken on other sources is stale."""
+    """sha256[:16] of every source that builds a kernel of the scans or the convolution, or plans its launch (all of
+    csrc/ but HASH_EXCLUDES): a profile taken on other sources is stale."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "selective_state_space_35_amd", "csrc")
     for f in sorted(os.listdir(csrc)):
@@ -722,7 +723,7 @@ def summarize(run_root, prefix, title, commands, profiled_hash=None):
     head = [f"# {title}", "# commands (from the repository root, on one MI355X; each --pmc set in a run of its own):"]
     head += [f"#   {c}" for c in commands]
     head += [f"# kernel source hash (bench.source_hash(): sha256[:16] of selective_state_space_35_amd/csrc/*.hip, *.h "
-             f"but ssm_api.hip): {sh}", "#"]
+             f"but {', '.join(HASH_EXCLUDES)}): {sh}", "#"]
     sub = lambda n: os.path.join(run_root, n)
     # kernel trace: per launch shape
     if os.path.isdir(sub("trace")):

@@ -9,6 +9,8 @@
 
 #include "ssm.h"
 #include "ssm_internal.h"
+#include "ssm_layernorm.h"
+#include "ssm_linattn.h"
 
 namespace {
 

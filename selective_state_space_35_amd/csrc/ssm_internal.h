@@ -142,61 +142,6 @@ int64_t ssd_head_dim();     // channels per head (P)
 int64_t ssd_max_channels(); // largest H * P the chunk kernels address with 32-bit offsets
 hipError_t launch_ssd(const SsdArgs& a);
 
-// Linear attention with a decay for each head (ssm_linattn.hip).
-struct LinAttnArgs {
-  const void* q;           // [b, L, G, Dk] (token form: [b, G, Dk])
-  const void* k;           // as q
-  const void* v;           // [b, L, H, Dv]
-  const void* g;           // [b, L, H], nullable
-  const float* A;          // [H], nullable
-  const int32_t* lengths;  // [b], nullable
-  float scale;
-  const float* h0;         // [b, H, Dk, Dv], nullable
-  void* y;                 // [b, L, H, Dv]
-  float* last;             // [b, H, Dk, Dv], nullable; token form: the state, in place
-  // backward
-  const void* dy;
-  const float* dlast;      // nullable
-  void* dq;
-  void* dk;
-  void* dv;
-  void* dg;                // null when g is
-  float* dh0;              // nullable
-  int64_t b, L, H, G, Dk, Dv;
-  int dtype;
-  hipStream_t stream;
-};
-int64_t linattn_max_dim();    // largest Dk and Dv
-int64_t linattn_max_heads();  // largest H: a chunk's rows are addressed with 32-bit offsets
-// Workspace of the forward or the backward of these sizes (nullable arguments taken as given).
-size_t linattn_workspace_bytes(const LinAttnArgs& a, bool backward);
-hipError_t launch_linattn_fwd(const LinAttnArgs& a, void* workspace);
-hipError_t launch_linattn_bwd(const LinAttnArgs& a, void* workspace);
-hipError_t launch_linattn_update(const LinAttnArgs& a);
-
-// Layer norm over rows of W elements (ssm_layernorm.hip).
-struct LayerNormArgs {
-  const void* x;        // [rows, H, W]
-  const float* weight;  // [H, W], nullable
-  const float* bias;    // [H, W], nullable
-  float eps;
-  void* y;
-  float* mean;          // [rows, H]: written by the forward (nullable), read by the backward
-  float* rstd;          // as mean
-  // backward
-  const void* dy;
-  void* dx;
-  float* dweight;       // [H, W]; both parameter gradients or neither
-  float* dbias;
-  int64_t rows, H, W;
-  int dtype;
-  hipStream_t stream;
-};
-int64_t layernorm_max_width();
-size_t layernorm_workspace_bytes(const LayerNormArgs& a);  // of the backward, for tensors of any alignment
-hipError_t launch_layernorm_fwd(const LayerNormArgs& a);
-hipError_t launch_layernorm_bwd(const LayerNormArgs& a, void* workspace);
-
 // The single-pass scan (ssm_fused.hip): a workgroup walks the whole sequence for a
 // slice of channels, in blocks of W chunks of 8 steps joined through LDS.
 constexpr int kFusedMaxWaves = 16;

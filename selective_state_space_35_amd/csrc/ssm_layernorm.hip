@@ -18,7 +18,7 @@
 #include <algorithm>
 
 #include "ssm_device.h"
-#include "ssm_internal.h"
+#include "ssm_layernorm.h"
 #include "ssm_profile.h"
 
 namespace ssm {

@@ -24,7 +24,7 @@
 
 #include "ssm_chain.h"
 #include "ssm_device.h"
-#include "ssm_internal.h"
+#include "ssm_linattn.h"
 #include "ssm_profile.h"
 
 namespace ssm {
