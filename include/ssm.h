@@ -431,14 +431,19 @@ SSM_API int ssm_conv_update(void* conv_state, const void* v, const float* q, con
  *   workspace, workspace_bytes        at least ssm_linattn_workspace() bytes, 256-byte aligned, used by
  *                                     this call's work until it has run; NULL: from the stream-ordered
  *                                     allocator on `stream`
- * 1 <= Dk, Dv <= 128 (else SSM_ERR_DIM); G divides H; H <= 65535; b H <= 2^21.  bf16: matrix products
- * take bf16 operands and accumulate in fp32; what is not given in bf16 (the mixing weights, the state) is
- * taken in two bf16 parts, high and low (written into a state that can be an output: in three), so that
- * an output is right to its own rounding; f32: fp32 matrix products.  NULL outputs change no bit of the others.  Log decays are usually negative; one below -10^4, minus infinity
- * included, counts as -10^4: a factor of zero, which drops the state (where a new
- * document starts; zero times a state that is not finite is NaN).  What is not finite reaches the
- * outputs that read it and no others; a value of v makes its column of y from its token on, and of the
- * state, NaN.
+ * 1 <= Dk, Dv <= 128; G divides H; H <= 65535; b H <= 2^21; L <= 2^31 - 4097; b (L / 256 + 1) (H /
+ * 16 + 1) < 2^24, divisions rounded down (the grid of the gates' gradient; asked of every call,
+ * also of those that do not launch it); else SSM_ERR_DIM.
+ * bf16: matrix products take bf16 operands and accumulate in fp32; what is not given in bf16 (the
+ * mixing weights, the state) is taken in two bf16 parts, high and low (written into a state that
+ * can be an output: in three), so that an output is right to its own rounding.  f32: fp32 matrix
+ * products.  NULL outputs change no bit of the others.
+ * Log decays are usually negative; positive ones may add up to 88 over 64 tokens (beyond, their
+ * factor is infinite in float).  One below -10^4, minus infinity included, counts as -10^4: a
+ * factor of zero, which drops the state (where a new document starts; zero times a state that is
+ * not finite is NaN).
+ * What is not finite reaches the outputs that read it and no others; a value of v makes its column
+ * of y from its token on, and of the state, NaN.
  * L == 0 copies initial_state (or zeros) to last_state; b == 0 or H == 0 is a no-op.
  */
 SSM_API int ssm_linattn_fwd(const void* q, const void* k, const void* v, const void* g, const float* A,
@@ -457,10 +462,11 @@ SSM_API int ssm_linattn_fwd(const void* q, const void* k, const void* v, const v
  *     d_initial_state [b, H, Dk, Dv] float (nullable; also when initial_state is NULL)
  * Nothing of the forward is kept: the states are recomputed.  Results are
  * deterministic.  Workspace as in ssm_linattn_fwd, of the backward's size.
- * As there, what is not finite reaches the outputs that read it and no others, but for dg, a sum over the tokens
- * from its own on: a k or v that is not finite makes the dg of the tokens before it NaN too, back to the last
- * reset.  A reset is a token whose log decay is below -104 (its factor is zero in float): its dg is zero, and nothing
- * of the tokens from it on comes into the dg of those before.
+ * As there, what is not finite reaches the outputs that read it and no others, but for dg, a sum
+ * over the tokens from its own on: a k or v that is not finite makes the dg of the tokens before it
+ * NaN too, back to the last reset.  A reset is a token whose log decay is below -104 (its factor is
+ * zero in float): its dg is zero, and nothing of the tokens from it on comes into the dg of those
+ * before.
  */
 SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const void* g, const float* A,
                             const int32_t* lengths, float scale, const float* initial_state, const void* dy,
@@ -495,7 +501,7 @@ SSM_API int64_t ssm_linattn_workspace(int64_t b, int64_t L, int64_t H, int64_t G
  *   x, y          [rows, H, W]  dtype
  *   weight, bias  [H, W]        float  (nullable: one, zero)
  *   mean, rstd    [rows, H]     float  (nullable; what the backward needs)
- * 1 <= W <= 16384; H <= 2^21; H W < 2^30 - 64; eps >= 0 (else SSM_ERR_DIM).
+ * 1 <= W <= 16384; H <= 2^21; H W < 2^30 - 64; rows H < 2^31; eps >= 0 (else SSM_ERR_DIM).
  */
 SSM_API int ssm_layernorm_fwd(const void* x, const float* weight, const float* bias, float eps, void* y, float* mean,
                               float* rstd, int64_t rows, int64_t H, int64_t W, int dtype, void* stream);

@@ -128,3 +128,21 @@ def test_what_is_not_finite_reaches_what_reads_it(size, bad, dtype):
             if name == "dy":
                 same(d["dq"][:, :t], d0["dq"][:, :t], at)
                 same(d["dq"][:, t + 1:], d0["dq"][:, t + 1:], at)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rate,L", [(0.4, 130), (1.2, 64)])
+def test_states_that_grow(rate, L, dtype):
+    """Positive log decays, which add up to some 20 and 60 over a chunk."""
+    import torch
+
+    x = make(b=1, L=L, H=2, G=2, Dk=40, Dv=64, dtype=dtype, seed=33, rate=-rate)
+    assert (x["g"] >= 0).all()
+    what = f"linattn growing {rate} {dtype}"
+    say(what)
+    y, last = fwd(x)
+    d = bwd(x)
+    torch.cuda.synchronize()
+    want, mag = {**ref.forward(x), **ref.backward(x)}, {**ref.forward(x, absolute=True), **ref.backward(x, absolute=True)}
+    for name, t in {"y": y, "last_state": last, **d}.items():
+        ref.within(t, want[name], mag[name], name, x, what)
