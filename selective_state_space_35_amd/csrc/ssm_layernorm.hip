@@ -6,9 +6,13 @@
 //   m = mean(x),  v = mean((x - m)^2),  r = 1 / sqrt(v + eps),  xh = (x - m) r
 //   y = xh w + b
 //   t = dy w,  dx = r (t - mean(t) - xh mean(t xh)),  dw = sum over rows of dy xh,  db = sum of dy
-// Both directions are bound by HBM: every streamed value is read once, held in registers for
-// the two sums of its row (the variance is taken around the mean, in a second pass over the
-// registers), and written once.  A group of threads keeps one head's parameters in registers and
+// Both directions read every streamed value once, hold it for the two sums of its row (the variance is taken around
+// the mean, in a second pass over the registers), and write once; rows of whole 16-byte vectors are bound by HBM up to a
+// width of 8192 (bf16; float 4096 backward, 16384 forward).  Wider rows take 1024 threads of 128 registers each,
+// too few for their backward, which keeps three values a column more: 289 (bf16), 125 (float) and, of odd widths
+// above 2048, 89 registers go through scratch.  TB/s of what has to be moved, at 2^27 elements, forward / backward: 5.1 / 5.4 at
+// 2560 and 5.6 / 2.9 at 8192 in float; 3.7 / 4.6 at 8192 and 2.2 / 0.6 at 16384 in bf16; of odd widths, whose lanes read one
+// element each, 3.8 / 5.1 at 1001 and 3.4 / 1.4 at 5001 in float, 2.5 / 2.4 and 1.7 / 0.7 in bf16.  A group of threads keeps one head's parameters in registers and
 // walks rows, the next row's loads under way while one is summed; without them, a row a group and
 // 1024 workgroups, the backward of 65536 rows of 2560 in bf16 took 338 us, with them 191 us (5.3 TB/s).
 // All sums are float.

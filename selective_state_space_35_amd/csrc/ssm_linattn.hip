@@ -185,7 +185,9 @@ __device__ __forceinline__ void frag_floats(const f32x8& f, float (&x)[8]) {
 }
 
 // ---------------------------------------------------------------------------
-// Waves of a SIMD that the registers are held to.  A sweep's workgroup alone is two.
+// Waves of a SIMD that the registers are held to.  A sweep's workgroup alone is two.  The bound is also an upper one: it
+// keeps a second workgroup off the CU where registers and LDS would allow it (float, widths of up to 64: 91 to 127
+// registers, at most 72 KB).  What a second one gives there is not measured.
 #define SSM_LIN_WAVES(n) __attribute__((amdgpu_waves_per_eu(n, n)))
 constexpr int kSweepWaves = 2;
 template <typename T>
@@ -793,11 +795,12 @@ __global__ __launch_bounds__(kThreads) SSM_LIN_WAVES(state_waves<T>(KDP, VDP)) v
 // and then compute its P, in the other half of P; two barriers a chunk.  One SIMD has a wave of each kind.  The rows of the
 // two chunks after are on their way into registers meanwhile.
 //
-// Measured (bf16): b8 L2048 H24 D64 forward 64 us (HBM floor 43 us; all eight waves doing all the work in turn 84 us in
-// segments, 105 us uncut); a chunk is 3700 cycles, of which the LDS is busy 1800 and each SIMD's VALU 1600, partly
-// one after the other.  b1 L65536 H40 D128: 990 us (floor 562 us) of which 300 us are the pass over k and v that the cut needs.
-// Backward, three sweeps: b8 L2048 H24 D64 235 us, b4 L4096 H32 G8 D128 640 us (floors 74, 113 us), bound by VALU and
-// MFMA issue of the sweeps with dots (8100 cycles a chunk at D128: 760 VALU and 150 MFMA instructions a state wave).
+// Measured (bf16): b8 L2048 H24 D64 forward 63 to 66 us (HBM floor 38 us; before the operands were split 59 us, and then
+// all eight waves doing all the work in turn 84 us in segments, 105 us uncut); a chunk is 4700 cycles, of which the
+// LDS is busy 2100 and each SIMD issues vector instructions in 2200, partly one after the other.  b1 L65536 H40 D128: 1030 us
+// (floor 498 us) of which 300 us are the pass over k and v that the cut needs.  Backward, three sweeps: b8 L2048 H24
+// D64 240 us, b4 L4096 H32 G8 D128 654 us (floors 66, 100 us), bound by the issue of VALU and MFMA instructions (a workgroup's
+// eight waves have 4500 a chunk at D128, 700 of them MFMA; 2400 at D64).
 // ---------------------------------------------------------------------------
 template <typename T, int KDP, int VDP, bool DOTS>
 struct SweepLds {
@@ -1223,7 +1226,7 @@ __global__ __launch_bounds__(2 * kThreads) SSM_LIN_WAVES(kSweepWaves) void lin_b
 // zero, and so is the sum up to it: the sum starts again there, so that nothing of a document comes into the one before
 // it.  Tiles of kGateTile tokens: first each tile's sum up to its first reset (and whether it has one), then each tile adds
 // the later ones' up to the first reset to its own running sum (double: the terms cancel over the sequence).
-// b8 L2048 H24: 9 and 7 us, by the latency of a row's 64-byte pieces.
+// b8 L2048 H24: 10 and 9 us, by the latency of a row's 64-byte pieces.
 constexpr int kGateTile = 256;
 constexpr int kGateHeads = 16;  // heads of a workgroup: 16 consecutive floats of a row, times 16 tokens
 // exp of a log decay below this is zero in float, denormal numbers included (2^-150)
@@ -1520,7 +1523,8 @@ hipError_t run_states(const Sweep& p, const Sweep& q, int sweeps) {
 }
 
 // The cut of a sequence: as many segments as give every CU a workgroup, and no second generation of them
-// (a cut costs another reading of keys and values); of at least kMinSeg chunks.  Measured, bf16, b8 L2048 H24 D64:
+// (a cut costs another reading of keys and values), so from 129 heads of batch rows on (43 in the backward) none; of at
+// least kMinSeg chunks.  Measured, bf16, b8 L2048 H24 D64:
 // 66 us in one piece, 96 us in two; b2 L8192 H32 D128: 422, 345, 246, 208 and 257 us in 1 to 5.
 constexpr int kMinSeg = 4;
 constexpr int64_t kAtOnce = 256;
