@@ -17,12 +17,15 @@
  *   ssm_linattn_fwd, ssm_linattn_bwd, ssm_linattn_update
  *                                     linear attention with a decay for each head: whole
  *                                     sequences, the gradients, one token
+ *   ssm_deltarule_fwd, ssm_deltarule_bwd, ssm_deltarule_update
+ *                                     the gated delta rule: whole sequences, the gradients, one
+ *                                     token
  *   ssm_layernorm_fwd, ssm_layernorm_bwd
  *                                     layer norm over the model's width or each head's
  *                                     channels, and its gradients
  *   ssm_conv_fwd, ssm_conv_update     the causal depthwise convolution + SiLU before
  *                                     the scan, and its token step
- *   ssm_linattn_workspace, ssm_layernorm_workspace,
+ *   ssm_linattn_workspace, ssm_deltarule_workspace, ssm_layernorm_workspace,
  *   ssm_scan_plan, ssm_profile_*, ssm_status_string, ssm_last_hip_error, ssm_version
  *                                     host-side queries
  *
@@ -46,10 +49,10 @@
  * backward and the per-head scan take a temporary workspace from the
  * stream-ordered allocator (hipMallocAsync / hipFreeAsync on `stream`), so
  * concurrent calls on different streams do not share memory.
- * ssm_state_update, ssm_conv_update, ssm_linattn_update and
+ * ssm_state_update, ssm_conv_update, ssm_linattn_update, ssm_deltarule_update and
  * ssm_layernorm_fwd take none and issue no memset: a caller can capture them
- * in a HIP graph.  ssm_linattn_fwd, ssm_linattn_bwd and ssm_layernorm_bwd take
- * a workspace of the caller's where one is given (then they allocate nothing
+ * in a HIP graph.  ssm_linattn_fwd, ssm_linattn_bwd, ssm_deltarule_fwd,
+ * ssm_deltarule_bwd and ssm_layernorm_bwd take a workspace of the caller's where one is given (then they allocate nothing
  * and can be captured too), else from the stream-ordered allocator.
  *
  * Data types.  `dtype` (ssm_dtype) is the element type of the streamed
@@ -59,7 +62,7 @@
  *
  * Sizes.  b (batch), L (sequence length), E (expanded channels) and
  * N (state size per channel).  Supported: 1 <= N <= 16 (ssm_ssd_fwd: N a
- * multiple of 16 up to 128); 0 <= b, L, E <= 2^48.  Linear attention: head widths
+ * multiple of 16 up to 128); 0 <= b, L, E <= 2^48.  Linear attention and the delta rule: head widths
  * Dk and Dv of 1..128, H a multiple of G.  b == 0 or E == 0 is a no-op.
  * L == 0 writes a zero last_state (or the incoming state, where one is given).
  *
@@ -493,6 +496,76 @@ SSM_API int64_t ssm_linattn_workspace(int64_t b, int64_t L, int64_t H, int64_t G
                                       int backward);
 
 /*
+ * The gated delta rule: linear attention whose write first takes out what the
+ * state already answers for the key.  For every batch row b and head h,
+ * starting from S = initial_state (or zero), a [Dk, Dv] state:
+ *   r        = exp(A[h] + g[b,t,h])
+ *   u        = beta[b,t,h] (v[b,t,h] - r S^T k[b,t,h'])
+ *   S        = r S + k[b,t,h'] u^T
+ *   y[b,t,h] = scale * S^T q[b,t,h']            (read after the write)
+ *   last_state[b,h] = S after the row's last token
+ * with h' = h / (H / G), as in ssm_linattn_fwd.  A write scales the state along k by 1 - beta |k|^2, so keys
+ * are to be of length one (ssm_blocknorm_fwd norms the channels of each head) and beta of 0..2, else the states grow
+ * without bound.  The whole sequence is computed in chunks of matrix products.
+ *
+ * Arguments: q, k, v, y, g, A, lengths, scale, initial_state, last_state and the workspace (of
+ * ssm_deltarule_workspace() bytes) as ssm_linattn_fwd's;
+ *   beta           [b, L, H]          dtype   strength of each token's write (nullable: one)
+ * 1 <= Dk, Dv <= 128; G divides H; H <= 65535; b H <= 2^21; b H (L / C + 1) < 2^23 with C = 64 (bf16) or 32 (f32),
+ * the division rounded down; else SSM_ERR_DIM.
+ * bf16: matrix products take bf16 operands and accumulate in fp32; what is not given in bf16 is taken in several bf16
+ * parts, three (all 24 bits of a float) in what becomes a state, two in what becomes an output alone.  f32: fp32 matrix
+ * products.  NULL outputs change no bit of the others.
+ * Log decays, resets (a log decay below -10^4, minus infinity included) and positive ones as in ssm_linattn_fwd.
+ * What is not finite reaches the outputs that read it and no others: a value of v makes its column of y from its token
+ * on, and of the state, NaN; one of k, beta or g every column; one of q its own row of y.
+ * L == 0 copies initial_state (or zeros) to last_state; b == 0 or H == 0 is a no-op.
+ */
+SSM_API int ssm_deltarule_fwd(const void* q, const void* k, const void* v, const void* beta, const void* g,
+                              const float* A, const int32_t* lengths, float scale, const float* initial_state, void* y,
+                              float* last_state, int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
+                              int dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of  sum dy * y + sum d_last_state * last_state  with respect to
+ * the inputs of ssm_deltarule_fwd (A is fixed: it has none).
+ *   inputs   the forward's; dy [b, L, H, Dv] dtype; d_last_state [b, H, Dk, Dv] float (nullable: zero)
+ *   outputs  (fully overwritten; zero rows behind a row's length)
+ *     dq, dk [b, L, G, Dk] dtype   (sums over a group's heads)
+ *     dv     [b, L, H, Dv] dtype
+ *     dbeta  [b, L, H]     dtype   (written when beta is given and dbeta is not NULL)
+ *     dg     [b, L, H]     dtype   (written when g is given and dg is not NULL)
+ *     d_initial_state [b, H, Dk, Dv] float (nullable; also when initial_state is NULL)
+ * Nothing of the forward is kept: the states are recomputed, and kept in the workspace for every chunk of 64 tokens
+ * (f32: 32), which so grows with b L H Dk Dv / 64 floats.  Results are deterministic.
+ * dg of a reset (a token whose log decay is below -104) is zero, and nothing of the tokens from it on comes into the dg of
+ * those before.  What is not finite may reach every gradient of the head's tokens.
+ */
+SSM_API int ssm_deltarule_bwd(const void* q, const void* k, const void* v, const void* beta, const void* g,
+                              const float* A, const int32_t* lengths, float scale, const float* initial_state,
+                              const void* dy, const float* d_last_state, void* dq, void* dk, void* dv, void* dbeta,
+                              void* dg, float* d_initial_state, int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk,
+                              int64_t Dv, int dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * One token of ssm_deltarule_fwd on a persistent state (generation):
+ *   state [b, H, Dk, Dv] float, in place;  q, k [b, G, Dk], v, y [b, H, Dv], beta, g [b, H] dtype.
+ * A batch row whose lengths[b] is zero or less takes no step: its state stays as it is and its
+ * row of y is zero.
+ */
+SSM_API int ssm_deltarule_update(float* state, const void* q, const void* k, const void* v, const void* beta,
+                                 const void* g, const float* A, const int32_t* lengths, float scale, void* y, int64_t b,
+                                 int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype, void* stream);
+
+/*
+ * Bytes of workspace that ssm_deltarule_fwd (backward == 0) or ssm_deltarule_bwd
+ * (backward != 0) needs at these sizes, whatever its nullable arguments; a
+ * negative ssm_status for sizes those calls refuse.  Host-only.
+ */
+SSM_API int64_t ssm_deltarule_workspace(int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype,
+                                        int backward);
+
+/*
  * Layer norm over the last axis, for every row i and head h (H = 1: over the
  * model's width; H > 1: over each head's channels, with the head's parameters):
  *   mean = sum_j x[i,h,j] / W,  rstd = 1 / sqrt(sum_j (x[i,h,j] - mean)^2 / W + eps)
@@ -548,7 +621,9 @@ SSM_API int ssm_scan_plan(int64_t b, int64_t L, int64_t E, int64_t N, int dtype,
  * 16 widen_rows (float copies of the bf16 B / C rows of a cut forward),
  * 17 linattn_sweep, 18 linattn_state, 19 linattn_chain, 20 linattn_gate,
  * 21 linattn_reduce, 22 linattn_update, 23 layernorm, 24 layernorm_bwd,
- * 25 layernorm_reduce; names
+ * 25 layernorm_reduce, 26 deltarule_tri, 27 deltarule_sweep, 28 deltarule_grad,
+ * 29 deltarule_reduce, 30 deltarule_update, 31 blocknorm, 32 blocknorm_bwd,
+ * 33 blocknorm_reduce; names
  * from ssm_profile_kind_name().  Off by default; the events add a few
  * microseconds per launch.  Process-wide, thread-safe.
  */

@@ -37,6 +37,11 @@ Functions (same names as the C entry points):
   ``(y, last_state)``: linear attention with a decay for each head over whole
   sequences; ``ssm_linattn_bwd`` its gradients, ``ssm_linattn_update`` its step
   for one token
+* ``ssm_deltarule_fwd(q, k, v, beta=None, g=None, A=None, scale=None,
+  lengths=None, initial_state=None, y=None, last_state=None,
+  return_last_state=True)`` -> ``(y, last_state)``: the gated delta rule over
+  whole sequences; ``ssm_deltarule_bwd`` its gradients,
+  ``ssm_deltarule_update`` its step for one token
 * ``ssm_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None)`` ->
   ``(y, mean, rstd)``: layer norm over the last axis; ``ssm_layernorm_bwd`` its
   gradients
@@ -48,8 +53,8 @@ Functions (same names as the C entry points):
 
 Shapes: u, delta, z, y [b, L, E]; A [E, N] (float32); B, C [b, L, N];
 D, delta_bias [E] (float32); state / last_state [b, E, N] (float32).
-Linear attention: q, k [b, L, G, Dk]; v, y [b, L, H, Dv]; g [b, L, H]; A [H]
-float32; lengths [b] int32; states [b, H, Dk, Dv] float32 (G divides H;
+Linear attention and the delta rule: q, k [b, L, G, Dk]; v, y [b, L, H, Dv];
+beta, g [b, L, H]; A [H] float32; lengths [b] int32; states [b, H, Dk, Dv] float32 (G divides H;
 Dk, Dv <= 128).
 Convolution: v, x [b, L, E]; weight [E, K] float32 (1 <= K <= 8); conv_bias
 [E] float32; convolution state [b, E, K] in the streamed dtype, oldest sample
@@ -62,6 +67,7 @@ import os
 __all__ = [
     "ssm_scan_fwd", "ssm_scan_fwd_from", "ssm_scan_fwd_noalloc", "ssm_scan_bwd", "ssm_ssd_fwd", "ssm_state_update", "ssm_conv_fwd", "ssm_conv_update",
     "ssm_linattn_fwd", "ssm_linattn_bwd", "ssm_linattn_update", "ssm_linattn_workspace",
+    "ssm_deltarule_fwd", "ssm_deltarule_bwd", "ssm_deltarule_update", "ssm_deltarule_workspace",
     "ssm_layernorm_fwd", "ssm_layernorm_bwd", "ssm_layernorm_workspace", "ssm_scan_plan", "ssm_profile_enable", "ssm_profile_read",
     "ssm_status_string", "library_path", "SSMError", "ScanTuning", "SCAN_PATHS",
     "SSM_F32", "SSM_BF16", "load_library",
@@ -158,6 +164,14 @@ def load_library():
     lib.ssm_linattn_update.argtypes = [_vp] * 7 + [_f32, _vp] + [_i64] * 5 + [_int, _vp]
     lib.ssm_linattn_workspace.restype = _i64
     lib.ssm_linattn_workspace.argtypes = [_i64] * 6 + [_int, _int]
+    lib.ssm_deltarule_fwd.restype = _int
+    lib.ssm_deltarule_fwd.argtypes = [_vp] * 7 + [_f32] + [_vp] * 3 + [_i64] * 6 + [_int, _vp, _i64, _vp]
+    lib.ssm_deltarule_bwd.restype = _int
+    lib.ssm_deltarule_bwd.argtypes = [_vp] * 7 + [_f32] + [_vp] * 9 + [_i64] * 6 + [_int, _vp, _i64, _vp]
+    lib.ssm_deltarule_update.restype = _int
+    lib.ssm_deltarule_update.argtypes = [_vp] * 8 + [_f32, _vp] + [_i64] * 5 + [_int, _vp]
+    lib.ssm_deltarule_workspace.restype = _i64
+    lib.ssm_deltarule_workspace.argtypes = [_i64] * 6 + [_int, _int]
     lib.ssm_layernorm_fwd.restype = _int
     lib.ssm_layernorm_fwd.argtypes = [_vp] * 3 + [_f32] + [_vp] * 3 + [_i64] * 3 + [_int, _vp]
     lib.ssm_layernorm_bwd.restype = _int
@@ -202,7 +216,7 @@ def ssm_scan_plan(b, L, E, N, dtype="bf16", tuning=None):
     return _PATH_NAMES[path.value], cl.value, nc.value
 
 
-PROFILE_KINDS = 26
+PROFILE_KINDS = 34
 _SCAN_KINDS = 17  # the kinds of the scans and the convolution, always in the answer
 
 
@@ -214,7 +228,7 @@ def ssm_profile_enable(on=True):
 def ssm_profile_read():
     """Wait for the recorded events; return {kind name: (total ms, launches)} and clear the record.
 
-    The kinds of linear attention and layer norm are there where they ran.
+    The kinds of linear attention, the delta rule and the norms are there where they ran.
     """
     lib = load_library()
     ms = (ctypes.c_double * PROFILE_KINDS)()
@@ -777,6 +791,115 @@ def ssm_linattn_update(state, q, k, v, g=None, A=None, scale=None, lengths=None,
         status = lib.ssm_linattn_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(A), _ptr(lengths),
                                         _scale(scale, Dk), _ptr(y), b, H, G, Dk, Dv, code, _stream_of(torch, device))
     _raise_on("ssm_linattn_update", status)
+    return y
+
+
+# ---------------------------------------------------------------------------
+# the gated delta rule
+# ---------------------------------------------------------------------------
+def ssm_deltarule_workspace(b, L, H, G, Dk, Dv, dtype="bf16", backward=False):
+    """Bytes of workspace of ``ssm_deltarule_fwd`` or ``ssm_deltarule_bwd`` at these sizes (host-only query)."""
+    code = {"f32": SSM_F32, "bf16": SSM_BF16}.get(dtype, dtype)
+    n = load_library().ssm_deltarule_workspace(int(b), int(L), int(H), int(G), int(Dk), int(Dv), int(code),
+                                               int(bool(backward)))
+    _raise_on("ssm_deltarule_workspace", min(n, 0))
+    return n
+
+
+def _deltarule_sizes(torch, q, k, v, beta, g, A, lengths, tokens):
+    """As ``_linattn_sizes``, with beta."""
+    sizes = _linattn_sizes(torch, q, k, v, g, A, lengths, tokens)
+    _check(torch, "beta", beta, v.shape[:-1], q.dtype, q.device, optional=True)
+    return sizes
+
+
+def ssm_deltarule_fwd(q, k, v, beta=None, g=None, A=None, scale=None, lengths=None, initial_state=None, y=None,
+                      last_state=None, return_last_state=True):
+    """The gated delta rule: ``(y, last_state)`` (None if not requested).
+
+    ``u = beta[b, t, h] (v - r S^T k)``, ``S = r S + k u^T``, ``y = scale S^T q`` for every token, with
+    ``r = exp(A[h] + g[b, t, h])``, from ``initial_state`` (None: zero).  beta [b, L, H] in the streamed dtype
+    (None: one); the others as in ``ssm_linattn_fwd``.  Keys are to be of length one.
+    """
+    import torch
+
+    lib = load_library()
+    b, L, H, G, Dk, Dv, io, code, device = _deltarule_sizes(torch, q, k, v, beta, g, A, lengths, 2)
+    f32 = torch.float32
+    _check(torch, "initial_state", initial_state, (b, H, Dk, Dv), f32, device, optional=True)
+    if y is None:
+        y = torch.empty((b, L, H, Dv), dtype=io, device=device)
+    else:
+        _check(torch, "y", y, (b, L, H, Dv), io, device)
+    if last_state is None and return_last_state:
+        last_state = torch.empty((b, H, Dk, Dv), dtype=f32, device=device)
+    elif last_state is not None:
+        _check(torch, "last_state", last_state, (b, H, Dk, Dv), f32, device)
+    if b * H and initial_state is not None and last_state is not None and (
+            initial_state.data_ptr() == last_state.data_ptr()):
+        raise ValueError("initial_state must not be the last_state buffer")
+    n = lib.ssm_deltarule_workspace(b, L, H, G, Dk, Dv, code, 0)
+    _raise_on("ssm_deltarule_fwd", min(n, 0))
+    ws = _workspace(torch, n, device)
+    with _on(torch, device):
+        status = lib.ssm_deltarule_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(A), _ptr(lengths),
+                                       _scale(scale, Dk), _ptr(initial_state), _ptr(y), _ptr(last_state), b, L, H, G, Dk,
+                                       Dv, code, _ptr(ws), n, _stream_of(torch, device))
+    _raise_on("ssm_deltarule_fwd", status)
+    return y, last_state
+
+
+def ssm_deltarule_bwd(q, k, v, dy, beta=None, g=None, A=None, scale=None, lengths=None, initial_state=None,
+                      d_last_state=None):
+    """Gradients of sum(dy * y) + sum(d_last_state * last_state) for ``ssm_deltarule_fwd``'s arguments.
+
+    Returns a dict: dq, dk [b, L, G, Dk], dv [b, L, H, Dv], dbeta and dg [b, L, H] (None without beta, g) in
+    the streamed dtype, d_initial_state [b, H, Dk, Dv] float32 (None without initial_state).
+    """
+    import torch
+
+    lib = load_library()
+    b, L, H, G, Dk, Dv, io, code, device = _deltarule_sizes(torch, q, k, v, beta, g, A, lengths, 2)
+    f32 = torch.float32
+    _check(torch, "dy", dy, (b, L, H, Dv), io, device)
+    _check(torch, "initial_state", initial_state, (b, H, Dk, Dv), f32, device, optional=True)
+    _check(torch, "d_last_state", d_last_state, (b, H, Dk, Dv), f32, device, optional=True)
+    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+           "dbeta": None if beta is None else torch.empty_like(beta), "dg": None if g is None else torch.empty_like(g),
+           "d_initial_state": None if initial_state is None else torch.empty_like(initial_state)}
+    n = lib.ssm_deltarule_workspace(b, L, H, G, Dk, Dv, code, 1)
+    _raise_on("ssm_deltarule_bwd", min(n, 0))
+    ws = _workspace(torch, n, device)
+    with _on(torch, device):
+        status = lib.ssm_deltarule_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(A), _ptr(lengths),
+                                       _scale(scale, Dk), _ptr(initial_state), _ptr(dy), _ptr(d_last_state),
+                                       _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dbeta"]),
+                                       _ptr(out["dg"]), _ptr(out["d_initial_state"]), b, L, H, G, Dk, Dv, code, _ptr(ws),
+                                       n, _stream_of(torch, device))
+    _raise_on("ssm_deltarule_bwd", status)
+    return out
+
+
+def ssm_deltarule_update(state, q, k, v, beta=None, g=None, A=None, scale=None, lengths=None, y=None):
+    """One token of ``ssm_deltarule_fwd``: ``state`` [b, H, Dk, Dv] float32 is updated in place; returns ``y``.
+
+    q, k [b, G, Dk]; v, y [b, H, Dv]; beta, g [b, H].  A batch row whose ``lengths`` is zero takes no step:
+    its state stays and its row of y is zero.
+    """
+    import torch
+
+    lib = load_library()
+    b, _, H, G, Dk, Dv, io, code, device = _deltarule_sizes(torch, q, k, v, beta, g, A, lengths, 1)
+    _check(torch, "state", state, (b, H, Dk, Dv), torch.float32, device)
+    if y is None:
+        y = torch.empty((b, H, Dv), dtype=io, device=device)
+    else:
+        _check(torch, "y", y, (b, H, Dv), io, device)
+    with _on(torch, device):
+        status = lib.ssm_deltarule_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(A),
+                                          _ptr(lengths), _scale(scale, Dk), _ptr(y), b, H, G, Dk, Dv, code,
+                                          _stream_of(torch, device))
+    _raise_on("ssm_deltarule_update", status)
     return y
 
 

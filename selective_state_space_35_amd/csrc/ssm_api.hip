@@ -10,6 +10,7 @@
 #include "ssm.h"
 #include "ssm_internal.h"
 #include "ssm_layernorm.h"
+#include "ssm_deltarule.h"
 #include "ssm_linattn.h"
 
 namespace {
@@ -469,6 +470,32 @@ int with_workspace(size_t need, void* workspace, int64_t bytes, hipStream_t stre
   return hip_status(err != hipSuccess ? err : ferr);
 }
 
+// Sizes and dtype of a gated-delta-rule call.
+int check_deltarule(int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype) {
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
+  const int64_t max_dim = ssm::deltarule_max_dim();
+  if (!size_ok(b) || !size_ok(L) || H < 0 || H > ssm::deltarule_max_heads() || G < 0) return SSM_ERR_DIM;
+  if (Dk < 1 || Dk > max_dim || Dv < 1 || Dv > max_dim) return SSM_ERR_DIM;
+  if (H > 0 && (G < 1 || H % G != 0)) return SSM_ERR_DIM;
+  // grids hold less than 2^32 threads: 512 a head of a batch row and 64 columns of the values, 512 a chunk of a head.
+  // That keeps every array and workspace below 2^63 bytes too
+  int64_t t = 0;
+  if (!mul_ok(b, H, &t) || t > (int64_t(1) << 21)) return SSM_ERR_DIM;
+  const int64_t chunk = dtype == SSM_F32 ? 32 : 64;
+  if (!mul_ok(t, L / chunk + 1, &t) || t >= (int64_t(1) << 23)) return SSM_ERR_DIM;
+  return SSM_OK;
+}
+
+ssm::DeltaRuleArgs deltarule_args(const void* q, const void* k, const void* v, const void* beta, const void* g, const float* A,
+                                  const int32_t* lengths, float scale, int64_t b, int64_t L, int64_t H, int64_t G,
+                                  int64_t Dk, int64_t Dv, int dtype, void* stream) {
+  ssm::DeltaRuleArgs a{};
+  a.q = q; a.k = k; a.v = v; a.beta = beta; a.g = g; a.A = A; a.lengths = lengths; a.scale = scale;
+  a.b = b; a.L = L; a.H = H; a.G = G; a.Dk = Dk; a.Dv = Dv; a.dtype = dtype;
+  a.stream = static_cast<hipStream_t>(stream);
+  return a;
+}
+
 int check_layernorm(int64_t rows, int64_t H, int64_t W, int dtype) {
   if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
   if (!size_ok(rows) || H < 0 || H > (int64_t(1) << 21) || W < 1 || W > ssm::layernorm_max_width()) return SSM_ERR_DIM;
@@ -538,6 +565,63 @@ int64_t ssm_linattn_workspace(int64_t b, int64_t L, int64_t H, int64_t G, int64_
   const ssm::LinAttnArgs a = linattn_args(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 1.f, b, L, H, G, Dk, Dv,
                                           dtype, nullptr);
   return int64_t(ssm::linattn_workspace_bytes(a, backward != 0));
+}
+
+int ssm_deltarule_fwd(const void* q, const void* k, const void* v, const void* beta, const void* g, const float* A,
+                      const int32_t* lengths, float scale, const float* initial_state, void* y, float* last_state,
+                      int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype, void* workspace,
+                      int64_t workspace_bytes, void* stream) {
+  const int st = check_deltarule(b, L, H, G, Dk, Dv, dtype);
+  if (st != SSM_OK || b == 0 || H == 0) return st;
+  if (L > 0 && (!q || !k || !v || !y)) return SSM_ERR_NULL;
+  const void* streamed[] = {q, k, v, beta, g, y};
+  const void* fl[] = {A, lengths, initial_state, last_state};
+  if (!all_aligned(streamed, 6, dtype == SSM_F32 ? 4 : 2) || !all_aligned(fl, 4, 4)) return SSM_ERR_ALIGN;
+  ssm::DeltaRuleArgs a = deltarule_args(q, k, v, beta, g, A, lengths, scale, b, L, H, G, Dk, Dv, dtype, stream);
+  a.h0 = initial_state; a.y = y; a.last = last_state;
+  return with_workspace(ssm::deltarule_workspace_bytes(a, false), workspace, workspace_bytes, a.stream,
+                        [&](void* ws) { return ssm::launch_deltarule_fwd(a, ws); });
+}
+
+int ssm_deltarule_bwd(const void* q, const void* k, const void* v, const void* beta, const void* g, const float* A,
+                      const int32_t* lengths, float scale, const float* initial_state, const void* dy,
+                      const float* d_last_state, void* dq, void* dk, void* dv, void* dbeta, void* dg,
+                      float* d_initial_state, int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
+                      int dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int st = check_deltarule(b, L, H, G, Dk, Dv, dtype);
+  if (st != SSM_OK || b == 0 || H == 0) return st;
+  if (L > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv)) return SSM_ERR_NULL;
+  const void* streamed[] = {q, k, v, beta, g, dy, dq, dk, dv, dbeta, dg};
+  const void* fl[] = {A, lengths, initial_state, d_last_state, d_initial_state};
+  if (!all_aligned(streamed, 11, dtype == SSM_F32 ? 4 : 2) || !all_aligned(fl, 5, 4)) return SSM_ERR_ALIGN;
+  ssm::DeltaRuleArgs a = deltarule_args(q, k, v, beta, g, A, lengths, scale, b, L, H, G, Dk, Dv, dtype, stream);
+  a.h0 = initial_state; a.dy = dy; a.dlast = d_last_state; a.dq = dq; a.dk = dk; a.dv = dv;
+  a.dbeta = beta ? dbeta : nullptr; a.dg = g ? dg : nullptr; a.dh0 = d_initial_state;
+  return with_workspace(ssm::deltarule_workspace_bytes(a, true), workspace, workspace_bytes, a.stream,
+                        [&](void* ws) { return ssm::launch_deltarule_bwd(a, ws); });
+}
+
+int ssm_deltarule_update(float* state, const void* q, const void* k, const void* v, const void* beta, const void* g,
+                         const float* A, const int32_t* lengths, float scale, void* y, int64_t b, int64_t H, int64_t G,
+                         int64_t Dk, int64_t Dv, int dtype, void* stream) {
+  const int st = check_deltarule(b, 1, H, G, Dk, Dv, dtype);
+  if (st != SSM_OK || b == 0 || H == 0) return st;
+  if (!state || !q || !k || !v || !y) return SSM_ERR_NULL;
+  const void* streamed[] = {q, k, v, beta, g, y};
+  const void* fl[] = {state, A, lengths};
+  if (!all_aligned(streamed, 6, dtype == SSM_F32 ? 4 : 2) || !all_aligned(fl, 3, 4)) return SSM_ERR_ALIGN;
+  ssm::DeltaRuleArgs a = deltarule_args(q, k, v, beta, g, A, lengths, scale, b, 1, H, G, Dk, Dv, dtype, stream);
+  a.y = y; a.last = state;
+  return hip_status(ssm::launch_deltarule_update(a));
+}
+
+int64_t ssm_deltarule_workspace(int64_t b, int64_t L, int64_t H, int64_t G, int64_t Dk, int64_t Dv, int dtype,
+                                int backward) {
+  const int st = check_deltarule(b, L, H, G, Dk, Dv, dtype);
+  if (st != SSM_OK) return st;
+  const ssm::DeltaRuleArgs a = deltarule_args(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 1.f, b, L, H, G,
+                                              Dk, Dv, dtype, nullptr);
+  return int64_t(ssm::deltarule_workspace_bytes(a, backward != 0));
 }
 
 int ssm_layernorm_fwd(const void* x, const float* weight, const float* bias, float eps, void* y, float* mean,

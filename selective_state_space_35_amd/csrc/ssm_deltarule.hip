@@ -1,0 +1,1518 @@
+// ssm_deltarule.hip -- the gated delta rule: whole sequences, the gradients, and the step for one token.
+//
+// Definition, for each batch row and head (q and k belong to the head's group):
+//   r_t = exp(A_h + g_t),  u_t = beta_t (v_t - r_t S_{t-1}^T k_t),  S_t = r_t S_{t-1} + k_t u_t^T  [Dk, Dv],
+//   y_t = scale S_t^T q_t
+// What a token writes is what its value differs by from what the state answers for its key.
+//
+// In chunks of C tokens, with G the running sum of the log decays inside the chunk, S the state entering it, products by
+// exp(G) taken row by row, and X_ts = exp(G_t - G_s) k_t . k_s for s < t (zero else):
+//   R = V - exp(G) K S,  (I + X diag(beta)) N = R,  U = beta N
+//   Y = scale (exp(G) Q S + P U),  P_ts = exp(G_t - G_s) q_t . k_s for s <= t
+//   S' = exp(G_C) S + K^T (exp(G_C - G) U)
+// The inverse Z = (I + X diag(beta))^-1 needs the keys only, so it is taken for all chunks at once (tri_kernel); what runs
+// from chunk to chunk are products with the state (sweep).
+//
+// Backward, D the gradient of the state leaving the chunk:
+//   dU = scale P^T dY + exp(G_C - G) K D,  dR = Z^T beta dU,  dV = dR
+//   D' = exp(G_C) D + scale (exp(G) Q)^T dY - (exp(G) K)^T dR
+// is the same sweep from the last chunk to the first.  With S, D, N and dR of every chunk the rest is each chunk's own
+// (grad_kernel), W = scale exp(G_t - G_s) dY U^T (s <= t), B = -exp(G_t - G_s) dR U^T (s < t):
+//   dQ = scale exp(G) dY S^T + W K,  dK = W^T Q + (B + B^T) K + exp(G_C - G) U D^T - exp(G) dR S^T
+//   dbeta_t = dR_t . N_t / beta_t
+// and dg_t sums, over the terms above that hold a factor exp(G) with token t's gate in it, the term: the entries of
+// W o QK^T + B o KK^T with row >= t > column, and the rows' products of q and k with the state parts.  It is computed as the
+// sum from t on of row sums less column sums, of the same rounded entries, so that what cancels cancels to float's
+// rounding of one chunk; at a reset (a factor that is zero in float) it is zero and the sum starts again.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "ssm_chunks.h"
+#include "ssm_deltarule.h"
+#include "ssm_device.h"
+#include "ssm_profile.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kMaxDim = 128;
+// exp of a log decay below this is zero in float, denormal numbers included (2^-150)
+constexpr float kZeroLog = -104.f;
+// The backward's dR is beta E, and dbeta needs E: where beta is nearer to zero than this, dR is computed with this in its
+// place, and its own part taken where dR itself is meant
+constexpr float kLeastBeta = 8.673617379884035e-19f;  // 2^-60
+
+struct Rule {
+  const void* q;
+  const void* k;
+  const void* v;           // the sweep's values: v, or (backwards) dy
+  const void* beta;
+  const void* g;
+  const float* A;
+  const int32_t* lengths;
+  float scale;
+  bool backward;           // a small beta is moved away from zero (tri_kernel)
+  const float* init;       // the state before the sweep's first chunk, or (backwards) the gradient behind its last
+  void* y;
+  float* last;             // the state after the sweep's last chunk
+  const float* tri;        // [b H n_chunks] inverses as operand fragments
+  float* states;           // [b H n_chunks][KP][VP]: states entering the chunks, or gradients of those leaving them
+  float* left;             // [b H n_chunks][C][VP]: N, or dR of the moved beta
+  int64_t b, L;
+  int H, share, Dk, Dv, KP, VP, n_chunks, n_tiles;
+  hipStream_t stream;
+};
+
+template <typename T>
+struct Shape {
+  static constexpr int kC = kChunk<T>;
+  static constexpr int TB = kC / 16;           // blocks of 16 tokens
+  static constexpr int kSteps = kC / 32;       // operand fragments along the tokens
+  static constexpr int kTri = TB == 4 ? 6 : 2; // fragments of a triangular matrix
+  static constexpr bool kTwo = sizeof(T) == 2; // operands that are not given in bf16 are taken in parts
+};
+// Which of the kTri fragments holds rows 16 tb.. and columns 32 ks.. of a lower triangular matrix, or of an upper one
+template <int TB>
+__device__ __forceinline__ constexpr int lower_frag(int tb, int ks) { return tb < 2 ? tb : 2 * tb - 2 + ks; }
+template <int TB>
+__device__ __forceinline__ constexpr int upper_frag(int tb, int ks) { return TB == 2 ? tb : tb < 2 ? 2 * tb + ks : tb + 2; }
+
+template <typename T>
+__device__ __forceinline__ float beta_of(const Rule& p, int64_t bi, int64_t t, int h, int n) {
+  if (t >= n) return 0.f;
+  return p.beta ? load_elem(static_cast<const T*>(p.beta) + (bi * p.L + t) * p.H + h) : 1.f;
+}
+__device__ __forceinline__ float moved_beta(float x) { return fabsf(x) < kLeastBeta ? copysignf(kLeastBeta, x) : x; }
+template <typename T>
+__device__ __forceinline__ float gate_of(const Rule& p, int64_t bi, int64_t t, int h, int n) {
+  if (t >= n) return 0.f;
+  return clamp_log((p.g ? load_elem(static_cast<const T*>(p.g) + (bi * p.L + t) * p.H + h) : 0.f) + (p.A ? p.A[h] : 0.f));
+}
+
+// A 16 x 16 product in float: rows of a, a lane's four contraction indices 4 (l / 16) .. + 3, with b, which has the layout
+// of a result
+__device__ __forceinline__ f32x4 mma16(const float4& a, const f32x4& b, f32x4 c) {
+  c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b[1], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b[2], c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b[3], c, 0, 0, 0);
+}
+
+// Rows r .. r + 3 (of a lane's group of 16) of column c0 + lane % 16 of an LDS tile
+__device__ __forceinline__ uint2 quad_bits(const bf16_bits* t, int ld, int r, int c0) {
+  const int m = threadIdx.x % 16;
+  const bf16_bits* p = t + (r + m / 4) * ld + c0 + 4 * (m % 4);
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)p));
+}
+__device__ __forceinline__ f32x4 quad_rows(const bf16_bits* t, int ld, int r, int c0) {
+  const uint2 v = quad_bits(t, ld, r, c0);
+  return f32x4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+               __uint_as_float(v.y & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4 quad_rows(const float* t, int ld, int r, int c0) {
+  const float* p = t + r * ld + c0 + threadIdx.x % 16;
+  return f32x4{p[0], p[ld], p[2 * ld], p[3 * ld]};
+}
+// the fragment of rows r .. r + 3 and r + 16 .. r + 19 of that column: the contraction in the order of two results
+__device__ __forceinline__ bf16x8 col_pair(const bf16_bits* t, int ld, int r, int c0) {
+  const uint2 a = quad_bits(t, ld, r, c0), b = quad_bits(t, ld, r + 16, c0);
+  return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
+}
+__device__ __forceinline__ f32x8 col_pair(const float* t, int ld, int r, int c0) {
+  const f32x4 a = quad_rows(t, ld, r, c0), b = quad_rows(t, ld, r + 16, c0);
+  return f32x8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+}
+
+// Floats as operand fragments: bf16 in N parts of 8 bits each (2^-9, 2^-17, 2^-25 of them is lost), float as they are
+template <typename T, int N>
+struct Parts {
+  static constexpr int kN = sizeof(T) == 2 ? N : 1;
+  Frag<T> f[kN];
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    if constexpr (sizeof(T) == 4) {
+      make_frag(x, f[0]);
+    } else {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) y[j] = x[j];
+#pragma unroll
+      for (int k = 0; k < kN; k++) {
+        make_frag(y, f[k]);
+#pragma unroll
+        for (int j = 0; j < 8; j++) y[j] -= static_cast<float>(f[k][j]);
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const f32x4& a, const f32x4& b) {
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    set(x);
+  }
+};
+// c + a b, of parts whose numbers add up to less than `least` (the products beyond are below the last part's rounding)
+template <typename T, int NA, int NB>
+__device__ __forceinline__ f32x4 mma_parts(const Parts<T, NA>& a, const Parts<T, NB>& b, f32x4 c) {
+  constexpr int na = Parts<T, NA>::kN, nb = Parts<T, NB>::kN, least = na > nb ? na : nb;
+#pragma unroll
+  for (int i = 0; i < na; i++)
+#pragma unroll
+    for (int j = 0; j < nb; j++)
+      if (i + j < least) c = mma(a.f[i], b.f[j], c);
+  return c;
+}
+
+// ---------------------------------------------------------------------------
+// Z = (I + X diag(beta))^-1 of every chunk, written as operand fragments in float: lane l of fragment (tb, ks) has row
+// 16 tb + l % 16 and columns 32 ks + 4 (l / 16) .. + 3 and 16 more; for the backward also those of Z^T beta.
+// The 16 x 16 blocks on the diagonal are inverted by forward substitution, a column a lane, and joined block by block,
+// Z_ij = -Z_ii (sum over j <= k < i of X_ik Z_kj), a column of blocks a wave, in float products.  An entry of X that is not
+// finite is taken as zero: the sweep makes NaN of everything from its token on.
+// ---------------------------------------------------------------------------
+template <typename T, int KDP, bool VEC>
+__global__ __launch_bounds__(kThreads) void tri_kernel(Rule p, float* lower, float* upper) {
+  typedef Shape<T> Z;
+  constexpr int kC = Z::kC, TB = Z::TB, KS = KDP / 32, ldk = Tile<T, KDP, kKey>::ld, ld = kC + 4;
+  __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP, kKey>::kElems];
+  __shared__ __attribute__((aligned(16))) float X[kC * ld], inv[kC * ld];
+  __shared__ Decays<kC> d;
+  __shared__ float beta[kC];
+  const int64_t id = blockIdx.x, bh = id / p.n_chunks, bi = bh / p.H;
+  const int c = int(id % p.n_chunks), h = int(bh % p.H), n = live_length(p.lengths, bi, p.L);
+  if (c * kC >= n) return;  // behind the sequence: not read
+  const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid / kWave), l = tid % kWave;
+  const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
+  Stage<T, KDP, kKey, VEC> sk;
+  uint4 rk[Tile<T, KDP, kKey>::kPieces];
+  const int G = p.H / p.share;
+  sk.init(static_cast<const T*>(p.k) + ((bi * p.L + int64_t(c) * kC) * G + h / p.share) * p.Dk, G * p.Dk, p.Dk, false, tid);
+  sk.load(rk, n - c * kC, tid);
+  if (wv == 0) {
+    const float g = l < kC ? gate_of<T>(p, bi, int64_t(c) * kC + l, h, n) : 0.f;
+    fill_decays(d, g, 1.f);
+  } else if (wv == 1 && l < kC) {
+    const float x = beta_of<T>(p, bi, int64_t(c) * kC + l, h, n);
+    beta[l] = p.backward ? moved_beta(x) : x;
+  }
+  sk.store(Ks, rk, tid);
+  __syncthreads();
+  for (int j = wv; j < TB * (TB + 1) / 2; j += 4) {  // X diag(beta), its blocks on and below the diagonal
+    int tb = 0, sb = j;
+    while (sb > tb) sb -= ++tb;
+    f32x4 a{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kk = 0; kk < KS; kk++)
+      a = mma(row_frag(Ks + (16 * sb + lr) * ldk + 32 * kk + g8), row_frag(Ks + (16 * tb + lr) * ldk + 32 * kk + g8), a);
+    const int t = 16 * tb + lr, s0 = 16 * sb + g4;
+    const float th = d.hi[t], tl = d.lo[t];
+    float x[4];
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      const float e = a[r] * exp2_fast((th - d.hi[s0 + r]) + (tl - d.lo[s0 + r])) * beta[s0 + r];
+      x[r] = s0 + r < t && e * 0.f == 0.f ? e : 0.f;
+    }
+    *reinterpret_cast<float4*>(X + t * ld + s0) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+  __syncthreads();
+  if (tid < kC) {  // lane l has column l % 16 of block l / 16
+    const int b0 = 16 * (l / 16);
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      float s = i == lr ? 1.f : 0.f;
+      const float4* row = reinterpret_cast<const float4*>(X + (b0 + i) * ld + b0);
+#pragma unroll
+      for (int k4 = 0; k4 < (i + 3) / 4; k4++) {
+        const float4 a = row[k4];
+        const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          if (4 * k4 + k < i) s = fmaf(-av[k], x[4 * k4 + k], s);
+      }
+      x[i] = s;
+      inv[(b0 + i) * ld + b0 + lr] = s;
+    }
+  }
+  __syncthreads();
+  if (wv < TB - 1) {
+    f32x4 col[TB];
+#pragma unroll
+    for (int r = 0; r < 4; r++) col[0][r] = inv[(16 * wv + g4 + r) * ld + 16 * wv + lr];
+#pragma unroll
+    for (int o = 1; o < TB; o++) {  // block row wv + o
+      const int i = wv + o;
+      if (i < TB) {
+        f32x4 t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < o; k++) t = mma16(lds4(X + (16 * i + lr) * ld + 16 * (wv + k) + g4), col[k], t);
+        f32x4 z{0.f, 0.f, 0.f, 0.f};
+        z = mma16(lds4(inv + (16 * i + lr) * ld + 16 * i + g4), t, z);
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          col[o][r] = -z[r];
+          inv[(16 * i + g4 + r) * ld + 16 * wv + lr] = -z[r];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  float4* out = reinterpret_cast<float4*>(lower + id * (Z::kTri * 512));
+  float4* out_t = upper ? reinterpret_cast<float4*>(upper + id * (Z::kTri * 512)) : nullptr;
+  for (int j = tid; j < Z::kTri * 64; j += kThreads) {
+    const int f = j / 64, ll = j % 64, r16 = ll % 16, q4 = 4 * (ll / 16);
+    int tb = 0, ks = 0;
+#pragma unroll
+    for (int a = 0; a < TB; a++)
+      for (int b = 0; b <= a / 2; b++)
+        if (lower_frag<TB>(a, b) == f) tb = a, ks = b;
+    const float* row = inv + (16 * tb + r16) * ld + 32 * ks + q4;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    out[2 * j] = lds4(row);
+    out[2 * j + 1] = 2 * ks + 1 <= tb ? lds4(row + 16) : zero;
+    if (out_t) {
+      int sb = 0;
+      ks = 0;
+#pragma unroll
+      for (int a = 0; a < TB; a++)
+        for (int b = a / 2; b < Z::kSteps; b++)
+          if (upper_frag<TB>(a, b) == f) sb = a, ks = b;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const int t = 32 * ks + q4 + e % 4 + 16 * (e / 4);
+        x[e] = t / 16 >= sb ? inv[t * ld + 16 * sb + r16] * beta[t] : 0.f;
+      }
+      out_t[2 * j] = make_float4(x[0], x[1], x[2], x[3]);
+      out_t[2 * j + 1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The sweep over a head's chunks, for VT columns of the values: columns of the state do not meet, so each of the state
+// waves has 16 NT of them to itself, with the state, R, N and U in registers.  A result of 16 x 16 has, in lane l, rows
+// 4 (l / 16) .. + 3 of column l % 16, so two results side by side are the next product's operand as they are, as long as the
+// other operand is read in that order of the contraction.
+// Four other waves stage the chunk after and compute its P; two barriers a chunk.
+// bf16: a product's operands that are not given in bf16 are taken in parts.  What a state or N is made of keeps all 24 bits
+// (three parts, six products where both sides are floats); what an output alone is made of two (2^-17).
+// ---------------------------------------------------------------------------
+enum Mode { kForward, kStates, kBackwards };
+
+constexpr int state_waves(int vt) { return vt >= 64 ? 4 : vt / 16; }
+
+template <typename T, int KDP, int VT>
+struct SweepLds {
+  typedef Shape<T> Z;
+  static constexpr int kC = Z::kC;
+  __attribute__((aligned(16))) T q[2][Tile<T, KDP, kQuery>::kElems];
+  __attribute__((aligned(16))) T k[2][Tile<T, KDP, kKey>::kElems];
+  __attribute__((aligned(16))) T v[2][Tile<T, VT, kValue>::kElems];
+  __attribute__((aligned(16))) T z[2][Z::kTwo ? 3 : 1][Z::kTri * 512];
+  __attribute__((aligned(16))) T P[2][Z::kTwo ? 2 : 1][Z::kTri * 512];
+  Decays<kC> d[4];  // written two chunks ahead
+  __attribute__((aligned(16))) float beta[4][kC];  // backwards the part of dR that is beta's own
+};
+
+template <typename T, int KDP, int VT, Mode MODE, bool VEC>
+__global__ __launch_bounds__(kThreads + kWave * state_waves(VT)) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void sweep_kernel(Rule p) {
+  typedef Shape<T> Z;
+  constexpr int kC = Z::kC, TB = Z::TB, kSteps = Z::kSteps, kTri = Z::kTri, KS = KDP / 32, MT = KDP / 16;
+  constexpr bool kTwo = Z::kTwo, kBack = MODE == kBackwards, kOut = MODE == kForward;
+  constexpr int SW = state_waves(VT), NT = VT / (16 * SW);
+  constexpr int ldq = Tile<T, KDP, kQuery>::ld, ldk = Tile<T, KDP, kKey>::ld, ldv = Tile<T, VT, kValue>::ld;
+  __shared__ SweepLds<T, KDP, VT> sh;
+  // Workgroups are dealt to the 8 XCDs in turn: those of a head, and of neighbouring ones that share rows, go to one
+  const int64_t units = p.b * p.H * p.n_tiles, wg = blockIdx.x;
+  const int64_t id = units % 8 == 0 ? (wg % 8) * (units / 8) + wg / 8 : wg;
+  const int v0 = int(id % p.n_tiles) * VT;
+  const int64_t bh = id / p.n_tiles, bi = bh / p.H;
+  const int h = int(bh % p.H), n = live_length(p.lengths, bi, p.L);
+  const int chunks = (n + kC - 1) / kC, G = p.H / p.share;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = threadIdx.x % kWave;
+  const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
+  auto chunk_of = [&](int i) { return kBack ? chunks - 1 - i : i; };
+
+  if (wv >= SW) {
+    // ------------------------------------------------------------------ staging and scores
+    const int pw = wv - SW, tid = threadIdx.x - kWave * SW;
+    if constexpr (MODE != kStates) {  // the halves of P's fragments beyond the diagonal stay zero
+      for (int i = tid; i < kSteps * 256; i += kThreads) {
+        const int f = kBack ? upper_frag<TB>(2 * (i / 256) + 1, i / 256) : lower_frag<TB>(2 * (i / 256), i / 256);
+        const int at = f * 512 + (i % 256) / 4 * 8 + i % 4 + (kBack ? 0 : 4);
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+          sh.P[b][0][at] = T(0);
+          if constexpr (kTwo) sh.P[b][1][at] = T(0);
+        }
+      }
+    }
+    Stage<T, KDP, kQuery, VEC> sq;
+    Stage<T, KDP, kKey, VEC> sk;
+    Stage<T, VT, kValue, VEC> sv;
+    const int64_t t0 = bi * p.L + int64_t(kBack ? std::max(chunks - 1, 0) : 0) * kC;
+    sq.init(static_cast<const T*>(p.q) + (t0 * G + h / p.share) * p.Dk, G * p.Dk, p.Dk, false, tid);
+    sk.init(static_cast<const T*>(p.k) + (t0 * G + h / p.share) * p.Dk, G * p.Dk, p.Dk, false, tid);
+    sv.init(static_cast<const T*>(p.v) + (t0 * p.H + h) * p.Dv + v0, p.H * p.Dv, p.Dv - v0, false, tid);
+    if (kBack) {
+      sq.chunk = -sq.chunk;
+      sk.chunk = -sk.chunk;
+      sv.chunk = -sv.chunk;
+    }
+    constexpr int kZ = (kTri * 64 + kThreads - 1) / kThreads;
+    struct Regs {
+      uint4 q[Tile<T, KDP, kQuery>::kPieces], k[Tile<T, KDP, kKey>::kPieces], v[Tile<T, VT, kValue>::kPieces];
+      float4 z[kZ][2];
+      float gate, beta;
+    };
+    Regs r0, r1;
+    auto live = [&](int i) { return i < chunks ? n - chunk_of(i) * kC : 0; };
+    const float* tri = p.tri + bh * p.n_chunks * (kTri * 512);
+    auto fetch = [&](Regs& r, int i) {  // the i-th chunk of the sweep; behind its end nothing is read and the rows are zero
+      const int nv = live(i);
+      if constexpr (MODE != kStates) sq.load(r.q, nv, tid);
+      sk.load(r.k, nv, tid);
+      sv.load(r.v, nv, tid);
+      if (i < chunks) {
+        const float4* from = reinterpret_cast<const float4*>(tri + int64_t(chunk_of(i)) * (kTri * 512));
+#pragma unroll
+        for (int j = 0; j < kZ; j++) {
+          const int at = tid + j * kThreads;
+          if (at < kTri * 64) {
+            r.z[j][0] = from[2 * at];
+            r.z[j][1] = from[2 * at + 1];
+          }
+        }
+        if (pw == 3 && l < kC) {
+          const int64_t t = int64_t(chunk_of(i)) * kC + l;
+          r.gate = gate_of<T>(p, bi, t, h, n);
+          r.beta = beta_of<T>(p, bi, t, h, n);
+        }
+      }
+    };
+    auto place = [&](const Regs& r, int i) {
+      if (i >= chunks) return;
+      const int b = i & 1;
+      if constexpr (MODE != kStates) sq.store(sh.q[b], r.q, tid);
+      sk.store(sh.k[b], r.k, tid);
+      sv.store(sh.v[b], r.v, tid);
+#pragma unroll
+      for (int j = 0; j < kZ; j++) {
+        const int at = tid + j * kThreads;
+        if (at < kTri * 64) {
+          const float x[8] = {r.z[j][0].x, r.z[j][0].y, r.z[j][0].z, r.z[j][0].w, r.z[j][1].x, r.z[j][1].y, r.z[j][1].z, r.z[j][1].w};
+          Parts<T, 3> f;
+          f.set(x);
+#pragma unroll
+          for (int k = 0; k < Parts<T, 3>::kN; k++) *reinterpret_cast<Frag<T>*>(sh.z[b][k] + at * 8) = f.f[k];
+        }
+      }
+    };
+    auto decays = [&](const Regs& r, int i) {  // by the wave with the fewest blocks of P
+      if (pw != 3 || i >= chunks) return;
+      fill_decays(sh.d[i & 3], l < kC ? r.gate : 0.f, 1.f);
+      if (l < kC) sh.beta[i & 3][l] = kBack ? r.beta / moved_beta(r.beta) : r.beta;
+    };
+    // one block of P, rows t of q with columns s of k, to its half of a fragment: forwards of P, backwards of its transpose
+    auto score_block = [&](int i, int tb, int sb) {
+      const T* Qs = sh.q[i & 1];
+      const T* Ks = sh.k[i & 1];
+      const Decays<kC>& d = sh.d[i & 3];
+      f32x4 a{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < KS; kk++) {
+        const Frag<T> qf = row_frag(Qs + (16 * tb + lr) * ldq + 32 * kk + g8);
+        const Frag<T> kf = row_frag(Ks + (16 * sb + lr) * ldk + 32 * kk + g8);
+        a = kBack ? mma(qf, kf, a) : mma(kf, qf, a);
+      }
+      const int cb = kBack ? sb : tb, rb = kBack ? tb : sb;  // the blocks that run along lanes, and along a lane's four
+      const float ch = d.hi[16 * cb + lr], cl = d.lo[16 * cb + lr];
+      const float4 h4 = lds4(d.hi + 16 * rb + g4), l4 = lds4(d.lo + 16 * rb + g4);
+      const float rh[4] = {h4.x, h4.y, h4.z, h4.w}, rl[4] = {l4.x, l4.y, l4.z, l4.w};
+      float x[4];
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const float diff = (ch - rh[r]) + (cl - rl[r]);
+        const bool in = tb > sb || (kBack ? lr <= g4 + r : g4 + r <= lr);
+        x[r] = in ? a[r] * exp2_fast(kBack ? -diff : diff) * p.scale : 0.f;
+      }
+      const int f = kBack ? upper_frag<TB>(sb, tb / 2) : lower_frag<TB>(tb, sb / 2);
+      const int at = f * 512 + l * 8 + 4 * (rb % 2);
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(sh.P[i & 1][0] + at) = make_float4(x[0], x[1], x[2], x[3]);
+      } else {
+        const uint2 hi = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        *reinterpret_cast<uint2*>(sh.P[i & 1][0] + at) = hi;
+        const float y[4] = {x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xffff0000u),
+                            x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xffff0000u)};
+        *reinterpret_cast<uint2*>(sh.P[i & 1][kTwo ? 1 : 0] + at) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+      }
+    };
+    auto score = [&](int i) {
+      if (MODE == kStates || i >= chunks) return;
+      if constexpr (TB == 4) {
+        if (pw < 3) {
+          score_block(i, 3 - pw, 0);
+          score_block(i, 3 - pw, 1);
+          score_block(i, pw == 2 ? 0 : 3 - pw, pw == 2 ? 0 : 2);
+        } else {
+          score_block(i, 3, 3);
+        }
+      } else {
+        if (pw < 3) score_block(i, pw > 0, pw > 1);
+      }
+    };
+    fetch(r0, 0);
+    fetch(r1, 1);
+    place(r0, 0);
+    decays(r0, 0);
+    fetch(r0, 2);
+    decays(r1, 1);
+    __syncthreads();
+    score(0);
+    __syncthreads();
+    // at the top of step i: chunk i is in the tiles and in P; chunks i + 1 (in r) and i + 2 (in the other set) are in
+    // registers or under way
+    auto step = [&](Regs& r, const Regs& other, int i) {
+      place(r, i + 1);
+      fetch(r, i + 3);
+      __syncthreads();
+      score(i + 1);
+      decays(other, i + 2);
+      __syncthreads();
+    };
+    for (int i = 0; i < chunks; i += 2) {
+      step(r1, r0, i);
+      step(r0, r1, i + 1);
+    }
+    if constexpr (kOut) {  // rows behind the length are zero
+      const int cols = std::min(VT, p.Dv - v0);
+      for (int64_t t = n + pw; t < p.L; t += 4) {
+        T* y = static_cast<T*>(p.y) + ((bi * p.L + t) * p.H + h) * p.Dv + v0;
+        for (int j = l; j < cols; j += kWave) store_elem(y + j, 0.f);
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------------- the state
+  const int vw = 16 * NT * wv;  // the wave's first column of the tile
+  f32x4 S[MT][NT];
+  const float* init = p.init ? p.init + bh * p.Dk * p.Dv : nullptr;
+#pragma unroll
+  for (int m = 0; m < MT; m++)
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int i = 16 * m + g4 + r, v = v0 + vw + 16 * j + lr;
+        S[m][j][r] = init && i < p.Dk && v < p.Dv ? init[i * p.Dv + v] : 0.f;
+      }
+  __syncthreads();
+  __syncthreads();
+  for (int i = 0; i < chunks; i++) {
+    const int c = chunk_of(i), nv = std::min(kC, n - c * kC);
+    const Decays<kC>& d = sh.d[i & 3];
+    const float* beta = sh.beta[i & 3];
+    const T* Qs = sh.q[i & 1];
+    const T* Ks = sh.k[i & 1];
+    const T* Vs = sh.v[i & 1];
+    if constexpr (MODE != kForward) {  // what grad_kernel reads: the state entering the chunk, or the gradient leaving it
+      float* to = p.states + (bh * p.n_chunks + c) * int64_t(p.KP) * p.VP;
+#pragma unroll
+      for (int m = 0; m < MT; m++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+          const int v = v0 + vw + 16 * j + lr;
+          if (16 * m < p.KP && v < p.VP)
+#pragma unroll
+            for (int r = 0; r < 4; r++) to[(16 * m + g4 + r) * p.VP + v] = S[m][j][r];
+        }
+    }
+    // ---- the state's answers for the keys (and, transposed, for the queries) ----
+    f32x4 x[TB][NT], o[TB][NT];
+#pragma unroll
+    for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+      for (int j = 0; j < NT; j++) x[tt][j] = o[tt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kk = 0; kk < KS; kk++) {
+      Parts<T, 3> s[NT];
+#pragma unroll
+      for (int j = 0; j < NT; j++) s[j].set(S[2 * kk][j], S[2 * kk + 1][j]);
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++) {
+        const T* at = Ks + (16 * tt + lr) * ldk + 32 * kk + g4;
+        const Frag<T> kf = pair_frag(at, at + 16);
+#pragma unroll
+        for (int e = 0; e < Parts<T, 3>::kN; e++)
+#pragma unroll
+          for (int j = 0; j < NT; j++) x[tt][j] = mma(kf, s[j].f[e], x[tt][j]);
+        if constexpr (kOut) {
+          const T* qt = Qs + (16 * tt + lr) * ldq + 32 * kk + g4;
+          const Frag<T> qf = pair_frag(qt, qt + 16);
+#pragma unroll
+          for (int e = 0; e < (kTwo ? 2 : 1); e++)
+#pragma unroll
+            for (int j = 0; j < NT; j++) o[tt][j] = mma(s[j].f[e], qf, o[tt][j]);
+        }
+      }
+    }
+    // ---- R, or dU ----
+    if constexpr (!kBack) {
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++) {
+        const float4 a4 = lds4(d.in + 16 * tt + g4), b4 = lds4(beta + 16 * tt + g4);
+        const float a[4] = {a4.x, a4.y, a4.z, a4.w}, be[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+          const f32x4 v = quad_rows(Vs, ldv, 16 * tt + g4, vw + 16 * j);
+#pragma unroll
+          for (int r = 0; r < 4; r++) x[tt][j][r] = fmaf(be[r], 0.f, fmaf(-a[r], x[tt][j][r], v[r]));  // NaN where beta is no number
+        }
+      }
+    } else {
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++) {
+        const float4 a4 = lds4(d.out + 16 * tt + g4);
+        const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) x[tt][j][r] *= a[r];
+      }
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ks++) {
+        Frag<T> yf[NT];
+#pragma unroll
+        for (int j = 0; j < NT; j++) yf[j] = col_pair(Vs, ldv, 32 * ks + g4, vw + 16 * j);
+#pragma unroll
+        for (int sb = 0; sb < TB; sb++)
+          if (sb / 2 <= ks)
+#pragma unroll
+            for (int e = 0; e < (kTwo ? 2 : 1); e++) {
+              const Frag<T> pf = row_frag(sh.P[i & 1][e] + upper_frag<TB>(sb, ks) * 512 + l * 8);
+#pragma unroll
+              for (int j = 0; j < NT; j++) x[sb][j] = mma(pf, yf[j], x[sb][j]);
+            }
+      }
+    }
+    // A row that is not finite must not meet Z's zeros: the rows before it would be no numbers.  From it on N is NaN, and so
+    // are the outputs and the state's column.
+    int first[NT];
+    bool bad = false;
+    if constexpr (!kBack) {
+      float z = 0.f;
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) z = fmaf(x[tt][j][r], 0.f, z);
+      bad = __ballot(!(z == 0.f)) != 0;
+#pragma unroll
+      for (int j = 0; j < NT; j++) first[j] = kC;
+      if (__builtin_expect(bad, 0)) {
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+#pragma unroll
+          for (int tt = TB - 1; tt >= 0; tt--)
+#pragma unroll
+            for (int r = 3; r >= 0; r--)
+              if (!(x[tt][j][r] * 0.f == 0.f)) {
+                first[j] = 16 * tt + g4 + r;
+                x[tt][j][r] = 0.f;
+              }
+          first[j] = std::min(first[j], __shfl_xor(first[j], 16));
+          first[j] = std::min(first[j], __shfl_xor(first[j], 32));
+        }
+      }
+    }
+    // ---- N = Z R, or dR = Z^T beta dU ----
+    f32x4 nn[TB][NT];
+#pragma unroll
+    for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+      for (int j = 0; j < NT; j++) nn[tt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ks++) {
+      Parts<T, 3> xf[NT];
+#pragma unroll
+      for (int j = 0; j < NT; j++) xf[j].set(x[2 * ks][j], x[2 * ks + 1][j]);
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++)
+        if (kBack ? tt / 2 <= ks : ks <= tt / 2) {
+          Parts<T, 3> zf;
+#pragma unroll
+          for (int e = 0; e < Parts<T, 3>::kN; e++)
+            zf.f[e] = row_frag(sh.z[i & 1][e] + (kBack ? upper_frag<TB>(tt, ks) : lower_frag<TB>(tt, ks)) * 512 + l * 8);
+#pragma unroll
+          for (int j = 0; j < NT; j++) nn[tt][j] = mma_parts(zf, xf[j], nn[tt][j]);
+        }
+    }
+    if constexpr (MODE != kForward) {
+      float* to = p.left + (bh * p.n_chunks + c) * int64_t(kC) * p.VP;
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+          const int v = v0 + vw + 16 * j + lr;
+          if (v < p.VP)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+              const int t = 16 * tt + g4 + r;
+              to[t * p.VP + v] = !kBack && t >= first[j] ? __builtin_nanf("") : nn[tt][j][r];
+            }
+        }
+    }
+    // ---- outputs ----
+    if constexpr (kOut) {
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++) {
+        const float a = d.in[16 * tt + lr] * p.scale;
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) o[tt][j][r] *= a;
+      }
+    }
+    // U, in the products' parts: as it is for the outputs, with its decay for the state; backwards the two rows that the
+    // state's gradient takes, of dY and of dR
+    Parts<T, 3> wf[kSteps][NT], yf[kBack ? kSteps : 1][NT];
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ks++) {
+      float w[2][4], be[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const float4 a4 = lds4((kBack ? d.in : d.out) + 32 * ks + 16 * e + g4), b4 = lds4(beta + 32 * ks + 16 * e + g4);
+        w[e][0] = a4.x; w[e][1] = a4.y; w[e][2] = a4.z; w[e][3] = a4.w;
+        be[e][0] = b4.x; be[e][1] = b4.y; be[e][2] = b4.z; be[e][3] = b4.w;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        float u[8];
+        if constexpr (kBack) {
+          float yv[8];
+          frag_floats(col_pair(Vs, ldv, 32 * ks + g4, vw + 16 * j), yv);
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            u[e] = -nn[2 * ks + e / 4][j][e % 4] * (w[e / 4][e % 4] * be[e / 4][e % 4]);
+            yv[e] *= w[e / 4][e % 4] * p.scale;
+          }
+          yf[ks][j].set(yv);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const float b = be[e / 4][e % 4];
+            u[e] = bad && !(b * 0.f == 0.f) ? 0.f : nn[2 * ks + e / 4][j][e % 4] * b;
+          }
+          if constexpr (kOut) {
+            Parts<T, 2> uf;
+            uf.set(u);
+#pragma unroll
+            for (int tt = 0; tt < TB; tt++)
+              if (ks <= tt / 2) {
+                Parts<T, 2> pf;
+#pragma unroll
+                for (int e = 0; e < Parts<T, 2>::kN; e++)
+                  pf.f[e] = row_frag(sh.P[i & 1][e] + lower_frag<TB>(tt, ks) * 512 + l * 8);
+                o[tt][j] = mma_parts(uf, pf, o[tt][j]);
+              }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; e++) u[e] *= w[e / 4][e % 4];
+        }
+        wf[ks][j].set(u);
+      }
+    }
+    if constexpr (kOut) {
+      if (__builtin_expect(bad, 0)) {
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) {
+            const int at = __shfl(first[j], g4 + r);
+#pragma unroll
+            for (int tt = 0; tt < TB; tt++) o[tt][j][r] = 16 * tt + lr >= at ? __builtin_nanf("") : o[tt][j][r];
+          }
+      }
+    }
+    __syncthreads();  // P and Z of this chunk have been read
+    if constexpr (kOut) {
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++) {
+        const int t = 16 * tt + lr;
+        if (t < nv) {
+          T* y = static_cast<T*>(p.y) + ((bi * p.L + int64_t(c) * kC + t) * p.H + h) * p.Dv;
+#pragma unroll
+          for (int j = 0; j < NT; j++) {
+            const int v = v0 + vw + 16 * j + g4;
+            if constexpr (VEC) {
+              if (v < p.Dv) {
+                if constexpr (kTwo) *reinterpret_cast<uint2*>(y + v) = make_uint2(pack_bf16(o[tt][j][0], o[tt][j][1]), pack_bf16(o[tt][j][2], o[tt][j][3]));
+                else *reinterpret_cast<float4*>(y + v) = make_float4(o[tt][j][0], o[tt][j][1], o[tt][j][2], o[tt][j][3]);
+              }
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; r++)
+                if (v + r < p.Dv) store_elem(y + v + r, o[tt][j][r]);
+            }
+          }
+        }
+      }
+    }
+    // ---- the state after the chunk ----
+    const float all = d.all;
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) S[m][j][r] *= all;
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ks++) {
+        const Frag<T> kf = col_pair(Ks, ldk, 32 * ks + g4, 16 * m);
+#pragma unroll
+        for (int e = 0; e < Parts<T, 3>::kN; e++)
+#pragma unroll
+          for (int j = 0; j < NT; j++) S[m][j] = mma(kf, wf[ks][j].f[e], S[m][j]);
+        if constexpr (kBack) {
+          const Frag<T> qf = col_pair(Qs, ldq, 32 * ks + g4, 16 * m);
+#pragma unroll
+          for (int e = 0; e < Parts<T, 3>::kN; e++)
+#pragma unroll
+            for (int j = 0; j < NT; j++) S[m][j] = mma(qf, yf[ks][j].f[e], S[m][j]);
+        }
+      }
+    }
+    if constexpr (!kBack) {
+      if (__builtin_expect(bad, 0)) {
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+          for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) S[m][j][r] = first[j] < kC ? __builtin_nanf("") : S[m][j][r];
+      }
+    }
+    __syncthreads();
+  }
+  if (chunks % 2) {  // the staging waves' steps go by twos
+    __syncthreads();
+    __syncthreads();
+  }
+  if (p.last) {
+    float* last = p.last + bh * p.Dk * p.Dv;
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const int i = 16 * m + g4 + r, v = v0 + vw + 16 * j + lr;
+          if (i < p.Dk && v < p.Dv) last[i * p.Dv + v] = S[m][j][r];
+        }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// What is a chunk's own of the backward: dq, dk, dv, dbeta and dg from S, D, N and dR.  A workgroup has one chunk of a
+// head, eight waves.  First the products along the values, 64 columns at a time: with the states (a wave has 16 of the
+// keys' elements), and dY U^T and dR U^T (a wave has a block or two of them); then, with W and B in LDS, those along the
+// tokens.  Results are transposed, so that a lane has consecutive elements of its own token.
+// ---------------------------------------------------------------------------
+struct Grad {
+  Rule p;                // v is v, y is dv
+  const void* dy;
+  const float* S;        // [b H n_chunks][KP][VP]
+  const float* D;
+  const float* N;        // [b H n_chunks][C][VP]
+  const float* dR;
+  void* dq;              // [b, L, H, Dk] float, or of the streamed type where heads share nothing
+  void* dk;
+  bool dqk_f32;
+  void* dbeta;           // nullable
+  void* dg;              // nullable
+};
+
+constexpr int kGradWaves = 8;
+template <typename T, int KDP>
+struct GradLds {
+  typedef Shape<T> Z;
+  static constexpr int kC = Z::kC, kN = Z::kTwo ? 2 : 1;
+  static constexpr int ldw = kC + 16 / int(sizeof(T));
+  static constexpr int ldv = Tile<T, 64, kValue>::ld;
+  __attribute__((aligned(16))) T q[Tile<T, KDP, kQuery>::kElems];
+  __attribute__((aligned(16))) T k[Tile<T, KDP, kKey>::kElems];
+  union {
+    struct {
+      __attribute__((aligned(16))) T dy[kC * ldv], u[kN][kC * ldv], r[kN][kC * ldv];
+    } a;
+    struct {
+      __attribute__((aligned(16))) T W[kN][kC * ldw], B[kN][kC * ldw];
+    } b;
+  };
+  Decays<kC> d;
+  float beta[kC];
+  float rows[Z::TB][kC], cols[Z::TB][kC];      // sums of a block's rows and columns
+  float dots[KDP / 16][kC], kept[KDP / 16][kC]; // of a token, over 16 of the keys' elements
+  double sd[kGradWaves];
+};
+
+// 8 floats from a 16-byte aligned address
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+// four floats to a row of an LDS tile, in its parts
+__device__ __forceinline__ void put4(float (&x)[4], float* a, float*) { *reinterpret_cast<float4*>(a) = make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void put4(float (&x)[4], bf16_bits* a, bf16_bits* b) {
+  const uint2 hi = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  *reinterpret_cast<uint2*>(a) = hi;
+  *reinterpret_cast<uint2*>(b) = make_uint2(pack_bf16(x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xffff0000u)),
+                                            pack_bf16(x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xffff0000u)));
+}
+__device__ __forceinline__ void put1(float x, float* a, float*) { *a = x; }
+__device__ __forceinline__ void put1(float x, bf16_bits* a, bf16_bits* b) {
+  store_elem(a, x);
+  store_elem(b, x - load_elem(a));
+}
+// four consecutive elements of a row in memory, of which `left` are inside
+template <typename T>
+__device__ __forceinline__ void store4(T* to, const float (&x)[4], int left, bool vec) {
+  if (vec) {
+    if (left <= 0) return;
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+    else *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+      if (r < left) store_elem(to + r, x[r]);
+  }
+}
+
+template <typename T, int KDP, bool VEC>
+__global__ __launch_bounds__(kGradWaves * kWave) void grad_kernel(Grad a) {
+  typedef Shape<T> Z;
+  typedef GradLds<T, KDP> Lds;
+  constexpr int kC = Z::kC, TB = Z::TB, kSteps = Z::kSteps, KS = KDP / 32, MT = KDP / 16;
+  constexpr int TT = TB * MT / kGradWaves;  // blocks of tokens a wave has
+  constexpr int ldq = Tile<T, KDP, kQuery>::ld, ldk = Tile<T, KDP, kKey>::ld, ldv = Lds::ldv, ldw = Lds::ldw, kN = Lds::kN;
+  constexpr int NB = TB == 4 ? 2 : 1;       // blocks of W and B a wave has, at most
+  const Rule& p = a.p;
+  __shared__ Lds sh;
+  const int64_t units = p.b * p.H * p.n_chunks, wg = blockIdx.x;
+  const int64_t id = units % 8 == 0 ? (wg % 8) * (units / 8) + wg / 8 : wg;
+  const int64_t bh = id / p.n_chunks, bi = bh / p.H;
+  const int c = int(id % p.n_chunks), h = int(bh % p.H), n = live_length(p.lengths, bi, p.L), G = p.H / p.share;
+  const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid / kWave), l = tid % kWave;
+  const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
+  const int64_t t0 = int64_t(c) * kC, row0 = bi * p.L + t0;
+  const int nv = std::max(0, std::min(kC, int(n - t0))), rows = int(std::min<int64_t>(kC, p.L - t0));
+  auto zero_rows = [&](void* x, bool f32, int heads, int hh, int D, int from) {
+    for (int j = tid; j < (rows - from) * D; j += kGradWaves * kWave) {
+      const int64_t at = ((row0 + from + j / D) * heads + hh) * D + j % D;
+      if (f32) static_cast<float*>(x)[at] = 0.f;
+      else store_elem(static_cast<T*>(x) + at, 0.f);
+    }
+  };
+  if (nv < rows) {  // behind the length
+    zero_rows(a.dq, a.dqk_f32, p.H, h, p.Dk, nv);
+    zero_rows(a.dk, a.dqk_f32, p.H, h, p.Dk, nv);
+    zero_rows(p.y, false, p.H, h, p.Dv, nv);
+    if (a.dbeta) zero_rows(a.dbeta, false, p.H, h, 1, nv);
+    if (a.dg) zero_rows(a.dg, false, p.H, h, 1, nv);
+  }
+  if (nv == 0) return;
+  const int64_t state = id * int64_t(p.KP) * p.VP, left = id * int64_t(kC) * p.VP;
+  {
+    if (wv < 4) {
+      Stage<T, KDP, kQuery, VEC> s;
+      uint4 r[Tile<T, KDP, kQuery>::kPieces];
+      s.init(static_cast<const T*>(p.q) + (row0 * G + h / p.share) * p.Dk, G * p.Dk, p.Dk, false, tid);
+      s.load(r, nv, tid);
+      s.store(sh.q, r, tid);
+    } else {
+      Stage<T, KDP, kKey, VEC> s;
+      uint4 r[Tile<T, KDP, kKey>::kPieces];
+      s.init(static_cast<const T*>(p.k) + (row0 * G + h / p.share) * p.Dk, G * p.Dk, p.Dk, false, tid - kThreads);
+      s.load(r, nv, tid - kThreads);
+      s.store(sh.k, r, tid - kThreads);
+    }
+    if (wv == 0) {
+      const float g = l < kC ? gate_of<T>(p, bi, t0 + l, h, n) : 0.f;
+      fill_decays(sh.d, g, 1.f);
+    } else if (wv == 1 && l < kC) {
+      sh.beta[l] = beta_of<T>(p, bi, t0 + l, h, n);
+    }
+  }
+  const int ib = wv % MT, tb0 = wv / MT * TT;  // the wave's 16 elements of the keys, and its first block of tokens
+  const int n_blocks = TB * (TB + 1) / 2;
+  f32x4 fq[TT], fk[TT], tk[TT], wu[NB], bu[NB];
+#pragma unroll
+  for (int j = 0; j < TT; j++) fq[j] = fk[j] = tk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NB; j++) wu[j] = bu[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int tbs[NB], sbs[NB];
+#pragma unroll
+  for (int j = 0; j < NB; j++) {
+    int tb = 0, sb = std::min(wv + j * kGradWaves, n_blocks - 1);
+    while (sb > tb) sb -= ++tb;
+    tbs[j] = tb;
+    sbs[j] = sb;
+  }
+  double sd = 0.0;
+  float db = 0.f;  // the part of dbeta that this thread's columns give
+  const int vt = tid / 8, vc = 8 * (tid % 8);  // token and columns that a thread brings of N and dR
+  __syncthreads();
+  for (int v0 = 0; v0 < p.Dv; v0 += 64) {
+    if (v0) __syncthreads();
+    if (wv < 4) {
+      Stage<T, 64, kValue, VEC> s;
+      uint4 r[Tile<T, 64, kValue>::kPieces];
+      s.init(static_cast<const T*>(a.dy) + (row0 * p.H + h) * p.Dv + v0, p.H * p.Dv, p.Dv - v0, false, tid);
+      s.load(r, nv, tid);
+      s.store(sh.a.dy, r, tid);
+    }
+    if (vt < kC) {
+      float x[8], y[8];
+      const int v = v0 + vc;
+      if (v < p.VP) {
+        load8(a.N + left + vt * p.VP + v, x);
+        load8(a.dR + left + vt * p.VP + v, y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] = y[j] = 0.f;
+      }
+      const float be = sh.beta[vt];
+      const float own = be / moved_beta(be);
+      float u[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        db = fmaf(x[j], y[j], db);
+        u[j] = x[j] * be;
+        y[j] *= own;
+      }
+      if (vt < nv) {
+        T* to = static_cast<T*>(p.y) + ((row0 + vt) * p.H + h) * p.Dv + v;
+        const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+        store4(to, lo, p.Dv - v, VEC);
+        store4(to + 4, hi, p.Dv - v - 4, VEC);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        float u4[4] = {u[e], u[e + 1], u[e + 2], u[e + 3]}, r4[4] = {y[e], y[e + 1], y[e + 2], y[e + 3]};
+        put4(u4, sh.a.u[0] + vt * ldv + vc + e, sh.a.u[kN - 1] + vt * ldv + vc + e);
+        put4(r4, sh.a.r[0] + vt * ldv + vc + e, sh.a.r[kN - 1] + vt * ldv + vc + e);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < 2; kk++) {
+      const int v = v0 + 32 * kk + g8;
+      float x[8], y[8];
+      if (16 * ib < p.KP && v < p.VP) {
+        load8(a.S + state + (16 * ib + lr) * int64_t(p.VP) + v, x);
+        load8(a.D + state + (16 * ib + lr) * int64_t(p.VP) + v, y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] = y[j] = 0.f;
+      }
+      if (wv < MT) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          if constexpr (sizeof(T) == 4) sd = fma(double(x[j]), double(y[j]), sd);
+          else s = fmaf(x[j], y[j], s);
+        }
+        if constexpr (sizeof(T) == 2) sd += double(s);
+      }
+      Parts<T, 2> sf, df;
+      sf.set(x);
+      df.set(y);
+#pragma unroll
+      for (int tt = 0; tt < TT; tt++) {
+        const int at = (16 * (tb0 + tt) + lr) * ldv + 32 * kk + g8;
+        const Frag<T> yf = row_frag(sh.a.dy + at);
+        Parts<T, 2> uf, rf;
+#pragma unroll
+        for (int e = 0; e < kN; e++) {
+          uf.f[e] = row_frag(sh.a.u[e] + at);
+          rf.f[e] = row_frag(sh.a.r[e] + at);
+          fq[tt] = mma(sf.f[e], yf, fq[tt]);
+        }
+        fk[tt] = mma_parts(sf, rf, fk[tt]);
+        tk[tt] = mma_parts(df, uf, tk[tt]);
+      }
+#pragma unroll
+      for (int j = 0; j < NB; j++) {
+        if (wv + j * kGradWaves < n_blocks) {
+          Parts<T, 2> uf, rf;
+          const int su = (16 * sbs[j] + lr) * ldv + 32 * kk + g8, st = (16 * tbs[j] + lr) * ldv + 32 * kk + g8;
+          const Frag<T> yf = row_frag(sh.a.dy + st);
+#pragma unroll
+          for (int e = 0; e < kN; e++) {
+            uf.f[e] = row_frag(sh.a.u[e] + su);
+            rf.f[e] = row_frag(sh.a.r[e] + st);
+            wu[j] = mma(uf.f[e], yf, wu[j]);
+          }
+          bu[j] = mma_parts(uf, rf, bu[j]);
+        }
+      }
+    }
+  }
+  // dbeta: 8 threads have a token
+  if (a.dbeta) {
+    db += __shfl_xor(db, 1);
+    db += __shfl_xor(db, 2);
+    db += __shfl_xor(db, 4);
+    if (tid % 8 == 0 && vt < nv) store_elem(static_cast<T*>(a.dbeta) + (row0 + vt) * p.H + h, db / moved_beta(sh.beta[vt]));
+  }
+  __syncthreads();
+  // ---- W and B + B^T, and what they give the gate ----
+#pragma unroll
+  for (int j = 0; j < NB; j++) {
+    if (wv + j * kGradWaves >= n_blocks) continue;
+    const int tb = tbs[j], sb = sbs[j], t = 16 * tb + lr, s0 = 16 * sb + g4;
+    const float th = sh.d.hi[t], tl = sh.d.lo[t];
+    float w[4], b[4];
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      const float m = exp2_fast((th - sh.d.hi[s0 + r]) + (tl - sh.d.lo[s0 + r]));
+      w[r] = s0 + r <= t ? wu[j][r] * m * p.scale : 0.f;
+      b[r] = s0 + r < t ? -bu[j][r] * m : 0.f;
+    }
+    if (a.dg) {
+      f32x4 qk{0.f, 0.f, 0.f, 0.f}, kk4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < KS; kk++) {
+        const Frag<T> kf = row_frag(sh.k + (16 * sb + lr) * ldk + 32 * kk + g8);
+        qk = mma(kf, row_frag(sh.q + t * ldq + 32 * kk + g8), qk);
+        kk4 = mma(kf, row_frag(sh.k + t * ldk + 32 * kk + g8), kk4);
+      }
+      float x[4], row = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        x[r] = s0 + r < t ? fmaf(w[r], qk[r], b[r] * kk4[r]) : 0.f;
+        row += x[r];
+      }
+      row += __shfl_xor(row, 16);
+      row += __shfl_xor(row, 32);
+      if (l < 16) sh.rows[sb][t] = row;
+#pragma unroll
+      for (int off = 1; off < 16; off *= 2)
+#pragma unroll
+        for (int r = 0; r < 4; r++) x[r] += __shfl_xor(x[r], off);
+      if (lr == 0) *reinterpret_cast<float4*>(&sh.cols[tb][s0]) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+    put4(w, sh.b.W[0] + t * ldw + s0, sh.b.W[kN - 1] + t * ldw + s0);
+    if (tb > sb) {
+      put4(b, sh.b.B[0] + t * ldw + s0, sh.b.B[kN - 1] + t * ldw + s0);
+#pragma unroll
+      for (int r = 0; r < 4; r++) put1(b[r], sh.b.B[0] + (s0 + r) * ldw + t, sh.b.B[kN - 1] + (s0 + r) * ldw + t);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int s = s0 + r;
+        if (s <= t) put1(b[r], sh.b.B[0] + t * ldw + s, sh.b.B[kN - 1] + t * ldw + s);
+        if (s < t) put1(b[r], sh.b.B[0] + s * ldw + t, sh.b.B[kN - 1] + s * ldw + t);
+      }
+      if (tb % 2 == 0 && tb + 1 < TB) {  // the block beside the diagonal that the products read
+        float z[4] = {0.f, 0.f, 0.f, 0.f};
+        put4(z, sh.b.W[0] + t * ldw + s0 + 16, sh.b.W[kN - 1] + t * ldw + s0 + 16);
+      }
+    }
+  }
+  __syncthreads();
+  // ---- dq, dk ----
+#pragma unroll
+  for (int tt = 0; tt < TT; tt++) {
+    const int tb = tb0 + tt, t = 16 * tb + lr, i = 16 * ib + g4;
+    const float in = sh.d.in[t], out = sh.d.out[t];
+    f32x4 dq, dk;
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      dq[r] = fq[tt][r] * (in * p.scale);
+      const float from = -fk[tt][r] * in, to = tk[tt][r] * out;
+      fk[tt][r] = from;
+      tk[tt][r] = to;
+      dk[r] = from + to;
+    }
+    if (a.dg) {
+      const float4 q4 = lds4(sh.q + t * ldq + i), k4 = lds4(sh.k + t * ldk + i);
+      const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, kv[4] = {k4.x, k4.y, k4.z, k4.w};
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        x = fmaf(qv[r], dq[r], fmaf(kv[r], fk[tt][r], x));
+        y = fmaf(kv[r], tk[tt][r], y);
+      }
+      x += __shfl_xor(x, 16);
+      x += __shfl_xor(x, 32);
+      y += __shfl_xor(y, 16);
+      y += __shfl_xor(y, 32);
+      if (l < 16) {
+        sh.dots[ib][t] = x;
+        sh.kept[ib][t] = y;
+      }
+    }
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ks++) {
+      const Frag<T> kf = col_frag(sh.k, ldk, 32 * ks + g8, 16 * ib, 4);
+      if (ks <= tb / 2) {
+#pragma unroll
+        for (int e = 0; e < kN; e++) dq = mma(kf, row_frag(sh.b.W[e] + t * ldw + 32 * ks + g8), dq);
+      }
+      if (ks >= tb / 2) {
+        const Frag<T> qf = col_frag(sh.q, ldq, 32 * ks + g8, 16 * ib, 4);
+#pragma unroll
+        for (int e = 0; e < kN; e++) dk = mma(qf, col_frag(sh.b.W[e], ldw, 32 * ks + g8, 16 * tb, 4), dk);
+      }
+#pragma unroll
+      for (int e = 0; e < kN; e++) dk = mma(kf, row_frag(sh.b.B[e] + t * ldw + 32 * ks + g8), dk);
+    }
+    if (t < nv) {
+      const int64_t at = ((row0 + t) * p.H + h) * p.Dk + i;
+      const float x[4] = {dq[0], dq[1], dq[2], dq[3]}, y[4] = {dk[0], dk[1], dk[2], dk[3]};
+      if (a.dqk_f32) {
+        store4(static_cast<float*>(a.dq) + at, x, p.Dk - i, VEC);
+        store4(static_cast<float*>(a.dk) + at, y, p.Dk - i, VEC);
+      } else {
+        store4(static_cast<T*>(a.dq) + at, x, p.Dk - i, VEC);
+        store4(static_cast<T*>(a.dk) + at, y, p.Dk - i, VEC);
+      }
+    }
+  }
+  if (!a.dg) return;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) sd += __shfl_xor(sd, off);
+  if (l == 0) sh.sd[wv] = sd;
+  __syncthreads();
+  if (wv != 0) return;
+  // dg, lane l with token l: sums from a token on, that start again at a reset
+  double x = 0.0, kept = 0.0;
+  bool reset = false;
+  if (l < nv) {
+    for (int j = 0; j < MT; j++) {
+      x += double(sh.dots[j][l]);
+      kept += double(sh.kept[j][l]);
+    }
+    for (int j = 0; j <= l / 16; j++) x += double(sh.rows[j][l]);
+    for (int j = l / 16; j < TB; j++) x -= double(sh.cols[j][l]);
+    x -= kept;
+    reset = gate_of<T>(p, bi, t0 + l, h, n) < kZeroLog;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) kept += __shfl_xor(kept, off);
+  double end = 0.0;
+  for (int j = 0; j < kGradWaves; j++) end += sh.sd[j];
+  end = end * double(sh.d.all) + kept;
+  if (l == kWave - 1) x += end;
+  if (reset) x = 0.0;
+#pragma unroll
+  for (int off = 1; off < kWave; off *= 2) {
+    const double later = __shfl_down(x, off);
+    const bool cut = __shfl_down(int(reset), off) != 0;
+    if (l + off < kWave && !reset) {
+      x += later;
+      reset = cut;
+    }
+  }
+  if (l < nv) store_elem(static_cast<T*>(a.dg) + (row0 + l) * p.H + h, float(x));
+}
+
+// ---------------------------------------------------------------------------
+// One token: a workgroup holds one head of one batch row, the whole state in registers (NR rows of VEC columns a thread):
+// lanes run along its columns, groups of them along its rows.  What the state answers for k and for q is summed over
+// the groups at once, in LDS: y = scale (r S^T q + (q . k) u).  The state is read and written once: bound by HBM.
+// ---------------------------------------------------------------------------
+template <typename T, int VEC, int NR>
+__global__ __launch_bounds__(256) void update_kernel(Rule p, float* __restrict__ state, int lanes) {
+  __shared__ float qs[kMaxDim], ks[kMaxDim], pk[256 * VEC], pq[256 * VEC], kq_part[4];
+  const int h = blockIdx.x % p.H, G = p.H / p.share;
+  const int64_t bi = blockIdx.x / p.H, bh = bi * p.H + h, qrow = bi * G + h / p.share;
+  const int Dk = p.Dk, Dv = p.Dv;
+  T* y = static_cast<T*>(p.y) + bh * Dv;
+  if (p.lengths && p.lengths[bi] <= 0) {
+    for (int j = threadIdx.x; j < Dv; j += 256) store_elem(y + j, 0.f);
+    return;
+  }
+  const int l = threadIdx.x % lanes, r0 = threadIdx.x / lanes, groups = 256 / lanes, c = l * VEC;
+  float* at = state + bh * Dk * Dv + c;
+  float S[NR][VEC];
+#pragma unroll
+  for (int i = 0; i < NR; i++) {
+    const int r = r0 + i * groups;
+#pragma unroll
+    for (int j = 0; j < VEC; j++) S[i][j] = 0.f;
+    if (r < Dk && c < Dv) {
+      if constexpr (VEC == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(at + r * Dv);
+        S[i][0] = u.x; S[i][1] = u.y; S[i][2] = u.z; S[i][3] = u.w;
+      } else {
+        S[i][0] = at[r * Dv];
+      }
+    }
+  }
+  float kq = 0.f;
+  if (int(threadIdx.x) < kMaxDim) {
+    const int j = threadIdx.x;
+    const float q = j < Dk ? load_elem(static_cast<const T*>(p.q) + qrow * Dk + j) : 0.f;
+    const float k = j < Dk ? load_elem(static_cast<const T*>(p.k) + qrow * Dk + j) : 0.f;
+    qs[j] = q;
+    ks[j] = k;
+    kq = q * k;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) kq += __shfl_xor(kq, off);
+  if (threadIdx.x % kWave == 0) kq_part[threadIdx.x / kWave] = kq;
+  const float beta = p.beta ? load_elem(static_cast<const T*>(p.beta) + bh) : 1.f;
+  const float dec = expf(clamp_log((p.A ? p.A[h] : 0.f) + (p.g ? load_elem(static_cast<const T*>(p.g) + bh) : 0.f)));
+  float v[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; j++) v[j] = c + j < Dv ? load_elem(static_cast<const T*>(p.v) + bh * Dv + c + j) : 0.f;
+  __syncthreads();
+  float ak[VEC], aq[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; j++) ak[j] = aq[j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NR; i++) {
+    const int r = r0 + i * groups;
+    if (r < Dk) {
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        S[i][j] *= dec;
+        ak[j] = fmaf(ks[r], S[i][j], ak[j]);
+        aq[j] = fmaf(qs[r], S[i][j], aq[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; j++) {
+    pk[(r0 * lanes + l) * VEC + j] = ak[j];
+    pq[(r0 * lanes + l) * VEC + j] = aq[j];
+  }
+  __syncthreads();
+  float u[VEC], o[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; j++) u[j] = o[j] = 0.f;
+  for (int r = 0; r < groups; r++) {
+#pragma unroll
+    for (int j = 0; j < VEC; j++) {
+      u[j] += pk[(r * lanes + l) * VEC + j];
+      o[j] += pq[(r * lanes + l) * VEC + j];
+    }
+  }
+  kq = kq_part[0] + kq_part[1];
+#pragma unroll
+  for (int j = 0; j < VEC; j++) {
+    u[j] = beta * (v[j] - u[j]);
+    o[j] = fmaf(kq, u[j], o[j]) * p.scale;
+  }
+  if (c >= Dv) return;
+#pragma unroll
+  for (int i = 0; i < NR; i++) {
+    const int r = r0 + i * groups;
+    if (r < Dk) {
+#pragma unroll
+      for (int j = 0; j < VEC; j++) S[i][j] = fmaf(ks[r], u[j], S[i][j]);
+      if constexpr (VEC == 4) *reinterpret_cast<float4*>(at + r * Dv) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+      else at[r * Dv] = S[i][0];
+    }
+  }
+  if (r0 == 0)
+#pragma unroll
+    for (int j = 0; j < VEC; j++)
+      if (c + j < Dv) store_elem(y + c + j, o[j]);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr int64_t kSumBlocks = int64_t(1) << 22;  // a grid holds less than 2^32 threads: beyond, a thread has several sums
+constexpr size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+constexpr int kTile = 64;  // columns of the values a workgroup of the sweep has
+
+// rows of whole 16-byte pieces, 16-byte aligned
+template <typename T>
+bool pieces(const void* x, int64_t D) {
+  return D % (16 / int(sizeof(T))) == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+}
+
+Rule rule_of(const DeltaRuleArgs& a) {
+  Rule p{};
+  p.q = a.q; p.k = a.k; p.v = a.v; p.beta = a.beta; p.g = a.g; p.A = a.A; p.lengths = a.lengths; p.scale = a.scale;
+  p.stream = a.stream;
+  p.b = a.b; p.L = a.L; p.H = int(a.H); p.share = int(a.H / a.G); p.Dk = int(a.Dk); p.Dv = int(a.Dv);
+  p.KP = int(ceil_div(a.Dk, 16) * 16);
+  p.VP = int(ceil_div(a.Dv, 16) * 16);
+  p.n_chunks = int(ceil_div(a.L, a.dtype == 0 ? kChunk<float> : kChunk<bf16_bits>));
+  p.n_tiles = int(ceil_div(a.Dv, kTile));
+  return p;
+}
+
+// Bytes from the workspace's start of its parts.
+struct Work {
+  size_t lower, upper, S, D, N, dR, dq, dk, total;
+};
+Work plan_work(const DeltaRuleArgs& a, bool backward) {
+  Work w{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += up256(bytes);
+    return r;
+  };
+  const Rule p = rule_of(a);
+  const size_t chunks = size_t(a.b) * a.H * p.n_chunks;
+  const size_t tri = chunks * (a.dtype == 0 ? Shape<float>::kTri : Shape<bf16_bits>::kTri) * 512 * 4;
+  w.lower = take(tri);
+  if (backward) {
+    const size_t state = chunks * p.KP * p.VP * 4;
+    const size_t rows = chunks * (a.dtype == 0 ? kChunk<float> : kChunk<bf16_bits>) * p.VP * 4;
+    w.upper = take(tri);
+    w.S = take(state);
+    w.D = take(state);
+    w.N = take(rows);
+    w.dR = take(rows);
+    if (a.G != a.H) {
+      w.dq = take(size_t(a.b) * a.L * a.H * a.Dk * 4);
+      w.dk = take(size_t(a.b) * a.L * a.H * a.Dk * 4);
+    }
+  }
+  w.total = at;
+  return w;
+}
+
+template <typename T>
+hipError_t run_tri(const Rule& p, float* lower, float* upper) {
+  const int64_t blocks = p.b * p.H * p.n_chunks;
+  const bool vec = pieces<T>(p.k, p.Dk);
+  auto go = [&](auto kern) { return launch_kind(kKindDeltaTri, kern, blocks, kThreads, p.stream, p, lower, upper); };
+  if (p.Dk <= 64) return vec ? go(tri_kernel<T, 64, true>) : go(tri_kernel<T, 64, false>);
+  return vec ? go(tri_kernel<T, 128, true>) : go(tri_kernel<T, 128, false>);
+}
+
+template <typename T, Mode MODE>
+hipError_t run_sweep(const Rule& p) {
+  const int64_t blocks = p.b * p.H * p.n_tiles;
+  const bool vec = pieces<T>(p.q, p.Dk) && pieces<T>(p.k, p.Dk) && pieces<T>(p.v, p.Dv) && (MODE != kForward || pieces<T>(p.y, p.Dv));
+  auto go = [&](auto kern) { return launch_kind(kKindDeltaSweep, kern, blocks, kThreads + kWave * state_waves(kTile), p.stream, p); };
+  if (p.Dk <= 64) return vec ? go(sweep_kernel<T, 64, kTile, MODE, true>) : go(sweep_kernel<T, 64, kTile, MODE, false>);
+  return vec ? go(sweep_kernel<T, 128, kTile, MODE, true>) : go(sweep_kernel<T, 128, kTile, MODE, false>);
+}
+
+template <typename T>
+hipError_t run_grad(const Grad& a) {
+  const Rule& p = a.p;
+  const int64_t blocks = p.b * p.H * p.n_chunks;
+  const bool vec = pieces<T>(p.q, p.Dk) && pieces<T>(p.k, p.Dk) && pieces<T>(a.dy, p.Dv) && pieces<T>(p.y, p.Dv) &&
+                   pieces<T>(a.dq, p.Dk) && pieces<T>(a.dk, p.Dk);
+  auto go = [&](auto kern) { return launch_kind(kKindDeltaGrad, kern, blocks, kGradWaves * kWave, p.stream, a); };
+  if (p.Dk <= 64) return vec ? go(grad_kernel<T, 64, true>) : go(grad_kernel<T, 64, false>);
+  return vec ? go(grad_kernel<T, 128, true>) : go(grad_kernel<T, 128, false>);
+}
+
+template <typename T>
+hipError_t fwd_impl(const DeltaRuleArgs& a, char* ws) {
+  const Work w = plan_work(a, false);
+  Rule p = rule_of(a);
+  float* lower = reinterpret_cast<float*>(ws + w.lower);
+  const hipError_t err = run_tri<T>(p, lower, nullptr);
+  if (err != hipSuccess) return err;
+  p.tri = lower;
+  p.init = a.h0;
+  p.y = a.y;
+  p.last = a.last;
+  return run_sweep<T, kForward>(p);
+}
+
+template <typename T>
+hipError_t bwd_impl(const DeltaRuleArgs& a, char* ws) {
+  const Work w = plan_work(a, true);
+  auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  Rule p = rule_of(a);
+  p.backward = true;
+  hipError_t err = run_tri<T>(p, at(w.lower), at(w.upper));
+  if (err != hipSuccess) return err;
+  Rule f = p, r = p;
+  f.tri = at(w.lower);
+  f.init = a.h0;
+  f.states = at(w.S);
+  f.left = at(w.N);
+  err = run_sweep<T, kStates>(f);
+  if (err != hipSuccess) return err;
+  r.v = a.dy;
+  r.tri = at(w.upper);
+  r.init = a.dlast;
+  r.states = at(w.D);
+  r.left = at(w.dR);
+  r.last = a.dh0;
+  err = run_sweep<T, kBackwards>(r);
+  if (err != hipSuccess || a.L == 0) return err;
+  const bool shared = p.share > 1;
+  Grad g{};
+  g.p = p;
+  g.p.y = a.dv;
+  g.dy = a.dy;
+  g.S = at(w.S); g.D = at(w.D); g.N = at(w.N); g.dR = at(w.dR);
+  g.dq = shared ? static_cast<void*>(at(w.dq)) : a.dq;
+  g.dk = shared ? static_cast<void*>(at(w.dk)) : a.dk;
+  g.dqk_f32 = shared;
+  g.dbeta = a.dbeta;
+  g.dg = a.dg;
+  err = run_grad<T>(g);
+  if (err != hipSuccess || !shared) return err;
+  const int64_t n = a.b * a.L * a.G * a.Dk;
+  for (int k = 0; k < 2; k++) {
+    const float* in = k ? at(w.dk) : at(w.dq);
+    T* out = static_cast<T*>(k ? a.dk : a.dq);
+    const bool vec = a.Dk % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
+    err = vec ? launch_kind(kKindDeltaReduce, lin_group_sum_kernel<T, 4>, std::min(ceil_div(n, 1024), kSumBlocks), 256, a.stream, in, out, n, p.share, int(a.Dk))
+              : launch_kind(kKindDeltaReduce, lin_group_sum_kernel<T, 1>, std::min(ceil_div(n, 256), kSumBlocks), 256, a.stream, in, out, n, p.share, int(a.Dk));
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+template <typename T>
+hipError_t update_impl(const DeltaRuleArgs& a) {
+  Rule p = rule_of(a);
+  p.y = a.y;
+  const bool vec = a.Dv % 4 == 0 && reinterpret_cast<uintptr_t>(a.last) % 16 == 0;
+  int lanes = 1;
+  while (lanes * (vec ? 4 : 1) < a.Dv) lanes *= 2;
+  const int64_t rows = ceil_div(a.Dk, 256 / lanes);  // of the state a thread has: at most 16 in vectors, 64 else
+  auto go = [&](auto kern) { return launch_kind(kKindDeltaUpdate, kern, a.b * a.H, 256, a.stream, p, a.last, lanes); };
+  if (vec) return rows <= 4 ? go(update_kernel<T, 4, 4>) : rows <= 8 ? go(update_kernel<T, 4, 8>) : go(update_kernel<T, 4, 16>);
+  return rows <= 16 ? go(update_kernel<T, 1, 16>) : go(update_kernel<T, 1, 64>);
+}
+
+}  // namespace
+
+int64_t deltarule_max_dim() { return kMaxDim; }
+int64_t deltarule_max_heads() { return 65535; }
+
+size_t deltarule_workspace_bytes(const DeltaRuleArgs& a, bool backward) {
+  if (a.b == 0 || a.H == 0) return 0;
+  return plan_work(a, backward).total;
+}
+
+hipError_t launch_deltarule_fwd(const DeltaRuleArgs& a, void* workspace) {
+  char* ws = static_cast<char*>(workspace);
+  return a.dtype == 0 ? fwd_impl<float>(a, ws) : fwd_impl<bf16_bits>(a, ws);
+}
+
+hipError_t launch_deltarule_bwd(const DeltaRuleArgs& a, void* workspace) {
+  char* ws = static_cast<char*>(workspace);
+  return a.dtype == 0 ? bwd_impl<float>(a, ws) : bwd_impl<bf16_bits>(a, ws);
+}
+
+hipError_t launch_deltarule_update(const DeltaRuleArgs& a) {
+  return a.dtype == 0 ? update_impl<float>(a) : update_impl<bf16_bits>(a);
+}
+
+}  // namespace ssm

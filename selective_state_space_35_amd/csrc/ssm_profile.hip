@@ -29,7 +29,9 @@ const char* const kNames[kNumKinds] = {"chunk_aggregate", "chunk_carry",   "scan
                                        "ssd_state",       "ssd_carry",     "ssd_scan",      "scan_fused",
                                        "widen_rows",      "linattn_sweep", "linattn_state", "linattn_chain",
                                        "linattn_gate",    "linattn_reduce", "linattn_update", "layernorm",
-                                       "layernorm_bwd",   "layernorm_reduce"};
+                                       "layernorm_bwd",   "layernorm_reduce", "deltarule_tri", "deltarule_sweep",
+                                       "deltarule_grad",  "deltarule_reduce", "deltarule_update", "blocknorm",
+                                       "blocknorm_bwd",   "blocknorm_reduce"};
 
 }  // namespace
 
