@@ -10,14 +10,14 @@
 //   R = V - exp(G) K S,  (I + X diag(beta)) N = R,  U = beta N
 //   Y = scale (exp(G) Q S + P U),  P_ts = exp(G_t - G_s) q_t . k_s for s <= t
 //   S' = exp(G_C) S + K^T (exp(G_C - G) U)
-// The inverse Z = (I + X diag(beta))^-1 needs the keys only, so it is taken for all chunks at once (tri_kernel); what runs
+// The inverse Z = (I + X diag(beta))^-1 needs the keys only, so it is taken for all chunks at once (delta_tri_kernel); what runs
 // from chunk to chunk are products with the state (sweep).
 //
 // Backward, D the gradient of the state leaving the chunk:
 //   dU = scale P^T dY + exp(G_C - G) K D,  dR = Z^T beta dU,  dV = dR
 //   D' = exp(G_C) D + scale (exp(G) Q)^T dY - (exp(G) K)^T dR
 // is the same sweep from the last chunk to the first.  With S, D, N and dR of every chunk the rest is each chunk's own
-// (grad_kernel), W = scale exp(G_t - G_s) dY U^T (s <= t), B = -exp(G_t - G_s) dR U^T (s < t):
+// (delta_grad_kernel), W = scale exp(G_t - G_s) dY U^T (s <= t), B = -exp(G_t - G_s) dR U^T (s < t):
 //   dQ = scale exp(G) dY S^T + W K,  dK = W^T Q + (B + B^T) K + exp(G_C - G) U D^T - exp(G) dR S^T
 //   dbeta_t = dR_t . N_t / beta_t
 // and dg_t sums, over the terms above that hold a factor exp(G) with token t's gate in it, the term: the entries of
@@ -54,13 +54,14 @@ struct Rule {
   const float* A;
   const int32_t* lengths;
   float scale;
-  bool backward;           // a small beta is moved away from zero (tri_kernel)
+  bool backward;           // a small beta is moved away from zero (delta_tri_kernel)
   const float* init;       // the state before the sweep's first chunk, or (backwards) the gradient behind its last
   void* y;
   float* last;             // the state after the sweep's last chunk
   const float* tri;        // [b H n_chunks] inverses as operand fragments
-  float* states;           // [b H n_chunks][KP][VP]: states entering the chunks, or gradients of those leaving them
-  float* left;             // [b H n_chunks][C][VP]: N, or dR of the moved beta
+  // what the backward keeps of a chunk, 16 rows by 16 rows and in those by columns, as a lane of the sweep has them
+  float* states;           // [b H n_chunks][KP / 16][VP][16]: states entering the chunks, or gradients of those leaving them
+  float* left;             // [b H n_chunks][C / 16][VP][16]: N, or dR of the moved beta
   int64_t b, L;
   int H, share, Dk, Dv, KP, VP, n_chunks, n_tiles;
   hipStream_t stream;
@@ -126,6 +127,35 @@ __device__ __forceinline__ f32x8 col_pair(const float* t, int ld, int r, int c0)
   return f32x8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
 }
 
+// One value a token of [b, L, H], as it comes from memory, lane l with the chunk's token l: nothing but the load, and no
+// branch around it, so that what waits for one chunk's does not wait for the next one's.
+template <typename T, int kC>
+struct Scalars {
+  const T* base;
+  int voff, chunk;
+  __device__ __forceinline__ void init(const void* x, int64_t row, int H, int h) {
+    const int l = threadIdx.x % kWave;
+    base = static_cast<const T*>(x) + row * H + h;
+    chunk = kC * H;
+    voff = x && l < kC ? l * H * int(sizeof(T)) : 0x7fffffff;
+  }
+  __device__ __forceinline__ uint32_t load(int nv) {
+    const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(base);
+    base += chunk;
+    const int at = int(threadIdx.x % kWave) < nv ? voff : 0x7fffffff;
+    if constexpr (sizeof(T) == 4) return __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0);
+  }
+  static __device__ __forceinline__ float value(uint32_t raw) { return __uint_as_float(sizeof(T) == 4 ? raw : raw << 16); }
+};
+
+// Two floats rounded to bf16, in one instruction
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+  typedef __attribute__((ext_vector_type(2))) float f2;
+  typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{lo, hi}), b2));
+}
+
 // Floats as operand fragments: bf16 in N parts of 8 bits each (2^-9, 2^-17, 2^-25 of them is lost), float as they are
 template <typename T, int N>
 struct Parts {
@@ -140,9 +170,16 @@ struct Parts {
       for (int j = 0; j < 8; j++) y[j] = x[j];
 #pragma unroll
       for (int k = 0; k < kN; k++) {
-        make_frag(y, f[k]);
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 8; j++) y[j] -= static_cast<float>(f[k][j]);
+        for (int j = 0; j < 4; j++) {
+          w[j] = pack_pair(y[2 * j], y[2 * j + 1]);
+          if (k + 1 < kN) {
+            y[2 * j] -= __uint_as_float(w[j] << 16);
+            y[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
+          }
+        }
+        f[k] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
       }
     }
   }
@@ -171,11 +208,11 @@ __device__ __forceinline__ f32x4 mma_parts(const Parts<T, NA>& a, const Parts<T,
 // finite is taken as zero: the sweep makes NaN of everything from its token on.
 // ---------------------------------------------------------------------------
 template <typename T, int KDP, bool VEC>
-__global__ __launch_bounds__(kThreads) void tri_kernel(Rule p, float* lower, float* upper) {
+__global__ __launch_bounds__(kThreads) void delta_tri_kernel(Rule p, float* lower, float* upper) {
   typedef Shape<T> Z;
   constexpr int kC = Z::kC, TB = Z::TB, KS = KDP / 32, ldk = Tile<T, KDP, kKey>::ld, ld = kC + 4;
   __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP, kKey>::kElems];
-  __shared__ __attribute__((aligned(16))) float X[kC * ld], inv[kC * ld];
+  __shared__ __attribute__((aligned(16))) float X[kC * ld];  // X diag(beta); block by block its inverse takes its place
   __shared__ Decays<kC> d;
   __shared__ float beta[kC];
   const int64_t id = blockIdx.x, bh = id / p.n_chunks, bi = bh / p.H;
@@ -217,28 +254,31 @@ __global__ __launch_bounds__(kThreads) void tri_kernel(Rule p, float* lower, flo
   __syncthreads();
   if (tid < kC) {  // lane l has column l % 16 of block l / 16
     const int b0 = 16 * (l / 16);
+    float4 a4[16][4];
+#pragma unroll
+    for (int i = 1; i < 16; i++)
+#pragma unroll
+      for (int k4 = 0; k4 < (i + 3) / 4; k4++) a4[i][k4] = lds4(X + (b0 + i) * ld + b0 + 4 * k4);
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; i++) {
-      float s = i == lr ? 1.f : 0.f;
-      const float4* row = reinterpret_cast<const float4*>(X + (b0 + i) * ld + b0);
+      float s[2] = {i == lr ? 1.f : 0.f, 0.f};
 #pragma unroll
-      for (int k4 = 0; k4 < (i + 3) / 4; k4++) {
-        const float4 a = row[k4];
-        const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-          if (4 * k4 + k < i) s = fmaf(-av[k], x[4 * k4 + k], s);
+      for (int k = 0; k < i; k++) {
+        const float4& r = a4[i][k / 4];
+        s[k % 2] = fmaf(-(k % 4 == 0 ? r.x : k % 4 == 1 ? r.y : k % 4 == 2 ? r.z : r.w), x[k], s[k % 2]);
       }
-      x[i] = s;
-      inv[(b0 + i) * ld + b0 + lr] = s;
+      x[i] = s[0] + s[1];
     }
+    __builtin_amdgcn_sched_barrier(0);  // one wave reads and writes the blocks, in this order
+#pragma unroll
+    for (int i = 0; i < 16; i++) X[(b0 + i) * ld + b0 + lr] = x[i];
   }
   __syncthreads();
+  f32x4 col[TB];
   if (wv < TB - 1) {
-    f32x4 col[TB];
 #pragma unroll
-    for (int r = 0; r < 4; r++) col[0][r] = inv[(16 * wv + g4 + r) * ld + 16 * wv + lr];
+    for (int r = 0; r < 4; r++) col[0][r] = X[(16 * wv + g4 + r) * ld + 16 * wv + lr];
 #pragma unroll
     for (int o = 1; o < TB; o++) {  // block row wv + o
       const int i = wv + o;
@@ -247,14 +287,19 @@ __global__ __launch_bounds__(kThreads) void tri_kernel(Rule p, float* lower, flo
 #pragma unroll
         for (int k = 0; k < o; k++) t = mma16(lds4(X + (16 * i + lr) * ld + 16 * (wv + k) + g4), col[k], t);
         f32x4 z{0.f, 0.f, 0.f, 0.f};
-        z = mma16(lds4(inv + (16 * i + lr) * ld + 16 * i + g4), t, z);
+        z = mma16(lds4(X + (16 * i + lr) * ld + 16 * i + g4), t, z);
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
-          col[o][r] = -z[r];
-          inv[(16 * i + g4 + r) * ld + 16 * wv + lr] = -z[r];
-        }
+        for (int r = 0; r < 4; r++) col[o][r] = -z[r];
       }
     }
+  }
+  __syncthreads();  // the blocks below the diagonal have been read by all
+  if (wv < TB - 1) {
+#pragma unroll
+    for (int o = 1; o < TB; o++)
+      if (wv + o < TB)
+#pragma unroll
+        for (int r = 0; r < 4; r++) X[(16 * (wv + o) + g4 + r) * ld + 16 * wv + lr] = col[o][r];
   }
   __syncthreads();
   float4* out = reinterpret_cast<float4*>(lower + id * (Z::kTri * 512));
@@ -266,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void tri_kernel(Rule p, float* lower, flo
     for (int a = 0; a < TB; a++)
       for (int b = 0; b <= a / 2; b++)
         if (lower_frag<TB>(a, b) == f) tb = a, ks = b;
-    const float* row = inv + (16 * tb + r16) * ld + 32 * ks + q4;
+    const float* row = X + (16 * tb + r16) * ld + 32 * ks + q4;
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     out[2 * j] = lds4(row);
     out[2 * j + 1] = 2 * ks + 1 <= tb ? lds4(row + 16) : zero;
@@ -281,7 +326,7 @@ __global__ __launch_bounds__(kThreads) void tri_kernel(Rule p, float* lower, flo
 #pragma unroll
       for (int e = 0; e < 8; e++) {
         const int t = 32 * ks + q4 + e % 4 + 16 * (e / 4);
-        x[e] = t / 16 >= sb ? inv[t * ld + 16 * sb + r16] * beta[t] : 0.f;
+        x[e] = t / 16 >= sb ? X[t * ld + 16 * sb + r16] * beta[t] : 0.f;
       }
       out_t[2 * j] = make_float4(x[0], x[1], x[2], x[3]);
       out_t[2 * j + 1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -317,7 +362,7 @@ struct SweepLds {
 
 template <typename T, int KDP, int VT, Mode MODE, bool VEC>
 __global__ __launch_bounds__(kThreads + kWave * state_waves(VT)) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void sweep_kernel(Rule p) {
+void delta_sweep_kernel(Rule p) {
   typedef Shape<T> Z;
   constexpr int kC = Z::kC, TB = Z::TB, kSteps = Z::kSteps, kTri = Z::kTri, KS = KDP / 32, MT = KDP / 16;
   constexpr bool kTwo = Z::kTwo, kBack = MODE == kBackwards, kOut = MODE == kForward;
@@ -365,32 +410,34 @@ void sweep_kernel(Rule p) {
     struct Regs {
       uint4 q[Tile<T, KDP, kQuery>::kPieces], k[Tile<T, KDP, kKey>::kPieces], v[Tile<T, VT, kValue>::kPieces];
       float4 z[kZ][2];
-      float gate, beta;
+      uint32_t gate, beta;
     };
     Regs r0, r1;
     auto live = [&](int i) { return i < chunks ? n - chunk_of(i) * kC : 0; };
+    const float fixed = p.A ? p.A[h] : 0.f;
+    Scalars<T, kC> sg, sb;
+    sg.init(p.g, t0, p.H, h);
+    sb.init(p.beta, t0, p.H, h);
+    if (kBack) {
+      sg.chunk = -sg.chunk;
+      sb.chunk = -sb.chunk;
+    }
+    const int last = std::max(chunks - 1, 0);
     const float* tri = p.tri + bh * p.n_chunks * (kTri * 512);
     auto fetch = [&](Regs& r, int i) {  // the i-th chunk of the sweep; behind its end nothing is read and the rows are zero
       const int nv = live(i);
       if constexpr (MODE != kStates) sq.load(r.q, nv, tid);
       sk.load(r.k, nv, tid);
       sv.load(r.v, nv, tid);
-      if (i < chunks) {
-        const float4* from = reinterpret_cast<const float4*>(tri + int64_t(chunk_of(i)) * (kTri * 512));
+      const float4* from = reinterpret_cast<const float4*>(tri + int64_t(chunk_of(std::min(i, last))) * (kTri * 512));
 #pragma unroll
-        for (int j = 0; j < kZ; j++) {
-          const int at = tid + j * kThreads;
-          if (at < kTri * 64) {
-            r.z[j][0] = from[2 * at];
-            r.z[j][1] = from[2 * at + 1];
-          }
-        }
-        if (pw == 3 && l < kC) {
-          const int64_t t = int64_t(chunk_of(i)) * kC + l;
-          r.gate = gate_of<T>(p, bi, t, h, n);
-          r.beta = beta_of<T>(p, bi, t, h, n);
-        }
+      for (int j = 0; j < kZ; j++) {
+        const int at = std::min(tid + j * kThreads, kTri * 64 - 1);
+        r.z[j][0] = from[2 * at];
+        r.z[j][1] = from[2 * at + 1];
       }
+      r.gate = sg.load(nv);
+      r.beta = sb.load(nv);
     };
     auto place = [&](const Regs& r, int i) {
       if (i >= chunks) return;
@@ -412,80 +459,112 @@ void sweep_kernel(Rule p) {
     };
     auto decays = [&](const Regs& r, int i) {  // by the wave with the fewest blocks of P
       if (pw != 3 || i >= chunks) return;
-      fill_decays(sh.d[i & 3], l < kC ? r.gate : 0.f, 1.f);
-      if (l < kC) sh.beta[i & 3][l] = kBack ? r.beta / moved_beta(r.beta) : r.beta;
+      const bool on = l < std::min(kC, live(i));
+      fill_decays(sh.d[i & 3], on ? clamp_log(sg.value(r.gate) + fixed) : 0.f, 1.f);
+      const float beta = on ? p.beta ? sb.value(r.beta) : 1.f : 0.f;
+      if (l < kC) sh.beta[i & 3][l] = kBack ? beta / moved_beta(beta) : beta;
     };
-    // one block of P, rows t of q with columns s of k, to its half of a fragment: forwards of P, backwards of its transpose
-    auto score_block = [&](int i, int tb, int sb) {
+    // N blocks of P, rows t of q with columns s of k, to their halves of fragments: forwards of P, backwards of its
+    // transpose.  All reads come first, all products next.
+    auto score_blocks = [&](int i, auto count, int t0, int s0, int t1, int s1, int t2, int s2) {
+      constexpr int N = decltype(count)::value;
+      const int tbs[3] = {t0, t1, t2}, sbs[3] = {s0, s1, s2};
       const T* Qs = sh.q[i & 1];
       const T* Ks = sh.k[i & 1];
       const Decays<kC>& d = sh.d[i & 3];
-      f32x4 a{0.f, 0.f, 0.f, 0.f};
+      Frag<T> qf[N][KS], kf[N][KS];
+      float ch[N], cl[N];
+      float4 h4[N], l4[N];
 #pragma unroll
-      for (int kk = 0; kk < KS; kk++) {
-        const Frag<T> qf = row_frag(Qs + (16 * tb + lr) * ldq + 32 * kk + g8);
-        const Frag<T> kf = row_frag(Ks + (16 * sb + lr) * ldk + 32 * kk + g8);
-        a = kBack ? mma(qf, kf, a) : mma(kf, qf, a);
-      }
-      const int cb = kBack ? sb : tb, rb = kBack ? tb : sb;  // the blocks that run along lanes, and along a lane's four
-      const float ch = d.hi[16 * cb + lr], cl = d.lo[16 * cb + lr];
-      const float4 h4 = lds4(d.hi + 16 * rb + g4), l4 = lds4(d.lo + 16 * rb + g4);
-      const float rh[4] = {h4.x, h4.y, h4.z, h4.w}, rl[4] = {l4.x, l4.y, l4.z, l4.w};
-      float x[4];
+      for (int j = 0; j < N; j++)
 #pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const float diff = (ch - rh[r]) + (cl - rl[r]);
-        const bool in = tb > sb || (kBack ? lr <= g4 + r : g4 + r <= lr);
-        x[r] = in ? a[r] * exp2_fast(kBack ? -diff : diff) * p.scale : 0.f;
+        for (int kk = 0; kk < KS; kk++) {
+          qf[j][kk] = row_frag(Qs + (16 * tbs[j] + lr) * ldq + 32 * kk + g8);
+          kf[j][kk] = row_frag(Ks + (16 * sbs[j] + lr) * ldk + 32 * kk + g8);
+        }
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        const int cb = kBack ? sbs[j] : tbs[j], rb = kBack ? tbs[j] : sbs[j];  // the blocks along lanes, and along a lane's four
+        ch[j] = d.hi[16 * cb + lr];
+        cl[j] = d.lo[16 * cb + lr];
+        h4[j] = lds4(d.hi + 16 * rb + g4);
+        l4[j] = lds4(d.lo + 16 * rb + g4);
       }
-      const int f = kBack ? upper_frag<TB>(sb, tb / 2) : lower_frag<TB>(tb, sb / 2);
-      const int at = f * 512 + l * 8 + 4 * (rb % 2);
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(sh.P[i & 1][0] + at) = make_float4(x[0], x[1], x[2], x[3]);
-      } else {
-        const uint2 hi = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-        *reinterpret_cast<uint2*>(sh.P[i & 1][0] + at) = hi;
-        const float y[4] = {x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xffff0000u),
-                            x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xffff0000u)};
-        *reinterpret_cast<uint2*>(sh.P[i & 1][kTwo ? 1 : 0] + at) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 a[N];
+#pragma unroll
+      for (int j = 0; j < N; j++) a[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < KS; kk++)
+#pragma unroll
+        for (int j = 0; j < N; j++) a[j] = kBack ? mma(qf[j][kk], kf[j][kk], a[j]) : mma(kf[j][kk], qf[j][kk], a[j]);
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        const int tb = tbs[j], sb = sbs[j], rb = kBack ? tb : sb;
+        const float rh[4] = {h4[j].x, h4[j].y, h4[j].z, h4[j].w}, rl[4] = {l4[j].x, l4[j].y, l4[j].z, l4[j].w};
+        float x[4];
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const float diff = (ch[j] - rh[r]) + (cl[j] - rl[r]);
+          const bool in = tb > sb || (kBack ? lr <= g4 + r : g4 + r <= lr);
+          x[r] = in ? a[j][r] * exp2_fast(kBack ? -diff : diff) * p.scale : 0.f;
+        }
+        const int f = kBack ? upper_frag<TB>(sb, tb / 2) : lower_frag<TB>(tb, sb / 2);
+        const int at = f * 512 + l * 8 + 4 * (rb % 2);
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<float4*>(sh.P[i & 1][0] + at) = make_float4(x[0], x[1], x[2], x[3]);
+        } else {
+          const uint2 hi = make_uint2(pack_pair(x[0], x[1]), pack_pair(x[2], x[3]));
+          *reinterpret_cast<uint2*>(sh.P[i & 1][0] + at) = hi;
+          *reinterpret_cast<uint2*>(sh.P[i & 1][kTwo ? 1 : 0] + at) =
+              make_uint2(pack_pair(x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xffff0000u)),
+                         pack_pair(x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xffff0000u)));
+        }
       }
     };
     auto score = [&](int i) {
       if (MODE == kStates || i >= chunks) return;
+      using std::integral_constant;
       if constexpr (TB == 4) {
         if (pw < 3) {
-          score_block(i, 3 - pw, 0);
-          score_block(i, 3 - pw, 1);
-          score_block(i, pw == 2 ? 0 : 3 - pw, pw == 2 ? 0 : 2);
-        } else {
-          score_block(i, 3, 3);
-        }
+          if constexpr (KDP == 64) {
+            score_blocks(i, integral_constant<int, 3>{}, 3 - pw, 0, 3 - pw, 1, pw == 2 ? 0 : 3 - pw, pw == 2 ? 0 : 2);
+          } else {
+            score_blocks(i, integral_constant<int, 2>{}, 3 - pw, 0, 3 - pw, 1, 0, 0);
+            score_blocks(i, integral_constant<int, 1>{}, pw == 2 ? 0 : 3 - pw, pw == 2 ? 0 : 2, 0, 0, 0, 0);
+          }
+        } else score_blocks(i, integral_constant<int, 1>{}, 3, 3, 0, 0, 0, 0);
       } else {
-        if (pw < 3) score_block(i, pw > 0, pw > 1);
+        if (pw < 3) score_blocks(i, integral_constant<int, 1>{}, pw > 0, pw > 1, 0, 0, 0, 0);
       }
     };
-    fetch(r0, 0);
-    fetch(r1, 1);
-    place(r0, 0);
-    decays(r0, 0);
-    fetch(r0, 2);
-    decays(r1, 1);
-    __syncthreads();
-    score(0);
-    __syncthreads();
-    // at the top of step i: chunk i is in the tiles and in P; chunks i + 1 (in r) and i + 2 (in the other set) are in
-    // registers or under way
-    auto step = [&](Regs& r, const Regs& other, int i) {
-      place(r, i + 1);
-      fetch(r, i + 3);
+    if (chunks > 0) {
+      fetch(r0, 0);
+      fetch(r1, 1);
+      place(r0, 0);
+      decays(r0, 0);
+      fetch(r0, 2);
+      decays(r1, 1);
       __syncthreads();
-      score(i + 1);
-      decays(other, i + 2);
+      score(0);
       __syncthreads();
-    };
-    for (int i = 0; i < chunks; i += 2) {
-      step(r1, r0, i);
-      step(r0, r1, i + 1);
+      // at the top of step i: chunk i is in the tiles and in P; chunks i + 1 (in r) and i + 2 (in the other set) are in
+      // registers or under way
+      auto step = [&](Regs& r, const Regs& other, int i) {
+        place(r, i + 1);
+        fetch(r, i + 3);
+        __syncthreads();
+        score(i + 1);
+        decays(other, i + 2);
+        __syncthreads();
+      };
+      for (int i = 0; i < chunks; i += 2) {
+        step(r1, r0, i);
+        step(r0, r1, i + 1);
+      }
+    } else {  // no chunk to bring (and maybe no inverses to read): the state waves' two barriers
+      __syncthreads();
+      __syncthreads();
     }
     if constexpr (kOut) {  // rows behind the length are zero
       const int cols = std::min(VT, p.Dv - v0);
@@ -510,8 +589,26 @@ void sweep_kernel(Rule p) {
         const int i = 16 * m + g4 + r, v = v0 + vw + 16 * j + lr;
         S[m][j][r] = init && i < p.Dk && v < p.Dv ? init[i * p.Dv + v] : 0.f;
       }
+  constexpr int kN3 = Parts<T, 3>::kN, kN2 = Parts<T, 2>::kN;
+  Frag<T> kf[2][TB], qf[2][TB];
+  auto read_rows = [&](int i, int kk) {  // 32 elements of the i-th chunk's keys (and queries)
+#pragma unroll
+    for (int tt = 0; tt < TB; tt++) {
+      const T* kt = sh.k[i & 1] + (16 * tt + lr) * ldk + 32 * kk + g4;
+      kf[kk % 2][tt] = pair_frag(kt, kt + 16);
+      if constexpr (kOut) {
+        const T* qt = sh.q[i & 1] + (16 * tt + lr) * ldq + 32 * kk + g4;
+        qf[kk % 2][tt] = pair_frag(qt, qt + 16);
+      }
+    }
+  };
+  // outputs: a lane has 4 columns of the tokens 16 tt + lane % 16
+  const int yrow = p.H * p.Dv, yoff = (lr * yrow + vw + g4) * int(sizeof(T));
+  T* ybase = kOut ? static_cast<T*>(p.y) + (bi * p.L * p.H + h) * p.Dv + v0 : nullptr;
+  __builtin_amdgcn_s_setprio(2);  // before the wave beside it, whose work is not waited for step by step
   __syncthreads();
   __syncthreads();
+  read_rows(0, 0);
   for (int i = 0; i < chunks; i++) {
     const int c = chunk_of(i), nv = std::min(kC, n - c * kC);
     const Decays<kC>& d = sh.d[i & 3];
@@ -519,7 +616,68 @@ void sweep_kernel(Rule p) {
     const T* Qs = sh.q[i & 1];
     const T* Ks = sh.k[i & 1];
     const T* Vs = sh.v[i & 1];
-    if constexpr (MODE != kForward) {  // what grad_kernel reads: the state entering the chunk, or the gradient leaving it
+    // ---- the state's answers for the keys (and, transposed, for the queries): reads a step ahead of their products ----
+    f32x4 x[TB][NT], o[TB][NT];
+#pragma unroll
+    for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+      for (int j = 0; j < NT; j++) x[tt][j] = o[tt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto times_state = [&](int kk) {
+      Parts<T, 3> s[NT];
+#pragma unroll
+      for (int j = 0; j < NT; j++) s[j].set(S[2 * kk][j], S[2 * kk + 1][j]);
+#pragma unroll
+      for (int e = 0; e < kN3; e++)
+#pragma unroll
+        for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+          for (int j = 0; j < NT; j++) {
+            x[tt][j] = mma(kf[kk % 2][tt], s[j].f[e], x[tt][j]);
+            if constexpr (kOut)
+              if (e < kN2) o[tt][j] = mma(s[j].f[e], qf[kk % 2][tt], o[tt][j]);
+          }
+    };
+#pragma unroll
+    for (int kk = 0; kk + 1 < KS; kk++) {
+      read_rows(i, kk + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      times_state(kk);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    Frag<T> zf[2][kTri], pf[kTri][kN2], yf[kBack ? kSteps : 1][NT];
+    f32x4 vq[kBack ? 1 : TB][NT];
+    float w4[TB][4], b4[TB][4];
+    auto read_z = [&](int e) {
+#pragma unroll
+      for (int f = 0; f < kTri; f++) zf[e % 2][f] = row_frag(sh.z[i & 1][e] + f * 512 + l * 8);
+    };
+    auto read_p = [&]() {
+#pragma unroll
+      for (int f = 0; f < kTri; f++)
+#pragma unroll
+        for (int e = 0; e < kN2; e++) pf[f][e] = row_frag(sh.P[i & 1][e] + f * 512 + l * 8);
+    };
+#pragma unroll
+    for (int tt = 0; tt < TB; tt++) {
+      const float4 a = lds4((kBack ? d.out : d.in) + 16 * tt + g4), be = lds4(beta + 16 * tt + g4);
+      w4[tt][0] = a.x; w4[tt][1] = a.y; w4[tt][2] = a.z; w4[tt][3] = a.w;
+      b4[tt][0] = be.x; b4[tt][1] = be.y; b4[tt][2] = be.z; b4[tt][3] = be.w;
+    }
+    if constexpr (kBack) {
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ks++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) yf[ks][j] = col_pair(Vs, ldv, 32 * ks + g4, vw + 16 * j);
+      read_p();
+    } else {
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) vq[tt][j] = quad_rows(Vs, ldv, 16 * tt + g4, vw + 16 * j);
+      read_z(0);
+    }
+    times_state(KS - 1);
+    if constexpr (MODE != kForward) {  // what delta_grad_kernel reads: the state entering the chunk, or the gradient leaving it
       float* to = p.states + (bh * p.n_chunks + c) * int64_t(p.KP) * p.VP;
 #pragma unroll
       for (int m = 0; m < MT; m++)
@@ -527,91 +685,51 @@ void sweep_kernel(Rule p) {
         for (int j = 0; j < NT; j++) {
           const int v = v0 + vw + 16 * j + lr;
           if (16 * m < p.KP && v < p.VP)
-#pragma unroll
-            for (int r = 0; r < 4; r++) to[(16 * m + g4 + r) * p.VP + v] = S[m][j][r];
+            *reinterpret_cast<float4*>(to + (m * p.VP + v) * 16 + g4) = make_float4(S[m][j][0], S[m][j][1], S[m][j][2], S[m][j][3]);
         }
     }
-    // ---- the state's answers for the keys (and, transposed, for the queries) ----
-    f32x4 x[TB][NT], o[TB][NT];
-#pragma unroll
-    for (int tt = 0; tt < TB; tt++)
-#pragma unroll
-      for (int j = 0; j < NT; j++) x[tt][j] = o[tt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int kk = 0; kk < KS; kk++) {
-      Parts<T, 3> s[NT];
-#pragma unroll
-      for (int j = 0; j < NT; j++) s[j].set(S[2 * kk][j], S[2 * kk + 1][j]);
-#pragma unroll
-      for (int tt = 0; tt < TB; tt++) {
-        const T* at = Ks + (16 * tt + lr) * ldk + 32 * kk + g4;
-        const Frag<T> kf = pair_frag(at, at + 16);
-#pragma unroll
-        for (int e = 0; e < Parts<T, 3>::kN; e++)
-#pragma unroll
-          for (int j = 0; j < NT; j++) x[tt][j] = mma(kf, s[j].f[e], x[tt][j]);
-        if constexpr (kOut) {
-          const T* qt = Qs + (16 * tt + lr) * ldq + 32 * kk + g4;
-          const Frag<T> qf = pair_frag(qt, qt + 16);
-#pragma unroll
-          for (int e = 0; e < (kTwo ? 2 : 1); e++)
-#pragma unroll
-            for (int j = 0; j < NT; j++) o[tt][j] = mma(s[j].f[e], qf, o[tt][j]);
-        }
-      }
-    }
+    __builtin_amdgcn_sched_barrier(0);
     // ---- R, or dU ----
-    if constexpr (!kBack) {
-#pragma unroll
-      for (int tt = 0; tt < TB; tt++) {
-        const float4 a4 = lds4(d.in + 16 * tt + g4), b4 = lds4(beta + 16 * tt + g4);
-        const float a[4] = {a4.x, a4.y, a4.z, a4.w}, be[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-        for (int j = 0; j < NT; j++) {
-          const f32x4 v = quad_rows(Vs, ldv, 16 * tt + g4, vw + 16 * j);
-#pragma unroll
-          for (int r = 0; r < 4; r++) x[tt][j][r] = fmaf(be[r], 0.f, fmaf(-a[r], x[tt][j][r], v[r]));  // NaN where beta is no number
-        }
-      }
-    } else {
-#pragma unroll
-      for (int tt = 0; tt < TB; tt++) {
-        const float4 a4 = lds4(d.out + 16 * tt + g4);
-        const float a[4] = {a4.x, a4.y, a4.z, a4.w};
-#pragma unroll
-        for (int j = 0; j < NT; j++)
-#pragma unroll
-          for (int r = 0; r < 4; r++) x[tt][j][r] *= a[r];
-      }
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ks++) {
-        Frag<T> yf[NT];
-#pragma unroll
-        for (int j = 0; j < NT; j++) yf[j] = col_pair(Vs, ldv, 32 * ks + g4, vw + 16 * j);
-#pragma unroll
-        for (int sb = 0; sb < TB; sb++)
-          if (sb / 2 <= ks)
-#pragma unroll
-            for (int e = 0; e < (kTwo ? 2 : 1); e++) {
-              const Frag<T> pf = row_frag(sh.P[i & 1][e] + upper_frag<TB>(sb, ks) * 512 + l * 8);
-#pragma unroll
-              for (int j = 0; j < NT; j++) x[sb][j] = mma(pf, yf[j], x[sb][j]);
-            }
-      }
-    }
-    // A row that is not finite must not meet Z's zeros: the rows before it would be no numbers.  From it on N is NaN, and so
-    // are the outputs and the state's column.
-    int first[NT];
-    bool bad = false;
-    if constexpr (!kBack) {
-      float z = 0.f;
+    if constexpr (kBack) {
+      read_z(0);
 #pragma unroll
       for (int tt = 0; tt < TB; tt++)
 #pragma unroll
         for (int j = 0; j < NT; j++)
 #pragma unroll
-          for (int r = 0; r < 4; r++) z = fmaf(x[tt][j][r], 0.f, z);
-      bad = __ballot(!(z == 0.f)) != 0;
+          for (int r = 0; r < 4; r++) x[tt][j][r] *= w4[tt][r];
+#pragma unroll
+      for (int e = 0; e < kN2; e++)
+#pragma unroll
+        for (int ks = kSteps - 1; ks >= 0; ks--)
+#pragma unroll
+          for (int sb = 0; sb < TB; sb++)
+            if (sb / 2 <= ks)
+#pragma unroll
+              for (int j = 0; j < NT; j++) x[sb][j] = mma(pf[upper_frag<TB>(sb, ks)][e], yf[ks][j], x[sb][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+          for (int r = 0; r < 4; r++)  // NaN where beta is no number
+            x[tt][j][r] = fmaf(b4[tt][r], 0.f, fmaf(-w4[tt][r], x[tt][j][r], vq[tt][j][r]));
+    }
+    // A row that is not finite must not meet Z's zeros: the rows before it would be no numbers.  From it on N is NaN, and so
+    // are the outputs and the state's column.
+    int first[NT] = {};
+    bool bad = false;
+    if constexpr (!kBack) {
+      float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) z[r] = fmaf(x[tt][j][r], 0.f, z[r]);
+      bad = __ballot(!((z[0] + z[1]) + (z[2] + z[3]) == 0.f)) != 0;
 #pragma unroll
       for (int j = 0; j < NT; j++) first[j] = kC;
       if (__builtin_expect(bad, 0)) {
@@ -636,22 +754,54 @@ void sweep_kernel(Rule p) {
     for (int tt = 0; tt < TB; tt++)
 #pragma unroll
       for (int j = 0; j < NT; j++) nn[tt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    {
+      Parts<T, 3> xf[kSteps][NT];
 #pragma unroll
-    for (int ks = 0; ks < kSteps; ks++) {
-      Parts<T, 3> xf[NT];
+      for (int ks = 0; ks < kSteps; ks++)
 #pragma unroll
-      for (int j = 0; j < NT; j++) xf[j].set(x[2 * ks][j], x[2 * ks + 1][j]);
+        for (int j = 0; j < NT; j++) xf[ks][j].set(x[2 * ks][j], x[2 * ks + 1][j]);
 #pragma unroll
-      for (int tt = 0; tt < TB; tt++)
-        if (kBack ? tt / 2 <= ks : ks <= tt / 2) {
-          Parts<T, 3> zf;
+      for (int ea = 0; ea < kN3; ea++) {
+        if (ea + 1 < kN3) read_z(ea + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int e = 0; e < Parts<T, 3>::kN; e++)
-            zf.f[e] = row_frag(sh.z[i & 1][e] + (kBack ? upper_frag<TB>(tt, ks) : lower_frag<TB>(tt, ks)) * 512 + l * 8);
+        for (int eb = 0; ea + eb < kN3; eb++)
 #pragma unroll
-          for (int j = 0; j < NT; j++) nn[tt][j] = mma_parts(zf, xf[j], nn[tt][j]);
-        }
+          for (int ks = 0; ks < kSteps; ks++)
+#pragma unroll
+            for (int tt = 0; tt < TB; tt++)
+              if (kBack ? tt / 2 <= ks : ks <= tt / 2)
+#pragma unroll
+                for (int j = 0; j < NT; j++)
+                  nn[tt][j] = mma(zf[ea % 2][kBack ? upper_frag<TB>(tt, ks) : lower_frag<TB>(tt, ks)], xf[ks][j].f[eb], nn[tt][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+    // the keys (and queries) as the state's update reads them, for 32 of its rows, a step ahead
+    Frag<T> kc[2][2][kSteps], qc[2][2][kSteps];
+    auto read_cols = [&](int step) {
+#pragma unroll
+      for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ks++) {
+          kc[step % 2][m][ks] = col_pair(Ks, ldk, 32 * ks + g4, 16 * (2 * step + m));
+          if constexpr (kBack) qc[step % 2][m][ks] = col_pair(Qs, ldq, 32 * ks + g4, 16 * (2 * step + m));
+        }
+    };
+    if constexpr (kOut) read_p();
+    read_cols(0);
+    float in[kOut ? TB : 1];
+    if constexpr (kOut) {
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++) in[tt] = d.in[16 * tt + lr] * p.scale;
+    }
+#pragma unroll
+    for (int tt = 0; tt < TB; tt++) {
+      const float4 a = lds4((kBack ? d.in : d.out) + 16 * tt + g4);
+      w4[tt][0] = a.x; w4[tt][1] = a.y; w4[tt][2] = a.z; w4[tt][3] = a.w;
+    }
+    const float all = d.all;
+    __syncthreads();  // the middle of a step: the other waves have the next chunk in its tiles
     if constexpr (MODE != kForward) {
       float* to = p.left + (bh * p.n_chunks + c) * int64_t(kC) * p.VP;
 #pragma unroll
@@ -659,74 +809,94 @@ void sweep_kernel(Rule p) {
 #pragma unroll
         for (int j = 0; j < NT; j++) {
           const int v = v0 + vw + 16 * j + lr;
-          if (v < p.VP)
+          float u[4];
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-              const int t = 16 * tt + g4 + r;
-              to[t * p.VP + v] = !kBack && t >= first[j] ? __builtin_nanf("") : nn[tt][j][r];
-            }
+          for (int r = 0; r < 4; r++) u[r] = bad && 16 * tt + g4 + r >= first[j] ? __builtin_nanf("") : nn[tt][j][r];
+          if (v < p.VP) *reinterpret_cast<float4*>(to + (tt * p.VP + v) * 16 + g4) = make_float4(u[0], u[1], u[2], u[3]);
         }
     }
-    // ---- outputs ----
-    if constexpr (kOut) {
-#pragma unroll
-      for (int tt = 0; tt < TB; tt++) {
-        const float a = d.in[16 * tt + lr] * p.scale;
-#pragma unroll
-        for (int j = 0; j < NT; j++)
-#pragma unroll
-          for (int r = 0; r < 4; r++) o[tt][j][r] *= a;
-      }
-    }
     // U, in the products' parts: as it is for the outputs, with its decay for the state; backwards the two rows that the
-    // state's gradient takes, of dY and of dR
-    Parts<T, 3> wf[kSteps][NT], yf[kBack ? kSteps : 1][NT];
+    // state's gradient takes, of dR and of dY
+    Parts<T, 3> wf[kSteps][NT], wy[kBack ? kSteps : 1][NT];
+    Parts<T, 2> uf[kOut ? kSteps : 1][NT];
 #pragma unroll
-    for (int ks = 0; ks < kSteps; ks++) {
-      float w[2][4], be[2][4];
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const float4 a4 = lds4((kBack ? d.in : d.out) + 32 * ks + 16 * e + g4), b4 = lds4(beta + 32 * ks + 16 * e + g4);
-        w[e][0] = a4.x; w[e][1] = a4.y; w[e][2] = a4.z; w[e][3] = a4.w;
-        be[e][0] = b4.x; be[e][1] = b4.y; be[e][2] = b4.z; be[e][3] = b4.w;
-      }
+    for (int ks = 0; ks < kSteps; ks++)
 #pragma unroll
       for (int j = 0; j < NT; j++) {
         float u[8];
         if constexpr (kBack) {
           float yv[8];
-          frag_floats(col_pair(Vs, ldv, 32 * ks + g4, vw + 16 * j), yv);
+          frag_floats(yf[ks][j], yv);
 #pragma unroll
           for (int e = 0; e < 8; e++) {
-            u[e] = -nn[2 * ks + e / 4][j][e % 4] * (w[e / 4][e % 4] * be[e / 4][e % 4]);
-            yv[e] *= w[e / 4][e % 4] * p.scale;
+            const int tt = 2 * ks + e / 4;
+            u[e] = -nn[tt][j][e % 4] * (w4[tt][e % 4] * b4[tt][e % 4]);
+            yv[e] *= w4[tt][e % 4] * p.scale;
           }
-          yf[ks][j].set(yv);
+          wy[ks][j].set(yv);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; e++) {
-            const float b = be[e / 4][e % 4];
-            u[e] = bad && !(b * 0.f == 0.f) ? 0.f : nn[2 * ks + e / 4][j][e % 4] * b;
+            const int tt = 2 * ks + e / 4;
+            const float b = b4[tt][e % 4];
+            u[e] = bad && !(b * 0.f == 0.f) ? 0.f : nn[tt][j][e % 4] * b;
           }
-          if constexpr (kOut) {
-            Parts<T, 2> uf;
-            uf.set(u);
+          if constexpr (kOut) uf[ks][j].set(u);
 #pragma unroll
-            for (int tt = 0; tt < TB; tt++)
-              if (ks <= tt / 2) {
-                Parts<T, 2> pf;
-#pragma unroll
-                for (int e = 0; e < Parts<T, 2>::kN; e++)
-                  pf.f[e] = row_frag(sh.P[i & 1][e] + lower_frag<TB>(tt, ks) * 512 + l * 8);
-                o[tt][j] = mma_parts(uf, pf, o[tt][j]);
-              }
-          }
-#pragma unroll
-          for (int e = 0; e < 8; e++) u[e] *= w[e / 4][e % 4];
+          for (int e = 0; e < 8; e++) u[e] *= w4[2 * ks + e / 4][e % 4];
         }
         wf[ks][j].set(u);
       }
+    // ---- the state after the chunk, 32 of its rows at a time ----
+    auto update = [&](int step) {
+#pragma unroll
+      for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) S[2 * step + m][j][r] *= all;
+#pragma unroll
+      for (int e = 0; e < kN3; e++)
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ks++)
+#pragma unroll
+          for (int m = 0; m < 2; m++)
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+              f32x4& to = S[2 * step + m][j];
+              to = mma(kc[step % 2][m][ks], wf[ks][j].f[e], to);
+              if constexpr (kBack) to = mma(qc[step % 2][m][ks], wy[ks][j].f[e], to);
+            }
+    };
+#pragma unroll
+    for (int step = 0; step + 1 < KS; step++) {
+      read_cols(step + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      update(step);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (kOut) {
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) o[tt][j][r] *= in[tt];
+#pragma unroll
+      for (int ea = 0; ea < kN2; ea++)
+#pragma unroll
+        for (int eb = 0; ea + eb < kN2; eb++)
+#pragma unroll
+          for (int ks = 0; ks < kSteps; ks++)
+#pragma unroll
+            for (int tt = 0; tt < TB; tt++)
+              if (ks <= tt / 2)
+#pragma unroll
+                for (int j = 0; j < NT; j++) o[tt][j] = mma(uf[ks][j].f[ea], pf[lower_frag<TB>(tt, ks)][eb], o[tt][j]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (i + 1 < chunks) read_rows(i + 1, 0);
+    update(KS - 1);
     if constexpr (kOut) {
       if (__builtin_expect(bad, 0)) {
 #pragma unroll
@@ -738,52 +908,27 @@ void sweep_kernel(Rule p) {
             for (int tt = 0; tt < TB; tt++) o[tt][j][r] = 16 * tt + lr >= at ? __builtin_nanf("") : o[tt][j][r];
           }
       }
-    }
-    __syncthreads();  // P and Z of this chunk have been read
-    if constexpr (kOut) {
+      const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(ybase + int64_t(c) * kC * yrow);
 #pragma unroll
       for (int tt = 0; tt < TB; tt++) {
-        const int t = 16 * tt + lr;
-        if (t < nv) {
-          T* y = static_cast<T*>(p.y) + ((bi * p.L + int64_t(c) * kC + t) * p.H + h) * p.Dv;
+        const bool row = 16 * tt + lr < nv;
 #pragma unroll
-          for (int j = 0; j < NT; j++) {
-            const int v = v0 + vw + 16 * j + g4;
-            if constexpr (VEC) {
-              if (v < p.Dv) {
-                if constexpr (kTwo) *reinterpret_cast<uint2*>(y + v) = make_uint2(pack_bf16(o[tt][j][0], o[tt][j][1]), pack_bf16(o[tt][j][2], o[tt][j][3]));
-                else *reinterpret_cast<float4*>(y + v) = make_float4(o[tt][j][0], o[tt][j][1], o[tt][j][2], o[tt][j][3]);
-              }
+        for (int j = 0; j < NT; j++) {
+          const int so = (16 * tt * yrow + 16 * j) * int(sizeof(T)), left = p.Dv - v0 - vw - 16 * j - g4;
+          if constexpr (VEC) {
+            const int at = row && left > 0 ? yoff : 0x7fffffff;
+            if constexpr (kTwo) {
+              typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+              __builtin_amdgcn_raw_buffer_store_b64(u2{pack_pair(o[tt][j][0], o[tt][j][1]), pack_pair(o[tt][j][2], o[tt][j][3])}, rs, at, so, 0);
             } else {
-#pragma unroll
-              for (int r = 0; r < 4; r++)
-                if (v + r < p.Dv) store_elem(y + v + r, o[tt][j][r]);
+              typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+              __builtin_amdgcn_raw_buffer_store_b128(u4{__float_as_uint(o[tt][j][0]), __float_as_uint(o[tt][j][1]), __float_as_uint(o[tt][j][2]),
+                                                        __float_as_uint(o[tt][j][3])}, rs, at, so, 0);
             }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; r++) buf_store(rs, row && r < left ? yoff + r * int(sizeof(T)) : 0x7fffffff, so, o[tt][j][r], static_cast<T*>(nullptr));
           }
-        }
-      }
-    }
-    // ---- the state after the chunk ----
-    const float all = d.all;
-#pragma unroll
-    for (int m = 0; m < MT; m++) {
-#pragma unroll
-      for (int j = 0; j < NT; j++)
-#pragma unroll
-        for (int r = 0; r < 4; r++) S[m][j][r] *= all;
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ks++) {
-        const Frag<T> kf = col_pair(Ks, ldk, 32 * ks + g4, 16 * m);
-#pragma unroll
-        for (int e = 0; e < Parts<T, 3>::kN; e++)
-#pragma unroll
-          for (int j = 0; j < NT; j++) S[m][j] = mma(kf, wf[ks][j].f[e], S[m][j]);
-        if constexpr (kBack) {
-          const Frag<T> qf = col_pair(Qs, ldq, 32 * ks + g4, 16 * m);
-#pragma unroll
-          for (int e = 0; e < Parts<T, 3>::kN; e++)
-#pragma unroll
-            for (int j = 0; j < NT; j++) S[m][j] = mma(qf, yf[ks][j].f[e], S[m][j]);
         }
       }
     }
@@ -826,9 +971,9 @@ void sweep_kernel(Rule p) {
 struct Grad {
   Rule p;                // v is v, y is dv
   const void* dy;
-  const float* S;        // [b H n_chunks][KP][VP]
+  const float* S;        // as Rule's states
   const float* D;
-  const float* N;        // [b H n_chunks][C][VP]
+  const float* N;        // as Rule's left
   const float* dR;
   void* dq;              // [b, L, H, Dk] float, or of the streamed type where heads share nothing
   void* dk;
@@ -858,14 +1003,10 @@ struct GradLds {
   float beta[kC];
   float rows[Z::TB][kC], cols[Z::TB][kC];      // sums of a block's rows and columns
   float dots[KDP / 16][kC], kept[KDP / 16][kC]; // of a token, over 16 of the keys' elements
+  float db[kGradWaves * kWave / kC][kC];        // a token's parts of dbeta
   double sd[kGradWaves];
 };
 
-// 8 floats from a 16-byte aligned address
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
 // four floats to a row of an LDS tile, in its parts
 __device__ __forceinline__ void put4(float (&x)[4], float* a, float*) { *reinterpret_cast<float4*>(a) = make_float4(x[0], x[1], x[2], x[3]); }
 __device__ __forceinline__ void put4(float (&x)[4], bf16_bits* a, bf16_bits* b) {
@@ -894,7 +1035,7 @@ __device__ __forceinline__ void store4(T* to, const float (&x)[4], int left, boo
 }
 
 template <typename T, int KDP, bool VEC>
-__global__ __launch_bounds__(kGradWaves * kWave) void grad_kernel(Grad a) {
+__global__ __launch_bounds__(kGradWaves * kWave) void delta_grad_kernel(Grad a) {
   typedef Shape<T> Z;
   typedef GradLds<T, KDP> Lds;
   constexpr int kC = Z::kC, TB = Z::TB, kSteps = Z::kSteps, KS = KDP / 32, MT = KDP / 16;
@@ -965,7 +1106,8 @@ __global__ __launch_bounds__(kGradWaves * kWave) void grad_kernel(Grad a) {
   }
   double sd = 0.0;
   float db = 0.f;  // the part of dbeta that this thread's columns give
-  const int vt = tid / 8, vc = 8 * (tid % 8);  // token and columns that a thread brings of N and dR
+  constexpr int kCols = 64 * kC / (kGradWaves * kWave);  // columns of one token that a thread brings of N and dR
+  const int vt = tid % kC, vc = kCols * (tid / kC);
   __syncthreads();
   for (int v0 = 0; v0 < p.Dv; v0 += 64) {
     if (v0) __syncthreads();
@@ -976,49 +1118,55 @@ __global__ __launch_bounds__(kGradWaves * kWave) void grad_kernel(Grad a) {
       s.load(r, nv, tid);
       s.store(sh.a.dy, r, tid);
     }
-    if (vt < kC) {
-      float x[8], y[8];
-      const int v = v0 + vc;
-      if (v < p.VP) {
-        load8(a.N + left + vt * p.VP + v, x);
-        load8(a.dR + left + vt * p.VP + v, y);
-      } else {
+    {
+      float x[kCols], y[kCols];
+      const int64_t at = left + (vt / 16 * int64_t(p.VP) + v0 + vc) * 16 + vt % 16;
 #pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = y[j] = 0.f;
+      for (int j = 0; j < kCols; j++) {
+        const bool in = v0 + vc + j < p.VP;
+        x[j] = in ? a.N[at + 16 * j] : 0.f;
+        y[j] = in ? a.dR[at + 16 * j] : 0.f;
       }
-      const float be = sh.beta[vt];
-      const float own = be / moved_beta(be);
-      float u[8];
+      const float be = sh.beta[vt], own = be / moved_beta(be);
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
+      for (int j = 0; j < kCols; j++) {
         db = fmaf(x[j], y[j], db);
-        u[j] = x[j] * be;
+        x[j] *= be;
         y[j] *= own;
       }
-      if (vt < nv) {
-        T* to = static_cast<T*>(p.y) + ((row0 + vt) * p.H + h) * p.Dv + v;
-        const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
-        store4(to, lo, p.Dv - v, VEC);
-        store4(to + 4, hi, p.Dv - v - 4, VEC);
-      }
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        float u4[4] = {u[e], u[e + 1], u[e + 2], u[e + 3]}, r4[4] = {y[e], y[e + 1], y[e + 2], y[e + 3]};
+      for (int e = 0; e < kCols; e += 4) {
+        float u4[4] = {x[e], x[e + 1], x[e + 2], x[e + 3]}, r4[4] = {y[e], y[e + 1], y[e + 2], y[e + 3]};
         put4(u4, sh.a.u[0] + vt * ldv + vc + e, sh.a.u[kN - 1] + vt * ldv + vc + e);
         put4(r4, sh.a.r[0] + vt * ldv + vc + e, sh.a.r[kN - 1] + vt * ldv + vc + e);
       }
     }
     __syncthreads();
+    {  // dv: the first part of dR is what rounding leaves of it
+      constexpr int kVec = 16 / int(sizeof(T)), kPieces = 64 / kVec;
+      for (int j = tid; j < kC * kPieces; j += kGradWaves * kWave) {
+        const int t = j / kPieces, v = v0 + kVec * (j % kPieces);
+        const T* from = sh.a.r[0] + t * ldv + kVec * (j % kPieces);
+        if (t >= nv || v >= p.Dv) continue;
+        T* to = static_cast<T*>(p.y) + ((row0 + t) * p.H + h) * p.Dv + v;
+        if constexpr (VEC) {
+          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+        } else {
+          for (int e = 0; e < kVec; e++)
+            if (v + e < p.Dv) to[e] = from[e];
+        }
+      }
+    }
 #pragma unroll
     for (int kk = 0; kk < 2; kk++) {
       const int v = v0 + 32 * kk + g8;
       float x[8], y[8];
-      if (16 * ib < p.KP && v < p.VP) {
-        load8(a.S + state + (16 * ib + lr) * int64_t(p.VP) + v, x);
-        load8(a.D + state + (16 * ib + lr) * int64_t(p.VP) + v, y);
-      } else {
+      const int64_t at = state + (ib * int64_t(p.VP) + v) * 16 + lr;
+      const bool in = 16 * ib < p.KP && v < p.VP;
 #pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = y[j] = 0.f;
+      for (int j = 0; j < 8; j++) {
+        x[j] = in ? a.S[at + 16 * j] : 0.f;
+        y[j] = in ? a.D[at + 16 * j] : 0.f;
       }
       if (wv < MT) {
         float s = 0.f;
@@ -1063,14 +1211,14 @@ __global__ __launch_bounds__(kGradWaves * kWave) void grad_kernel(Grad a) {
       }
     }
   }
-  // dbeta: 8 threads have a token
-  if (a.dbeta) {
-    db += __shfl_xor(db, 1);
-    db += __shfl_xor(db, 2);
-    db += __shfl_xor(db, 4);
-    if (tid % 8 == 0 && vt < nv) store_elem(static_cast<T*>(a.dbeta) + (row0 + vt) * p.H + h, db / moved_beta(sh.beta[vt]));
-  }
+  sh.db[tid / kC][vt] = db;
   __syncthreads();
+  if (a.dbeta && tid < nv) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kGradWaves * kWave / kC; j++) s += sh.db[j][tid];
+    store_elem(static_cast<T*>(a.dbeta) + (row0 + tid) * p.H + h, s / moved_beta(sh.beta[tid]));
+  }
   // ---- W and B + B^T, and what they give the gate ----
 #pragma unroll
   for (int j = 0; j < NB; j++) {
@@ -1229,7 +1377,7 @@ __global__ __launch_bounds__(kGradWaves * kWave) void grad_kernel(Grad a) {
 // the groups at once, in LDS: y = scale (r S^T q + (q . k) u).  The state is read and written once: bound by HBM.
 // ---------------------------------------------------------------------------
 template <typename T, int VEC, int NR>
-__global__ __launch_bounds__(256) void update_kernel(Rule p, float* __restrict__ state, int lanes) {
+__global__ __launch_bounds__(256) void delta_update_kernel(Rule p, float* __restrict__ state, int lanes) {
   __shared__ float qs[kMaxDim], ks[kMaxDim], pk[256 * VEC], pq[256 * VEC], kq_part[4];
   const int h = blockIdx.x % p.H, G = p.H / p.share;
   const int64_t bi = blockIdx.x / p.H, bh = bi * p.H + h, qrow = bi * G + h / p.share;
@@ -1392,8 +1540,8 @@ hipError_t run_tri(const Rule& p, float* lower, float* upper) {
   const int64_t blocks = p.b * p.H * p.n_chunks;
   const bool vec = pieces<T>(p.k, p.Dk);
   auto go = [&](auto kern) { return launch_kind(kKindDeltaTri, kern, blocks, kThreads, p.stream, p, lower, upper); };
-  if (p.Dk <= 64) return vec ? go(tri_kernel<T, 64, true>) : go(tri_kernel<T, 64, false>);
-  return vec ? go(tri_kernel<T, 128, true>) : go(tri_kernel<T, 128, false>);
+  if (p.Dk <= 64) return vec ? go(delta_tri_kernel<T, 64, true>) : go(delta_tri_kernel<T, 64, false>);
+  return vec ? go(delta_tri_kernel<T, 128, true>) : go(delta_tri_kernel<T, 128, false>);
 }
 
 template <typename T, Mode MODE>
@@ -1401,8 +1549,8 @@ hipError_t run_sweep(const Rule& p) {
   const int64_t blocks = p.b * p.H * p.n_tiles;
   const bool vec = pieces<T>(p.q, p.Dk) && pieces<T>(p.k, p.Dk) && pieces<T>(p.v, p.Dv) && (MODE != kForward || pieces<T>(p.y, p.Dv));
   auto go = [&](auto kern) { return launch_kind(kKindDeltaSweep, kern, blocks, kThreads + kWave * state_waves(kTile), p.stream, p); };
-  if (p.Dk <= 64) return vec ? go(sweep_kernel<T, 64, kTile, MODE, true>) : go(sweep_kernel<T, 64, kTile, MODE, false>);
-  return vec ? go(sweep_kernel<T, 128, kTile, MODE, true>) : go(sweep_kernel<T, 128, kTile, MODE, false>);
+  if (p.Dk <= 64) return vec ? go(delta_sweep_kernel<T, 64, kTile, MODE, true>) : go(delta_sweep_kernel<T, 64, kTile, MODE, false>);
+  return vec ? go(delta_sweep_kernel<T, 128, kTile, MODE, true>) : go(delta_sweep_kernel<T, 128, kTile, MODE, false>);
 }
 
 template <typename T>
@@ -1412,8 +1560,8 @@ hipError_t run_grad(const Grad& a) {
   const bool vec = pieces<T>(p.q, p.Dk) && pieces<T>(p.k, p.Dk) && pieces<T>(a.dy, p.Dv) && pieces<T>(p.y, p.Dv) &&
                    pieces<T>(a.dq, p.Dk) && pieces<T>(a.dk, p.Dk);
   auto go = [&](auto kern) { return launch_kind(kKindDeltaGrad, kern, blocks, kGradWaves * kWave, p.stream, a); };
-  if (p.Dk <= 64) return vec ? go(grad_kernel<T, 64, true>) : go(grad_kernel<T, 64, false>);
-  return vec ? go(grad_kernel<T, 128, true>) : go(grad_kernel<T, 128, false>);
+  if (p.Dk <= 64) return vec ? go(delta_grad_kernel<T, 64, true>) : go(delta_grad_kernel<T, 64, false>);
+  return vec ? go(delta_grad_kernel<T, 128, true>) : go(delta_grad_kernel<T, 128, false>);
 }
 
 template <typename T>
@@ -1487,8 +1635,8 @@ hipError_t update_impl(const DeltaRuleArgs& a) {
   while (lanes * (vec ? 4 : 1) < a.Dv) lanes *= 2;
   const int64_t rows = ceil_div(a.Dk, 256 / lanes);  // of the state a thread has: at most 16 in vectors, 64 else
   auto go = [&](auto kern) { return launch_kind(kKindDeltaUpdate, kern, a.b * a.H, 256, a.stream, p, a.last, lanes); };
-  if (vec) return rows <= 4 ? go(update_kernel<T, 4, 4>) : rows <= 8 ? go(update_kernel<T, 4, 8>) : go(update_kernel<T, 4, 16>);
-  return rows <= 16 ? go(update_kernel<T, 1, 16>) : go(update_kernel<T, 1, 64>);
+  if (vec) return rows <= 4 ? go(delta_update_kernel<T, 4, 4>) : rows <= 8 ? go(delta_update_kernel<T, 4, 8>) : go(delta_update_kernel<T, 4, 16>);
+  return rows <= 16 ? go(delta_update_kernel<T, 1, 16>) : go(delta_update_kernel<T, 1, 64>);
 }
 
 }  // namespace
