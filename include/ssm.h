@@ -23,9 +23,12 @@
  *   ssm_layernorm_fwd, ssm_layernorm_bwd
  *                                     layer norm over the model's width or each head's
  *                                     channels, and its gradients
+ *   ssm_blocknorm_fwd, ssm_blocknorm_bwd
+ *                                     what stands between two blocks: RMS norm after one, gate,
+ *                                     scale, residual, RMS norm before the next; its gradients
  *   ssm_conv_fwd, ssm_conv_update     the causal depthwise convolution + SiLU before
  *                                     the scan, and its token step
- *   ssm_linattn_workspace, ssm_deltarule_workspace, ssm_layernorm_workspace,
+ *   ssm_linattn_workspace, ssm_deltarule_workspace, ssm_layernorm_workspace, ssm_blocknorm_workspace,
  *   ssm_scan_plan, ssm_profile_*, ssm_status_string, ssm_last_hip_error, ssm_version
  *                                     host-side queries
  *
@@ -49,10 +52,10 @@
  * backward and the per-head scan take a temporary workspace from the
  * stream-ordered allocator (hipMallocAsync / hipFreeAsync on `stream`), so
  * concurrent calls on different streams do not share memory.
- * ssm_state_update, ssm_conv_update, ssm_linattn_update, ssm_deltarule_update and
- * ssm_layernorm_fwd take none and issue no memset: a caller can capture them
+ * ssm_state_update, ssm_conv_update, ssm_linattn_update, ssm_deltarule_update,
+ * ssm_layernorm_fwd and ssm_blocknorm_fwd take none and issue no memset: a caller can capture them
  * in a HIP graph.  ssm_linattn_fwd, ssm_linattn_bwd, ssm_deltarule_fwd,
- * ssm_deltarule_bwd and ssm_layernorm_bwd take a workspace of the caller's where one is given (then they allocate nothing
+ * ssm_deltarule_bwd, ssm_layernorm_bwd and ssm_blocknorm_bwd take a workspace of the caller's where one is given (then they allocate nothing
  * and can be captured too), else from the stream-ordered allocator.
  *
  * Data types.  `dtype` (ssm_dtype) is the element type of the streamed
@@ -593,6 +596,57 @@ SSM_API int ssm_layernorm_bwd(const void* x, const float* weight, const float* m
 
 /* Bytes of workspace of ssm_layernorm_bwd; a negative ssm_status for sizes it refuses.  Host-only. */
 SSM_API int64_t ssm_layernorm_workspace(int64_t rows, int64_t H, int64_t W, int dtype);
+
+/*
+ * What stands between two blocks: the norm after one, its gate, the scale of
+ * each channel, the residual, and the norm before the next.  For every row i
+ * and head h (H = 1: over the model's width; H > 1: over each head's channels,
+ * with the head's parameters), elementwise in j:
+ *   p = x * rstd_post * post_weight,  rstd_post = 1 / sqrt(sum_j x^2 / W + eps)     (SSM_NORM_POST; else p = x)
+ *   u = p * silu(z)                                                                 (z given; else u = p)
+ *   h = residual + scale * u                                                        (each where given)
+ *   n = h * rstd_pre * pre_weight,    rstd_pre = 1 / sqrt(sum_j h^2 / W + eps)      (SSM_NORM_PRE)
+ * n is computed from h before h is rounded.  With SSM_NORM_PRE alone and neither z nor residual it is the RMS norm
+ * of x (with the weight 1 / sqrt(W) its rows have length one, as the keys of ssm_deltarule_fwd want them).
+ *
+ * Arguments (device pointers):
+ *   x, z, n            [rows, H, W]  dtype           (z nullable; n with SSM_NORM_PRE)
+ *   residual, h        [rows, H, W]  residual_dtype  (residual nullable; h nullable with SSM_NORM_PRE)
+ *   post_weight, scale, pre_weight
+ *                      [H, W]        float           (nullable: one; a weight without its norm is not read)
+ *   rstd_post, rstd_pre [rows, H]    float           (nullable; what the backward needs, of the norms there are)
+ *   norms              SSM_NORM_POST, SSM_NORM_PRE or both
+ *   residual_dtype     dtype, or SSM_F32: the residual stream in float
+ * 1 <= W <= 16384; H <= 2^21; H W < 2^28; rows H < 2^31; eps >= 0 (else SSM_ERR_DIM).
+ */
+#define SSM_NORM_POST 1
+#define SSM_NORM_PRE 2
+SSM_API int ssm_blocknorm_fwd(const void* x, const float* post_weight, const void* z, const float* scale,
+                              const void* residual, const float* pre_weight, float eps, int norms, void* h, void* n,
+                              float* rstd_post, float* rstd_pre, int64_t rows, int64_t H, int64_t W, int dtype,
+                              int residual_dtype, void* stream);
+
+/*
+ * Gradients of  sum dh * h + sum dn * n  of ssm_blocknorm_fwd, from its inputs and the rstd of the norms there are:
+ *   dh                 [rows, H, W]  residual_dtype  (nullable with SSM_NORM_PRE: zero)
+ *   dn                 [rows, H, W]  dtype           (with SSM_NORM_PRE)
+ *   dx, dz             [rows, H, W]  dtype           (dz required when z is given, ignored otherwise)
+ *   dresidual          [rows, H, W]  residual_dtype  (nullable; the gradient reaching h, also when residual is NULL)
+ *   dpost_weight, dscale, dpre_weight [H, W] float   (nullable each; also where the parameter is NULL; those of a norm
+ *                                                     that is not there are not written; rows == 0 writes zeros)
+ * The parameters' gradients are sums over the rows, added in a fixed order (deterministic).  Their partial sums take a
+ * workspace: at least ssm_blocknorm_workspace() bytes at `workspace`, or NULL for the stream-ordered allocator; none
+ * where no parameter's gradient is asked for.
+ */
+SSM_API int ssm_blocknorm_bwd(const void* x, const float* post_weight, const void* z, const float* scale,
+                              const void* residual, const float* pre_weight, int norms, const float* rstd_post,
+                              const float* rstd_pre, const void* dh, const void* dn, void* dx, void* dz,
+                              void* dresidual, float* dpost_weight, float* dscale, float* dpre_weight, int64_t rows,
+                              int64_t H, int64_t W, int dtype, int residual_dtype, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of ssm_blocknorm_bwd; a negative ssm_status for sizes it refuses.  Host-only. */
+SSM_API int64_t ssm_blocknorm_workspace(int64_t rows, int64_t H, int64_t W, int dtype, int residual_dtype);
 
 /*
  * How a forward scan of this size runs (tuning NULL: as ssm_scan_fwd): *path

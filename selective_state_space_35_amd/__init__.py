@@ -45,6 +45,11 @@ Functions (same names as the C entry points):
 * ``ssm_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None)`` ->
   ``(y, mean, rstd)``: layer norm over the last axis; ``ssm_layernorm_bwd`` its
   gradients
+* ``ssm_blocknorm_fwd(x, post_weight=None, z=None, scale=None, residual=None,
+  pre_weight=None, norms="both", eps=1e-5, return_h=True, h=None, n=None)`` ->
+  ``(h, n, rstd_post, rstd_pre)``: what stands between two blocks, RMS norm
+  after one, gate, scale, residual, RMS norm before the next;
+  ``ssm_blocknorm_bwd`` its gradients
 * ``ssm_conv_fwd(v, weight, conv_bias=None, state_in=None, x=None,
   state_out=None, return_state=True)`` -> ``(x, state_out)``: causal depthwise
   convolution + SiLU over the sequence
@@ -68,7 +73,8 @@ __all__ = [
     "ssm_scan_fwd", "ssm_scan_fwd_from", "ssm_scan_fwd_noalloc", "ssm_scan_bwd", "ssm_ssd_fwd", "ssm_state_update", "ssm_conv_fwd", "ssm_conv_update",
     "ssm_linattn_fwd", "ssm_linattn_bwd", "ssm_linattn_update", "ssm_linattn_workspace",
     "ssm_deltarule_fwd", "ssm_deltarule_bwd", "ssm_deltarule_update", "ssm_deltarule_workspace",
-    "ssm_layernorm_fwd", "ssm_layernorm_bwd", "ssm_layernorm_workspace", "ssm_scan_plan", "ssm_profile_enable", "ssm_profile_read",
+    "ssm_layernorm_fwd", "ssm_layernorm_bwd", "ssm_layernorm_workspace",
+    "ssm_blocknorm_fwd", "ssm_blocknorm_bwd", "ssm_blocknorm_workspace", "ssm_scan_plan", "ssm_profile_enable", "ssm_profile_read",
     "ssm_status_string", "library_path", "SSMError", "ScanTuning", "SCAN_PATHS",
     "SSM_F32", "SSM_BF16", "load_library",
 ]
@@ -178,6 +184,12 @@ def load_library():
     lib.ssm_layernorm_bwd.argtypes = [_vp] * 8 + [_i64] * 3 + [_int, _vp, _i64, _vp]
     lib.ssm_layernorm_workspace.restype = _i64
     lib.ssm_layernorm_workspace.argtypes = [_i64] * 3 + [_int]
+    lib.ssm_blocknorm_fwd.restype = _int
+    lib.ssm_blocknorm_fwd.argtypes = [_vp] * 6 + [_f32, _int] + [_vp] * 4 + [_i64] * 3 + [_int, _int, _vp]
+    lib.ssm_blocknorm_bwd.restype = _int
+    lib.ssm_blocknorm_bwd.argtypes = [_vp] * 6 + [_int] + [_vp] * 10 + [_i64] * 3 + [_int, _int, _vp, _i64, _vp]
+    lib.ssm_blocknorm_workspace.restype = _i64
+    lib.ssm_blocknorm_workspace.argtypes = [_i64] * 3 + [_int, _int]
     lib.ssm_status_string.restype = ctypes.c_char_p
     lib.ssm_status_string.argtypes = [_int]
     lib.ssm_last_hip_error.restype = ctypes.c_char_p
@@ -990,4 +1002,114 @@ def ssm_layernorm_bwd(x, dy, mean, rstd, weight=None, heads=None, param_grads=Tr
                                        _ptr(out["dweight"]), _ptr(out["dbias"]), rows, H, W, code, _ptr(ws), n,
                                        _stream_of(torch, device))
     _raise_on("ssm_layernorm_bwd", status)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the norms around a block
+# ---------------------------------------------------------------------------
+_NORMS = {"post": 1, "pre": 2, "both": 3}
+
+
+def ssm_blocknorm_workspace(rows, H, W, dtype="bf16", residual_dtype=None):
+    """Bytes of workspace of ``ssm_blocknorm_bwd`` at these sizes (host-only query); the residual is of ``dtype`` (None)."""
+    names = {"f32": SSM_F32, "bf16": SSM_BF16}
+    code = names.get(dtype, dtype)
+    rcode = code if residual_dtype is None else names.get(residual_dtype, residual_dtype)
+    n = load_library().ssm_blocknorm_workspace(int(rows), int(H), int(W), int(code), int(rcode))
+    _raise_on("ssm_blocknorm_workspace", min(n, 0))
+    return n
+
+
+def _blocknorm_sizes(torch, x, post_weight, z, scale, residual, pre_weight, norms, heads):
+    """Checks the inputs of the norms around a block; returns (parameters' shape, rows, H, W, codes, the norms' flags,
+    the residual's dtype)."""
+    if norms not in _NORMS:
+        raise ValueError(f"norms must be one of {sorted(_NORMS)}, got {norms!r}")
+    if post_weight is not None and norms == "pre":
+        raise ValueError("post_weight is given, but norms has no norm after the block")
+    if pre_weight is not None and norms == "post":
+        raise ValueError("pre_weight is given, but norms has no norm before the next block")
+    like = next((p for p in (post_weight, scale, pre_weight) if p is not None), None if heads is None else int(heads))
+    par, rows, H, W, code, device = _norm_sizes(torch, x, like)
+    for name, p in (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)):
+        _check(torch, name, p, par, torch.float32, device, optional=True)
+    _check(torch, "z", z, x.shape, x.dtype, device, optional=True)
+    rdt = x.dtype
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual must be a torch.Tensor")
+        rdt = residual.dtype if residual.dtype == torch.float32 else x.dtype
+        _check(torch, "residual", residual, x.shape, rdt, device)
+    return par, rows, H, W, code, _dtype_code(torch, rdt), device, _NORMS[norms], rdt
+
+
+def ssm_blocknorm_fwd(x, post_weight=None, z=None, scale=None, residual=None, pre_weight=None, norms="both", eps=1e-5,
+                      return_h=True, h=None, n=None, heads=None):
+    """RMS norm after a block, gate, scale, residual, RMS norm before the next: ``(h, n, rstd_post, rstd_pre)``.
+
+    ``u = x rstd_post post_weight silu(z)``, ``h = residual + scale u``, ``n = h rstd_pre pre_weight``; ``norms`` is
+    "post", "pre" or "both", a norm that is not there leaves its rstd (and n) None; z, scale and residual None leave
+    their step out.  x, z, n [..., W] in the streamed dtype; residual and h in it or in float32; the parameters are
+    float32, [W], or [H, W] for x [..., H, W] (None: one; ``heads`` says H where there are none).  ``return_h=False``
+    does not compute h where n is what is wanted.  rstd_post, rstd_pre [...] float32 are for the backward.
+    """
+    import torch
+
+    lib = load_library()
+    par, rows, H, W, code, rcode, device, flags, rdt = _blocknorm_sizes(torch, x, post_weight, z, scale, residual, pre_weight,
+                                                                       norms, heads)
+    if h is not None:
+        _check(torch, "h", h, x.shape, rdt, device)
+    elif return_h or not flags & 2:
+        h = torch.empty(x.shape, dtype=rdt, device=device)
+    if n is not None:
+        if not flags & 2:
+            raise ValueError("n is given, but norms has no norm before the next block")
+        _check(torch, "n", n, x.shape, x.dtype, device)
+    elif flags & 2:
+        n = torch.empty_like(x)
+    rstd = [torch.empty(x.shape[:-1], dtype=torch.float32, device=device) if flags & f else None for f in (1, 2)]
+    with _on(torch, device):
+        status = lib.ssm_blocknorm_fwd(_ptr(x), _ptr(post_weight), _ptr(z), _ptr(scale), _ptr(residual), _ptr(pre_weight),
+                                       float(eps), flags, _ptr(h), _ptr(n), _ptr(rstd[0]), _ptr(rstd[1]), rows, H, W, code,
+                                       rcode, _stream_of(torch, device))
+    _raise_on("ssm_blocknorm_fwd", status)
+    return h, n, rstd[0], rstd[1]
+
+
+def ssm_blocknorm_bwd(x, rstd_post=None, rstd_pre=None, dh=None, dn=None, post_weight=None, z=None, scale=None, residual=None,
+                      pre_weight=None, norms="both", param_grads=True, heads=None):
+    """Gradients of sum(dh * h) + sum(dn * n) of ``ssm_blocknorm_fwd``, from its inputs and its rstd.
+
+    dh may be None where there is a norm before the next block, and is of the residual's dtype.  Returns a dict: dx, dz
+    (None without z), dresidual (None without residual) and, float32, dpost_weight, dscale, dpre_weight (None without
+    the parameter, or with ``param_grads=False``).
+    """
+    import torch
+
+    lib = load_library()
+    par, rows, H, W, code, rcode, device, flags, rdt = _blocknorm_sizes(torch, x, post_weight, z, scale, residual, pre_weight,
+                                                                       norms, heads)
+    f32 = torch.float32
+    lead = x.shape[:-1]
+    _check(torch, "rstd_post", rstd_post, lead, f32, device, optional=not flags & 1)
+    _check(torch, "rstd_pre", rstd_pre, lead, f32, device, optional=not flags & 2)
+    _check(torch, "dn", dn, x.shape, x.dtype, device, optional=not flags & 2)
+    _check(torch, "dh", dh, x.shape, rdt, device, optional=bool(flags & 2))
+    grad = lambda p: torch.empty_like(p) if p is not None and param_grads else None  # noqa: E731
+    out = {"dx": torch.empty_like(x), "dz": None if z is None else torch.empty_like(z),
+           "dresidual": None if residual is None else torch.empty_like(residual),
+           "dpost_weight": grad(post_weight), "dscale": grad(scale), "dpre_weight": grad(pre_weight)}
+    params = any(out[k] is not None for k in ("dpost_weight", "dscale", "dpre_weight"))
+    size = lib.ssm_blocknorm_workspace(rows, H, W, code, rcode) if params else 0
+    _raise_on("ssm_blocknorm_bwd", min(size, 0))
+    ws = _workspace(torch, size, device)
+    with _on(torch, device):
+        status = lib.ssm_blocknorm_bwd(_ptr(x), _ptr(post_weight), _ptr(z), _ptr(scale), _ptr(residual), _ptr(pre_weight), flags,
+                                       _ptr(rstd_post), _ptr(rstd_pre), _ptr(dh), _ptr(dn), _ptr(out["dx"]), _ptr(out["dz"]),
+                                       _ptr(out["dresidual"]), _ptr(out["dpost_weight"]), _ptr(out["dscale"]),
+                                       _ptr(out["dpre_weight"]), rows, H, W, code, rcode, _ptr(ws), size,
+                                       _stream_of(torch, device))
+    _raise_on("ssm_blocknorm_bwd", status)
     return out

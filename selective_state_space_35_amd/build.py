@@ -20,7 +20,7 @@ CALIB_SRC = os.path.join(PKG, "calib", "ssm_calib.hip")
 CALIB_LIB = os.path.join(PKG, "libssm_calib.so")
 SOURCES = ["ssm_kernels.hip", "ssm_fused.hip", "ssm_conv.hip", "ssm_bwd.hip", "ssm_ssd.hip", "ssm_api.hip", "ssm_profile.hip",
            "ssm_noalloc.hip", "ssm_linattn.hip", "ssm_layernorm.hip",
-           "ssm_deltarule.hip"]
+           "ssm_deltarule.hip", "ssm_blocknorm.hip"]
 ARCH = os.environ.get("SSM_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

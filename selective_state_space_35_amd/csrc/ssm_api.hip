@@ -10,6 +10,7 @@
 #include "ssm.h"
 #include "ssm_internal.h"
 #include "ssm_layernorm.h"
+#include "ssm_blocknorm.h"
 #include "ssm_deltarule.h"
 #include "ssm_linattn.h"
 
@@ -496,6 +497,19 @@ ssm::DeltaRuleArgs deltarule_args(const void* q, const void* k, const void* v, c
   return a;
 }
 
+// Sizes and types of a call of the norms around a block.
+int check_blocknorm(int64_t rows, int64_t H, int64_t W, int dtype, int rdtype, int norms) {
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
+  if (rdtype != SSM_F32 && rdtype != dtype) return SSM_ERR_DTYPE;
+  if (norms < 1 || norms > 3) return SSM_ERR_DIM;
+  if (!size_ok(rows) || H < 0 || H > (int64_t(1) << 21) || W < 1 || W > ssm::blocknorm_max_width()) return SSM_ERR_DIM;
+  int64_t t = 0;
+  if (!mul_ok(rows, H, &t) || t > INT32_MAX || !mul_ok(t, W * 16, &t)) return SSM_ERR_DIM;
+  // grids hold less than 2^32 threads: up to 1024 for each head, and 3 x 256 for 64 columns of the parameters' sums
+  if (H * W >= (int64_t(1) << 28)) return SSM_ERR_DIM;
+  return SSM_OK;
+}
+
 int check_layernorm(int64_t rows, int64_t H, int64_t W, int dtype) {
   if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
   if (!size_ok(rows) || H < 0 || H > (int64_t(1) << 21) || W < 1 || W > ssm::layernorm_max_width()) return SSM_ERR_DIM;
@@ -664,6 +678,65 @@ int64_t ssm_layernorm_workspace(int64_t rows, int64_t H, int64_t W, int dtype) {
   ssm::LayerNormArgs a{};
   a.rows = rows; a.H = H; a.W = W; a.dtype = dtype;
   return int64_t(ssm::layernorm_workspace_bytes(a));
+}
+
+int ssm_blocknorm_fwd(const void* x, const float* post_weight, const void* z, const float* scale, const void* residual,
+                      const float* pre_weight, float eps, int norms, void* h, void* n, float* rstd_post, float* rstd_pre,
+                      int64_t rows, int64_t H, int64_t W, int dtype, int residual_dtype, void* stream) {
+  const int st = check_blocknorm(rows, H, W, dtype, residual_dtype, norms);
+  if (st != SSM_OK) return st;
+  if (!(eps >= 0.f)) return SSM_ERR_DIM;
+  if (rows == 0 || H == 0) return SSM_OK;
+  const bool pre = norms & SSM_NORM_PRE;
+  if (!x || (pre && !n) || (!pre && !h)) return SSM_ERR_NULL;
+  const void* streamed[] = {x, z, n};
+  const void* stream_r[] = {residual, h};
+  const void* fl[] = {post_weight, scale, pre_weight, rstd_post, rstd_pre};
+  if (!all_aligned(streamed, 3, dtype == SSM_F32 ? 4 : 2) || !all_aligned(stream_r, 2, residual_dtype == SSM_F32 ? 4 : 2) ||
+      !all_aligned(fl, 5, 4))
+    return SSM_ERR_ALIGN;
+  ssm::BlockNormArgs a{};
+  a.x = x; a.post_weight = post_weight; a.z = z; a.scale = scale; a.residual = residual; a.pre_weight = pre_weight;
+  a.eps = eps; a.post = norms & SSM_NORM_POST; a.pre = pre; a.h = h; a.n = n; a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+  a.rows = rows; a.H = H; a.W = W; a.dtype = dtype; a.rdtype = residual_dtype; a.stream = static_cast<hipStream_t>(stream);
+  return hip_status(ssm::launch_blocknorm_fwd(a));
+}
+
+int ssm_blocknorm_bwd(const void* x, const float* post_weight, const void* z, const float* scale, const void* residual,
+                      const float* pre_weight, int norms, const float* rstd_post, const float* rstd_pre, const void* dh,
+                      const void* dn, void* dx, void* dz, void* dresidual, float* dpost_weight, float* dscale,
+                      float* dpre_weight, int64_t rows, int64_t H, int64_t W, int dtype, int residual_dtype,
+                      void* workspace, int64_t workspace_bytes, void* stream) {
+  const int st = check_blocknorm(rows, H, W, dtype, residual_dtype, norms);
+  if (st != SSM_OK || H == 0) return st;
+  const bool post = norms & SSM_NORM_POST, pre = norms & SSM_NORM_PRE;
+  if (rows > 0) {
+    if (!x || !dx || (z && !dz)) return SSM_ERR_NULL;
+    if ((post && !rstd_post) || (pre && (!rstd_pre || !dn)) || (!pre && !dh)) return SSM_ERR_NULL;
+  }
+  const void* streamed[] = {x, z, dn, dx, dz};
+  const void* stream_r[] = {residual, dh, dresidual};
+  const void* fl[] = {post_weight, scale, pre_weight, rstd_post, rstd_pre, dpost_weight, dscale, dpre_weight};
+  if (!all_aligned(streamed, 5, dtype == SSM_F32 ? 4 : 2) || !all_aligned(stream_r, 3, residual_dtype == SSM_F32 ? 4 : 2) ||
+      !all_aligned(fl, 8, 4))
+    return SSM_ERR_ALIGN;
+  ssm::BlockNormArgs a{};
+  a.x = x; a.post_weight = post_weight; a.z = z; a.scale = scale; a.residual = residual; a.pre_weight = pre_weight;
+  a.post = post; a.pre = pre; a.rstd_post = const_cast<float*>(rstd_post); a.rstd_pre = const_cast<float*>(rstd_pre);
+  a.dh = dh; a.dn = pre ? dn : nullptr; a.dx = dx; a.dz = z ? dz : nullptr; a.dresidual = dresidual;
+  a.dpost_weight = post ? dpost_weight : nullptr; a.dscale = dscale; a.dpre_weight = pre ? dpre_weight : nullptr;
+  a.rows = rows; a.H = H; a.W = W; a.dtype = dtype; a.rdtype = residual_dtype; a.stream = static_cast<hipStream_t>(stream);
+  const bool params = a.dpost_weight || a.dscale || a.dpre_weight;
+  return with_workspace(params ? ssm::blocknorm_workspace_bytes(a) : 0, workspace, workspace_bytes, a.stream,
+                        [&](void* ws) { return ssm::launch_blocknorm_bwd(a, ws); });
+}
+
+int64_t ssm_blocknorm_workspace(int64_t rows, int64_t H, int64_t W, int dtype, int residual_dtype) {
+  const int st = check_blocknorm(rows, H, W, dtype, residual_dtype, SSM_NORM_POST);
+  if (st != SSM_OK) return st;
+  ssm::BlockNormArgs a{};
+  a.rows = rows; a.H = H; a.W = W; a.dtype = dtype; a.rdtype = residual_dtype;
+  return int64_t(ssm::blocknorm_workspace_bytes(a));
 }
 
 const char* ssm_status_string(int status) {

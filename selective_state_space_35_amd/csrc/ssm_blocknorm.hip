@@ -1,0 +1,569 @@
+// ssm_blocknorm.hip -- what stands between two blocks: the RMS norm after one, its gate, the scale of each channel, the
+// residual, and the RMS norm before the next, forward and backward, with the sums of the parameters' gradients.
+//
+// A row is one [W] slice of x [rows, H, W]; the parameters are [H, W] (H = 1: over the model's width; H > 1: each head's
+// channels).  Every step can be left out.
+//   p = x r1 w1,  r1 = 1 / sqrt(mean(x^2) + eps);  u = p silu(z);  h = residual + s u;  n = h r2 w2,  r2 as r1 of h
+// Backward, with xh = x r1 and hh = h r2 (h is computed again, in float):
+//   t = dn w2,  e = dh + r2 (t - hh mean(t hh))  (the gradient of h, and of the residual)
+//   c = e s,  dz = c p silu'(z),  d = c silu(z) w1,  dx = r1 (d - xh mean(d xh))
+//   dw1 = sum over rows of c silu(z) xh,  ds = sum of e u,  dw2 = sum of dn hh
+// Both directions read every streamed value once, hold it for the two sums of its row, one after the other, and write
+// once: bound by HBM.  A group of threads keeps one head's parameters, and in the backward its part of their gradients, in
+// registers and walks rows, the next row's loads under way while one is summed.  All sums are float.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ssm_blocknorm.h"
+#include "ssm_device.h"
+#include "ssm_profile.h"
+
+namespace ssm {
+namespace {
+
+// N consecutive elements as they come from memory: whole 16-byte (or 8-byte) pieces, or (N = 1) one element
+template <typename T, int N>
+struct Raw {
+  uint32_t w[N * int(sizeof(T)) / 4];
+};
+template <typename T>
+struct Raw<T, 1> {
+  T w;
+};
+template <typename T, int N>
+__device__ __forceinline__ void load_raw(Raw<T, N>& r, const T* p) {
+  if constexpr (N == 1) {
+    r.w = *p;
+  } else {
+#pragma unroll
+    for (int k = 0; k < N * int(sizeof(T)) / 16; k++) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[k];
+      r.w[4 * k] = u.x; r.w[4 * k + 1] = u.y; r.w[4 * k + 2] = u.z; r.w[4 * k + 3] = u.w;
+    }
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void floats(const Raw<T, N>& r, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = load_elem(&r.w);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < N; j++) v[j] = __uint_as_float(r.w[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N / 2; j++) {
+      v[2 * j] = __uint_as_float(r.w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(r.w[j] & 0xffff0000u);
+    }
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store(T* p, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    store_elem(p, v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < N / 4; k++) reinterpret_cast<float4*>(p)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  } else {
+    typedef __attribute__((ext_vector_type(2))) float f2;
+    typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int j = 0; j < N / 2; j++) w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2 * j], v[2 * j + 1]}), b2));
+#pragma unroll
+    for (int k = 0; k < N / 8; k++) reinterpret_cast<uint4*>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
+}
+// The sum over the TPR threads of a row, the same in every one of them: shuffles, and for wider rows LDS, two calls in
+// turn with a buffer each, so that one barrier a call is enough (the whole workgroup comes to it).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float s, float* buf) {
+#pragma unroll
+  for (int off = (TPR < kWave ? TPR : kWave) / 2; off > 0; off >>= 1) s += __shfl_xor(s, off);
+  if constexpr (TPR > kWave) {
+    constexpr int kWaves = TPR / kWave;
+    if (threadIdx.x % kWave == 0) buf[threadIdx.x / kWave % kWaves] = s;
+    __syncthreads();
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) s += buf[w];
+  }
+  return s;
+}
+
+constexpr int block_threads(int tpr) { return tpr > 128 ? tpr : 256; }
+
+// A parameter of a group's head, one where there is none: in registers, or for the rows of many threads, whose registers
+// are few, read again for every row (from the caches).
+template <int NV, int VEC, int TPR>
+struct Par {
+  static constexpr bool kHeld = TPR < 640;
+  const float* w;
+  int lane, W;
+  float v[kHeld ? NV : 1][VEC];
+  __device__ __forceinline__ void init(const float* weight, int64_t at, int lane_, int W_) {
+    w = weight ? weight + at : nullptr;
+    lane = lane_;
+    W = W_;
+    if constexpr (kHeld)
+#pragma unroll
+      for (int j = 0; j < NV; j++) load(j, v[j]);
+  }
+  __device__ __forceinline__ void load(int j, float (&o)[VEC]) const {
+#pragma unroll
+    for (int e = 0; e < VEC; e++) o[e] = 1.f;
+    const int c = (j * TPR + lane) * VEC;
+    if (w && c < W) __builtin_memcpy(o, w + c, VEC * 4);  // only 4-byte aligned
+  }
+  __device__ __forceinline__ void get(int j, float (&o)[VEC]) const {
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int e = 0; e < VEC; e++) o[e] = v[j][e];
+    } else {
+      load(j, o);
+    }
+  }
+};
+
+// One group of TPR threads walks the rows slice, slice + n_slices, ... of head h; each thread has NV vectors of VEC
+// elements of a row, at columns (j TPR + lane) VEC.  R: the residual stream's type.
+template <typename T, typename R, int VEC, int NV, int TPR>
+__global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArgs a, int64_t n_slices) {
+  constexpr int kGroups = block_threads(TPR) / TPR;
+  __shared__ float buf[2][kGroups][TPR > kWave ? TPR / kWave : 1];
+  const int W = int(a.W), H = int(a.H);
+  const int group = threadIdx.x / TPR, lane = threadIdx.x % TPR;
+  const int64_t gid = int64_t(blockIdx.x) * kGroups + group;
+  const bool live = gid < n_slices * H;  // the others keep the workgroup's barriers
+  const int h = live ? int(gid % H) : 0;
+  const int64_t slice = live ? gid / H : a.rows;
+  const T* x = static_cast<const T*>(a.x);
+  const T* z = static_cast<const T*>(a.z);
+  const R* res = static_cast<const R*>(a.residual);
+  Par<NV, VEC, TPR> p1, ps, p2;
+  p1.init(a.post ? a.post_weight : nullptr, int64_t(h) * W, lane, W);
+  ps.init(a.scale, int64_t(h) * W, lane, W);
+  p2.init(a.pre ? a.pre_weight : nullptr, int64_t(h) * W, lane, W);
+  Raw<T, VEC> xn[NV], zn[NV];
+  Raw<R, VEC> rn[NV];
+  auto fetch = [&](int64_t i) {
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      const int c = (j * TPR + lane) * VEC;
+      const int64_t at = (i * H + h) * W + c;
+      if (c < W) {
+        load_raw(xn[j], x + at);
+        if (z) load_raw(zn[j], z + at);
+        if (res) load_raw(rn[j], res + at);
+      }
+    }
+  };
+  if (slice < a.rows) fetch(slice);
+  const float inv_w = 1.f / float(W);
+  const int64_t first = int64_t(blockIdx.x) * kGroups / H;  // the workgroup's first slice: it has the most rows
+  for (int64_t k = first; k < a.rows; k += n_slices) {
+    const int64_t i0 = slice + (k - first);
+    const bool on = live && i0 < a.rows;
+    float v[NV][VEC], g[NV][VEC], r[NV][VEC];
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      const bool in = on && (j * TPR + lane) * VEC < W;
+#pragma unroll
+      for (int e = 0; e < VEC; e++) v[j][e] = g[j][e] = r[j][e] = 0.f;
+      if (in) {
+        floats(xn[j], v[j]);
+        if (z) floats(zn[j], g[j]);
+        if (res) floats(rn[j], r[j]);
+      }
+    }
+    if (live && i0 + n_slices < a.rows) fetch(i0 + n_slices);
+    float r1 = 1.f, r2 = 1.f;
+    if (a.post) {
+#pragma unroll
+      for (int j = 0; j < NV; j++)
+#pragma unroll
+        for (int e = 0; e < VEC; e++) s = fmaf(v[j][e], v[j][e], s);
+      s = row_sum<TPR>(s, buf[0][group]);
+      r1 = 1.f / sqrtf(fmaf(s, inv_w, a.eps));
+    }
+    s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      float w1[VEC], sc[VEC];
+      p1.get(j, w1);
+      ps.get(j, sc);
+#pragma unroll
+      for (int e = 0; e < VEC; e++) {
+        float u = v[j][e] * r1 * w1[e];
+        if (z) u *= g[j][e] / (1.f + expf(-g[j][e]));
+        v[j][e] = fmaf(u, sc[e], r[j][e]);
+        s = fmaf(v[j][e], v[j][e], s);  // columns behind the width are zero: so is silu(0)
+      }
+    }
+    const int64_t row = i0 * H + h;
+    if (a.h && on) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) {
+        const int c = (j * TPR + lane) * VEC;
+        if (c < W) store(static_cast<R*>(a.h) + row * W + c, v[j]);
+      }
+    }
+    if (a.pre) {
+      s = row_sum<TPR>(s, buf[1][group]);
+      r2 = 1.f / sqrtf(fmaf(s, inv_w, a.eps));
+      if (on) {
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+          const int c = (j * TPR + lane) * VEC;
+          if (c < W) {
+            float o[VEC], w2[VEC];
+            p2.get(j, w2);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) o[e] = v[j][e] * r2 * w2[e];
+            store(static_cast<T*>(a.n) + row * W + c, o);
+          }
+        }
+      }
+    }
+    if (on && lane == 0) {
+      if (a.post && a.rstd_post) a.rstd_post[row] = r1;
+      if (a.pre && a.rstd_pre) a.rstd_pre[row] = r2;
+    }
+  }
+}
+
+// As the forward; a group writes its own row of the partial sums [3][n_slices][H W] (of w1, the scale, w2), which
+// bn_reduce_kernel adds in a fixed order.
+template <typename T, typename R, int VEC, int NV, int TPR>
+__global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArgs a, int64_t n_slices, float* part) {
+  constexpr int kGroups = block_threads(TPR) / TPR;
+  __shared__ float buf[2][kGroups][TPR > kWave ? TPR / kWave : 1];
+  const int W = int(a.W), H = int(a.H);
+  const int group = threadIdx.x / TPR, lane = threadIdx.x % TPR;
+  const int64_t gid = int64_t(blockIdx.x) * kGroups + group;
+  const bool live = gid < n_slices * H;
+  const int h = live ? int(gid % H) : 0;
+  const int64_t slice = live ? gid / H : a.rows;
+  const T* x = static_cast<const T*>(a.x);
+  const T* z = static_cast<const T*>(a.z);
+  const T* dn = a.pre ? static_cast<const T*>(a.dn) : nullptr;
+  // h is needed for the norm before the next block only
+  const R* res = a.pre ? static_cast<const R*>(a.residual) : nullptr;
+  const R* dh = static_cast<const R*>(a.dh);
+  Par<NV, VEC, TPR> p1, ps, p2;
+  p1.init(a.post ? a.post_weight : nullptr, int64_t(h) * W, lane, W);
+  ps.init(a.scale, int64_t(h) * W, lane, W);
+  p2.init(a.pre ? a.pre_weight : nullptr, int64_t(h) * W, lane, W);
+  float dw1[NV][VEC], ds[NV][VEC], dw2[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; j++)
+#pragma unroll
+    for (int e = 0; e < VEC; e++) dw1[j][e] = ds[j][e] = dw2[j][e] = 0.f;
+  Raw<T, VEC> xn[NV], zn[NV], nn[NV];
+  Raw<R, VEC> rn[NV], hn[NV];
+  float r1n = 1.f, r2n = 1.f;
+  auto fetch = [&](int64_t i) {
+    const int64_t row = i * H + h;
+    if (a.post) r1n = a.rstd_post[row];
+    if (a.pre) r2n = a.rstd_pre[row];
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      const int c = (j * TPR + lane) * VEC;
+      const int64_t at = row * W + c;
+      if (c < W) {
+        load_raw(xn[j], x + at);
+        if (z) load_raw(zn[j], z + at);
+        if (res) load_raw(rn[j], res + at);
+        if (dh) load_raw(hn[j], dh + at);
+        if (dn) load_raw(nn[j], dn + at);
+      }
+    }
+  };
+  if (slice < a.rows) fetch(slice);
+  const float inv_w = 1.f / float(W);
+  const int64_t first = int64_t(blockIdx.x) * kGroups / H;
+  for (int64_t k = first; k < a.rows; k += n_slices) {
+    const int64_t i0 = slice + (k - first), row = i0 * H + h;
+    const bool on = live && i0 < a.rows;
+    const float r1 = r1n, r2 = r2n;
+    float xh[NV][VEC], g[NV][VEC], hh[NV][VEC], d[NV][VEC], t[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      const bool in = on && (j * TPR + lane) * VEC < W;
+#pragma unroll
+      for (int e = 0; e < VEC; e++) xh[j][e] = g[j][e] = hh[j][e] = d[j][e] = t[j][e] = 0.f;
+      if (in) {
+        floats(xn[j], xh[j]);
+        if (z) floats(zn[j], g[j]);
+        if (res) floats(rn[j], hh[j]);
+        if (dh) floats(hn[j], d[j]);
+        if (dn) floats(nn[j], t[j]);
+#pragma unroll
+        for (int e = 0; e < VEC; e++) xh[j][e] *= r1;
+      }
+    }
+    if (live && i0 + n_slices < a.rows) fetch(i0 + n_slices);
+    // silu(z), and its derivative over what it multiplies, from one exponential
+    float sl[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+      for (int e = 0; e < VEC; e++) {
+        sl[j][e] = 1.f;
+        if (z) {
+          const float sg = 1.f / (1.f + expf(-g[j][e]));
+          sl[j][e] = g[j][e] * sg;
+          g[j][e] = sg * fmaf(g[j][e], 1.f - sg, 1.f);
+        }
+      }
+    if (a.pre) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; j++) {
+        float w1[VEC], sc[VEC], w2[VEC];
+        p1.get(j, w1);
+        ps.get(j, sc);
+        p2.get(j, w2);
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+          hh[j][e] = fmaf(xh[j][e] * w1[e] * sl[j][e], sc[e], hh[j][e]) * r2;
+          dw2[j][e] = fmaf(t[j][e], hh[j][e], dw2[j][e]);
+          t[j][e] *= w2[e];
+          s = fmaf(t[j][e], hh[j][e], s);
+        }
+      }
+      const float m = row_sum<TPR>(s, buf[0][group]) * inv_w;
+#pragma unroll
+      for (int j = 0; j < NV; j++)
+#pragma unroll
+        for (int e = 0; e < VEC; e++) d[j][e] = fmaf(r2, fmaf(-hh[j][e], m, t[j][e]), d[j][e]);
+    }
+    if (a.dresidual && on) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) {
+        const int c = (j * TPR + lane) * VEC;
+        if (c < W) store(static_cast<R*>(a.dresidual) + row * W + c, d[j]);
+      }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      float w1[VEC], sc[VEC];
+      p1.get(j, w1);
+      ps.get(j, sc);
+#pragma unroll
+      for (int e = 0; e < VEC; e++) {
+        const float p = xh[j][e] * w1[e], c = d[j][e] * sc[e];
+        ds[j][e] = fmaf(d[j][e], p * sl[j][e], ds[j][e]);
+        g[j][e] *= c * p;
+        const float o = c * sl[j][e];
+        dw1[j][e] = fmaf(o, xh[j][e], dw1[j][e]);
+        d[j][e] = o * w1[e];
+        s = fmaf(d[j][e], xh[j][e], s);
+      }
+    }
+    if (z && on) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) {
+        const int c = (j * TPR + lane) * VEC;
+        if (c < W) store(static_cast<T*>(a.dz) + row * W + c, g[j]);
+      }
+    }
+    if (a.post) {
+      const float m = row_sum<TPR>(s, buf[1][group]) * inv_w;
+#pragma unroll
+      for (int j = 0; j < NV; j++)
+#pragma unroll
+        for (int e = 0; e < VEC; e++) d[j][e] = r1 * fmaf(-xh[j][e], m, d[j][e]);
+    }
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) {
+        const int c = (j * TPR + lane) * VEC;
+        if (c < W) store(static_cast<T*>(a.dx) + row * W + c, d[j]);
+      }
+    }
+  }
+  if (!part || !live) return;
+  const int64_t at = (slice * H + h) * int64_t(W), all = n_slices * H * W;
+#pragma unroll
+  for (int j = 0; j < NV; j++) {
+    const int c = (j * TPR + lane) * VEC;
+    if (c < W) {
+#pragma unroll
+      for (int e = 0; e < VEC; e++) {
+        if (a.dpost_weight) part[at + c + e] = dw1[j][e];
+        if (a.dscale) part[all + at + c + e] = ds[j][e];
+        if (a.dpre_weight) part[2 * all + at + c + e] = dw2[j][e];
+      }
+    }
+  }
+}
+
+struct Sums {
+  const float* in[3];
+  float* out[3];  // null: not asked for
+};
+// out[k][c] = sum of in[k per .. k per + per - 1][c] over its rows below n, in order: 64 columns and 4 row strides a
+// workgroup; blockIdx.z chooses the parameter
+__global__ __launch_bounds__(256) void bn_reduce_kernel(Sums a, int64_t n, int64_t per, int64_t cols) {
+  __shared__ float sh[4][64];
+  const float* in = a.in[blockIdx.z];
+  float* out = a.out[blockIdx.z];
+  if (!out) return;
+  const int l = threadIdx.x % 64, g = threadIdx.x / 64;
+  const int64_t c = int64_t(blockIdx.x) * 64 + l;
+  const int64_t r0 = int64_t(blockIdx.y) * per, r1 = r0 + per < n ? r0 + per : n;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < cols) {
+    int64_t r = r0 + g;
+    for (; r + 12 < r1; r += 16) {
+#pragma unroll
+      for (int u = 0; u < 4; u++) s[u] += in[(r + 4 * u) * cols + c];
+    }
+    for (; r < r1; r += 4) s[0] += in[r * cols + c];
+  }
+  sh[g][l] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (g == 0 && c < cols) out[blockIdx.y * cols + c] = (sh[0][l] + sh[1][l]) + (sh[2][l] + sh[3][l]);
+}
+
+// Workgroups of a launch: of the forward, and of the backward, whose partial sums grow with them
+constexpr int64_t kFwdBlocks = 2048, kBwdBlocks = 512;
+
+constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <typename T, typename R, int VEC, int NV, int TPR>
+struct Form {
+  static hipError_t fwd(const BlockNormArgs& a, int64_t n_slices) {
+    constexpr int threads = block_threads(TPR), groups = threads / TPR;
+    return launch_kind(kKindBlockNormFwd, bn_fwd_kernel<T, R, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices);
+  }
+  static hipError_t bwd(const BlockNormArgs& a, int64_t n_slices, float* part) {
+    constexpr int threads = block_threads(TPR), groups = threads / TPR;
+    return launch_kind(kKindBlockNormBwd, bn_bwd_kernel<T, R, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices, part);
+  }
+  static constexpr int tpr = TPR;
+};
+
+// rows read and written in 16-byte vectors: whole vectors a row, aligned tensors
+template <typename T, typename R>
+bool whole_vectors(const BlockNormArgs& a) {
+  constexpr int VEC = 16 / sizeof(T);
+  const void* all[] = {a.x, a.z, a.residual, a.h, a.n, a.dh, a.dn, a.dx, a.dz, a.dresidual};
+  uintptr_t p = 0;
+  for (const void* q : all) p |= reinterpret_cast<uintptr_t>(q);
+  return a.W % VEC == 0 && p % 16 == 0;
+}
+
+// The form of rows of W elements: one vector a thread, in whole waves above one; more only above 1024 threads.  Elements
+// one at a time (odd widths): up to eight a thread, sixteen in the widest rows.
+template <typename T, typename R, typename Go>
+auto with_form(bool vec, int64_t W, Go go) {
+  constexpr int V = 16 / sizeof(T);
+  if (!vec) {
+    if (W <= 64) return go(Form<T, R, 1, 8, 8>{});
+    if (W <= 512) return go(Form<T, R, 1, 8, 64>{});
+    if (W <= 2048) return go(Form<T, R, 1, 8, 256>{});
+    if (W <= 8192) return go(Form<T, R, 1, 8, 1024>{});
+    return go(Form<T, R, 1, 16, 1024>{});
+  }
+  const int64_t n = W / V;
+  if (n <= 8) return go(Form<T, R, V, 1, 8>{});
+  if (n <= 16) return go(Form<T, R, V, 1, 16>{});
+  if (n <= 32) return go(Form<T, R, V, 1, 32>{});
+  if (n <= 64) return go(Form<T, R, V, 1, 64>{});
+  if (n <= 128) return go(Form<T, R, V, 1, 128>{});
+  if (n <= 192) return go(Form<T, R, V, 1, 192>{});
+  if (n <= 256) return go(Form<T, R, V, 1, 256>{});
+  if (n <= 320) return go(Form<T, R, V, 1, 320>{});
+  if (n <= 512) return go(Form<T, R, V, 1, 512>{});
+  if (n <= 640) return go(Form<T, R, V, 1, 640>{});
+  if (n <= 1024) return go(Form<T, R, V, 1, 1024>{});
+  if (V == 4 && n <= 2048) return go(Form<T, R, V, 8 / V, 1024>{});
+  return go(Form<T, R, V, 16 / V, 1024>{});
+}
+
+template <typename Go>
+auto with_types(int dtype, int rdtype, Go go) {
+  if (dtype == 0) return go(float{}, float{});
+  return rdtype == 0 ? go(bf16_bits{}, float{}) : go(bf16_bits{}, bf16_bits{});
+}
+
+// Rows in flight: the groups of `blocks` workgroups, shared out over the heads.
+int64_t slices_of(const BlockNormArgs& a, int tpr, int64_t blocks) {
+  return std::max<int64_t>(1, std::min<int64_t>(a.rows, ceil_div(blocks * (block_threads(tpr) / tpr), a.H)));
+}
+
+// How the backward's parameter sums are cut: n_slices partial rows [H W], added in n_parts parts of `per` rows and then
+// together.
+struct NormPlan {
+  int64_t n_slices, n_parts, per;
+};
+NormPlan plan_bwd(const BlockNormArgs& a, bool vec) {
+  NormPlan p;
+  const int tpr = with_types(a.dtype, a.rdtype, [&](auto t, auto r) {
+    return with_form<decltype(t), decltype(r)>(vec, a.W, [](auto f) { return int(f.tpr); });
+  });
+  p.n_slices = slices_of(a, tpr, kBwdBlocks);
+  const int64_t blocks = 3 * ceil_div(a.H * a.W, 64);
+  p.n_parts = std::max<int64_t>(1, std::min<int64_t>(ceil_div(512, blocks), p.n_slices / 32));
+  p.per = ceil_div(p.n_slices, p.n_parts);
+  p.n_parts = ceil_div(p.n_slices, p.per);
+  return p;
+}
+int64_t plan_floats(const BlockNormArgs& a, const NormPlan& p) {
+  return 3 * (p.n_slices + (p.n_parts > 1 ? p.n_parts : 0)) * a.H * a.W;
+}
+
+}  // namespace
+
+int64_t blocknorm_max_width() { return 16384; }
+
+size_t blocknorm_workspace_bytes(const BlockNormArgs& a) {
+  if (a.rows == 0 || a.H == 0 || a.W == 0) return 0;
+  // tensors of any alignment: the larger of the two forms
+  const int64_t n = std::max(plan_floats(a, plan_bwd(a, true)), plan_floats(a, plan_bwd(a, false)));
+  return size_t(n) * sizeof(float);
+}
+
+hipError_t launch_blocknorm_fwd(const BlockNormArgs& a) {
+  return with_types(a.dtype, a.rdtype, [&](auto t, auto r) {
+    typedef decltype(t) T;
+    typedef decltype(r) R;
+    return with_form<T, R>(whole_vectors<T, R>(a), a.W, [&](auto f) { return f.fwd(a, slices_of(a, f.tpr, kFwdBlocks)); });
+  });
+}
+
+hipError_t launch_blocknorm_bwd(const BlockNormArgs& a, void* workspace) {
+  const int64_t cols = a.H * a.W, blocks = ceil_div(cols, 64);
+  const bool params = a.dpost_weight || a.dscale || a.dpre_weight;
+  auto reduce = [&](const float* in, int64_t in_stride, float* o0, float* o1, float* o2, int64_t n, int64_t per, int64_t parts) {
+    const Sums s{{in, in + in_stride, in + 2 * in_stride}, {o0, o1, o2}};
+    return launch_kind_3d(kKindBlockNormReduce, bn_reduce_kernel, dim3(unsigned(blocks), unsigned(parts), 3), 256, a.stream, s, n, per, cols);
+  };
+  float* part = params ? static_cast<float*>(workspace) : nullptr;
+  if (a.rows == 0)  // sums over no rows
+    return params ? reduce(part, 0, a.dpost_weight, a.dscale, a.dpre_weight, 0, 0, 1) : hipSuccess;
+  NormPlan p{};
+  const hipError_t err = with_types(a.dtype, a.rdtype, [&](auto t, auto r) {
+    typedef decltype(t) T;
+    typedef decltype(r) R;
+    const bool vec = whole_vectors<T, R>(a);
+    p = plan_bwd(a, vec);
+    return with_form<T, R>(vec, a.W, [&](auto f) { return f.bwd(a, p.n_slices, part); });
+  });
+  if (err != hipSuccess || !params) return err;
+  const int64_t all = p.n_slices * cols, some = p.n_parts * cols;
+  if (p.n_parts == 1) return reduce(part, all, a.dpost_weight, a.dscale, a.dpre_weight, p.n_slices, p.n_slices, 1);
+  float* q = part + 3 * all;
+  const hipError_t e = reduce(part, all, a.dpost_weight ? q : nullptr, a.dscale ? q + some : nullptr, a.dpre_weight ? q + 2 * some : nullptr,
+                              p.n_slices, p.per, p.n_parts);
+  if (e != hipSuccess) return e;
+  return reduce(q, some, a.dpost_weight, a.dscale, a.dpre_weight, p.n_parts, p.n_parts, 1);
+}
+
+}  // namespace ssm
