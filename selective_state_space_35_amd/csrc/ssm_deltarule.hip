@@ -963,10 +963,12 @@ void delta_sweep_kernel(Rule p) {
 }
 
 // ---------------------------------------------------------------------------
-// What is a chunk's own of the backward: dq, dk, dv, dbeta and dg from S, D, N and dR.  A workgroup has one chunk of a
-// head, eight waves.  First the products along the values, 64 columns at a time: with the states (a wave has 16 of the
-// keys' elements), and dY U^T and dR U^T (a wave has a block or two of them); then, with W and B in LDS, those along the
-// tokens.  Results are transposed, so that a lane has consecutive elements of its own token.
+// What is a chunk's own of the backward: dq, dk, dv, dbeta and dg from S, D, N and dR.  A workgroup has one chunk of
+// `heads` heads that share their q and k, one after the other (so that their dq and dk are summed in registers), eight waves.
+// First the products along the values, 32 columns at a time: with the states (a wave has 16 of the keys' elements), and
+// dY U^T and dR U^T (a wave has a block or two of them); then, with W and B in LDS, those along the tokens.  Results are
+// transposed, so that a lane has consecutive elements of its own token.  S, D, U and dR lie in LDS by columns, as the
+// sweeps wrote them, and are read transposed.
 // ---------------------------------------------------------------------------
 struct Grad {
   Rule p;                // v is v, y is dv
@@ -975,9 +977,10 @@ struct Grad {
   const float* D;
   const float* N;        // as Rule's left
   const float* dR;
-  void* dq;              // [b, L, H, Dk] float, or of the streamed type where heads share nothing
+  void* dq;              // [b, L, H / heads, Dk]: of the streamed type, or (where a group's heads are not one workgroup's) float
   void* dk;
   bool dqk_f32;
+  int heads;
   void* dbeta;           // nullable
   void* dg;              // nullable
 };
@@ -988,32 +991,35 @@ struct GradLds {
   typedef Shape<T> Z;
   static constexpr int kC = Z::kC, kN = Z::kTwo ? 2 : 1;
   static constexpr int ldw = kC + 16 / int(sizeof(T));
-  static constexpr int ldv = Tile<T, 64, kValue>::ld;
+  static constexpr int ldv = 32 + 16 / int(sizeof(T));        // rows of 32 values
+  static constexpr int ldt = kC + 32 / int(sizeof(T));        // columns: rows of kC tokens
+  static constexpr int lds = KDP + 32 / int(sizeof(T));       // rows of KDP elements of the keys
   __attribute__((aligned(16))) T q[Tile<T, KDP, kQuery>::kElems];
   __attribute__((aligned(16))) T k[Tile<T, KDP, kKey>::kElems];
   union {
     struct {
-      __attribute__((aligned(16))) T dy[kC * ldv], u[kN][kC * ldv], r[kN][kC * ldv];
+      __attribute__((aligned(16))) T dy[kC * ldv], u[kN][32 * ldt], r[kN][32 * ldt], S[kN][32 * lds], D[kN][32 * lds];
     } a;
     struct {
       __attribute__((aligned(16))) T W[kN][kC * ldw], B[kN][kC * ldw];
     } b;
   };
   Decays<kC> d;
-  float beta[kC];
-  float rows[Z::TB][kC], cols[Z::TB][kC];      // sums of a block's rows and columns
-  float dots[KDP / 16][kC], kept[KDP / 16][kC]; // of a token, over 16 of the keys' elements
-  float db[kGradWaves * kWave / kC][kC];        // a token's parts of dbeta
+  __attribute__((aligned(16))) float beta[kC], own[kC];  // own: the part of dR that is beta's own
+  __attribute__((aligned(16))) float rows[Z::TB][kC], cols[Z::TB][kC];      // sums of a block's rows and columns
+  float dots[KDP / 16][kC], kept[KDP / 16][kC];  // of a token, over 16 of the keys' elements
+  __attribute__((aligned(16))) float db[8][kC];  // a token's parts of dbeta
+  float gate[kC];
   double sd[kGradWaves];
 };
 
 // four floats to a row of an LDS tile, in its parts
-__device__ __forceinline__ void put4(float (&x)[4], float* a, float*) { *reinterpret_cast<float4*>(a) = make_float4(x[0], x[1], x[2], x[3]); }
-__device__ __forceinline__ void put4(float (&x)[4], bf16_bits* a, bf16_bits* b) {
-  const uint2 hi = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+__device__ __forceinline__ void put4(const float (&x)[4], float* a, float*) { *reinterpret_cast<float4*>(a) = make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void put4(const float (&x)[4], bf16_bits* a, bf16_bits* b) {
+  const uint2 hi = make_uint2(pack_pair(x[0], x[1]), pack_pair(x[2], x[3]));
   *reinterpret_cast<uint2*>(a) = hi;
-  *reinterpret_cast<uint2*>(b) = make_uint2(pack_bf16(x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xffff0000u)),
-                                            pack_bf16(x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xffff0000u)));
+  *reinterpret_cast<uint2*>(b) = make_uint2(pack_pair(x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xffff0000u)),
+                                            pack_pair(x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xffff0000u)));
 }
 __device__ __forceinline__ void put1(float x, float* a, float*) { *a = x; }
 __device__ __forceinline__ void put1(float x, bf16_bits* a, bf16_bits* b) {
@@ -1026,76 +1032,106 @@ __device__ __forceinline__ void store4(T* to, const float (&x)[4], int left, boo
   if (vec) {
     if (left <= 0) return;
     if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-    else *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    else *reinterpret_cast<uint2*>(to) = make_uint2(pack_pair(x[0], x[1]), pack_pair(x[2], x[3]));
   } else {
 #pragma unroll
     for (int r = 0; r < 4; r++)
       if (r < left) store_elem(to + r, x[r]);
   }
 }
+__device__ __forceinline__ void store8(bf16_bits* to, const bf16x8& x) { *reinterpret_cast<bf16x8*>(to) = x; }
+__device__ __forceinline__ void store8(float* to, const f32x8& x) {
+  reinterpret_cast<float4*>(to)[0] = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
+  reinterpret_cast<float4*>(to)[1] = make_float4(x.v[4], x.v[5], x.v[6], x.v[7]);
+}
 
-template <typename T, int KDP, bool VEC>
-__global__ __launch_bounds__(kGradWaves * kWave) void delta_grad_kernel(Grad a) {
+// x and that of the lane 16 or 32 away, added
+__device__ __forceinline__ float add_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float add_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// x and that of the lane N places on in its row of 16, added
+template <int N>
+__device__ __forceinline__ float add_ror(float x) {
+  return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(x)), 0x120 + N, 0xF, 0xF, false));
+}
+// One step of a running sum over the lanes that starts again where `cut` is
+template <int CTRL, int ROWS>
+__device__ __forceinline__ void scan_step(double& x, int& cut) {
+  const double before = dpp_or_zero<CTRL, ROWS>(x);
+  const int c = __builtin_amdgcn_update_dpp(0, cut, CTRL, ROWS, 0xF, false);
+  x += cut ? 0.0 : before;
+  cut |= c;
+}
+__device__ __forceinline__ void running_sum(double& x, int cut) {
+  scan_step<0x111, 0xF>(x, cut);
+  scan_step<0x112, 0xF>(x, cut);
+  scan_step<0x114, 0xF>(x, cut);
+  scan_step<0x118, 0xF>(x, cut);
+  scan_step<0x142, 0xA>(x, cut);
+  scan_step<0x143, 0xC>(x, cut);
+}
+__device__ __forceinline__ double last_lane(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(u)), kWave - 1));
+  const uint64_t hi = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(u >> 32)), kWave - 1));
+  return __builtin_bit_cast(double, (hi << 32) | lo);
+}
+
+template <typename T, int KDP, bool MULTI, bool VEC>
+__global__ __launch_bounds__(kGradWaves * kWave) __attribute__((amdgpu_waves_per_eu(KDP == 64 ? 4 : 2)))
+void delta_grad_kernel(Grad a) {
   typedef Shape<T> Z;
   typedef GradLds<T, KDP> Lds;
-  constexpr int kC = Z::kC, TB = Z::TB, kSteps = Z::kSteps, KS = KDP / 32, MT = KDP / 16;
+  constexpr int kC = Z::kC, TB = Z::TB, kSteps = Z::kSteps, KS = KDP / 32, MT = KDP / 16, kAll = kGradWaves * kWave;
   constexpr int TT = TB * MT / kGradWaves;  // blocks of tokens a wave has
-  constexpr int ldq = Tile<T, KDP, kQuery>::ld, ldk = Tile<T, KDP, kKey>::ld, ldv = Lds::ldv, ldw = Lds::ldw, kN = Lds::kN;
-  constexpr int NB = TB == 4 ? 2 : 1;       // blocks of W and B a wave has, at most
+  constexpr int ldq = Tile<T, KDP, kQuery>::ld, ldk = Tile<T, KDP, kKey>::ld, ldv = Lds::ldv, ldt = Lds::ldt, lds = Lds::lds, ldw = Lds::ldw;
+  constexpr int kN = Lds::kN, NB = TB == 4 ? 2 : 1;  // blocks of W and B a wave has, at most
   const Rule& p = a.p;
   __shared__ Lds sh;
-  const int64_t units = p.b * p.H * p.n_chunks, wg = blockIdx.x;
+  const int sets = p.H / a.heads;  // sets of heads of one workgroup
+  const int64_t units = p.b * sets * p.n_chunks, wg = blockIdx.x;
   const int64_t id = units % 8 == 0 ? (wg % 8) * (units / 8) + wg / 8 : wg;
-  const int64_t bh = id / p.n_chunks, bi = bh / p.H;
-  const int c = int(id % p.n_chunks), h = int(bh % p.H), n = live_length(p.lengths, bi, p.L), G = p.H / p.share;
+  const int64_t bset = id / p.n_chunks, bi = bset / sets;
+  const int c = int(id % p.n_chunks), set = int(bset % sets), n = live_length(p.lengths, bi, p.L), G = p.H / p.share;
+  const int h0 = set * a.heads, gr = h0 / p.share;
   const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid / kWave), l = tid % kWave;
   const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
   const int64_t t0 = int64_t(c) * kC, row0 = bi * p.L + t0;
   const int nv = std::max(0, std::min(kC, int(n - t0))), rows = int(std::min<int64_t>(kC, p.L - t0));
   auto zero_rows = [&](void* x, bool f32, int heads, int hh, int D, int from) {
-    for (int j = tid; j < (rows - from) * D; j += kGradWaves * kWave) {
+    for (int j = tid; j < (rows - from) * D; j += kAll) {
       const int64_t at = ((row0 + from + j / D) * heads + hh) * D + j % D;
       if (f32) static_cast<float*>(x)[at] = 0.f;
       else store_elem(static_cast<T*>(x) + at, 0.f);
     }
   };
   if (nv < rows) {  // behind the length
-    zero_rows(a.dq, a.dqk_f32, p.H, h, p.Dk, nv);
-    zero_rows(a.dk, a.dqk_f32, p.H, h, p.Dk, nv);
-    zero_rows(p.y, false, p.H, h, p.Dv, nv);
-    if (a.dbeta) zero_rows(a.dbeta, false, p.H, h, 1, nv);
-    if (a.dg) zero_rows(a.dg, false, p.H, h, 1, nv);
+    zero_rows(a.dq, a.dqk_f32, sets, set, p.Dk, nv);
+    zero_rows(a.dk, a.dqk_f32, sets, set, p.Dk, nv);
+    for (int h = h0; h < h0 + a.heads; h++) {
+      zero_rows(p.y, false, p.H, h, p.Dv, nv);
+      if (a.dbeta) zero_rows(a.dbeta, false, p.H, h, 1, nv);
+      if (a.dg) zero_rows(a.dg, false, p.H, h, 1, nv);
+    }
   }
   if (nv == 0) return;
-  const int64_t state = id * int64_t(p.KP) * p.VP, left = id * int64_t(kC) * p.VP;
+  // waves 0..3 bring q, the others k
+  const bool brings_q = wv < 4;
+  constexpr int kRowsPieces = Tile<T, KDP, kQuery>::kPieces;
+  static_assert(kRowsPieces == Tile<T, KDP, kKey>::kPieces, "q and k come alike");
+  uint4 rqk[kRowsPieces];
   {
-    if (wv < 4) {
-      Stage<T, KDP, kQuery, VEC> s;
-      uint4 r[Tile<T, KDP, kQuery>::kPieces];
-      s.init(static_cast<const T*>(p.q) + (row0 * G + h / p.share) * p.Dk, G * p.Dk, p.Dk, false, tid);
-      s.load(r, nv, tid);
-      s.store(sh.q, r, tid);
-    } else {
-      Stage<T, KDP, kKey, VEC> s;
-      uint4 r[Tile<T, KDP, kKey>::kPieces];
-      s.init(static_cast<const T*>(p.k) + (row0 * G + h / p.share) * p.Dk, G * p.Dk, p.Dk, false, tid - kThreads);
-      s.load(r, nv, tid - kThreads);
-      s.store(sh.k, r, tid - kThreads);
-    }
-    if (wv == 0) {
-      const float g = l < kC ? gate_of<T>(p, bi, t0 + l, h, n) : 0.f;
-      fill_decays(sh.d, g, 1.f);
-    } else if (wv == 1 && l < kC) {
-      sh.beta[l] = beta_of<T>(p, bi, t0 + l, h, n);
-    }
+    Stage<T, KDP, kQuery, VEC> st;
+    st.init(static_cast<const T*>(brings_q ? p.q : p.k) + (row0 * G + gr) * p.Dk, G * p.Dk, p.Dk, false, tid % kThreads);
+    st.load(rqk, nv, tid % kThreads);
   }
   const int ib = wv % MT, tb0 = wv / MT * TT;  // the wave's 16 elements of the keys, and its first block of tokens
   const int n_blocks = TB * (TB + 1) / 2;
-  f32x4 fq[TT], fk[TT], tk[TT], wu[NB], bu[NB];
-#pragma unroll
-  for (int j = 0; j < TT; j++) fq[j] = fk[j] = tk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < NB; j++) wu[j] = bu[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   int tbs[NB], sbs[NB];
 #pragma unroll
   for (int j = 0; j < NB; j++) {
@@ -1104,271 +1140,357 @@ __global__ __launch_bounds__(kGradWaves * kWave) void delta_grad_kernel(Grad a) 
     tbs[j] = tb;
     sbs[j] = sb;
   }
-  double sd = 0.0;
-  float db = 0.f;  // the part of dbeta that this thread's columns give
-  constexpr int kCols = 64 * kC / (kGradWaves * kWave);  // columns of one token that a thread brings of N and dR
-  const int vt = tid % kC, vc = kCols * (tid / kC);
-  __syncthreads();
-  for (int v0 = 0; v0 < p.Dv; v0 += 64) {
-    if (v0) __syncthreads();
-    if (wv < 4) {
-      Stage<T, 64, kValue, VEC> s;
-      uint4 r[Tile<T, 64, kValue>::kPieces];
-      s.init(static_cast<const T*>(a.dy) + (row0 * p.H + h) * p.Dv + v0, p.H * p.Dv, p.Dv - v0, false, tid);
-      s.load(r, nv, tid);
-      s.store(sh.a.dy, r, tid);
+  f32x4 sum_q[MULTI ? TT : 1], sum_k[MULTI ? TT : 1];
+  if constexpr (MULTI)
+#pragma unroll
+    for (int j = 0; j < TT; j++) sum_q[j] = sum_k[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto store_qk = [&](int tt, const f32x4& dq, const f32x4& dk) {
+    const int t = 16 * (tb0 + tt) + lr, i = 16 * ib + g4;
+    if (t >= nv) return;
+    const int64_t at = ((row0 + t) * sets + set) * p.Dk + i;
+    const float x[4] = {dq[0], dq[1], dq[2], dq[3]}, y[4] = {dk[0], dk[1], dk[2], dk[3]};
+    if (a.dqk_f32) {
+      store4(static_cast<float*>(a.dq) + at, x, p.Dk - i, VEC);
+      store4(static_cast<float*>(a.dk) + at, y, p.Dk - i, VEC);
+    } else {
+      store4(static_cast<T*>(a.dq) + at, x, p.Dk - i, VEC);
+      store4(static_cast<T*>(a.dk) + at, y, p.Dk - i, VEC);
     }
-    {
-      float x[kCols], y[kCols];
-      const int64_t at = left + (vt / 16 * int64_t(p.VP) + v0 + vc) * 16 + vt % 16;
+  };
+
+  // what a thread brings of 32 columns: a piece of dY's rows, four tokens of one column of N and dR, four of the keys'
+  // elements of one column of S and D
+  constexpr int kVec = 16 / int(sizeof(T)), kRowPieces = 32 / kVec;           // pieces of a row of dY
+  constexpr int kDy = (kC * kRowPieces + kAll - 1) / kAll;
+  constexpr int kLeft = kC * 8;                                                // float4 pieces of N, of dR
+  constexpr int kStates = KDP * 8 / kAll;                                      // of S, of D, a thread
+  struct Regs {
+    uint4 dy[kDy];
+    float4 n, r, S[kStates], D[kStates];
+  };
+  const bool has_left = tid < kLeft;
+  const int lt = tid % 4 * 4 + tid / 128 * 16, lv = tid / 4 % 32;  // its tokens and column of N and dR
+
+#pragma unroll 1
+  for (int h = h0; h < h0 + (MULTI ? a.heads : 1); h++) {
+    if constexpr (MULTI) asm volatile("" ::: "memory");  // what is read of q and k is not kept in registers over the heads
+    const int64_t at_chunk = (bi * p.H + h) * p.n_chunks + c;
+    const float* gN = a.N + at_chunk * kC * p.VP;
+    const float* gR = a.dR + at_chunk * kC * p.VP;
+    const float* gS = a.S + at_chunk * p.KP * p.VP;
+    const float* gD = a.D + at_chunk * p.KP * p.VP;
+    const T* gY = static_cast<const T*>(a.dy) + (row0 * p.H + h) * p.Dv;
+    auto fetch = [&](Regs& r, int v0) {
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < kCols; j++) {
-        const bool in = v0 + vc + j < p.VP;
-        x[j] = in ? a.N[at + 16 * j] : 0.f;
-        y[j] = in ? a.dR[at + 16 * j] : 0.f;
-      }
-      const float be = sh.beta[vt], own = be / moved_beta(be);
+      for (int j = 0; j < kDy; j++) {
+        const int i = tid + j * kAll, t = i / kRowPieces, v = v0 + kVec * (i % kRowPieces);
+        r.dy[j] = make_uint4(0, 0, 0, 0);
+        if (t < nv && v < p.Dv) {
+          const T* from = gY + int64_t(t) * p.H * p.Dv + v;
+          if constexpr (VEC) {
+            r.dy[j] = *reinterpret_cast<const uint4*>(from);
+          } else {
+            T x[kVec];
 #pragma unroll
-      for (int j = 0; j < kCols; j++) {
-        db = fmaf(x[j], y[j], db);
-        x[j] *= be;
-        y[j] *= own;
-      }
-#pragma unroll
-      for (int e = 0; e < kCols; e += 4) {
-        float u4[4] = {x[e], x[e + 1], x[e + 2], x[e + 3]}, r4[4] = {y[e], y[e + 1], y[e + 2], y[e + 3]};
-        put4(u4, sh.a.u[0] + vt * ldv + vc + e, sh.a.u[kN - 1] + vt * ldv + vc + e);
-        put4(r4, sh.a.r[0] + vt * ldv + vc + e, sh.a.r[kN - 1] + vt * ldv + vc + e);
-      }
-    }
-    __syncthreads();
-    {  // dv: the first part of dR is what rounding leaves of it
-      constexpr int kVec = 16 / int(sizeof(T)), kPieces = 64 / kVec;
-      for (int j = tid; j < kC * kPieces; j += kGradWaves * kWave) {
-        const int t = j / kPieces, v = v0 + kVec * (j % kPieces);
-        const T* from = sh.a.r[0] + t * ldv + kVec * (j % kPieces);
-        if (t >= nv || v >= p.Dv) continue;
-        T* to = static_cast<T*>(p.y) + ((row0 + t) * p.H + h) * p.Dv + v;
-        if constexpr (VEC) {
-          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
-        } else {
-          for (int e = 0; e < kVec; e++)
-            if (v + e < p.Dv) to[e] = from[e];
+            for (int e = 0; e < kVec; e++) x[e] = v + e < p.Dv ? from[e] : T(0);
+            __builtin_memcpy(&r.dy[j], x, 16);
+          }
         }
       }
-    }
+      const bool in = has_left && v0 + lv < p.VP;
+      const int at = (lt / 16 * p.VP + v0 + lv) * 16 + lt % 16;
+      r.n = in ? *reinterpret_cast<const float4*>(gN + at) : zero;
+      r.r = in ? *reinterpret_cast<const float4*>(gR + at) : zero;
 #pragma unroll
-    for (int kk = 0; kk < 2; kk++) {
-      const int v = v0 + 32 * kk + g8;
-      float x[8], y[8];
-      const int64_t at = state + (ib * int64_t(p.VP) + v) * 16 + lr;
-      const bool in = 16 * ib < p.KP && v < p.VP;
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        x[j] = in ? a.S[at + 16 * j] : 0.f;
-        y[j] = in ? a.D[at + 16 * j] : 0.f;
+      for (int j = 0; j < kStates; j++) {
+        const int i = tid + j * kAll, e = i % 4 * 4 + i / 128 * 16, v = v0 + i / 4 % 32;
+        const bool ok = e < p.KP && v < p.VP;
+        const int so = (e / 16 * p.VP + v) * 16 + e % 16;
+        r.S[j] = ok ? *reinterpret_cast<const float4*>(gS + so) : zero;
+        r.D[j] = ok ? *reinterpret_cast<const float4*>(gD + so) : zero;
       }
-      if (wv < MT) {
+    };
+    const float gate = wv == 0 && l < kC ? gate_of<T>(p, bi, t0 + l, h, n) : 0.f;
+    const float beta = wv == 1 && l < kC ? beta_of<T>(p, bi, t0 + l, h, n) : 0.f;
+    Regs r;
+    fetch(r, 0);
+    if (wv == 0) {
+      fill_decays(sh.d, gate, 1.f);
+      if (l < kC) sh.gate[l] = gate;
+    } else if (wv == 1 && l < kC) {
+      sh.beta[l] = beta;
+      sh.own[l] = beta / moved_beta(beta);
+    }
+    if (h == h0) {
+      if (brings_q) Stage<T, KDP, kQuery, VEC>::store(sh.q, rqk, tid);
+      else Stage<T, KDP, kKey, VEC>::store(sh.k, rqk, tid - kThreads);
+    }
+    f32x4 fq[TT], fk[TT], tk[TT], wu[NB], bu[NB];
+#pragma unroll
+    for (int j = 0; j < TT; j++) fq[j] = fk[j] = tk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NB; j++) wu[j] = bu[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    double sd = 0.0;
+    float db[4] = {0.f, 0.f, 0.f, 0.f};  // the part of dbeta that this thread's columns give
+    __syncthreads();
+#pragma unroll 1
+    for (int v0 = 0; v0 < p.Dv; v0 += 32) {
+      if (v0) __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kDy; j++) {
+        const int i = tid + j * kAll;
+        if (i < kC * kRowPieces) *reinterpret_cast<uint4*>(sh.a.dy + i / kRowPieces * ldv + kVec * (i % kRowPieces)) = r.dy[j];
+      }
+      if (has_left) {
+        const float4 be4 = lds4(sh.beta + lt), ow4 = lds4(sh.own + lt);
+        const float be[4] = {be4.x, be4.y, be4.z, be4.w}, own[4] = {ow4.x, ow4.y, ow4.z, ow4.w};
+        const float x[4] = {r.n.x, r.n.y, r.n.z, r.n.w}, y[4] = {r.r.x, r.r.y, r.r.z, r.r.w};
+        float u[4], w[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          db[e] = fmaf(x[e], y[e], db[e]);
+          u[e] = x[e] * be[e];
+          w[e] = y[e] * own[e];
+        }
+        put4(u, sh.a.u[0] + lv * ldt + lt, sh.a.u[kN - 1] + lv * ldt + lt);
+        put4(w, sh.a.r[0] + lv * ldt + lt, sh.a.r[kN - 1] + lv * ldt + lt);
+      }
+#pragma unroll
+      for (int j = 0; j < kStates; j++) {
+        const int i = tid + j * kAll, at = i / 4 % 32 * lds + i % 4 * 4 + i / 128 * 16;
+        const float x[4] = {r.S[j].x, r.S[j].y, r.S[j].z, r.S[j].w}, y[4] = {r.D[j].x, r.D[j].y, r.D[j].z, r.D[j].w};
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          if constexpr (sizeof(T) == 4) sd = fma(double(x[j]), double(y[j]), sd);
-          else s = fmaf(x[j], y[j], s);
+        for (int e = 0; e < 4; e++) {
+          if constexpr (sizeof(T) == 4) sd = fma(double(x[e]), double(y[e]), sd);
+          else s = fmaf(x[e], y[e], s);
         }
         if constexpr (sizeof(T) == 2) sd += double(s);
+        put4(x, sh.a.S[0] + at, sh.a.S[kN - 1] + at);
+        put4(y, sh.a.D[0] + at, sh.a.D[kN - 1] + at);
       }
-      Parts<T, 2> sf, df;
-      sf.set(x);
-      df.set(y);
+      __syncthreads();
+      if (v0 + 32 < p.Dv) fetch(r, v0 + 32);
+      if (wv < TB) {  // dv: the first part of dR is what rounding leaves of it
+        const int t = 16 * wv + lr, v = v0 + g8;
+        const Frag<T> f = col_frag(sh.a.r[0], ldt, g8, 16 * wv, 4);
+        if (t < nv && v < p.Dv) {
+          T* to = static_cast<T*>(p.y) + ((row0 + t) * p.H + h) * p.Dv + v;
+          if constexpr (VEC) {
+            if (v + 8 <= p.Dv) {
+              store8(to, f);
+            } else {  // (float) rows of whole 16-byte pieces may end inside the eight
+              float x[8];
+              frag_floats(f, x);
+              const float x4[4] = {x[0], x[1], x[2], x[3]};
+              store4(to, x4, p.Dv - v, true);
+            }
+          } else {
+            float x[8];
+            frag_floats(f, x);
 #pragma unroll
-      for (int tt = 0; tt < TT; tt++) {
-        const int at = (16 * (tb0 + tt) + lr) * ldv + 32 * kk + g8;
-        const Frag<T> yf = row_frag(sh.a.dy + at);
-        Parts<T, 2> uf, rf;
+            for (int e = 0; e < 8; e++)
+              if (v + e < p.Dv) store_elem(to + e, x[e]);
+          }
+        }
+      }
+      {
+        Parts<T, 2> sf, df;
 #pragma unroll
         for (int e = 0; e < kN; e++) {
-          uf.f[e] = row_frag(sh.a.u[e] + at);
-          rf.f[e] = row_frag(sh.a.r[e] + at);
-          fq[tt] = mma(sf.f[e], yf, fq[tt]);
+          sf.f[e] = col_frag(sh.a.S[e], lds, g8, 16 * ib, 4);
+          df.f[e] = col_frag(sh.a.D[e], lds, g8, 16 * ib, 4);
         }
-        fk[tt] = mma_parts(sf, rf, fk[tt]);
-        tk[tt] = mma_parts(df, uf, tk[tt]);
+#pragma unroll
+        for (int tt = 0; tt < TT; tt++) {
+          const Frag<T> yf = row_frag(sh.a.dy + (16 * (tb0 + tt) + lr) * ldv + g8);
+          Parts<T, 2> uf, rf;
+#pragma unroll
+          for (int e = 0; e < kN; e++) {
+            uf.f[e] = col_frag(sh.a.u[e], ldt, g8, 16 * (tb0 + tt), 4);
+            rf.f[e] = col_frag(sh.a.r[e], ldt, g8, 16 * (tb0 + tt), 4);
+            fq[tt] = mma(sf.f[e], yf, fq[tt]);
+          }
+          fk[tt] = mma_parts(sf, rf, fk[tt]);
+          tk[tt] = mma_parts(df, uf, tk[tt]);
+        }
       }
 #pragma unroll
       for (int j = 0; j < NB; j++) {
         if (wv + j * kGradWaves < n_blocks) {
           Parts<T, 2> uf, rf;
-          const int su = (16 * sbs[j] + lr) * ldv + 32 * kk + g8, st = (16 * tbs[j] + lr) * ldv + 32 * kk + g8;
-          const Frag<T> yf = row_frag(sh.a.dy + st);
+          const Frag<T> yf = row_frag(sh.a.dy + (16 * tbs[j] + lr) * ldv + g8);
 #pragma unroll
           for (int e = 0; e < kN; e++) {
-            uf.f[e] = row_frag(sh.a.u[e] + su);
-            rf.f[e] = row_frag(sh.a.r[e] + st);
+            uf.f[e] = col_frag(sh.a.u[e], ldt, g8, 16 * sbs[j], 4);
+            rf.f[e] = col_frag(sh.a.r[e], ldt, g8, 16 * tbs[j], 4);
             wu[j] = mma(uf.f[e], yf, wu[j]);
           }
           bu[j] = mma_parts(uf, rf, bu[j]);
         }
       }
     }
-  }
-  sh.db[tid / kC][vt] = db;
-  __syncthreads();
-  if (a.dbeta && tid < nv) {
-    float s = 0.f;
+    // dbeta: a row of 16 lanes has four columns of 16 tokens, four a lane
 #pragma unroll
-    for (int j = 0; j < kGradWaves * kWave / kC; j++) s += sh.db[j][tid];
-    store_elem(static_cast<T*>(a.dbeta) + (row0 + tid) * p.H + h, s / moved_beta(sh.beta[tid]));
-  }
-  // ---- W and B + B^T, and what they give the gate ----
+    for (int e = 0; e < 4; e++) db[e] = add_ror<4>(add_ror<8>(db[e]));
+    if (has_left && lr < 4) *reinterpret_cast<float4*>(&sh.db[wv % 2 * 4 + l / 16][lt]) = make_float4(db[0], db[1], db[2], db[3]);
+    __syncthreads();
+    if (a.dbeta && tid < nv) {
+      float x = 0.f;
 #pragma unroll
-  for (int j = 0; j < NB; j++) {
-    if (wv + j * kGradWaves >= n_blocks) continue;
-    const int tb = tbs[j], sb = sbs[j], t = 16 * tb + lr, s0 = 16 * sb + g4;
-    const float th = sh.d.hi[t], tl = sh.d.lo[t];
-    float w[4], b[4];
-#pragma unroll
-    for (int r = 0; r < 4; r++) {
-      const float m = exp2_fast((th - sh.d.hi[s0 + r]) + (tl - sh.d.lo[s0 + r]));
-      w[r] = s0 + r <= t ? wu[j][r] * m * p.scale : 0.f;
-      b[r] = s0 + r < t ? -bu[j][r] * m : 0.f;
+      for (int j = 0; j < 8; j++) x += sh.db[j][tid];
+      store_elem(static_cast<T*>(a.dbeta) + (row0 + tid) * p.H + h, x / moved_beta(sh.beta[tid]));
     }
-    if (a.dg) {
-      f32x4 qk{0.f, 0.f, 0.f, 0.f}, kk4{0.f, 0.f, 0.f, 0.f};
+    // ---- W and B + B^T, and what they give the gate ----
 #pragma unroll
-      for (int kk = 0; kk < KS; kk++) {
-        const Frag<T> kf = row_frag(sh.k + (16 * sb + lr) * ldk + 32 * kk + g8);
-        qk = mma(kf, row_frag(sh.q + t * ldq + 32 * kk + g8), qk);
-        kk4 = mma(kf, row_frag(sh.k + t * ldk + 32 * kk + g8), kk4);
-      }
-      float x[4], row = 0.f;
+    for (int j = 0; j < NB; j++) {
+      if (wv + j * kGradWaves >= n_blocks) continue;
+      const int tb = tbs[j], sb = sbs[j], t = 16 * tb + lr, s0 = 16 * sb + g4;
+      const float th = sh.d.hi[t], tl = sh.d.lo[t];
+      float w[4], b[4];
 #pragma unroll
       for (int r = 0; r < 4; r++) {
-        x[r] = s0 + r < t ? fmaf(w[r], qk[r], b[r] * kk4[r]) : 0.f;
-        row += x[r];
+        const float m = exp2_fast((th - sh.d.hi[s0 + r]) + (tl - sh.d.lo[s0 + r]));
+        w[r] = s0 + r <= t ? wu[j][r] * m * p.scale : 0.f;
+        b[r] = s0 + r < t ? -bu[j][r] * m : 0.f;
       }
-      row += __shfl_xor(row, 16);
-      row += __shfl_xor(row, 32);
-      if (l < 16) sh.rows[sb][t] = row;
+      if (a.dg) {
+        f32x4 qk{0.f, 0.f, 0.f, 0.f}, kk4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int off = 1; off < 16; off *= 2)
+        for (int kk = 0; kk < KS; kk++) {
+          const Frag<T> kf = row_frag(sh.k + (16 * sb + lr) * ldk + 32 * kk + g8);
+          qk = mma(kf, row_frag(sh.q + t * ldq + 32 * kk + g8), qk);
+          kk4 = mma(kf, row_frag(sh.k + t * ldk + 32 * kk + g8), kk4);
+        }
+        float x[4], row = 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; r++) x[r] += __shfl_xor(x[r], off);
-      if (lr == 0) *reinterpret_cast<float4*>(&sh.cols[tb][s0]) = make_float4(x[0], x[1], x[2], x[3]);
-    }
-    put4(w, sh.b.W[0] + t * ldw + s0, sh.b.W[kN - 1] + t * ldw + s0);
-    if (tb > sb) {
-      put4(b, sh.b.B[0] + t * ldw + s0, sh.b.B[kN - 1] + t * ldw + s0);
+        for (int r = 0; r < 4; r++) {
+          x[r] = s0 + r < t ? fmaf(w[r], qk[r], b[r] * kk4[r]) : 0.f;
+          row += x[r];
+        }
+        row = add_xor32(add_xor16(row));
+        if (l < 16) sh.rows[sb][t] = row;
 #pragma unroll
-      for (int r = 0; r < 4; r++) put1(b[r], sh.b.B[0] + (s0 + r) * ldw + t, sh.b.B[kN - 1] + (s0 + r) * ldw + t);
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const int s = s0 + r;
-        if (s <= t) put1(b[r], sh.b.B[0] + t * ldw + s, sh.b.B[kN - 1] + t * ldw + s);
-        if (s < t) put1(b[r], sh.b.B[0] + s * ldw + t, sh.b.B[kN - 1] + s * ldw + t);
+        for (int r = 0; r < 4; r++) x[r] = add_ror<1>(add_ror<2>(add_ror<4>(add_ror<8>(x[r]))));
+        if (lr == 0) *reinterpret_cast<float4*>(&sh.cols[tb][s0]) = make_float4(x[0], x[1], x[2], x[3]);
       }
-      if (tb % 2 == 0 && tb + 1 < TB) {  // the block beside the diagonal that the products read
-        float z[4] = {0.f, 0.f, 0.f, 0.f};
-        put4(z, sh.b.W[0] + t * ldw + s0 + 16, sh.b.W[kN - 1] + t * ldw + s0 + 16);
-      }
-    }
-  }
-  __syncthreads();
-  // ---- dq, dk ----
+      put4(w, sh.b.W[0] + t * ldw + s0, sh.b.W[kN - 1] + t * ldw + s0);
+      if (tb > sb) {
+        put4(b, sh.b.B[0] + t * ldw + s0, sh.b.B[kN - 1] + t * ldw + s0);
 #pragma unroll
-  for (int tt = 0; tt < TT; tt++) {
-    const int tb = tb0 + tt, t = 16 * tb + lr, i = 16 * ib + g4;
-    const float in = sh.d.in[t], out = sh.d.out[t];
-    f32x4 dq, dk;
-#pragma unroll
-    for (int r = 0; r < 4; r++) {
-      dq[r] = fq[tt][r] * (in * p.scale);
-      const float from = -fk[tt][r] * in, to = tk[tt][r] * out;
-      fk[tt][r] = from;
-      tk[tt][r] = to;
-      dk[r] = from + to;
-    }
-    if (a.dg) {
-      const float4 q4 = lds4(sh.q + t * ldq + i), k4 = lds4(sh.k + t * ldk + i);
-      const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, kv[4] = {k4.x, k4.y, k4.z, k4.w};
-      float x = 0.f, y = 0.f;
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        x = fmaf(qv[r], dq[r], fmaf(kv[r], fk[tt][r], x));
-        y = fmaf(kv[r], tk[tt][r], y);
-      }
-      x += __shfl_xor(x, 16);
-      x += __shfl_xor(x, 32);
-      y += __shfl_xor(y, 16);
-      y += __shfl_xor(y, 32);
-      if (l < 16) {
-        sh.dots[ib][t] = x;
-        sh.kept[ib][t] = y;
-      }
-    }
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ks++) {
-      const Frag<T> kf = col_frag(sh.k, ldk, 32 * ks + g8, 16 * ib, 4);
-      if (ks <= tb / 2) {
-#pragma unroll
-        for (int e = 0; e < kN; e++) dq = mma(kf, row_frag(sh.b.W[e] + t * ldw + 32 * ks + g8), dq);
-      }
-      if (ks >= tb / 2) {
-        const Frag<T> qf = col_frag(sh.q, ldq, 32 * ks + g8, 16 * ib, 4);
-#pragma unroll
-        for (int e = 0; e < kN; e++) dk = mma(qf, col_frag(sh.b.W[e], ldw, 32 * ks + g8, 16 * tb, 4), dk);
-      }
-#pragma unroll
-      for (int e = 0; e < kN; e++) dk = mma(kf, row_frag(sh.b.B[e] + t * ldw + 32 * ks + g8), dk);
-    }
-    if (t < nv) {
-      const int64_t at = ((row0 + t) * p.H + h) * p.Dk + i;
-      const float x[4] = {dq[0], dq[1], dq[2], dq[3]}, y[4] = {dk[0], dk[1], dk[2], dk[3]};
-      if (a.dqk_f32) {
-        store4(static_cast<float*>(a.dq) + at, x, p.Dk - i, VEC);
-        store4(static_cast<float*>(a.dk) + at, y, p.Dk - i, VEC);
+        for (int r = 0; r < 4; r++) put1(b[r], sh.b.B[0] + (s0 + r) * ldw + t, sh.b.B[kN - 1] + (s0 + r) * ldw + t);
       } else {
-        store4(static_cast<T*>(a.dq) + at, x, p.Dk - i, VEC);
-        store4(static_cast<T*>(a.dk) + at, y, p.Dk - i, VEC);
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const int s = s0 + r;
+          if (s <= t) put1(b[r], sh.b.B[0] + t * ldw + s, sh.b.B[kN - 1] + t * ldw + s);
+          if (s < t) put1(b[r], sh.b.B[0] + s * ldw + t, sh.b.B[kN - 1] + s * ldw + t);
+        }
+        if (tb % 2 == 0 && tb + 1 < TB) {  // the block beside the diagonal that the products read
+          const float z[4] = {0.f, 0.f, 0.f, 0.f};
+          put4(z, sh.b.W[0] + t * ldw + s0 + 16, sh.b.W[kN - 1] + t * ldw + s0 + 16);
+        }
       }
     }
-  }
-  if (!a.dg) return;
+    __syncthreads();
+    // ---- dq, dk ----
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) sd += __shfl_xor(sd, off);
-  if (l == 0) sh.sd[wv] = sd;
-  __syncthreads();
-  if (wv != 0) return;
-  // dg, lane l with token l: sums from a token on, that start again at a reset
-  double x = 0.0, kept = 0.0;
-  bool reset = false;
-  if (l < nv) {
-    for (int j = 0; j < MT; j++) {
-      x += double(sh.dots[j][l]);
-      kept += double(sh.kept[j][l]);
+    for (int tt = 0; tt < TT; tt++) {
+      const int tb = tb0 + tt, t = 16 * tb + lr, i = 16 * ib + g4;
+      const float in = sh.d.in[t], out = sh.d.out[t];
+      f32x4 dq, dk;
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        fq[tt][r] *= in * p.scale;
+        fk[tt][r] *= -in;
+        tk[tt][r] *= out;
+        dq[r] = fq[tt][r];
+        dk[r] = fk[tt][r] + tk[tt][r];
+      }
+      if constexpr (MULTI) {
+        dq += sum_q[tt];
+        dk += sum_k[tt];
+      }
+      if (a.dg) {
+        const float4 q4 = lds4(sh.q + t * ldq + i), k4 = lds4(sh.k + t * ldk + i);
+        const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, kv[4] = {k4.x, k4.y, k4.z, k4.w};
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          x = fmaf(qv[r], fq[tt][r], fmaf(kv[r], fk[tt][r], x));
+          y = fmaf(kv[r], tk[tt][r], y);
+        }
+        x = add_xor32(add_xor16(x));
+        y = add_xor32(add_xor16(y));
+        if (l < 16) {
+          sh.dots[ib][t] = x;
+          sh.kept[ib][t] = y;
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ks++) {
+        const Frag<T> kf = col_frag(sh.k, ldk, 32 * ks + g8, 16 * ib, 4);
+        if (ks <= tb / 2) {
+#pragma unroll
+          for (int e = 0; e < kN; e++) dq = mma(kf, row_frag(sh.b.W[e] + t * ldw + 32 * ks + g8), dq);
+        }
+        if (ks >= tb / 2) {
+          const Frag<T> qf = col_frag(sh.q, ldq, 32 * ks + g8, 16 * ib, 4);
+#pragma unroll
+          for (int e = 0; e < kN; e++) dk = mma(qf, col_frag(sh.b.W[e], ldw, 32 * ks + g8, 16 * tb, 4), dk);
+        }
+#pragma unroll
+        for (int e = 0; e < kN; e++) dk = mma(kf, row_frag(sh.b.B[e] + t * ldw + 32 * ks + g8), dk);
+      }
+      if constexpr (MULTI) {
+        sum_q[tt] = dq;
+        sum_k[tt] = dk;
+      } else {
+        store_qk(tt, dq, dk);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // the next block's reads would not fit in the registers
     }
-    for (int j = 0; j <= l / 16; j++) x += double(sh.rows[j][l]);
-    for (int j = l / 16; j < TB; j++) x -= double(sh.cols[j][l]);
-    x -= kept;
-    reset = gate_of<T>(p, bi, t0 + l, h, n) < kZeroLog;
-  }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) kept += __shfl_xor(kept, off);
-  double end = 0.0;
-  for (int j = 0; j < kGradWaves; j++) end += sh.sd[j];
-  end = end * double(sh.d.all) + kept;
-  if (l == kWave - 1) x += end;
-  if (reset) x = 0.0;
-#pragma unroll
-  for (int off = 1; off < kWave; off *= 2) {
-    const double later = __shfl_down(x, off);
-    const bool cut = __shfl_down(int(reset), off) != 0;
-    if (l + off < kWave && !reset) {
-      x += later;
-      reset = cut;
+    if (a.dg) {
+      running_sum(sd, 0);
+      if (l == kWave - 1) sh.sd[wv] = sd;
     }
+    __syncthreads();  // dots and sums are there; W and B have been read
+    // dg: sums from a token on, that start again at a reset; lane l has the l-th token from the last
+    if (a.dg && wv == 0) {
+      const int t = kWave - 1 - l;
+      double x = 0.0, kept = 0.0;
+      int reset = 0;
+      if (t < nv) {
+#pragma unroll
+        for (int j = 0; j < MT; j++) {
+          x += double(sh.dots[j][t]);
+          kept += double(sh.kept[j][t]);
+        }
+#pragma unroll
+        for (int j = 0; j < TB; j++) {
+          if (j <= t / 16) x += double(sh.rows[j][t]);
+          if (j >= t / 16) x -= double(sh.cols[j][t]);
+        }
+        x -= kept;
+        reset = sh.gate[t] < kZeroLog;
+      }
+      double all_kept = kept;
+      running_sum(all_kept, 0);
+      double end = 0.0;
+#pragma unroll
+      for (int j = 0; j < kGradWaves; j++) end += sh.sd[j];
+      end = end * double(sh.d.all) + last_lane(all_kept);
+      if (l == 0) x += end;
+      if (reset) x = 0.0;
+      running_sum(x, reset);
+      if (t < nv) store_elem(static_cast<T*>(a.dg) + (row0 + t) * p.H + h, float(x));
+    }
+    if (MULTI && h + 1 < h0 + a.heads) __syncthreads();  // the small arrays have been read
   }
-  if (l < nv) store_elem(static_cast<T*>(a.dg) + (row0 + l) * p.H + h, float(x));
+  if constexpr (MULTI)
+#pragma unroll
+    for (int tt = 0; tt < TT; tt++) store_qk(tt, sum_q[tt], sum_k[tt]);
 }
 
 // ---------------------------------------------------------------------------
@@ -1502,6 +1624,15 @@ Rule rule_of(const DeltaRuleArgs& a) {
   return p;
 }
 
+// Heads of a group that delta_grad_kernel takes one after the other, their dq and dk summed in registers: as many as leave
+// the chip two generations of workgroups (a CU holds one or two), so that the others' partial sums, in float, are few.
+int heads_together(const DeltaRuleArgs& a, int64_t chunks) {
+  const int64_t share = a.H / a.G;
+  int64_t heads = share;
+  while (heads > 1 && (share % heads || a.b * (a.H / heads) * chunks < 1024)) heads--;
+  return int(heads);
+}
+
 // Bytes from the workspace's start of its parts.
 struct Work {
   size_t lower, upper, S, D, N, dR, dq, dk, total;
@@ -1526,9 +1657,10 @@ Work plan_work(const DeltaRuleArgs& a, bool backward) {
     w.D = take(state);
     w.N = take(rows);
     w.dR = take(rows);
-    if (a.G != a.H) {
-      w.dq = take(size_t(a.b) * a.L * a.H * a.Dk * 4);
-      w.dk = take(size_t(a.b) * a.L * a.H * a.Dk * 4);
+    const int64_t sets = a.H / heads_together(a, p.n_chunks);
+    if (sets != a.G) {
+      w.dq = take(size_t(a.b) * a.L * sets * a.Dk * 4);
+      w.dk = take(size_t(a.b) * a.L * sets * a.Dk * 4);
     }
   }
   w.total = at;
@@ -1556,12 +1688,16 @@ hipError_t run_sweep(const Rule& p) {
 template <typename T>
 hipError_t run_grad(const Grad& a) {
   const Rule& p = a.p;
-  const int64_t blocks = p.b * p.H * p.n_chunks;
+  const int64_t blocks = p.b * (p.H / a.heads) * p.n_chunks;
   const bool vec = pieces<T>(p.q, p.Dk) && pieces<T>(p.k, p.Dk) && pieces<T>(a.dy, p.Dv) && pieces<T>(p.y, p.Dv) &&
                    pieces<T>(a.dq, p.Dk) && pieces<T>(a.dk, p.Dk);
   auto go = [&](auto kern) { return launch_kind(kKindDeltaGrad, kern, blocks, kGradWaves * kWave, p.stream, a); };
-  if (p.Dk <= 64) return vec ? go(delta_grad_kernel<T, 64, true>) : go(delta_grad_kernel<T, 64, false>);
-  return vec ? go(delta_grad_kernel<T, 128, true>) : go(delta_grad_kernel<T, 128, false>);
+  auto width = [&](auto multi) {
+    constexpr bool M = decltype(multi)::value;
+    if (p.Dk <= 64) return vec ? go(delta_grad_kernel<T, 64, M, true>) : go(delta_grad_kernel<T, 64, M, false>);
+    return vec ? go(delta_grad_kernel<T, 128, M, true>) : go(delta_grad_kernel<T, 128, M, false>);
+  };
+  return a.heads > 1 ? width(std::true_type{}) : width(std::false_type{});
 }
 
 template <typename T>
@@ -1601,8 +1737,10 @@ hipError_t bwd_impl(const DeltaRuleArgs& a, char* ws) {
   r.last = a.dh0;
   err = run_sweep<T, kBackwards>(r);
   if (err != hipSuccess || a.L == 0) return err;
-  const bool shared = p.share > 1;
   Grad g{};
+  g.heads = heads_together(a, p.n_chunks);
+  const int rest = p.share / g.heads;  // partial sums of a group
+  const bool shared = rest > 1;
   g.p = p;
   g.p.y = a.dv;
   g.dy = a.dy;
@@ -1619,8 +1757,8 @@ hipError_t bwd_impl(const DeltaRuleArgs& a, char* ws) {
     const float* in = k ? at(w.dk) : at(w.dq);
     T* out = static_cast<T*>(k ? a.dk : a.dq);
     const bool vec = a.Dk % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
-    err = vec ? launch_kind(kKindDeltaReduce, lin_group_sum_kernel<T, 4>, std::min(ceil_div(n, 1024), kSumBlocks), 256, a.stream, in, out, n, p.share, int(a.Dk))
-              : launch_kind(kKindDeltaReduce, lin_group_sum_kernel<T, 1>, std::min(ceil_div(n, 256), kSumBlocks), 256, a.stream, in, out, n, p.share, int(a.Dk));
+    err = vec ? launch_kind(kKindDeltaReduce, lin_group_sum_kernel<T, 4>, std::min(ceil_div(n, 1024), kSumBlocks), 256, a.stream, in, out, n, rest, int(a.Dk))
+              : launch_kind(kKindDeltaReduce, lin_group_sum_kernel<T, 1>, std::min(ceil_div(n, 256), kSumBlocks), 256, a.stream, in, out, n, rest, int(a.Dk));
     if (err != hipSuccess) return err;
   }
   return hipSuccess;

@@ -378,3 +378,12 @@ def test_graph_and_stream(dtype):
         assert torch.equal(y, y0) and torch.equal(last, l0) and torch.equal(yt, t0) and torch.equal(state, s0)
         for n in d:
             assert torch.equal(d[n], d0[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,G,Dk", [(32, 8, 40), (12, 2, 72)])
+def test_heads_that_share_one_workgroup(H, G, Dk, dtype):
+    """So many chunks that the backward takes the heads of a group, or some of them, one after the other."""
+    b, L = (16, 520) if G == 8 else (16, 200 if dtype == "f32" else 400)
+    check(make(b=b, L=L, H=H, G=G, Dk=Dk, Dv=8, dtype=dtype, seed=33, lengths=[L - 3 * i for i in range(b)]),
+          f"deltarule shared H={H} G={G} {dtype}")
