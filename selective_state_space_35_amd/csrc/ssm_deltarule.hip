@@ -1100,7 +1100,7 @@ void delta_grad_kernel(Grad a) {
   const int c = int(id % p.n_chunks), set = int(bset % sets), n = live_length(p.lengths, bi, p.L), G = p.H / p.share;
   const int h0 = set * a.heads, gr = h0 / p.share;
   const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid / kWave), l = tid % kWave;
-  const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
+  const int lr = l % 16, g4 = 4 * (l / 16);
   const int64_t t0 = int64_t(c) * kC, row0 = bi * p.L + t0;
   const int nv = std::max(0, std::min(kC, int(n - t0))), rows = int(std::min<int64_t>(kC, p.L - t0));
   auto zero_rows = [&](void* x, bool f32, int heads, int hh, int D, int from) {
@@ -1168,12 +1168,14 @@ void delta_grad_kernel(Grad a) {
     uint4 dy[kDy];
     float4 n, r, S[kStates], D[kStates];
   };
-  const bool has_left = tid < kLeft;
-  const int lt = tid % 4 * 4 + tid / 128 * 16, lv = tid / 4 % 32;  // its tokens and column of N and dR
-
 #pragma unroll 1
   for (int h = h0; h < h0 + (MULTI ? a.heads : 1); h++) {
-    if constexpr (MULTI) asm volatile("" ::: "memory");  // what is read of q and k is not kept in registers over the heads
+    // Over the heads neither what is read of q and k nor the lane's places in the tiles are kept: there are no registers
+    int tid_here = threadIdx.x;
+    if constexpr (MULTI) asm volatile("" : "+v"(tid_here) : : "memory");
+    const int tid = tid_here, l = tid % kWave, lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
+    const bool has_left = tid < kLeft;
+    const int lt = tid % 4 * 4 + tid / 128 * 16, lv = tid / 4 % 32;  // a thread's tokens and column of N and dR
     const int64_t at_chunk = (bi * p.H + h) * p.n_chunks + c;
     const float* gN = a.N + at_chunk * kC * p.VP;
     const float* gR = a.dR + at_chunk * kC * p.VP;
@@ -1314,6 +1316,7 @@ void delta_grad_kernel(Grad a) {
           }
           fk[tt] = mma_parts(sf, rf, fk[tt]);
           tk[tt] = mma_parts(df, uf, tk[tt]);
+          if (tt % 2 == 1) __builtin_amdgcn_sched_barrier(0);
         }
       }
 #pragma unroll
@@ -1329,6 +1332,7 @@ void delta_grad_kernel(Grad a) {
           }
           bu[j] = mma_parts(uf, rf, bu[j]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     // dbeta: a row of 16 lanes has four columns of 16 tokens, four a lane
@@ -1376,6 +1380,7 @@ void delta_grad_kernel(Grad a) {
         if (lr == 0) *reinterpret_cast<float4*>(&sh.cols[tb][s0]) = make_float4(x[0], x[1], x[2], x[3]);
       }
       put4(w, sh.b.W[0] + t * ldw + s0, sh.b.W[kN - 1] + t * ldw + s0);
+      __builtin_amdgcn_sched_barrier(0);
       if (tb > sb) {
         put4(b, sh.b.B[0] + t * ldw + s0, sh.b.B[kN - 1] + t * ldw + s0);
 #pragma unroll
