@@ -334,6 +334,18 @@ __global__ __launch_bounds__(kThreads) void delta_tri_kernel(Rule p, float* lowe
   }
 }
 
+// In the block of code around it: FIRST vector instructions, then N matrix instructions with EACH vector ones after each (a
+// wave's matrix instructions run beside its vector ones, if they are issued in turn)
+template <int FIRST, int N, int EACH>
+__device__ __forceinline__ void interleave() {
+  if constexpr (FIRST > 0) __builtin_amdgcn_sched_group_barrier(0x2, FIRST, 0);
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x2, EACH, 0);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // The sweep over a head's chunks, for VT columns of the values: columns of the state do not meet, so each of the state
 // waves has 16 NT of them to itself, with the state, R, N and U in registers.  A result of 16 x 16 has, in lane l, rows
@@ -462,7 +474,10 @@ void delta_sweep_kernel(Rule p) {
       const bool on = l < std::min(kC, live(i));
       fill_decays(sh.d[i & 3], on ? clamp_log(sg.value(r.gate) + fixed) : 0.f, 1.f);
       const float beta = on ? p.beta ? sb.value(r.beta) : 1.f : 0.f;
-      if (l < kC) sh.beta[i & 3][l] = kBack ? beta / moved_beta(beta) : beta;
+      const bool finite = beta * 0.f == 0.f;
+      if (l < kC) sh.beta[i & 3][l] = kBack ? beta / moved_beta(beta) : finite ? beta : 0.f;
+      // a beta that is no number makes its token's R, and so all from it on, NaN
+      if (!kBack && l < kC && !finite) sh.d[i & 3].in[l] = beta * 0.f;
     };
     // N blocks of P, rows t of q with columns s of k, to their halves of fragments: forwards of P, backwards of its
     // transpose.  All reads come first, all products next.
@@ -642,6 +657,7 @@ void delta_sweep_kernel(Rule p) {
       read_rows(i, kk + 1);
       __builtin_amdgcn_sched_barrier(0);
       times_state(kk);
+      if constexpr (kTwo) interleave<14, kOut ? 20 : 12, kOut ? 2 : 3>();
       __builtin_amdgcn_sched_barrier(0);
     }
     Frag<T> zf[2][kTri], pf[kTri][kN2], yf[kBack ? kSteps : 1][NT];
@@ -714,8 +730,7 @@ void delta_sweep_kernel(Rule p) {
 #pragma unroll
         for (int j = 0; j < NT; j++)
 #pragma unroll
-          for (int r = 0; r < 4; r++)  // NaN where beta is no number
-            x[tt][j][r] = fmaf(b4[tt][r], 0.f, fmaf(-w4[tt][r], x[tt][j][r], vq[tt][j][r]));
+          for (int r = 0; r < 4; r++) x[tt][j][r] = fmaf(-w4[tt][r], x[tt][j][r], vq[tt][j][r]);
     }
     // A row that is not finite must not meet Z's zeros: the rows before it would be no numbers.  From it on N is NaN, and so
     // are the outputs and the state's column.
@@ -760,23 +775,34 @@ void delta_sweep_kernel(Rule p) {
       for (int ks = 0; ks < kSteps; ks++)
 #pragma unroll
         for (int j = 0; j < NT; j++) xf[ks][j].set(x[2 * ks][j], x[2 * ks + 1][j]);
+      auto times = [&](int ea, int eb) {
 #pragma unroll
-      for (int ea = 0; ea < kN3; ea++) {
-        if (ea + 1 < kN3) read_z(ea + 1);
+        for (int ks = 0; ks < kSteps; ks++)
+#pragma unroll
+          for (int tt = 0; tt < TB; tt++)
+            if (kBack ? tt / 2 <= ks : ks <= tt / 2)
+#pragma unroll
+              for (int j = 0; j < NT; j++)
+                nn[tt][j] = mma(zf[ea % 2][kBack ? upper_frag<TB>(tt, ks) : lower_frag<TB>(tt, ks)], xf[ks][j].f[eb], nn[tt][j]);
+      };
+      if constexpr (kTwo) {  // Z's parts in the order 0, 1, 2 and each read while the one before is multiplied
+        read_z(1);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int eb = 0; ea + eb < kN3; eb++)
-#pragma unroll
-          for (int ks = 0; ks < kSteps; ks++)
-#pragma unroll
-            for (int tt = 0; tt < TB; tt++)
-              if (kBack ? tt / 2 <= ks : ks <= tt / 2)
-#pragma unroll
-                for (int j = 0; j < NT; j++)
-                  nn[tt][j] = mma(zf[ea % 2][kBack ? upper_frag<TB>(tt, ks) : lower_frag<TB>(tt, ks)], xf[ks][j].f[eb], nn[tt][j]);
+        times(0, 0);
+        times(0, 1);
+        times(0, 2);
+        interleave<28, 18, 4>();
         __builtin_amdgcn_sched_barrier(0);
+        read_z(2);
+        times(1, 0);
+        times(1, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        times(2, 0);
+      } else {
+        times(0, 0);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
     // the keys (and queries) as the state's update reads them, for 32 of its rows, a step ahead
     Frag<T> kc[2][2][kSteps], qc[2][2][kSteps];
     auto read_cols = [&](int step) {
@@ -838,8 +864,7 @@ void delta_sweep_kernel(Rule p) {
 #pragma unroll
           for (int e = 0; e < 8; e++) {
             const int tt = 2 * ks + e / 4;
-            const float b = b4[tt][e % 4];
-            u[e] = bad && !(b * 0.f == 0.f) ? 0.f : nn[tt][j][e % 4] * b;
+            u[e] = nn[tt][j][e % 4] * b4[tt][e % 4];
           }
           if constexpr (kOut) uf[ks][j].set(u);
 #pragma unroll
@@ -847,6 +872,27 @@ void delta_sweep_kernel(Rule p) {
         }
         wf[ks][j].set(u);
       }
+    if constexpr (kOut) {
+#pragma unroll
+      for (int tt = 0; tt < TB; tt++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) o[tt][j][r] *= in[tt];
+#pragma unroll
+      for (int ea = 0; ea < kN2; ea++)
+#pragma unroll
+        for (int eb = 0; ea + eb < kN2; eb++)
+#pragma unroll
+          for (int ks = 0; ks < kSteps; ks++)
+#pragma unroll
+            for (int tt = 0; tt < TB; tt++)
+              if (ks <= tt / 2)
+#pragma unroll
+                for (int j = 0; j < NT; j++) o[tt][j] = mma(uf[ks][j].f[ea], pf[lower_frag<TB>(tt, ks)][eb], o[tt][j]);
+      if constexpr (kTwo) interleave<60, 18, 6>();
+    }
+    __builtin_amdgcn_sched_barrier(0);
     // ---- the state after the chunk, 32 of its rows at a time ----
     auto update = [&](int step) {
 #pragma unroll
@@ -874,25 +920,6 @@ void delta_sweep_kernel(Rule p) {
       __builtin_amdgcn_sched_barrier(0);
       update(step);
       __builtin_amdgcn_sched_barrier(0);
-    }
-    if constexpr (kOut) {
-#pragma unroll
-      for (int tt = 0; tt < TB; tt++)
-#pragma unroll
-        for (int j = 0; j < NT; j++)
-#pragma unroll
-          for (int r = 0; r < 4; r++) o[tt][j][r] *= in[tt];
-#pragma unroll
-      for (int ea = 0; ea < kN2; ea++)
-#pragma unroll
-        for (int eb = 0; ea + eb < kN2; eb++)
-#pragma unroll
-          for (int ks = 0; ks < kSteps; ks++)
-#pragma unroll
-            for (int tt = 0; tt < TB; tt++)
-              if (ks <= tt / 2)
-#pragma unroll
-                for (int j = 0; j < NT; j++) o[tt][j] = mma(uf[ks][j].f[ea], pf[lower_frag<TB>(tt, ks)][eb], o[tt][j]);
     }
     __builtin_amdgcn_sched_barrier(0);
     if (i + 1 < chunks) read_rows(i + 1, 0);
