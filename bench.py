@@ -713,7 +713,7 @@ LIB_KERNELS = ("scan_main_kernel", "scan_chunk_agg_kernel", "chain_kernel", "sca
                "conv_fwd_vec_kernel", "conv_update_kernel", "conv_state_copy_kernel",
                "lin_fwd_kernel", "lin_bwd_kernel", "lin_state_kernel", "lin_gate_tiles_kernel", "lin_gate_kernel",
                "lin_group_sum_kernel", "lin_update_kernel", "ln_fwd_kernel", "ln_bwd_kernel", "ln_reduce_kernel",
-               "delta_tri_kernel", "delta_sweep_kernel", "delta_grad_kernel", "delta_update_kernel", "bn_fwd_kernel",
+               "delta_tri_kernel", "delta_sweep_kernel", "delta_chain_kernel", "delta_grad_kernel", "delta_update_kernel", "bn_fwd_kernel",
                "bn_bwd_kernel", "bn_reduce_kernel")
 
 

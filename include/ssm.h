@@ -677,7 +677,7 @@ SSM_API int ssm_scan_plan(int64_t b, int64_t L, int64_t E, int64_t N, int dtype,
  * 21 linattn_reduce, 22 linattn_update, 23 layernorm, 24 layernorm_bwd,
  * 25 layernorm_reduce, 26 deltarule_tri, 27 deltarule_sweep, 28 deltarule_grad,
  * 29 deltarule_reduce, 30 deltarule_update, 31 blocknorm, 32 blocknorm_bwd,
- * 33 blocknorm_reduce; names
+ * 33 blocknorm_reduce, 34 deltarule_chain; names
  * from ssm_profile_kind_name().  Off by default; the events add a few
  * microseconds per launch.  Process-wide, thread-safe.
  */

@@ -228,7 +228,7 @@ def ssm_scan_plan(b, L, E, N, dtype="bf16", tuning=None):
     return _PATH_NAMES[path.value], cl.value, nc.value
 
 
-PROFILE_KINDS = 34
+PROFILE_KINDS = 35
 _SCAN_KINDS = 17  # the kinds of the scans and the convolution, always in the answer
 
 

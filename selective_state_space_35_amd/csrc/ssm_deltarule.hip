@@ -62,6 +62,11 @@ struct Rule {
   // what the backward keeps of a chunk, 16 rows by 16 rows and in those by columns, as a lane of the sweep has them
   float* states;           // [b H n_chunks][KP / 16][VP][16]: states entering the chunks, or gradients of those leaving them
   float* left;             // [b H n_chunks][C / 16][VP][16]: N, or dR of the moved beta
+  // the cut, in the sweep's order of the chunks: n_segs segments of `parts` parts of part_chunks chunks.  With more than one
+  // segment, what the n_parts parts of all but the last do to a state is S -> map S + own
+  float* part_own;         // [b H n_parts][KP / 16][VP][16]; after the chain the states leaving the parts
+  float* part_map;         // [b H n_parts][KP / 16][KP][16]
+  int n_segs, parts, part_chunks, n_parts;
   int64_t b, L;
   int H, share, Dk, Dv, KP, VP, n_chunks, n_tiles;
   hipStream_t stream;
@@ -372,7 +377,10 @@ struct SweepLds {
   __attribute__((aligned(16))) float beta[4][kC];  // backwards the part of dR that is beta's own
 };
 
-template <typename T, int KDP, int VT, Mode MODE, bool VEC>
+// PART: the pass that a cut needs before.  A workgroup takes one part of a head's chunks, from a state of zero for VT columns
+// of the values, or from the unit matrix and without values for VT columns of the part's map; nothing is kept but where the
+// state arrives.
+template <typename T, int KDP, int VT, Mode MODE, bool PART, bool VEC>
 __global__ __launch_bounds__(kThreads + kWave * state_waves(VT)) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void delta_sweep_kernel(Rule p) {
   typedef Shape<T> Z;
@@ -382,15 +390,21 @@ void delta_sweep_kernel(Rule p) {
   constexpr int ldq = Tile<T, KDP, kQuery>::ld, ldk = Tile<T, KDP, kKey>::ld, ldv = Tile<T, VT, kValue>::ld;
   __shared__ SweepLds<T, KDP, VT> sh;
   // Workgroups are dealt to the 8 XCDs in turn: those of a head, and of neighbouring ones that share rows, go to one
-  const int64_t units = p.b * p.H * p.n_tiles, wg = blockIdx.x;
+  const int tiles = PART ? p.n_tiles + (p.KP + VT - 1) / VT : p.n_tiles, pieces = PART ? p.n_parts : p.n_segs;
+  const int64_t units = p.b * p.H * tiles * pieces, wg = blockIdx.x;
   const int64_t id = units % 8 == 0 ? (wg % 8) * (units / 8) + wg / 8 : wg;
-  const int v0 = int(id % p.n_tiles) * VT;
-  const int64_t bh = id / p.n_tiles, bi = bh / p.H;
-  const int h = int(bh % p.H), n = live_length(p.lengths, bi, p.L);
-  const int chunks = (n + kC - 1) / kC, G = p.H / p.share;
+  const bool unit = PART && int(id % tiles) >= p.n_tiles;  // columns of the map
+  const int v0 = (int(id % tiles) - (unit ? p.n_tiles : 0)) * VT;
+  const int piece = int(id / tiles % pieces);
+  const int64_t bh = id / tiles / pieces, bi = bh / p.H;
+  const int h = int(bh % p.H), n = live_length(p.lengths, bi, p.L), G = p.H / p.share;
+  // its chunks first .. first + chunks - 1
+  const int per = PART ? p.part_chunks : p.parts * p.part_chunks;
+  const int from = kBack ? p.n_chunks - (piece + 1) * per : piece * per;
+  const int lo = std::max(from, 0), chunks = std::max(0, std::min(from + per, (n + kC - 1) / kC) - lo);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = threadIdx.x % kWave;
   const int lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
-  auto chunk_of = [&](int i) { return kBack ? chunks - 1 - i : i; };
+  auto chunk_of = [&](int i) { return lo + (kBack ? chunks - 1 - i : i); };
 
   if (wv >= SW) {
     // ------------------------------------------------------------------ staging and scores
@@ -409,7 +423,7 @@ void delta_sweep_kernel(Rule p) {
     Stage<T, KDP, kQuery, VEC> sq;
     Stage<T, KDP, kKey, VEC> sk;
     Stage<T, VT, kValue, VEC> sv;
-    const int64_t t0 = bi * p.L + int64_t(kBack ? std::max(chunks - 1, 0) : 0) * kC;
+    const int64_t t0 = bi * p.L + int64_t(chunk_of(0)) * kC;
     sq.init(static_cast<const T*>(p.q) + (t0 * G + h / p.share) * p.Dk, G * p.Dk, p.Dk, false, tid);
     sk.init(static_cast<const T*>(p.k) + (t0 * G + h / p.share) * p.Dk, G * p.Dk, p.Dk, false, tid);
     sv.init(static_cast<const T*>(p.v) + (t0 * p.H + h) * p.Dv + v0, p.H * p.Dv, p.Dv - v0, false, tid);
@@ -440,7 +454,7 @@ void delta_sweep_kernel(Rule p) {
       const int nv = live(i);
       if constexpr (MODE != kStates) sq.load(r.q, nv, tid);
       sk.load(r.k, nv, tid);
-      sv.load(r.v, nv, tid);
+      sv.load(r.v, unit ? 0 : nv, tid);
       const float4* from = reinterpret_cast<const float4*>(tri + int64_t(chunk_of(std::min(i, last))) * (kTri * 512));
 #pragma unroll
       for (int j = 0; j < kZ; j++) {
@@ -581,7 +595,7 @@ void delta_sweep_kernel(Rule p) {
       __syncthreads();
       __syncthreads();
     }
-    if constexpr (kOut) {  // rows behind the length are zero
+    if (kOut && piece == p.n_segs - 1) {  // rows behind the length are zero
       const int cols = std::min(VT, p.Dv - v0);
       for (int64_t t = n + pw; t < p.L; t += 4) {
         T* y = static_cast<T*>(p.y) + ((bi * p.L + t) * p.H + h) * p.Dv + v0;
@@ -594,16 +608,28 @@ void delta_sweep_kernel(Rule p) {
   // -------------------------------------------------------------------- the state
   const int vw = 16 * NT * wv;  // the wave's first column of the tile
   f32x4 S[MT][NT];
-  const float* init = p.init ? p.init + bh * p.Dk * p.Dv : nullptr;
+  if (!PART && piece > 0) {
+    const float* init = p.part_own + (bh * p.n_parts + piece * p.parts - 1) * p.KP * p.VP;
 #pragma unroll
-  for (int m = 0; m < MT; m++)
+    for (int m = 0; m < MT; m++)
 #pragma unroll
-    for (int j = 0; j < NT; j++)
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const int i = 16 * m + g4 + r, v = v0 + vw + 16 * j + lr;
-        S[m][j][r] = init && i < p.Dk && v < p.Dv ? init[i * p.Dv + v] : 0.f;
+      for (int j = 0; j < NT; j++) {
+        const int v = v0 + vw + 16 * j + lr;
+        const float4 x = 16 * m < p.KP && v < p.VP ? lds4(init + (m * p.VP + v) * 16 + g4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        S[m][j] = f32x4{x.x, x.y, x.z, x.w};
       }
+  } else {
+    const float* init = !PART && p.init ? p.init + bh * p.Dk * p.Dv : nullptr;
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const int i = 16 * m + g4 + r, v = v0 + vw + 16 * j + lr;
+          S[m][j][r] = unit ? (i == v ? 1.f : 0.f) : init && i < p.Dk && v < p.Dv ? init[i * p.Dv + v] : 0.f;
+        }
+  }
   constexpr int kN3 = Parts<T, 3>::kN, kN2 = Parts<T, 2>::kN;
   Frag<T> kf[2][TB], qf[2][TB];
   auto read_rows = [&](int i, int kk) {  // 32 elements of the i-th chunk's keys (and queries)
@@ -693,7 +719,7 @@ void delta_sweep_kernel(Rule p) {
       read_z(0);
     }
     times_state(KS - 1);
-    if constexpr (MODE != kForward) {  // what delta_grad_kernel reads: the state entering the chunk, or the gradient leaving it
+    if constexpr (MODE != kForward && !PART) {  // what delta_grad_kernel reads: the state entering the chunk, or the gradient leaving it
       float* to = p.states + (bh * p.n_chunks + c) * int64_t(p.KP) * p.VP;
 #pragma unroll
       for (int m = 0; m < MT; m++)
@@ -828,7 +854,7 @@ void delta_sweep_kernel(Rule p) {
     }
     const float all = d.all;
     __syncthreads();  // the middle of a step: the other waves have the next chunk in its tiles
-    if constexpr (MODE != kForward) {
+    if constexpr (MODE != kForward && !PART) {
       float* to = p.left + (bh * p.n_chunks + c) * int64_t(kC) * p.VP;
 #pragma unroll
       for (int tt = 0; tt < TB; tt++)
@@ -975,7 +1001,18 @@ void delta_sweep_kernel(Rule p) {
     __syncthreads();
     __syncthreads();
   }
-  if (p.last) {
+  if constexpr (PART) {
+    const int VP = unit ? p.KP : p.VP;
+    float* to = (unit ? p.part_map : p.part_own) + (bh * p.n_parts + piece) * p.KP * int64_t(VP);
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        const int v = v0 + vw + 16 * j + lr;
+        if (16 * m < p.KP && v < VP)
+          *reinterpret_cast<float4*>(to + (m * VP + v) * 16 + g4) = make_float4(S[m][j][0], S[m][j][1], S[m][j][2], S[m][j][3]);
+      }
+  } else if (p.last && piece == p.n_segs - 1) {
     float* last = p.last + bh * p.Dk * p.Dv;
 #pragma unroll
     for (int m = 0; m < MT; m++)
@@ -986,6 +1023,55 @@ void delta_sweep_kernel(Rule p) {
           const int i = 16 * m + g4 + r, v = v0 + vw + 16 * j + lr;
           if (i < p.Dk && v < p.Dv) last[i * p.Dv + v] = S[m][j][r];
         }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The states leaving the parts of a cut sequence, one after the other: S = map S + own, 16 columns a wave, in float products.
+// ---------------------------------------------------------------------------
+template <int KDP>
+__global__ __launch_bounds__(kWave) void delta_chain_kernel(Rule p) {
+  constexpr int MT = KDP / 16;
+  const int l = threadIdx.x, lr = l % 16, g4 = 4 * (l / 16), blocks = p.KP / 16;
+  const int64_t bh = blockIdx.x / (p.VP / 16);
+  const int v = int(blockIdx.x % (p.VP / 16)) * 16 + lr;
+  f32x4 S[MT];
+  const float* init = p.init ? p.init + bh * p.Dk * p.Dv : nullptr;
+#pragma unroll
+  for (int m = 0; m < MT; m++)
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      const int i = 16 * m + g4 + r;
+      S[m][r] = init && i < p.Dk && v < p.Dv ? init[i * p.Dv + v] : 0.f;
+    }
+  for (int k = 0; k < p.n_parts; k++) {
+    float* own = p.part_own + (bh * p.n_parts + k) * p.KP * p.VP + v * 16 + g4;
+    const float* map = p.part_map + (bh * p.n_parts + k) * p.KP * p.KP + lr;
+    f32x4 next[MT];
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      next[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (m >= blocks) continue;
+      const float4 x = lds4(own + m * p.VP * 16);
+      float4 a[MT];
+#pragma unroll
+      for (int kb = 0; kb < MT; kb++) {
+        const float* at = map + (m * p.KP + 16 * kb + g4) * 16;
+        a[kb] = kb < blocks ? make_float4(at[0], at[16], at[32], at[48]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      f32x4 even{x.x, x.y, x.z, x.w}, odd{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < MT; kb += 2) {
+        if (kb < blocks) even = mma16(a[kb], S[kb], even);
+        if (kb + 1 < blocks) odd = mma16(a[kb + 1], S[kb + 1], odd);
+      }
+      next[m] = even + odd;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      S[m] = next[m];
+      if (m < blocks) *reinterpret_cast<float4*>(own + m * p.VP * 16) = make_float4(S[m][0], S[m][1], S[m][2], S[m][3]);
+    }
   }
 }
 
@@ -1644,6 +1730,36 @@ bool pieces(const void* x, int64_t D) {
   return D % (16 / int(sizeof(T))) == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
 }
 
+// The cut of a sequence.  A CU holds one workgroup of the sweep, so with fewer heads (times tiles of columns) than CUs the
+// sequence is cut into segments, whose entering states a pass before gives: the part's own state and its map, Dk columns more.
+// Of the cuts into up to 64 segments and 1, 2, 3 or 4 parts each the one whose generations of workgroups take the fewest chunks
+// one after the other: a chunk of the pass before counts 3/4 of one of the sweep (measured: bf16, D128, 2.9 and 3.7 us), a step
+// of the chain 1/3 or, above 64 elements of the keys, one, the launches 3.
+constexpr int64_t kAtOnce = 256;
+struct Cut {
+  int n_segs = 1, parts = 1, part_chunks = 1, n_parts = 0;
+};
+Cut cut_of(const DeltaRuleArgs& a) {
+  const int64_t chunks = ceil_div(a.L, a.dtype == 0 ? kChunk<float> : kChunk<bf16_bits>), heads = a.b * a.H;
+  const int64_t tiles = ceil_div(a.Dv, kTile), more = tiles + ceil_div(ceil_div(a.Dk, 16) * 16, kTile);
+  Cut best;
+  best.part_chunks = int(std::max<int64_t>(1, chunks));
+  double least = double(ceil_div(heads * tiles, kAtOnce) * chunks);
+  if (heads * tiles >= kAtOnce) return best;
+  for (int64_t segs = 2; segs <= std::min<int64_t>(64, chunks / 2); segs++)
+    for (int64_t parts = 1; parts <= 4; parts++) {
+      const int64_t pc = ceil_div(chunks, segs * parts), n = ceil_div(chunks, pc * parts), n_parts = (n - 1) * parts;
+      if (n < 2) continue;
+      const double cost = double(ceil_div(heads * tiles * n, kAtOnce) * pc * parts) + 0.75 * double(ceil_div(heads * more * n_parts, kAtOnce) * pc) +
+                          (a.Dk <= 64 ? 0.35 : 1.0) * double(n_parts) + 3.0;
+      if (cost < least) {
+        least = cost;
+        best.n_segs = int(n); best.parts = int(parts); best.part_chunks = int(pc); best.n_parts = int(n_parts);
+      }
+    }
+  return best;
+}
+
 Rule rule_of(const DeltaRuleArgs& a) {
   Rule p{};
   p.q = a.q; p.k = a.k; p.v = a.v; p.beta = a.beta; p.g = a.g; p.A = a.A; p.lengths = a.lengths; p.scale = a.scale;
@@ -1653,6 +1769,8 @@ Rule rule_of(const DeltaRuleArgs& a) {
   p.VP = int(ceil_div(a.Dv, 16) * 16);
   p.n_chunks = int(ceil_div(a.L, a.dtype == 0 ? kChunk<float> : kChunk<bf16_bits>));
   p.n_tiles = int(ceil_div(a.Dv, kTile));
+  const Cut c = cut_of(a);
+  p.n_segs = c.n_segs; p.parts = c.parts; p.part_chunks = c.part_chunks; p.n_parts = c.n_parts;
   return p;
 }
 
@@ -1667,7 +1785,7 @@ int heads_together(const DeltaRuleArgs& a, int64_t chunks) {
 
 // Bytes from the workspace's start of its parts.
 struct Work {
-  size_t lower, upper, S, D, N, dR, dq, dk, total;
+  size_t lower, upper, own, map, S, D, N, dR, dq, dk, total;
 };
 Work plan_work(const DeltaRuleArgs& a, bool backward) {
   Work w{};
@@ -1681,6 +1799,8 @@ Work plan_work(const DeltaRuleArgs& a, bool backward) {
   const size_t chunks = size_t(a.b) * a.H * p.n_chunks;
   const size_t tri = chunks * (a.dtype == 0 ? Shape<float>::kTri : Shape<bf16_bits>::kTri) * 512 * 4;
   w.lower = take(tri);
+  w.own = take(size_t(a.b) * a.H * p.n_parts * p.KP * p.VP * 4);  // one direction after the other
+  w.map = take(size_t(a.b) * a.H * p.n_parts * p.KP * p.KP * 4);
   if (backward) {
     const size_t state = chunks * p.KP * p.VP * 4;
     const size_t rows = chunks * (a.dtype == 0 ? kChunk<float> : kChunk<bf16_bits>) * p.VP * 4;
@@ -1710,11 +1830,23 @@ hipError_t run_tri(const Rule& p, float* lower, float* upper) {
 
 template <typename T, Mode MODE>
 hipError_t run_sweep(const Rule& p) {
-  const int64_t blocks = p.b * p.H * p.n_tiles;
+  const int64_t heads = p.b * p.H;
   const bool vec = pieces<T>(p.q, p.Dk) && pieces<T>(p.k, p.Dk) && pieces<T>(p.v, p.Dv) && (MODE != kForward || pieces<T>(p.y, p.Dv));
-  auto go = [&](auto kern) { return launch_kind(kKindDeltaSweep, kern, blocks, kThreads + kWave * state_waves(kTile), p.stream, p); };
-  if (p.Dk <= 64) return vec ? go(delta_sweep_kernel<T, 64, kTile, MODE, true>) : go(delta_sweep_kernel<T, 64, kTile, MODE, false>);
-  return vec ? go(delta_sweep_kernel<T, 128, kTile, MODE, true>) : go(delta_sweep_kernel<T, 128, kTile, MODE, false>);
+  auto go = [&](auto kern, int64_t blocks) { return launch_kind(kKindDeltaSweep, kern, blocks, kThreads + kWave * state_waves(kTile), p.stream, p); };
+  if (p.n_segs > 1) {
+    constexpr Mode PM = MODE == kForward ? kStates : MODE;
+    const int64_t blocks = heads * (p.n_tiles + ceil_div(p.KP, kTile)) * p.n_parts;
+    hipError_t err = p.Dk <= 64 ? (vec ? go(delta_sweep_kernel<T, 64, kTile, PM, true, true>, blocks) : go(delta_sweep_kernel<T, 64, kTile, PM, true, false>, blocks))
+                                : (vec ? go(delta_sweep_kernel<T, 128, kTile, PM, true, true>, blocks) : go(delta_sweep_kernel<T, 128, kTile, PM, true, false>, blocks));
+    if (err != hipSuccess) return err;
+    const int64_t waves = heads * (p.VP / 16);
+    err = p.Dk <= 64 ? launch_kind(kKindDeltaChain, delta_chain_kernel<64>, waves, kWave, p.stream, p)
+                     : launch_kind(kKindDeltaChain, delta_chain_kernel<128>, waves, kWave, p.stream, p);
+    if (err != hipSuccess) return err;
+  }
+  const int64_t blocks = heads * p.n_tiles * p.n_segs;
+  if (p.Dk <= 64) return vec ? go(delta_sweep_kernel<T, 64, kTile, MODE, false, true>, blocks) : go(delta_sweep_kernel<T, 64, kTile, MODE, false, false>, blocks);
+  return vec ? go(delta_sweep_kernel<T, 128, kTile, MODE, false, true>, blocks) : go(delta_sweep_kernel<T, 128, kTile, MODE, false, false>, blocks);
 }
 
 template <typename T>
@@ -1740,6 +1872,8 @@ hipError_t fwd_impl(const DeltaRuleArgs& a, char* ws) {
   const hipError_t err = run_tri<T>(p, lower, nullptr);
   if (err != hipSuccess) return err;
   p.tri = lower;
+  p.part_own = reinterpret_cast<float*>(ws + w.own);
+  p.part_map = reinterpret_cast<float*>(ws + w.map);
   p.init = a.h0;
   p.y = a.y;
   p.last = a.last;
@@ -1752,6 +1886,8 @@ hipError_t bwd_impl(const DeltaRuleArgs& a, char* ws) {
   auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   Rule p = rule_of(a);
   p.backward = true;
+  p.part_own = at(w.own);
+  p.part_map = at(w.map);
   hipError_t err = run_tri<T>(p, at(w.lower), at(w.upper));
   if (err != hipSuccess) return err;
   Rule f = p, r = p;

@@ -41,7 +41,8 @@ enum : int {
   kKindBlockNormFwd = 31,    // norms around a block
   kKindBlockNormBwd = 32,    // norms around a block, backward: gradients, partial parameter gradients
   kKindBlockNormReduce = 33, // norms around a block, backward: sums of the partial parameter gradients
-  kNumKinds = 34
+  kKindDeltaChain = 34, // gated delta rule: states leaving the parts of a cut sequence
+  kNumKinds = 35
 };
 
 // When profiling is on, creates and records the start event on `s` and returns true.

@@ -31,7 +31,7 @@ const char* const kNames[kNumKinds] = {"chunk_aggregate", "chunk_carry",   "scan
                                        "linattn_gate",    "linattn_reduce", "linattn_update", "layernorm",
                                        "layernorm_bwd",   "layernorm_reduce", "deltarule_tri", "deltarule_sweep",
                                        "deltarule_grad",  "deltarule_reduce", "deltarule_update", "blocknorm",
-                                       "blocknorm_bwd",   "blocknorm_reduce"};
+                                       "blocknorm_bwd",   "blocknorm_reduce", "deltarule_chain"};
 
 }  // namespace
 

@@ -387,3 +387,13 @@ def test_heads_that_share_one_workgroup(H, G, Dk, dtype):
     b, L = (16, 520) if G == 8 else (16, 200 if dtype == "f32" else 400)
     check(make(b=b, L=L, H=H, G=G, Dk=Dk, Dv=8, dtype=dtype, seed=33, lengths=[L - 3 * i for i in range(b)]),
           f"deltarule shared H={H} G={G} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("b,L,H,G,Dk,Dv,lengths", [(1, 1500, 2, 1, 64, 48, None), (2, 2100, 1, 1, 128, 128, [2100, 700]),
+                                                   (3, 900, 2, 2, 40, 72, [0, 1, 899]), (1, 3000, 5, 5, 16, 16, None),
+                                                   (1, 640, 1, 1, 100, 24, [513])])
+def test_cut_sequences(b, L, H, G, Dk, Dv, lengths, dtype):
+    """Few heads and a long sequence: the sequence is cut, and its pieces' states are joined by their maps."""
+    check(make(b=b, L=L, H=H, G=G, Dk=Dk, Dv=Dv, dtype=dtype, rate=0.01, seed=L, lengths=lengths),
+          f"deltarule cut b={b} L={L} H={H} Dk={Dk} Dv={Dv} {lengths} {dtype}")
