@@ -300,11 +300,12 @@ __global__ __launch_bounds__(kThreads) void delta_tri_kernel(Rule p, float* lowe
   }
   __syncthreads();  // the blocks below the diagonal have been read by all
   if (wv < TB - 1) {
+    float* here = X + (16 * wv + g4) * ld + 16 * wv + lr;
 #pragma unroll
     for (int o = 1; o < TB; o++)
       if (wv + o < TB)
 #pragma unroll
-        for (int r = 0; r < 4; r++) X[(16 * (wv + o) + g4 + r) * ld + 16 * wv + lr] = col[o][r];
+        for (int r = 0; r < 4; r++) here[(16 * o + r) * ld] = col[o][r];
   }
   __syncthreads();
   float4* out = reinterpret_cast<float4*>(lower + id * (Z::kTri * 512));
