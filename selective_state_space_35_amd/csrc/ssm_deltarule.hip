@@ -213,13 +213,13 @@ __device__ __forceinline__ f32x4 mma_parts(const Parts<T, NA>& a, const Parts<T,
 // finite is taken as zero: the sweep makes NaN of everything from its token on.
 // ---------------------------------------------------------------------------
 template <typename T, int KDP, bool VEC>
-__global__ __launch_bounds__(kThreads) void delta_tri_kernel(Rule p, float* lower, float* upper) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void delta_tri_kernel(Rule p, float* lower, float* upper) {
   typedef Shape<T> Z;
   constexpr int kC = Z::kC, TB = Z::TB, KS = KDP / 32, ldk = Tile<T, KDP, kKey>::ld, ld = kC + 4;
   __shared__ __attribute__((aligned(16))) T Ks[Tile<T, KDP, kKey>::kElems];
   __shared__ __attribute__((aligned(16))) float X[kC * ld];  // X diag(beta); block by block its inverse takes its place
   __shared__ Decays<kC> d;
-  __shared__ float beta[kC];
+  __shared__ __attribute__((aligned(16))) float beta[kC];
   const int64_t id = blockIdx.x, bh = id / p.n_chunks, bi = bh / p.H;
   const int c = int(id % p.n_chunks), h = int(bh % p.H), n = live_length(p.lengths, bi, p.L);
   if (c * kC >= n) return;  // behind the sequence: not read
@@ -248,10 +248,12 @@ __global__ __launch_bounds__(kThreads) void delta_tri_kernel(Rule p, float* lowe
       a = mma(row_frag(Ks + (16 * sb + lr) * ldk + 32 * kk + g8), row_frag(Ks + (16 * tb + lr) * ldk + 32 * kk + g8), a);
     const int t = 16 * tb + lr, s0 = 16 * sb + g4;
     const float th = d.hi[t], tl = d.lo[t];
+    const float4 h4 = lds4(d.hi + s0), l4 = lds4(d.lo + s0), b4 = lds4(beta + s0);
+    const float sh[4] = {h4.x, h4.y, h4.z, h4.w}, sl[4] = {l4.x, l4.y, l4.z, l4.w}, be[4] = {b4.x, b4.y, b4.z, b4.w};
     float x[4];
 #pragma unroll
     for (int r = 0; r < 4; r++) {
-      const float e = a[r] * exp2_fast((th - d.hi[s0 + r]) + (tl - d.lo[s0 + r])) * beta[s0 + r];
+      const float e = a[r] * exp2_fast((th - sh[r]) + (tl - sl[r])) * be[r];
       x[r] = s0 + r < t && e * 0.f == 0.f ? e : 0.f;
     }
     *reinterpret_cast<float4*>(X + t * ld + s0) = make_float4(x[0], x[1], x[2], x[3]);
@@ -259,21 +261,25 @@ __global__ __launch_bounds__(kThreads) void delta_tri_kernel(Rule p, float* lowe
   __syncthreads();
   if (tid < kC) {  // lane l has column l % 16 of block l / 16
     const int b0 = 16 * (l / 16);
-    float4 a4[16][4];
+    float4 a4[4][4];  // four rows at a time, read two rows ahead
+    auto read = [&](int i) {
 #pragma unroll
-    for (int i = 1; i < 16; i++)
-#pragma unroll
-      for (int k4 = 0; k4 < (i + 3) / 4; k4++) a4[i][k4] = lds4(X + (b0 + i) * ld + b0 + 4 * k4);
+      for (int k4 = 0; k4 < (i + 3) / 4; k4++) a4[i % 4][k4] = lds4(X + (b0 + i) * ld + b0 + 4 * k4);
+    };
+    read(1);
+    read(2);
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; i++) {
+      if (i > 0 && i + 2 < 16) read(i + 2);
       float s[2] = {i == lr ? 1.f : 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < i; k++) {
-        const float4& r = a4[i][k / 4];
+        const float4& r = a4[i % 4][k / 4];
         s[k % 2] = fmaf(-(k % 4 == 0 ? r.x : k % 4 == 1 ? r.y : k % 4 == 2 ? r.z : r.w), x[k], s[k % 2]);
       }
       x[i] = s[0] + s[1];
+      __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_sched_barrier(0);  // one wave reads and writes the blocks, in this order
 #pragma unroll
