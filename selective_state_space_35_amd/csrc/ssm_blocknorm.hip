@@ -9,12 +9,17 @@
 //   c = e s,  dz = c p silu'(z),  d = c silu(z) w1,  dx = r1 (d - xh mean(d xh))
 //   dw1 = sum over rows of c silu(z) xh,  ds = sum of e u,  dw2 = sum of dn hh
 // Both directions read every streamed value once, hold it for the two sums of its row, one after the other, and write
-// once: bound by HBM.  A group of threads keeps one head's parameters, and in the backward its part of their gradients, in
-// registers and walks rows, the next row's loads under way while one is summed.  All sums are float.
+// once: bound by HBM (65536 rows of 2560 in bf16 with both norms and the residual: forward 259 us, 5.2 TB/s, backward 450 us,
+// 4.5 TB/s, and 15 us for the parameters' sums).  A group of threads keeps one head's parameters, and in the backward its
+// part of their gradients, in registers and walks rows, the next row's loads under way while one is summed (the parameters
+// read again for every row, 16 registers a thread fewer: 742 us); the gate is a form of its own (with its values in
+// registers that nobody used 510 us).  Rows above 8192 elements, and in the backward odd ones above 2048, keep more than
+// 128 registers a thread and go through scratch.  All sums are float.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ssm_blocknorm.h"
 #include "ssm_device.h"
@@ -129,7 +134,7 @@ struct Par {
 
 // One group of TPR threads walks the rows slice, slice + n_slices, ... of head h; each thread has NV vectors of VEC
 // elements of a row, at columns (j TPR + lane) VEC.  R: the residual stream's type.
-template <typename T, typename R, int VEC, int NV, int TPR>
+template <typename T, typename R, bool GATE, int VEC, int NV, int TPR>
 __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArgs a, int64_t n_slices) {
   constexpr int kGroups = block_threads(TPR) / TPR;
   __shared__ float buf[2][kGroups][TPR > kWave ? TPR / kWave : 1];
@@ -146,7 +151,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
   p1.init(a.post ? a.post_weight : nullptr, int64_t(h) * W, lane, W);
   ps.init(a.scale, int64_t(h) * W, lane, W);
   p2.init(a.pre ? a.pre_weight : nullptr, int64_t(h) * W, lane, W);
-  Raw<T, VEC> xn[NV], zn[NV];
+  Raw<T, VEC> xn[NV], zn[GATE ? NV : 1];
   Raw<R, VEC> rn[NV];
   auto fetch = [&](int64_t i) {
 #pragma unroll
@@ -155,7 +160,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
       const int64_t at = (i * H + h) * W + c;
       if (c < W) {
         load_raw(xn[j], x + at);
-        if (z) load_raw(zn[j], z + at);
+        if constexpr (GATE) load_raw(zn[j], z + at);
         if (res) load_raw(rn[j], res + at);
       }
     }
@@ -175,7 +180,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
       for (int e = 0; e < VEC; e++) v[j][e] = g[j][e] = r[j][e] = 0.f;
       if (in) {
         floats(xn[j], v[j]);
-        if (z) floats(zn[j], g[j]);
+        if constexpr (GATE) floats(zn[j], g[j]);
         if (res) floats(rn[j], r[j]);
       }
     }
@@ -198,7 +203,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
 #pragma unroll
       for (int e = 0; e < VEC; e++) {
         float u = v[j][e] * r1 * w1[e];
-        if (z) u *= g[j][e] / (1.f + expf(-g[j][e]));
+        if constexpr (GATE) u *= g[j][e] / (1.f + expf(-g[j][e]));
         v[j][e] = fmaf(u, sc[e], r[j][e]);
         s = fmaf(v[j][e], v[j][e], s);  // columns behind the width are zero: so is silu(0)
       }
@@ -237,7 +242,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
 
 // As the forward; a group writes its own row of the partial sums [3][n_slices][H W] (of w1, the scale, w2), which
 // bn_reduce_kernel adds in a fixed order.
-template <typename T, typename R, int VEC, int NV, int TPR>
+template <typename T, typename R, bool GATE, int VEC, int NV, int TPR>
 __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArgs a, int64_t n_slices, float* part) {
   constexpr int kGroups = block_threads(TPR) / TPR;
   __shared__ float buf[2][kGroups][TPR > kWave ? TPR / kWave : 1];
@@ -262,7 +267,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
   for (int j = 0; j < NV; j++)
 #pragma unroll
     for (int e = 0; e < VEC; e++) dw1[j][e] = ds[j][e] = dw2[j][e] = 0.f;
-  Raw<T, VEC> xn[NV], zn[NV], nn[NV];
+  Raw<T, VEC> xn[NV], zn[GATE ? NV : 1], nn[NV];
   Raw<R, VEC> rn[NV], hn[NV];
   float r1n = 1.f, r2n = 1.f;
   auto fetch = [&](int64_t i) {
@@ -275,7 +280,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
       const int64_t at = row * W + c;
       if (c < W) {
         load_raw(xn[j], x + at);
-        if (z) load_raw(zn[j], z + at);
+        if constexpr (GATE) load_raw(zn[j], z + at);
         if (res) load_raw(rn[j], res + at);
         if (dh) load_raw(hn[j], dh + at);
         if (dn) load_raw(nn[j], dn + at);
@@ -297,7 +302,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
       for (int e = 0; e < VEC; e++) xh[j][e] = g[j][e] = hh[j][e] = d[j][e] = t[j][e] = 0.f;
       if (in) {
         floats(xn[j], xh[j]);
-        if (z) floats(zn[j], g[j]);
+        if constexpr (GATE) floats(zn[j], g[j]);
         if (res) floats(rn[j], hh[j]);
         if (dh) floats(hn[j], d[j]);
         if (dn) floats(nn[j], t[j]);
@@ -313,7 +318,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
 #pragma unroll
       for (int e = 0; e < VEC; e++) {
         sl[j][e] = 1.f;
-        if (z) {
+        if constexpr (GATE) {
           const float sg = 1.f / (1.f + expf(-g[j][e]));
           sl[j][e] = g[j][e] * sg;
           g[j][e] = sg * fmaf(g[j][e], 1.f - sg, 1.f);
@@ -365,7 +370,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
         s = fmaf(d[j][e], xh[j][e], s);
       }
     }
-    if (z && on) {
+    if (GATE && on) {
 #pragma unroll
       for (int j = 0; j < NV; j++) {
         const int c = (j * TPR + lane) * VEC;
@@ -431,20 +436,23 @@ __global__ __launch_bounds__(256) void bn_reduce_kernel(Sums a, int64_t n, int64
   if (g == 0 && c < cols) out[blockIdx.y * cols + c] = (sh[0][l] + sh[1][l]) + (sh[2][l] + sh[3][l]);
 }
 
-// Workgroups of a launch: of the forward, and of the backward, whose partial sums grow with them
-constexpr int64_t kFwdBlocks = 2048, kBwdBlocks = 512;
+// Workgroups of a launch.  Forward, 65536 rows of 2560 in bf16 with both norms and the residual: 2048, 4096, 8192 of them 320,
+// 275, 259 us.  The backward's partial sums grow with them: 512 or 768 of rows of many threads 464 or 472 us (with the sums),
+// of rows of at most a wave (16384 rows of 24 heads of 64, gated) 91 or 74 us.
+constexpr int64_t kFwdBlocks = 8192;
+constexpr int64_t bwd_blocks(int tpr) { return tpr > kWave ? 512 : 768; }
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <typename T, typename R, int VEC, int NV, int TPR>
+template <typename T, typename R, bool GATE, int VEC, int NV, int TPR>
 struct Form {
   static hipError_t fwd(const BlockNormArgs& a, int64_t n_slices) {
     constexpr int threads = block_threads(TPR), groups = threads / TPR;
-    return launch_kind(kKindBlockNormFwd, bn_fwd_kernel<T, R, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices);
+    return launch_kind(kKindBlockNormFwd, bn_fwd_kernel<T, R, GATE, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices);
   }
   static hipError_t bwd(const BlockNormArgs& a, int64_t n_slices, float* part) {
     constexpr int threads = block_threads(TPR), groups = threads / TPR;
-    return launch_kind(kKindBlockNormBwd, bn_bwd_kernel<T, R, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices, part);
+    return launch_kind(kKindBlockNormBwd, bn_bwd_kernel<T, R, GATE, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices, part);
   }
   static constexpr int tpr = TPR;
 };
@@ -461,36 +469,39 @@ bool whole_vectors(const BlockNormArgs& a) {
 
 // The form of rows of W elements: one vector a thread, in whole waves above one; more only above 1024 threads.  Elements
 // one at a time (odd widths): up to eight a thread, sixteen in the widest rows.
-template <typename T, typename R, typename Go>
+template <typename T, typename R, bool GATE, typename Go>
 auto with_form(bool vec, int64_t W, Go go) {
   constexpr int V = 16 / sizeof(T);
   if (!vec) {
-    if (W <= 64) return go(Form<T, R, 1, 8, 8>{});
-    if (W <= 512) return go(Form<T, R, 1, 8, 64>{});
-    if (W <= 2048) return go(Form<T, R, 1, 8, 256>{});
-    if (W <= 8192) return go(Form<T, R, 1, 8, 1024>{});
-    return go(Form<T, R, 1, 16, 1024>{});
+    if (W <= 64) return go(Form<T, R, GATE, 1, 8, 8>{});
+    if (W <= 512) return go(Form<T, R, GATE, 1, 8, 64>{});
+    if (W <= 2048) return go(Form<T, R, GATE, 1, 8, 256>{});
+    if (W <= 8192) return go(Form<T, R, GATE, 1, 8, 1024>{});
+    return go(Form<T, R, GATE, 1, 16, 1024>{});
   }
   const int64_t n = W / V;
-  if (n <= 8) return go(Form<T, R, V, 1, 8>{});
-  if (n <= 16) return go(Form<T, R, V, 1, 16>{});
-  if (n <= 32) return go(Form<T, R, V, 1, 32>{});
-  if (n <= 64) return go(Form<T, R, V, 1, 64>{});
-  if (n <= 128) return go(Form<T, R, V, 1, 128>{});
-  if (n <= 192) return go(Form<T, R, V, 1, 192>{});
-  if (n <= 256) return go(Form<T, R, V, 1, 256>{});
-  if (n <= 320) return go(Form<T, R, V, 1, 320>{});
-  if (n <= 512) return go(Form<T, R, V, 1, 512>{});
-  if (n <= 640) return go(Form<T, R, V, 1, 640>{});
-  if (n <= 1024) return go(Form<T, R, V, 1, 1024>{});
-  if (V == 4 && n <= 2048) return go(Form<T, R, V, 8 / V, 1024>{});
-  return go(Form<T, R, V, 16 / V, 1024>{});
+  if (n <= 8) return go(Form<T, R, GATE, V, 1, 8>{});
+  if (n <= 16) return go(Form<T, R, GATE, V, 1, 16>{});
+  if (n <= 32) return go(Form<T, R, GATE, V, 1, 32>{});
+  if (n <= 64) return go(Form<T, R, GATE, V, 1, 64>{});
+  if (n <= 128) return go(Form<T, R, GATE, V, 1, 128>{});
+  if (n <= 192) return go(Form<T, R, GATE, V, 1, 192>{});
+  if (n <= 256) return go(Form<T, R, GATE, V, 1, 256>{});
+  if (n <= 320) return go(Form<T, R, GATE, V, 1, 320>{});
+  if (n <= 512) return go(Form<T, R, GATE, V, 1, 512>{});
+  if (n <= 640) return go(Form<T, R, GATE, V, 1, 640>{});
+  if (n <= 1024) return go(Form<T, R, GATE, V, 1, 1024>{});
+  if (V == 4 && n <= 2048) return go(Form<T, R, GATE, V, 8 / V, 1024>{});
+  return go(Form<T, R, GATE, V, 16 / V, 1024>{});
 }
 
 template <typename Go>
-auto with_types(int dtype, int rdtype, Go go) {
-  if (dtype == 0) return go(float{}, float{});
-  return rdtype == 0 ? go(bf16_bits{}, float{}) : go(bf16_bits{}, bf16_bits{});
+auto with_types(const BlockNormArgs& a, Go go) {
+  auto types = [&](auto gate) {
+    if (a.dtype == 0) return go(float{}, float{}, gate);
+    return a.rdtype == 0 ? go(bf16_bits{}, float{}, gate) : go(bf16_bits{}, bf16_bits{}, gate);
+  };
+  return a.z ? types(std::true_type{}) : types(std::false_type{});
 }
 
 // Rows in flight: the groups of `blocks` workgroups, shared out over the heads.
@@ -505,10 +516,10 @@ struct NormPlan {
 };
 NormPlan plan_bwd(const BlockNormArgs& a, bool vec) {
   NormPlan p;
-  const int tpr = with_types(a.dtype, a.rdtype, [&](auto t, auto r) {
-    return with_form<decltype(t), decltype(r)>(vec, a.W, [](auto f) { return int(f.tpr); });
+  const int tpr = with_types(a, [&](auto t, auto r, auto gate) {
+    return with_form<decltype(t), decltype(r), decltype(gate)::value>(vec, a.W, [](auto f) { return int(f.tpr); });
   });
-  p.n_slices = slices_of(a, tpr, kBwdBlocks);
+  p.n_slices = slices_of(a, tpr, bwd_blocks(tpr));
   const int64_t blocks = 3 * ceil_div(a.H * a.W, 64);
   p.n_parts = std::max<int64_t>(1, std::min<int64_t>(ceil_div(512, blocks), p.n_slices / 32));
   p.per = ceil_div(p.n_slices, p.n_parts);
@@ -531,10 +542,10 @@ size_t blocknorm_workspace_bytes(const BlockNormArgs& a) {
 }
 
 hipError_t launch_blocknorm_fwd(const BlockNormArgs& a) {
-  return with_types(a.dtype, a.rdtype, [&](auto t, auto r) {
+  return with_types(a, [&](auto t, auto r, auto gate) {
     typedef decltype(t) T;
     typedef decltype(r) R;
-    return with_form<T, R>(whole_vectors<T, R>(a), a.W, [&](auto f) { return f.fwd(a, slices_of(a, f.tpr, kFwdBlocks)); });
+    return with_form<T, R, decltype(gate)::value>(whole_vectors<T, R>(a), a.W, [&](auto f) { return f.fwd(a, slices_of(a, f.tpr, kFwdBlocks)); });
   });
 }
 
@@ -549,12 +560,12 @@ hipError_t launch_blocknorm_bwd(const BlockNormArgs& a, void* workspace) {
   if (a.rows == 0)  // sums over no rows
     return params ? reduce(part, 0, a.dpost_weight, a.dscale, a.dpre_weight, 0, 0, 1) : hipSuccess;
   NormPlan p{};
-  const hipError_t err = with_types(a.dtype, a.rdtype, [&](auto t, auto r) {
+  const hipError_t err = with_types(a, [&](auto t, auto r, auto gate) {
     typedef decltype(t) T;
     typedef decltype(r) R;
     const bool vec = whole_vectors<T, R>(a);
     p = plan_bwd(a, vec);
-    return with_form<T, R>(vec, a.W, [&](auto f) { return f.bwd(a, p.n_slices, part); });
+    return with_form<T, R, decltype(gate)::value>(vec, a.W, [&](auto f) { return f.bwd(a, p.n_slices, part); });
   });
   if (err != hipSuccess || !params) return err;
   const int64_t all = p.n_slices * cols, some = p.n_parts * cols;
