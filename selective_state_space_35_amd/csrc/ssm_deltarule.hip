@@ -586,10 +586,12 @@ void delta_sweep_kernel(Rule p) {
       __syncthreads();
       // at the top of step i: chunk i is in the tiles and in P; chunks i + 1 (in r) and i + 2 (in the other set) are in
       // registers or under way
+      constexpr bool kLate = MODE != kForward;
       auto step = [&](Regs& r, const Regs& other, int i) {
         place(r, i + 1);
-        fetch(r, i + 3);
+        if (!kLate) fetch(r, i + 3);
         __syncthreads();
+        if (kLate) fetch(r, i + 3);
         score(i + 1);
         decays(other, i + 2);
         __syncthreads();
