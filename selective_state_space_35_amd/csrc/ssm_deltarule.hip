@@ -151,6 +151,14 @@ struct Scalars {
     if constexpr (sizeof(T) == 4) return __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
     else return __builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0);
   }
+  // those of the chunk whose first token's value is x[at]
+  static __device__ __forceinline__ uint32_t load_at(const void* x, int64_t at, int H, int nv) {
+    const int l = threadIdx.x % kWave;
+    const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(static_cast<const T*>(x) + at);
+    const int o = x && l < nv ? l * H * int(sizeof(T)) : 0x7fffffff;
+    if constexpr (sizeof(T) == 4) return __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0);
+  }
   static __device__ __forceinline__ float value(uint32_t raw) { return __uint_as_float(sizeof(T) == 4 ? raw : raw << 16); }
 };
 
@@ -1289,7 +1297,10 @@ void delta_grad_kernel(Grad a) {
   struct Regs {
     uint4 dy[kDy];
     float4 n, r, S[kStates], D[kStates];
+    uint32_t gate, beta;
   };
+  Regs r;
+
 #pragma unroll 1
   for (int h = h0; h < h0 + (MULTI ? a.heads : 1); h++) {
     // Over the heads neither what is read of q and k nor the lane's places in the tiles are kept: there are no registers
@@ -1298,23 +1309,26 @@ void delta_grad_kernel(Grad a) {
     const int tid = tid_here, l = tid % kWave, lr = l % 16, g4 = 4 * (l / 16), g8 = 8 * (l / 16);
     const bool has_left = tid < kLeft;
     const int lt = tid % 4 * 4 + tid / 128 * 16, lv = tid / 4 % 32;  // a thread's tokens and column of N and dR
-    const int64_t at_chunk = (bi * p.H + h) * p.n_chunks + c;
-    const float* gN = a.N + at_chunk * kC * p.VP;
-    const float* gR = a.dR + at_chunk * kC * p.VP;
-    const float* gS = a.S + at_chunk * p.KP * p.VP;
-    const float* gD = a.D + at_chunk * p.KP * p.VP;
-    const T* gY = static_cast<const T*>(a.dy) + (row0 * p.H + h) * p.Dv;
-    auto fetch = [&](Regs& r, int v0) {
-      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    // 32 columns of head hh from v0 on, through descriptors: what lies outside is zero, and no branch is around a load
+    auto fetch = [&](int hh, int v0) {
+      const int64_t at_chunk = (bi * p.H + hh) * p.n_chunks + c;
+      const T* gY = static_cast<const T*>(a.dy) + (row0 * p.H + hh) * p.Dv;
+      const __amdgpu_buffer_rsrc_t ry = uniform_rsrc(gY), rn = uniform_rsrc(a.N + at_chunk * kC * p.VP), rr = uniform_rsrc(a.dR + at_chunk * kC * p.VP);
+      const __amdgpu_buffer_rsrc_t rS = uniform_rsrc(a.S + at_chunk * p.KP * p.VP), rD = uniform_rsrc(a.D + at_chunk * p.KP * p.VP);
+      auto load = [](const __amdgpu_buffer_rsrc_t& rs, int at) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
+        return make_uint4(v[0], v[1], v[2], v[3]);
+      };
+      auto quad = [&](const __amdgpu_buffer_rsrc_t& rs, int at) { return __builtin_bit_cast(float4, load(rs, at)); };
 #pragma unroll
       for (int j = 0; j < kDy; j++) {
         const int i = tid + j * kAll, t = i / kRowPieces, v = v0 + kVec * (i % kRowPieces);
-        r.dy[j] = make_uint4(0, 0, 0, 0);
-        if (t < nv && v < p.Dv) {
-          const T* from = gY + int64_t(t) * p.H * p.Dv + v;
-          if constexpr (VEC) {
-            r.dy[j] = *reinterpret_cast<const uint4*>(from);
-          } else {
+        if constexpr (VEC) {
+          r.dy[j] = load(ry, t < nv && v < p.Dv ? (t * p.H * p.Dv + v) * int(sizeof(T)) : 0x7fffffff);
+        } else {
+          r.dy[j] = make_uint4(0, 0, 0, 0);
+          if (t < nv && v < p.Dv) {
+            const T* from = gY + int64_t(t) * p.H * p.Dv + v;
             T x[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; e++) x[e] = v + e < p.Dv ? from[e] : T(0);
@@ -1322,23 +1336,24 @@ void delta_grad_kernel(Grad a) {
           }
         }
       }
-      const bool in = has_left && v0 + lv < p.VP;
-      const int at = (lt / 16 * p.VP + v0 + lv) * 16 + lt % 16;
-      r.n = in ? *reinterpret_cast<const float4*>(gN + at) : zero;
-      r.r = in ? *reinterpret_cast<const float4*>(gR + at) : zero;
+      const int at = has_left && v0 + lv < p.VP ? 4 * ((lt / 16 * p.VP + v0 + lv) * 16 + lt % 16) : 0x7fffffff;
+      r.n = quad(rn, at);
+      r.r = quad(rr, at);
 #pragma unroll
       for (int j = 0; j < kStates; j++) {
         const int i = tid + j * kAll, e = i % 4 * 4 + i / 128 * 16, v = v0 + i / 4 % 32;
-        const bool ok = e < p.KP && v < p.VP;
-        const int so = (e / 16 * p.VP + v) * 16 + e % 16;
-        r.S[j] = ok ? *reinterpret_cast<const float4*>(gS + so) : zero;
-        r.D[j] = ok ? *reinterpret_cast<const float4*>(gD + so) : zero;
+        const int so = e < p.KP && v < p.VP ? 4 * ((e / 16 * p.VP + v) * 16 + e % 16) : 0x7fffffff;
+        r.S[j] = quad(rS, so);
+        r.D[j] = quad(rD, so);
+      }
+      if (v0 == 0) {  // a head's first
+        r.gate = Scalars<T, kC>::load_at(p.g, (row0 * p.H + hh), p.H, nv);
+        r.beta = Scalars<T, kC>::load_at(p.beta, (row0 * p.H + hh), p.H, nv);
       }
     };
-    const float gate = wv == 0 && l < kC ? gate_of<T>(p, bi, t0 + l, h, n) : 0.f;
-    const float beta = wv == 1 && l < kC ? beta_of<T>(p, bi, t0 + l, h, n) : 0.f;
-    Regs r;
-    fetch(r, 0);
+    if (h == h0) fetch(h, 0);
+    const float gate = l < nv ? clamp_log(Scalars<T, kC>::value(r.gate) + (p.A ? p.A[h] : 0.f)) : 0.f;
+    const float beta = l < nv ? p.beta ? Scalars<T, kC>::value(r.beta) : 1.f : 0.f;
     if (wv == 0) {
       fill_decays(sh.d, gate, 1.f);
       if (l < kC) sh.gate[l] = gate;
@@ -1395,7 +1410,7 @@ void delta_grad_kernel(Grad a) {
         put4(y, sh.a.D[0] + at, sh.a.D[kN - 1] + at);
       }
       __syncthreads();
-      if (v0 + 32 < p.Dv) fetch(r, v0 + 32);
+      if (v0 + 32 < p.Dv) fetch(h, v0 + 32);
       if (wv < TB) {  // dv: the first part of dR is what rounding leaves of it
         const int t = 16 * wv + lr, v = v0 + g8;
         const Frag<T> f = col_frag(sh.a.r[0], ldt, g8, 16 * wv, 4);
@@ -1457,6 +1472,7 @@ void delta_grad_kernel(Grad a) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    if (MULTI && h + 1 < h0 + a.heads) fetch(h + 1, 0);
     // dbeta: a row of 16 lanes has four columns of 16 tokens, four a lane
 #pragma unroll
     for (int e = 0; e < 4; e++) db[e] = add_ror<4>(add_ror<8>(db[e]));
