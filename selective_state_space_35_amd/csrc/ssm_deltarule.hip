@@ -1044,50 +1044,67 @@ void delta_sweep_kernel(Rule p) {
 }
 
 // ---------------------------------------------------------------------------
-// The states leaving the parts of a cut sequence, one after the other: S = map S + own, 16 columns a wave, in float products.
+// The states leaving the parts of a cut sequence, one after the other: S = map S + own, 16 columns a workgroup, a quarter of
+// the rows a wave, in float products.  The state goes through LDS, the next part's map is under way meanwhile.
 // ---------------------------------------------------------------------------
 template <int KDP>
-__global__ __launch_bounds__(kWave) void delta_chain_kernel(Rule p) {
-  constexpr int MT = KDP / 16;
-  const int l = threadIdx.x, lr = l % 16, g4 = 4 * (l / 16), blocks = p.KP / 16;
+__global__ __launch_bounds__(kThreads) void delta_chain_kernel(Rule p) {
+  constexpr int MT = KDP / 16, MW = MT / 4;
+  __shared__ f32x4 S[2][MT][kWave];
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), l = threadIdx.x % kWave, lr = l % 16, g4 = 4 * (l / 16);
+  const int blocks = p.KP / 16;
   const int64_t bh = blockIdx.x / (p.VP / 16);
   const int v = int(blockIdx.x % (p.VP / 16)) * 16 + lr;
-  f32x4 S[MT];
   const float* init = p.init ? p.init + bh * p.Dk * p.Dv : nullptr;
 #pragma unroll
-  for (int m = 0; m < MT; m++)
+  for (int k = 0; k < MW; k++) {
+    f32x4 x;
 #pragma unroll
     for (int r = 0; r < 4; r++) {
-      const int i = 16 * m + g4 + r;
-      S[m][r] = init && i < p.Dk && v < p.Dv ? init[i * p.Dv + v] : 0.f;
+      const int i = 16 * (wv * MW + k) + g4 + r;
+      x[r] = init && i < p.Dk && v < p.Dv ? init[i * p.Dv + v] : 0.f;
     }
-  for (int k = 0; k < p.n_parts; k++) {
-    float* own = p.part_own + (bh * p.n_parts + k) * p.KP * p.VP + v * 16 + g4;
-    const float* map = p.part_map + (bh * p.n_parts + k) * p.KP * p.KP + lr;
-    f32x4 next[MT];
+    S[0][wv * MW + k][l] = x;
+  }
+  float4 a[MW][MT], own[MW];
+  auto fetch = [&](int part) {
+    const float* from = p.part_own + (bh * p.n_parts + part) * p.KP * p.VP + v * 16 + g4;
+    const float* map = p.part_map + (bh * p.n_parts + part) * p.KP * p.KP + lr;
 #pragma unroll
-    for (int m = 0; m < MT; m++) {
-      next[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (m >= blocks) continue;
-      const float4 x = lds4(own + m * p.VP * 16);
-      float4 a[MT];
+    for (int k = 0; k < MW; k++) {
+      const int m = std::min(wv * MW + k, blocks - 1);  // rows behind the state's: read again, not written
+      own[k] = lds4(from + m * p.VP * 16);
 #pragma unroll
       for (int kb = 0; kb < MT; kb++) {
-        const float* at = map + (m * p.KP + 16 * kb + g4) * 16;
-        a[kb] = kb < blocks ? make_float4(at[0], at[16], at[32], at[48]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float* at = map + (m * p.KP + 16 * std::min(kb, blocks - 1) + g4) * 16;
+        a[k][kb] = make_float4(at[0], at[16], at[32], at[48]);
       }
-      f32x4 even{x.x, x.y, x.z, x.w}, odd{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+  fetch(0);
+  for (int part = 0; part < p.n_parts; part++) {
+    __syncthreads();
+    f32x4 x[MT], y[MW][2];
 #pragma unroll
-      for (int kb = 0; kb < MT; kb += 2) {
-        if (kb < blocks) even = mma16(a[kb], S[kb], even);
-        if (kb + 1 < blocks) odd = mma16(a[kb + 1], S[kb + 1], odd);
-      }
-      next[m] = even + odd;
+    for (int kb = 0; kb < MT; kb++) x[kb] = kb < blocks ? S[part % 2][kb][l] : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < MW; k++) {
+      y[k][0] = f32x4{own[k].x, own[k].y, own[k].z, own[k].w};
+      y[k][1] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 #pragma unroll
-    for (int m = 0; m < MT; m++) {
-      S[m] = next[m];
-      if (m < blocks) *reinterpret_cast<float4*>(own + m * p.VP * 16) = make_float4(S[m][0], S[m][1], S[m][2], S[m][3]);
+    for (int kb = 0; kb < MT; kb++)
+      if (kb < blocks)  // not a product with zero of what may be no number
+#pragma unroll
+        for (int k = 0; k < MW; k++) y[k][kb % 2] = mma16(a[k][kb], x[kb], y[k][kb % 2]);
+    if (part + 1 < p.n_parts) fetch(part + 1);
+    float* to = p.part_own + (bh * p.n_parts + part) * p.KP * p.VP + v * 16 + g4;
+#pragma unroll
+    for (int k = 0; k < MW; k++) {
+      const int m = wv * MW + k;
+      const f32x4 z = y[k][0] + y[k][1];
+      S[(part + 1) % 2][m][l] = z;
+      if (m < blocks) *reinterpret_cast<float4*>(to + m * p.VP * 16) = make_float4(z[0], z[1], z[2], z[3]);
     }
   }
 }
@@ -1759,7 +1776,8 @@ bool pieces(const void* x, int64_t D) {
 // sequence is cut into segments, whose entering states a pass before gives: the part's own state and its map, Dk columns more.
 // Of the cuts into up to 64 segments and 1, 2, 3 or 4 parts each the one whose generations of workgroups take the fewest chunks
 // one after the other: a chunk of the pass before counts 3/4 of one of the sweep (measured: bf16, D128, 2.9 and 3.7 us), a step
-// of the chain 1/3 or, above 64 elements of the keys, one, the launches 3.
+// of the chain 1/3 or, above 64 elements of the keys, one (it is shorter, but with 1/5 and 2/5 b1 L2048 H32 D128 took 128 us, so 107),
+// the launches 3.
 constexpr int64_t kAtOnce = 256;
 struct Cut {
   int n_segs = 1, parts = 1, part_chunks = 1, n_parts = 0;
@@ -1864,9 +1882,9 @@ hipError_t run_sweep(const Rule& p) {
     hipError_t err = p.Dk <= 64 ? (vec ? go(delta_sweep_kernel<T, 64, kTile, PM, true, true>, blocks) : go(delta_sweep_kernel<T, 64, kTile, PM, true, false>, blocks))
                                 : (vec ? go(delta_sweep_kernel<T, 128, kTile, PM, true, true>, blocks) : go(delta_sweep_kernel<T, 128, kTile, PM, true, false>, blocks));
     if (err != hipSuccess) return err;
-    const int64_t waves = heads * (p.VP / 16);
-    err = p.Dk <= 64 ? launch_kind(kKindDeltaChain, delta_chain_kernel<64>, waves, kWave, p.stream, p)
-                     : launch_kind(kKindDeltaChain, delta_chain_kernel<128>, waves, kWave, p.stream, p);
+    const int64_t tiles = heads * (p.VP / 16);
+    err = p.Dk <= 64 ? launch_kind(kKindDeltaChain, delta_chain_kernel<64>, tiles, kThreads, p.stream, p)
+                     : launch_kind(kKindDeltaChain, delta_chain_kernel<128>, tiles, kThreads, p.stream, p);
     if (err != hipSuccess) return err;
   }
   const int64_t blocks = heads * p.n_tiles * p.n_segs;
