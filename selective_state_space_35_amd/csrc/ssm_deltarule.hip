@@ -45,6 +45,8 @@ constexpr float kZeroLog = -104.f;
 // place, and its own part taken where dR itself is meant
 constexpr float kLeastBeta = 8.673617379884035e-19f;  // 2^-60
 
+constexpr int kTile = 64;  // columns of the values a workgroup of the sweep or of the token step has
+
 struct Rule {
   const void* q;
   const void* k;
@@ -1654,36 +1656,37 @@ void delta_grad_kernel(Grad a) {
 }
 
 // ---------------------------------------------------------------------------
-// One token: a workgroup holds one head of one batch row, the whole state in registers (NR rows of VEC columns a thread):
-// lanes run along its columns, groups of them along its rows.  What the state answers for k and for q is summed over
+// One token: a workgroup holds up to kTile columns of one head's state in registers (NR rows of VEC columns a thread): lanes
+// run along its columns, groups of them along its rows.  What the state answers for k and for q is summed over
 // the groups at once, in LDS: y = scale (r S^T q + (q . k) u).  The state is read and written once: bound by HBM.
 // ---------------------------------------------------------------------------
 template <typename T, int VEC, int NR>
 __global__ __launch_bounds__(256) void delta_update_kernel(Rule p, float* __restrict__ state, int lanes) {
   __shared__ float qs[kMaxDim], ks[kMaxDim], pk[256 * VEC], pq[256 * VEC], kq_part[4];
-  const int h = blockIdx.x % p.H, G = p.H / p.share;
-  const int64_t bi = blockIdx.x / p.H, bh = bi * p.H + h, qrow = bi * G + h / p.share;
+  const int G = p.H / p.share;
+  const int64_t bh = blockIdx.x / p.n_tiles, bi = bh / p.H;
+  const int h = int(bh % p.H), c0 = int(blockIdx.x % p.n_tiles) * kTile;
+  const int64_t qrow = bi * G + h / p.share;
   const int Dk = p.Dk, Dv = p.Dv;
   T* y = static_cast<T*>(p.y) + bh * Dv;
   if (p.lengths && p.lengths[bi] <= 0) {
-    for (int j = threadIdx.x; j < Dv; j += 256) store_elem(y + j, 0.f);
+    for (int j = c0 + threadIdx.x; j < Dv && j < c0 + kTile; j += 256) store_elem(y + j, 0.f);
     return;
   }
-  const int l = threadIdx.x % lanes, r0 = threadIdx.x / lanes, groups = 256 / lanes, c = l * VEC;
-  float* at = state + bh * Dk * Dv + c;
+  const int l = threadIdx.x % lanes, r0 = threadIdx.x / lanes, groups = 256 / lanes, c = c0 + l * VEC;
+  // the state through a descriptor: one lane offset, rows `groups` apart in steps of a scalar one
+  const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(state + bh * Dk * Dv);
+  const int at = 4 * (r0 * Dv + c), step = 4 * groups * Dv;
+  auto place = [&](int i) { return r0 + i * groups < Dk && c < Dv ? at : 0x7fffffff; };
   float S[NR][VEC];
 #pragma unroll
   for (int i = 0; i < NR; i++) {
-    const int r = r0 + i * groups;
+    if constexpr (VEC == 4) {
+      const auto u = __builtin_amdgcn_raw_buffer_load_b128(rs, place(i), i * step, 0);
 #pragma unroll
-    for (int j = 0; j < VEC; j++) S[i][j] = 0.f;
-    if (r < Dk && c < Dv) {
-      if constexpr (VEC == 4) {
-        const float4 u = *reinterpret_cast<const float4*>(at + r * Dv);
-        S[i][0] = u.x; S[i][1] = u.y; S[i][2] = u.z; S[i][3] = u.w;
-      } else {
-        S[i][0] = at[r * Dv];
-      }
+      for (int j = 0; j < 4; j++) S[i][j] = __uint_as_float(u[j]);
+    } else {
+      S[i][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, place(i), i * step, 0));
     }
   }
   float kq = 0.f;
@@ -1709,8 +1712,8 @@ __global__ __launch_bounds__(256) void delta_update_kernel(Rule p, float* __rest
   for (int j = 0; j < VEC; j++) ak[j] = aq[j] = 0.f;
 #pragma unroll
   for (int i = 0; i < NR; i++) {
-    const int r = r0 + i * groups;
-    if (r < Dk) {
+    const int r = std::min(r0 + i * groups, kMaxDim - 1);  // rows behind the state's are zero
+    if (r0 + i * groups < Dk) {
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
         S[i][j] *= dec;
@@ -1741,15 +1744,17 @@ __global__ __launch_bounds__(256) void delta_update_kernel(Rule p, float* __rest
     u[j] = beta * (v[j] - u[j]);
     o[j] = fmaf(kq, u[j], o[j]) * p.scale;
   }
-  if (c >= Dv) return;
 #pragma unroll
   for (int i = 0; i < NR; i++) {
-    const int r = r0 + i * groups;
-    if (r < Dk) {
+    const float k = ks[std::min(r0 + i * groups, kMaxDim - 1)];
+    if constexpr (VEC == 4) {
+      typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+      u4 w;
 #pragma unroll
-      for (int j = 0; j < VEC; j++) S[i][j] = fmaf(ks[r], u[j], S[i][j]);
-      if constexpr (VEC == 4) *reinterpret_cast<float4*>(at + r * Dv) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
-      else at[r * Dv] = S[i][0];
+      for (int j = 0; j < 4; j++) w[j] = __float_as_uint(fmaf(k, u[j], S[i][j]));
+      __builtin_amdgcn_raw_buffer_store_b128(w, rs, place(i), i * step, 0);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(fmaf(k, u[0], S[i][0])), rs, place(i), i * step, 0);
     }
   }
   if (r0 == 0)
@@ -1764,7 +1769,6 @@ __global__ __launch_bounds__(256) void delta_update_kernel(Rule p, float* __rest
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kSumBlocks = int64_t(1) << 22;  // a grid holds less than 2^32 threads: beyond, a thread has several sums
 constexpr size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-constexpr int kTile = 64;  // columns of the values a workgroup of the sweep has
 
 // rows of whole 16-byte pieces, 16-byte aligned
 template <typename T>
@@ -1981,11 +1985,11 @@ hipError_t update_impl(const DeltaRuleArgs& a) {
   p.y = a.y;
   const bool vec = a.Dv % 4 == 0 && reinterpret_cast<uintptr_t>(a.last) % 16 == 0;
   int lanes = 1;
-  while (lanes * (vec ? 4 : 1) < a.Dv) lanes *= 2;
-  const int64_t rows = ceil_div(a.Dk, 256 / lanes);  // of the state a thread has: at most 16 in vectors, 64 else
-  auto go = [&](auto kern) { return launch_kind(kKindDeltaUpdate, kern, a.b * a.H, 256, a.stream, p, a.last, lanes); };
-  if (vec) return rows <= 4 ? go(delta_update_kernel<T, 4, 4>) : rows <= 8 ? go(delta_update_kernel<T, 4, 8>) : go(delta_update_kernel<T, 4, 16>);
-  return rows <= 16 ? go(delta_update_kernel<T, 1, 16>) : go(delta_update_kernel<T, 1, 64>);
+  while (lanes * (vec ? 4 : 1) < std::min<int64_t>(a.Dv, kTile)) lanes *= 2;
+  const int64_t rows = ceil_div(a.Dk, 256 / lanes);  // of the state a thread has: at most 8 in vectors, 32 else
+  auto go = [&](auto kern) { return launch_kind(kKindDeltaUpdate, kern, a.b * a.H * p.n_tiles, 256, a.stream, p, a.last, lanes); };
+  if (vec) return rows <= 4 ? go(delta_update_kernel<T, 4, 4>) : go(delta_update_kernel<T, 4, 8>);
+  return rows <= 16 ? go(delta_update_kernel<T, 1, 16>) : go(delta_update_kernel<T, 1, 32>);
 }
 
 }  // namespace
