@@ -35,7 +35,7 @@ struct BlockNormArgs {
   hipStream_t stream;
 };
 int64_t blocknorm_max_width();
-size_t blocknorm_workspace_bytes(const BlockNormArgs& a);  // of the backward, for tensors of any alignment and all gradients
+size_t blocknorm_workspace_bytes(const BlockNormArgs& a);  // of the backward, for all gradients
 hipError_t launch_blocknorm_fwd(const BlockNormArgs& a);
 hipError_t launch_blocknorm_bwd(const BlockNormArgs& a, void* workspace);
 

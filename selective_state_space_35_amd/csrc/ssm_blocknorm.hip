@@ -13,8 +13,8 @@
 // 4.5 TB/s, and 15 us for the parameters' sums).  A group of threads keeps one head's parameters, and in the backward its
 // part of their gradients, in registers and walks rows, the next row's loads under way while one is summed (the parameters
 // read again for every row, 16 registers a thread fewer: 742 us); the gate is a form of its own (with its values in
-// registers that nobody used 510 us).  Rows above 8192 elements, and in the backward odd ones above 2048, keep more than
-// 128 registers a thread and go through scratch.  All sums are float.
+// registers that nobody used 510 us).  Rows above 8192 elements keep more than 128 registers a thread and go through
+// scratch.  All sums are float.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,32 +28,56 @@
 namespace ssm {
 namespace {
 
-// N consecutive elements as they come from memory: whole 16-byte (or 8-byte) pieces, or (N = 1) one element
+// N consecutive elements of a row as they come from memory, 16 bytes at once from any address (unaligned access is on for
+// global memory).  TAIL: the width is not whole pieces, and `left` elements from here on are inside the row.  A row's last
+// piece of 8 is then read so that it ends with the row, and shifted into place, zeros behind it, when it is used.  65536 rows
+// of 2561 in bf16, backward, 624 us; shifted when it is loaded, that is, waited for, 1089; 40000 gated rows of 4095 789 us
+// and 1214, element by element 1210.  Pieces of 4 and rows shorter than a piece go element by element (65536 float rows of
+// 1001, backward, 305 us; shifted 515).
+__host__ __device__ constexpr bool shifted(int n, int W) { return n == 8 && W >= n; }
 template <typename T, int N>
 struct Raw {
   uint32_t w[N * int(sizeof(T)) / 4];
 };
-template <typename T>
-struct Raw<T, 1> {
-  T w;
-};
-template <typename T, int N>
-__device__ __forceinline__ void load_raw(Raw<T, N>& r, const T* p) {
-  if constexpr (N == 1) {
-    r.w = *p;
+template <bool TAIL, typename T, int N>
+__device__ __forceinline__ void load_raw(Raw<T, N>& r, const T* p, int left, int W) {
+  constexpr int kPer = 16 / int(sizeof(T)), kPieces = N / kPer;
+  if constexpr (!TAIL) {
+    __builtin_memcpy(r.w, p, N * sizeof(T));
+  } else if (shifted(N, W)) {
+#pragma unroll
+    for (int k = 0; k < kPieces; k++) {
+      const int over = max((k + 1) * kPer - left, 0);
+      __builtin_memcpy(r.w + 4 * k, p + k * kPer - over, 16);
+    }
+  } else if (left >= N) {
+    __builtin_memcpy(r.w, p, N * sizeof(T));
   } else {
 #pragma unroll
-    for (int k = 0; k < N * int(sizeof(T)) / 16; k++) {
-      const uint4 u = reinterpret_cast<const uint4*>(p)[k];
-      r.w[4 * k] = u.x; r.w[4 * k + 1] = u.y; r.w[4 * k + 2] = u.z; r.w[4 * k + 3] = u.w;
+    for (int k = 0; k < N * int(sizeof(T)) / 4; k++) r.w[k] = 0;
+#pragma unroll
+    for (int j = 0; j < N - 1; j++) {
+      if (j < left) {
+        if constexpr (sizeof(T) == 4) r.w[j] = __float_as_uint(p[j]);
+        else r.w[j / 2] |= uint32_t(p[j]) << (16 * (j % 2));
+      }
     }
   }
 }
-template <typename T, int N>
-__device__ __forceinline__ void floats(const Raw<T, N>& r, float (&v)[N]) {
-  if constexpr (N == 1) {
-    v[0] = load_elem(&r.w);
-  } else if constexpr (sizeof(T) == 4) {
+template <bool TAIL, typename T, int N>
+__device__ __forceinline__ void floats(Raw<T, N> r, float (&v)[N], int left, int W) {
+  if constexpr (TAIL && N == 8) {
+    constexpr int kPer = 16 / int(sizeof(T)), kPieces = N / kPer;
+#pragma unroll
+    for (int k = 0; k < kPieces; k++) {
+      const int bits = !shifted(N, W) ? 0 : min(max((k + 1) * kPer - left, 0), kPer) * 8 * int(sizeof(T));
+      unsigned __int128 x;
+      __builtin_memcpy(&x, r.w + 4 * k, 16);
+      x = kPieces == 1 ? x >> bits : x >> (bits / 2) >> (bits / 2);  // a piece behind the row shifts by all 128
+      __builtin_memcpy(r.w + 4 * k, &x, 16);
+    }
+  }
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int j = 0; j < N; j++) v[j] = __uint_as_float(r.w[j]);
   } else {
@@ -64,23 +88,27 @@ __device__ __forceinline__ void floats(const Raw<T, N>& r, float (&v)[N]) {
     }
   }
 }
-template <typename T, int N>
-__device__ __forceinline__ void store(T* p, const float (&v)[N]) {
-  if constexpr (N == 1) {
-    store_elem(p, v[0]);
-  } else if constexpr (sizeof(T) == 4) {
+template <bool TAIL, typename T, int N>
+__device__ __forceinline__ void store(T* p, const float (&v)[N], int left) {
+  if (!TAIL || left >= N) {
+    uint32_t w[N * int(sizeof(T)) / 4];
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int k = 0; k < N / 4; k++) reinterpret_cast<float4*>(p)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      for (int j = 0; j < N; j++) w[j] = __float_as_uint(v[j]);
+    } else {
+      typedef __attribute__((ext_vector_type(2))) float f2;
+      typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+#pragma unroll
+      for (int j = 0; j < N / 2; j++) w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2 * j], v[2 * j + 1]}), b2));
+    }
+    __builtin_memcpy(p, w, N * sizeof(T));
   } else {
-    typedef __attribute__((ext_vector_type(2))) float f2;
-    typedef __attribute__((ext_vector_type(2))) __bf16 b2;
-    uint32_t w[N / 2];
 #pragma unroll
-    for (int j = 0; j < N / 2; j++) w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2 * j], v[2 * j + 1]}), b2));
-#pragma unroll
-    for (int k = 0; k < N / 8; k++) reinterpret_cast<uint4*>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    for (int j = 0; j < N - 1; j++)
+      if (j < left) store_elem(p + j, v[j]);
   }
 }
+
 // The sum over the TPR threads of a row, the same in every one of them: shuffles, and for wider rows LDS, two calls in
 // turn with a buffer each, so that one barrier a call is enough (the whole workgroup comes to it).
 template <int TPR>
@@ -102,7 +130,7 @@ constexpr int block_threads(int tpr) { return tpr > 128 ? tpr : 256; }
 
 // A parameter of a group's head, one where there is none: in registers, or for the rows of many threads, whose registers
 // are few, read again for every row (from the caches).
-template <int NV, int VEC, int TPR>
+template <bool TAIL, int NV, int VEC, int TPR>
 struct Par {
   static constexpr bool kHeld = TPR < 640;
   const float* w;
@@ -120,7 +148,14 @@ struct Par {
 #pragma unroll
     for (int e = 0; e < VEC; e++) o[e] = 1.f;
     const int c = (j * TPR + lane) * VEC;
-    if (w && c < W) __builtin_memcpy(o, w + c, VEC * 4);  // only 4-byte aligned
+    if (!w || c >= W) return;
+    if (!TAIL || c + VEC <= W) {
+      __builtin_memcpy(o, w + c, VEC * 4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC - 1; e++)
+        if (c + e < W) o[e] = w[c + e];
+    }
   }
   __device__ __forceinline__ void get(int j, float (&o)[VEC]) const {
     if constexpr (kHeld) {
@@ -133,8 +168,8 @@ struct Par {
 };
 
 // One group of TPR threads walks the rows slice, slice + n_slices, ... of head h; each thread has NV vectors of VEC
-// elements of a row, at columns (j TPR + lane) VEC.  R: the residual stream's type.
-template <typename T, typename R, bool GATE, int VEC, int NV, int TPR>
+// elements of a row, at columns (j TPR + lane) VEC.  TAIL: the width is not whole vectors.  R: the residual stream's type.
+template <typename T, typename R, bool GATE, bool TAIL, int VEC, int NV, int TPR>
 __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArgs a, int64_t n_slices) {
   constexpr int kGroups = block_threads(TPR) / TPR;
   __shared__ float buf[2][kGroups][TPR > kWave ? TPR / kWave : 1];
@@ -147,7 +182,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
   const T* x = static_cast<const T*>(a.x);
   const T* z = static_cast<const T*>(a.z);
   const R* res = static_cast<const R*>(a.residual);
-  Par<NV, VEC, TPR> p1, ps, p2;
+  Par<TAIL, NV, VEC, TPR> p1, ps, p2;
   p1.init(a.post ? a.post_weight : nullptr, int64_t(h) * W, lane, W);
   ps.init(a.scale, int64_t(h) * W, lane, W);
   p2.init(a.pre ? a.pre_weight : nullptr, int64_t(h) * W, lane, W);
@@ -159,9 +194,9 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
       const int c = (j * TPR + lane) * VEC;
       const int64_t at = (i * H + h) * W + c;
       if (c < W) {
-        load_raw(xn[j], x + at);
-        if constexpr (GATE) load_raw(zn[j], z + at);
-        if (res) load_raw(rn[j], res + at);
+        load_raw<TAIL>(xn[j], x + at, W - c, W);
+        if constexpr (GATE) load_raw<TAIL>(zn[j], z + at, W - c, W);
+        if (res) load_raw<TAIL>(rn[j], res + at, W - c, W);
       }
     }
   };
@@ -179,9 +214,9 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
 #pragma unroll
       for (int e = 0; e < VEC; e++) v[j][e] = g[j][e] = r[j][e] = 0.f;
       if (in) {
-        floats(xn[j], v[j]);
-        if constexpr (GATE) floats(zn[j], g[j]);
-        if (res) floats(rn[j], r[j]);
+        floats<TAIL>(xn[j], v[j], W - (j * TPR + lane) * VEC, W);
+        if constexpr (GATE) floats<TAIL>(zn[j], g[j], W - (j * TPR + lane) * VEC, W);
+        if (res) floats<TAIL>(rn[j], r[j], W - (j * TPR + lane) * VEC, W);
       }
     }
     if (live && i0 + n_slices < a.rows) fetch(i0 + n_slices);
@@ -213,7 +248,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
 #pragma unroll
       for (int j = 0; j < NV; j++) {
         const int c = (j * TPR + lane) * VEC;
-        if (c < W) store(static_cast<R*>(a.h) + row * W + c, v[j]);
+        if (c < W) store<TAIL>(static_cast<R*>(a.h) + row * W + c, v[j], W - c);
       }
     }
     if (a.pre) {
@@ -228,7 +263,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
             p2.get(j, w2);
 #pragma unroll
             for (int e = 0; e < VEC; e++) o[e] = v[j][e] * r2 * w2[e];
-            store(static_cast<T*>(a.n) + row * W + c, o);
+            store<TAIL>(static_cast<T*>(a.n) + row * W + c, o, W - c);
           }
         }
       }
@@ -242,7 +277,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
 
 // As the forward; a group writes its own row of the partial sums [3][n_slices][H W] (of w1, the scale, w2), which
 // bn_reduce_kernel adds in a fixed order.
-template <typename T, typename R, bool GATE, int VEC, int NV, int TPR>
+template <typename T, typename R, bool GATE, bool TAIL, int VEC, int NV, int TPR>
 __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArgs a, int64_t n_slices, float* part) {
   constexpr int kGroups = block_threads(TPR) / TPR;
   __shared__ float buf[2][kGroups][TPR > kWave ? TPR / kWave : 1];
@@ -258,7 +293,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
   // h is needed for the norm before the next block only
   const R* res = a.pre ? static_cast<const R*>(a.residual) : nullptr;
   const R* dh = static_cast<const R*>(a.dh);
-  Par<NV, VEC, TPR> p1, ps, p2;
+  Par<TAIL, NV, VEC, TPR> p1, ps, p2;
   p1.init(a.post ? a.post_weight : nullptr, int64_t(h) * W, lane, W);
   ps.init(a.scale, int64_t(h) * W, lane, W);
   p2.init(a.pre ? a.pre_weight : nullptr, int64_t(h) * W, lane, W);
@@ -279,11 +314,11 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
       const int c = (j * TPR + lane) * VEC;
       const int64_t at = row * W + c;
       if (c < W) {
-        load_raw(xn[j], x + at);
-        if constexpr (GATE) load_raw(zn[j], z + at);
-        if (res) load_raw(rn[j], res + at);
-        if (dh) load_raw(hn[j], dh + at);
-        if (dn) load_raw(nn[j], dn + at);
+        load_raw<TAIL>(xn[j], x + at, W - c, W);
+        if constexpr (GATE) load_raw<TAIL>(zn[j], z + at, W - c, W);
+        if (res) load_raw<TAIL>(rn[j], res + at, W - c, W);
+        if (dh) load_raw<TAIL>(hn[j], dh + at, W - c, W);
+        if (dn) load_raw<TAIL>(nn[j], dn + at, W - c, W);
       }
     }
   };
@@ -301,11 +336,11 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
 #pragma unroll
       for (int e = 0; e < VEC; e++) xh[j][e] = g[j][e] = hh[j][e] = d[j][e] = t[j][e] = 0.f;
       if (in) {
-        floats(xn[j], xh[j]);
-        if constexpr (GATE) floats(zn[j], g[j]);
-        if (res) floats(rn[j], hh[j]);
-        if (dh) floats(hn[j], d[j]);
-        if (dn) floats(nn[j], t[j]);
+        floats<TAIL>(xn[j], xh[j], W - (j * TPR + lane) * VEC, W);
+        if constexpr (GATE) floats<TAIL>(zn[j], g[j], W - (j * TPR + lane) * VEC, W);
+        if (res) floats<TAIL>(rn[j], hh[j], W - (j * TPR + lane) * VEC, W);
+        if (dh) floats<TAIL>(hn[j], d[j], W - (j * TPR + lane) * VEC, W);
+        if (dn) floats<TAIL>(nn[j], t[j], W - (j * TPR + lane) * VEC, W);
 #pragma unroll
         for (int e = 0; e < VEC; e++) xh[j][e] *= r1;
       }
@@ -350,7 +385,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
 #pragma unroll
       for (int j = 0; j < NV; j++) {
         const int c = (j * TPR + lane) * VEC;
-        if (c < W) store(static_cast<R*>(a.dresidual) + row * W + c, d[j]);
+        if (c < W) store<TAIL>(static_cast<R*>(a.dresidual) + row * W + c, d[j], W - c);
       }
     }
     float s = 0.f;
@@ -374,7 +409,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
 #pragma unroll
       for (int j = 0; j < NV; j++) {
         const int c = (j * TPR + lane) * VEC;
-        if (c < W) store(static_cast<T*>(a.dz) + row * W + c, g[j]);
+        if (c < W) store<TAIL>(static_cast<T*>(a.dz) + row * W + c, g[j], W - c);
       }
     }
     if (a.post) {
@@ -388,7 +423,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
 #pragma unroll
       for (int j = 0; j < NV; j++) {
         const int c = (j * TPR + lane) * VEC;
-        if (c < W) store(static_cast<T*>(a.dx) + row * W + c, d[j]);
+        if (c < W) store<TAIL>(static_cast<T*>(a.dx) + row * W + c, d[j], W - c);
       }
     }
   }
@@ -397,9 +432,10 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
 #pragma unroll
   for (int j = 0; j < NV; j++) {
     const int c = (j * TPR + lane) * VEC;
-    if (c < W) {
+    {
 #pragma unroll
       for (int e = 0; e < VEC; e++) {
+        if (c + e >= W) continue;
         if (a.dpost_weight) part[at + c + e] = dw1[j][e];
         if (a.dscale) part[all + at + c + e] = ds[j][e];
         if (a.dpre_weight) part[2 * all + at + c + e] = dw2[j][e];
@@ -444,55 +480,41 @@ constexpr int64_t bwd_blocks(int tpr) { return tpr > kWave ? 512 : 768; }
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <typename T, typename R, bool GATE, int VEC, int NV, int TPR>
+template <typename T, typename R, bool GATE, bool TAIL, int VEC, int NV, int TPR>
 struct Form {
   static hipError_t fwd(const BlockNormArgs& a, int64_t n_slices) {
     constexpr int threads = block_threads(TPR), groups = threads / TPR;
-    return launch_kind(kKindBlockNormFwd, bn_fwd_kernel<T, R, GATE, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices);
+    return launch_kind(kKindBlockNormFwd, bn_fwd_kernel<T, R, GATE, TAIL, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices);
   }
   static hipError_t bwd(const BlockNormArgs& a, int64_t n_slices, float* part) {
     constexpr int threads = block_threads(TPR), groups = threads / TPR;
-    return launch_kind(kKindBlockNormBwd, bn_bwd_kernel<T, R, GATE, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices, part);
+    return launch_kind(kKindBlockNormBwd, bn_bwd_kernel<T, R, GATE, TAIL, VEC, NV, TPR>, ceil_div(n_slices * a.H, groups), threads, a.stream, a, n_slices, part);
   }
   static constexpr int tpr = TPR;
 };
 
-// rows read and written in 16-byte vectors: whole vectors a row, aligned tensors
-template <typename T, typename R>
-bool whole_vectors(const BlockNormArgs& a) {
-  constexpr int VEC = 16 / sizeof(T);
-  const void* all[] = {a.x, a.z, a.residual, a.h, a.n, a.dh, a.dn, a.dx, a.dz, a.dresidual};
-  uintptr_t p = 0;
-  for (const void* q : all) p |= reinterpret_cast<uintptr_t>(q);
-  return a.W % VEC == 0 && p % 16 == 0;
-}
-
-// The form of rows of W elements: one vector a thread, in whole waves above one; more only above 1024 threads.  Elements
-// one at a time (odd widths): up to eight a thread, sixteen in the widest rows.
-template <typename T, typename R, bool GATE, typename Go>
-auto with_form(bool vec, int64_t W, Go go) {
+// The form of rows of W elements: one vector a thread, in whole waves above one; more only above 1024 threads.
+template <typename T, typename R, bool GATE, bool TAIL, typename Go>
+auto with_size(int64_t W, Go go) {
   constexpr int V = 16 / sizeof(T);
-  if (!vec) {
-    if (W <= 64) return go(Form<T, R, GATE, 1, 8, 8>{});
-    if (W <= 512) return go(Form<T, R, GATE, 1, 8, 64>{});
-    if (W <= 2048) return go(Form<T, R, GATE, 1, 8, 256>{});
-    if (W <= 8192) return go(Form<T, R, GATE, 1, 8, 1024>{});
-    return go(Form<T, R, GATE, 1, 16, 1024>{});
-  }
-  const int64_t n = W / V;
-  if (n <= 8) return go(Form<T, R, GATE, V, 1, 8>{});
-  if (n <= 16) return go(Form<T, R, GATE, V, 1, 16>{});
-  if (n <= 32) return go(Form<T, R, GATE, V, 1, 32>{});
-  if (n <= 64) return go(Form<T, R, GATE, V, 1, 64>{});
-  if (n <= 128) return go(Form<T, R, GATE, V, 1, 128>{});
-  if (n <= 192) return go(Form<T, R, GATE, V, 1, 192>{});
-  if (n <= 256) return go(Form<T, R, GATE, V, 1, 256>{});
-  if (n <= 320) return go(Form<T, R, GATE, V, 1, 320>{});
-  if (n <= 512) return go(Form<T, R, GATE, V, 1, 512>{});
-  if (n <= 640) return go(Form<T, R, GATE, V, 1, 640>{});
-  if (n <= 1024) return go(Form<T, R, GATE, V, 1, 1024>{});
-  if (V == 4 && n <= 2048) return go(Form<T, R, GATE, V, 8 / V, 1024>{});
-  return go(Form<T, R, GATE, V, 16 / V, 1024>{});
+  const int64_t n = ceil_div(W, V);
+  if (n <= 8) return go(Form<T, R, GATE, TAIL, V, 1, 8>{});
+  if (n <= 16) return go(Form<T, R, GATE, TAIL, V, 1, 16>{});
+  if (n <= 32) return go(Form<T, R, GATE, TAIL, V, 1, 32>{});
+  if (n <= 64) return go(Form<T, R, GATE, TAIL, V, 1, 64>{});
+  if (n <= 128) return go(Form<T, R, GATE, TAIL, V, 1, 128>{});
+  if (n <= 192) return go(Form<T, R, GATE, TAIL, V, 1, 192>{});
+  if (n <= 256) return go(Form<T, R, GATE, TAIL, V, 1, 256>{});
+  if (n <= 320) return go(Form<T, R, GATE, TAIL, V, 1, 320>{});
+  if (n <= 512) return go(Form<T, R, GATE, TAIL, V, 1, 512>{});
+  if (n <= 640) return go(Form<T, R, GATE, TAIL, V, 1, 640>{});
+  if (n <= 1024) return go(Form<T, R, GATE, TAIL, V, 1, 1024>{});
+  if (V == 4 && n <= 2048) return go(Form<T, R, GATE, TAIL, V, 8 / V, 1024>{});
+  return go(Form<T, R, GATE, TAIL, V, 16 / V, 1024>{});
+}
+template <typename T, typename R, bool GATE, typename Go>
+auto with_form(int64_t W, Go go) {
+  return W % (16 / sizeof(T)) ? with_size<T, R, GATE, true>(W, go) : with_size<T, R, GATE, false>(W, go);
 }
 
 template <typename Go>
@@ -514,10 +536,10 @@ int64_t slices_of(const BlockNormArgs& a, int tpr, int64_t blocks) {
 struct NormPlan {
   int64_t n_slices, n_parts, per;
 };
-NormPlan plan_bwd(const BlockNormArgs& a, bool vec) {
+NormPlan plan_bwd(const BlockNormArgs& a) {
   NormPlan p;
   const int tpr = with_types(a, [&](auto t, auto r, auto gate) {
-    return with_form<decltype(t), decltype(r), decltype(gate)::value>(vec, a.W, [](auto f) { return int(f.tpr); });
+    return with_form<decltype(t), decltype(r), decltype(gate)::value>(a.W, [](auto f) { return int(f.tpr); });
   });
   p.n_slices = slices_of(a, tpr, bwd_blocks(tpr));
   const int64_t blocks = 3 * ceil_div(a.H * a.W, 64);
@@ -536,16 +558,14 @@ int64_t blocknorm_max_width() { return 16384; }
 
 size_t blocknorm_workspace_bytes(const BlockNormArgs& a) {
   if (a.rows == 0 || a.H == 0 || a.W == 0) return 0;
-  // tensors of any alignment: the larger of the two forms
-  const int64_t n = std::max(plan_floats(a, plan_bwd(a, true)), plan_floats(a, plan_bwd(a, false)));
-  return size_t(n) * sizeof(float);
+  return size_t(plan_floats(a, plan_bwd(a))) * sizeof(float);
 }
 
 hipError_t launch_blocknorm_fwd(const BlockNormArgs& a) {
   return with_types(a, [&](auto t, auto r, auto gate) {
     typedef decltype(t) T;
     typedef decltype(r) R;
-    return with_form<T, R, decltype(gate)::value>(whole_vectors<T, R>(a), a.W, [&](auto f) { return f.fwd(a, slices_of(a, f.tpr, kFwdBlocks)); });
+    return with_form<T, R, decltype(gate)::value>(a.W, [&](auto f) { return f.fwd(a, slices_of(a, f.tpr, kFwdBlocks)); });
   });
 }
 
@@ -563,9 +583,8 @@ hipError_t launch_blocknorm_bwd(const BlockNormArgs& a, void* workspace) {
   const hipError_t err = with_types(a, [&](auto t, auto r, auto gate) {
     typedef decltype(t) T;
     typedef decltype(r) R;
-    const bool vec = whole_vectors<T, R>(a);
-    p = plan_bwd(a, vec);
-    return with_form<T, R, decltype(gate)::value>(vec, a.W, [&](auto f) { return f.bwd(a, p.n_slices, part); });
+    p = plan_bwd(a);
+    return with_form<T, R, decltype(gate)::value>(a.W, [&](auto f) { return f.bwd(a, p.n_slices, part); });
   });
   if (err != hipSuccess || !params) return err;
   const int64_t all = p.n_slices * cols, some = p.n_parts * cols;
