@@ -221,6 +221,8 @@ __device__ __forceinline__ f32x4 mma_parts(const Parts<T, NA>& a, const Parts<T,
 // The 16 x 16 blocks on the diagonal are inverted by forward substitution, a column a lane, and joined block by block,
 // Z_ij = -Z_ii (sum over j <= k < i of X_ik Z_kj), a column of blocks a wave, in float products.  An entry of X that is not
 // finite is taken as zero: the sweep makes NaN of everything from its token on.
+// Bound by the latency of its phases (scores, blocks, joining, a barrier between): b8 L2048 H24 D64 bf16 36 us, of the backward,
+// with both forms, 49; b1 L32768 H40 D128 bf16 128 us, 3 TB/s of keys and inverses.  Four workgroups a CU hide some of it.
 // ---------------------------------------------------------------------------
 template <typename T, int KDP, bool VEC>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void delta_tri_kernel(Rule p, float* lower, float* upper) {
@@ -394,6 +396,12 @@ struct SweepLds {
   __attribute__((aligned(16))) float beta[4][kC];  // backwards the part of dR that is beta's own
 };
 
+// A wave's step of a chunk is a chain: K S and Q S, R, Z R, U, the state; 64 columns a workgroup give each SIMD one wave of state
+// and one that stages, and the chain bounds the sweep: at D64 in bf16 6000 to 7000 cycles a chunk (products 1900, splitting
+// operands into bf16 parts 2000, reads of LDS 2600), at D128 9000.  b8 L2048 H24 D64 bf16 101 us, keeping S and N 106, backwards
+// 131; b4 L4096 H32 D128 bf16 keeping S and N 263, backwards
+// 321 (0.8 GB of states and values written by each, beside what it reads).
+//
 // PART: the pass that a cut needs before.  A workgroup takes one part of a head's chunks, from a state of zero for VT columns
 // of the values, or from the unit matrix and without values for VT columns of the part's map; nothing is kept but where the
 // state arrives.
@@ -1047,7 +1055,8 @@ void delta_sweep_kernel(Rule p) {
 
 // ---------------------------------------------------------------------------
 // The states leaving the parts of a cut sequence, one after the other: S = map S + own, 16 columns a workgroup, a quarter of
-// the rows a wave, in float products.  The state goes through LDS, the next part's map is under way meanwhile.
+// the rows a wave, in float products.  The state goes through LDS, the next part's map is under way meanwhile.  Bound by the
+// length of the chain: b1 L32768 H40 D128 42 us.
 // ---------------------------------------------------------------------------
 template <int KDP>
 __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Rule p) {
@@ -1117,7 +1126,8 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Rule p) {
 // First the products along the values, 32 columns at a time: with the states (a wave has 16 of the keys' elements), and
 // dY U^T and dR U^T (a wave has a block or two of them); then, with W and B in LDS, those along the tokens.  Results are
 // transposed, so that a lane has consecutive elements of its own token.  S, D, U and dR lie in LDS by columns, as the
-// sweeps wrote them, and are read transposed.
+// sweeps wrote them, and are read transposed.  Bound by the latency of its loads with few workgroups a CU (one at D128, two at
+// D64, by their LDS): b8 L2048 H24 D64 bf16 197 us; b4 L4096 H32 G8 D128 bf16 594, four heads a workgroup.
 // ---------------------------------------------------------------------------
 struct Grad {
   Rule p;                // v is v, y is dv
@@ -1658,7 +1668,8 @@ void delta_grad_kernel(Grad a) {
 // ---------------------------------------------------------------------------
 // One token: a workgroup holds up to kTile columns of one head's state in registers (NR rows of VEC columns a thread): lanes
 // run along its columns, groups of them along its rows.  What the state answers for k and for q is summed over
-// the groups at once, in LDS: y = scale (r S^T q + (q . k) u).  The state is read and written once: bound by HBM.
+// the groups at once, in LDS: y = scale (r S^T q + (q . k) u).  The state is read and written once: bound by HBM (b256 H40
+// D128 bf16 268 us, 5 TB/s).
 // ---------------------------------------------------------------------------
 template <typename T, int VEC, int NR>
 __global__ __launch_bounds__(256) void delta_update_kernel(Rule p, float* __restrict__ state, int lanes) {
