@@ -294,3 +294,35 @@ def test_graph(dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [3, 7, 9, 12, 14, 77, 1029, 5115])
+def test_rows_that_end_inside_a_piece(W, dtype):
+    """Widths that are not whole 16-byte pieces, from any address: what lies around the tensors is not read into a result
+    (it is NaN), and not written."""
+    import torch
+
+    import selective_state_space_35_amd as ssm
+
+    for form in (0, 1, 2, 6):
+        x, d = make(rows=5, W=W, dtype=dtype, seed=W + form, **FORMS[form])
+        for off, src in ((3, x), (5, d)):
+            for k, t in src.items():
+                if isinstance(t, torch.Tensor):
+                    room = torch.full((t.numel() + 16,), float("nan"), dtype=t.dtype, device="cuda")
+                    room[off:off + t.numel()] = t.reshape(-1)
+                    src[k] = room[off:off + t.numel()].view(t.shape)
+        check(x, d, f"blocknorm piece W={W} form {form} {dtype}")
+        given = {k: x[k] for k in x if k != "x"}
+        h0, n0, _, _ = ssm.ssm_blocknorm_fwd(x["x"], **given)
+        into = {}
+        for k, t in (("h", h0), ("n", n0)):
+            if t is not None:
+                room = torch.full((t.numel() + 24,), 7.0, dtype=t.dtype, device="cuda")
+                into[k] = (room, t, room[11:11 + t.numel()].view(t.shape))
+        ssm.ssm_blocknorm_fwd(x["x"], **given, **{k: v[2] for k, v in into.items()})
+        torch.cuda.synchronize()
+        for k, (room, want, got) in into.items():
+            assert torch.equal(got, want), k
+            assert (room[:11] == 7).all() and (room[11 + want.numel():] == 7).all(), k
