@@ -109,8 +109,9 @@ __device__ __forceinline__ void store(T* p, const float (&v)[N], int left) {
   }
 }
 
-// The sum over the TPR threads of a row, the same in every one of them: shuffles, and for wider rows LDS, two calls in
-// turn with a buffer each, so that one barrier a call is enough (the whole workgroup comes to it).
+// The sum over the TPR threads of a row, the same in every one of them: shuffles, and for wider rows LDS with one barrier
+// a call (the whole workgroup comes to it).  That is enough only if no two calls in a row have the same buffer, over the rows
+// too: a wave may be at the next call's write while another still reads this one's sums.  Callers alternate two of them.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float s, float* buf) {
 #pragma unroll
@@ -203,6 +204,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
   if (slice < a.rows) fetch(slice);
   const float inv_w = 1.f / float(W);
   const int64_t first = int64_t(blockIdx.x) * kGroups / H;  // the workgroup's first slice: it has the most rows
+  int phase = 0;  // the buffer of the next row_sum, whichever norms there are
   for (int64_t k = first; k < a.rows; k += n_slices) {
     const int64_t i0 = slice + (k - first);
     const bool on = live && i0 < a.rows;
@@ -226,7 +228,8 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
       for (int j = 0; j < NV; j++)
 #pragma unroll
         for (int e = 0; e < VEC; e++) s = fmaf(v[j][e], v[j][e], s);
-      s = row_sum<TPR>(s, buf[0][group]);
+      s = row_sum<TPR>(s, buf[phase][group]);
+      phase ^= 1;
       r1 = 1.f / sqrtf(fmaf(s, inv_w, a.eps));
     }
     s = 0.f;
@@ -252,7 +255,8 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_fwd_kernel(BlockNormArg
       }
     }
     if (a.pre) {
-      s = row_sum<TPR>(s, buf[1][group]);
+      s = row_sum<TPR>(s, buf[phase][group]);
+      phase ^= 1;
       r2 = 1.f / sqrtf(fmaf(s, inv_w, a.eps));
       if (on) {
 #pragma unroll
@@ -325,6 +329,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
   if (slice < a.rows) fetch(slice);
   const float inv_w = 1.f / float(W);
   const int64_t first = int64_t(blockIdx.x) * kGroups / H;
+  int phase = 0;
   for (int64_t k = first; k < a.rows; k += n_slices) {
     const int64_t i0 = slice + (k - first), row = i0 * H + h;
     const bool on = live && i0 < a.rows;
@@ -375,7 +380,8 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
           s = fmaf(t[j][e], hh[j][e], s);
         }
       }
-      const float m = row_sum<TPR>(s, buf[0][group]) * inv_w;
+      const float m = row_sum<TPR>(s, buf[phase][group]) * inv_w;
+      phase ^= 1;
 #pragma unroll
       for (int j = 0; j < NV; j++)
 #pragma unroll
@@ -413,7 +419,8 @@ __global__ __launch_bounds__(block_threads(TPR)) void bn_bwd_kernel(BlockNormArg
       }
     }
     if (a.post) {
-      const float m = row_sum<TPR>(s, buf[1][group]) * inv_w;
+      const float m = row_sum<TPR>(s, buf[phase][group]) * inv_w;
+      phase ^= 1;
 #pragma unroll
       for (int j = 0; j < NV; j++)
 #pragma unroll
