@@ -132,7 +132,7 @@ def conv_update_bytes(b, E, K, s, bias=True):
 
 # what no kernel of the scans is built from: the C ABI's argument checks, the event timing, linear attention, the gated delta
 # rule and the norms
-HASH_EXCLUDES = ("ssm_api.hip", "ssm_profile.hip", "ssm_chunks.h", "ssm_linattn.hip", "ssm_linattn.h", "ssm_deltarule.hip",
+HASH_EXCLUDES = ("ssm_api.hip", "ssm_profile.hip", "ssm_kinds.h", "ssm_chunks.h", "ssm_linattn.hip", "ssm_linattn.h", "ssm_deltarule.hip",
                  "ssm_deltarule.h", "ssm_layernorm.hip", "ssm_layernorm.h", "ssm_blocknorm.hip", "ssm_blocknorm.h")
 
 

@@ -23,7 +23,7 @@
 
 #include "ssm_blocknorm.h"
 #include "ssm_device.h"
-#include "ssm_profile.h"
+#include "ssm_kinds.h"
 
 namespace ssm {
 namespace {

@@ -33,7 +33,7 @@
 #include "ssm_chunks.h"
 #include "ssm_deltarule.h"
 #include "ssm_device.h"
-#include "ssm_profile.h"
+#include "ssm_kinds.h"
 
 namespace ssm {
 namespace {

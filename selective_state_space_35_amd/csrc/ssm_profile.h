@@ -33,16 +33,7 @@ enum : int {
   kKindNormFwd = 23,    // layer norm
   kKindNormBwd = 24,    // layer norm backward: input gradient, partial parameter gradients
   kKindNormReduce = 25, // layer norm backward: sums of the partial parameter gradients
-  kKindDeltaTri = 26,   // gated delta rule: triangular inverses of the chunks
-  kKindDeltaSweep = 27, // gated delta rule: a sweep over the sequence (outputs, states, or their gradients)
-  kKindDeltaGrad = 28,  // gated delta rule backward: the chunks' gradients
-  kKindDeltaReduce = 29,// gated delta rule backward: sums over the heads of a group
-  kKindDeltaUpdate = 30,// gated delta rule: single-token state update
-  kKindBlockNormFwd = 31,    // norms around a block
-  kKindBlockNormBwd = 32,    // norms around a block, backward: gradients, partial parameter gradients
-  kKindBlockNormReduce = 33, // norms around a block, backward: sums of the partial parameter gradients
-  kKindDeltaChain = 34, // gated delta rule: states leaving the parts of a cut sequence
-  kNumKinds = 35
+  kNumKinds = 26
 };
 
 // When profiling is on, creates and records the start event on `s` and returns true.

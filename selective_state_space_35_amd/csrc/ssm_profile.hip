@@ -9,7 +9,7 @@
 #include <vector>
 
 #include "ssm.h"
-#include "ssm_profile.h"
+#include "ssm_kinds.h"
 
 namespace ssm {
 namespace {
@@ -23,7 +23,7 @@ std::atomic<bool> g_enabled{false};
 std::mutex g_mu;
 std::vector<Pending> g_pending;
 
-const char* const kNames[kNumKinds] = {"chunk_aggregate", "chunk_carry",   "scan_main",     "fill_state",
+const char* const kNames[kAllKinds] = {"chunk_aggregate", "chunk_carry",   "scan_main",     "fill_state",
                                        "state_update",    "conv",          "conv_update",   "bwd_rows",
                                        "bwd_aggregate",   "bwd_carry",     "bwd_main",      "bwd_reduce",
                                        "ssd_state",       "ssd_carry",     "ssd_scan",      "scan_fused",
@@ -97,7 +97,7 @@ int ssm_profile_read(double* total_ms, int64_t* launches, int n_kinds) {
 }
 
 const char* ssm_profile_kind_name(int kind) {
-  return (kind >= 0 && kind < ssm::kNumKinds) ? ssm::kNames[kind] : "";
+  return (kind >= 0 && kind < ssm::kAllKinds) ? ssm::kNames[kind] : "";
 }
 
 }  // extern "C"
