@@ -521,7 +521,9 @@ SSM_API int64_t ssm_linattn_workspace(int64_t b, int64_t L, int64_t H, int64_t G
  * products.  NULL outputs change no bit of the others.
  * Log decays, resets (a log decay below -10^4, minus infinity included) and positive ones as in ssm_linattn_fwd.
  * What is not finite reaches the outputs that read it and no others: a value of v makes its column of y from its token
- * on, and of the state, NaN; one of k, beta or g every column; one of q its own row of y.
+ * on, and of the state, NaN; one of k, beta or g every column; one of q its own row of y.  This is of inputs (whose
+ * keys' products with each other are to be floats): where finite ones make a state larger than a float holds, y may be NaN
+ * from the first token of the chunk on.
  * L == 0 copies initial_state (or zeros) to last_state; b == 0 or H == 0 is a no-op.
  */
 SSM_API int ssm_deltarule_fwd(const void* q, const void* k, const void* v, const void* beta, const void* g,

@@ -9,12 +9,15 @@
 //   c = e s,  dz = c p silu'(z),  d = c silu(z) w1,  dx = r1 (d - xh mean(d xh))
 //   dw1 = sum over rows of c silu(z) xh,  ds = sum of e u,  dw2 = sum of dn hh
 // Both directions read every streamed value once, hold it for the two sums of its row, one after the other, and write
-// once: bound by HBM (65536 rows of 2560 in bf16 with both norms and the residual: forward 259 us, 5.2 TB/s, backward 450 us,
-// 4.5 TB/s, and 15 us for the parameters' sums).  A group of threads keeps one head's parameters, and in the backward its
-// part of their gradients, in registers and walks rows, the next row's loads under way while one is summed (the parameters
-// read again for every row, 16 registers a thread fewer: 742 us); the gate is a form of its own (with its values in
-// registers that nobody used 510 us).  Rows of two vectors a thread keep more registers than there are
-// and go through scratch.  All sums are float.
+// once: bound by HBM (65536 rows of 2560 in bf16 with the residual: both norms, forward 254 us, 5.3 TB/s, backward with the
+// parameters' sums 430 us, 4.7 TB/s; the norm before the next block alone 254 and 395 us).  A group of threads keeps one
+// head's parameters, and in the backward its part of their gradients, in registers and walks rows, the next row's loads under
+// way while one is summed (the parameters read again for every row, 16 registers a thread fewer: 742 us; rows of 640 threads
+// and more do); the gate is a form of its own (with its values in registers that nobody used 510 us).  What does not fit in
+// the registers goes through scratch: in the backward, rows of more than 512 threads that are gated or not whole pieces (6 to
+// 514 registers) and nearly all of two or four vectors a thread (13 to 1321 registers; 2^27 bf16 elements in rows of 8192,
+// one vector, 376 us, of 8200, two, 1515 us); in the forward, those of two or four vectors that are gated or not whole pieces
+// (up to 280).  All sums are float.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -500,9 +503,11 @@ struct Form {
   static constexpr int tpr = TPR;
 };
 
-// The form of rows of W elements: one vector a thread, in whole waves above one; more only above 1024 threads.
-// 768 threads may have 168 registers, 1024 of them 128: 16384 float rows of 5120, backward, 425 us with 768 and 535 with 1024,
-// gated 857 and 1259; 8192 gated bf16 rows of 12288 1480 and 3046.
+// The form of rows of W elements: one vector a thread, two only above 1024 threads.  The steps leave up to half of the
+// threads of a row idle: 2^27 bf16 elements in rows of 2560 on 320 of 320 threads 205 us forward and 347 backward, of 2568 on
+// 321 of 512 217 and 352, of 4096 on 512 of 512 197 and 315, of 4104 on 513 of 640 249 and 474, of 6400 on 800 of 1024
+// 218 and 419.  768 threads may have 168 registers, 1024 of them 128: 16384 float rows of 5120, backward, 425 us with 768 and
+// 535 with 1024, gated 857 and 1259; 8192 gated bf16 rows of 12288 1480 and 3046.
 template <typename T, typename R, bool GATE, bool TAIL, typename Go>
 auto with_size(int64_t W, Go go) {
   constexpr int V = 16 / sizeof(T);

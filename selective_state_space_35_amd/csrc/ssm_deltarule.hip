@@ -220,7 +220,8 @@ __device__ __forceinline__ f32x4 mma_parts(const Parts<T, NA>& a, const Parts<T,
 // 16 tb + l % 16 and columns 32 ks + 4 (l / 16) .. + 3 and 16 more; for the backward also those of Z^T beta.
 // The 16 x 16 blocks on the diagonal are inverted by forward substitution, a column a lane, and joined block by block,
 // Z_ij = -Z_ii (sum over j <= k < i of X_ik Z_kj), a column of blocks a wave, in float products.  An entry of X that is not
-// finite is taken as zero: the sweep makes NaN of everything from its token on.
+// finite is taken as zero: where a key, a beta or a gate is not finite the sweep makes NaN of everything from its token on by
+// itself.
 // Bound by the latency of its phases (scores, blocks, joining, a barrier between): b8 L2048 H24 D64 bf16 36 us, of the backward,
 // with both forms, 49; b1 L32768 H40 D128 bf16 128 us, 3 TB/s of keys and inverses.  Four workgroups a CU hide some of it.
 // ---------------------------------------------------------------------------
@@ -397,10 +398,11 @@ struct SweepLds {
 };
 
 // A wave's step of a chunk is a chain: K S and Q S, R, Z R, U, the state; 64 columns a workgroup give each SIMD one wave of state
-// and one that stages, and the chain bounds the sweep: at D64 in bf16 6000 to 7000 cycles a chunk (products 1900, splitting
-// operands into bf16 parts 2000, reads of LDS 2600), at D128 9000.  b8 L2048 H24 D64 bf16 101 us, keeping S and N 106, backwards
-// 131; b4 L4096 H32 D128 bf16 keeping S and N 263, backwards
-// 321 (0.8 GB of states and values written by each, beside what it reads).
+// and one that stages, and the chain bounds the sweep: at D64 in bf16 a wave takes 6400 cycles a chunk, in which a SIMD's matrix
+// units are busy for 1970, its vector instructions issue for 2850 and the CU's LDS is busy for 2900 (840 of them bank conflicts);
+// at D128 8800, 3070, 3240 and 5190 (2220).  Keeping S and N it takes 7200 and 8900, backwards 8000 and 10800.
+// b8 L2048 H24 D64 bf16 101 us, keeping S and N 106, backwards 131; b4 L4096 H32 D128 bf16 keeping S and N 263, backwards 321
+// (0.8 GB of states and values written by each, beside what it reads).
 //
 // PART: the pass that a cut needs before.  A workgroup takes one part of a head's chunks, from a state of zero for VT columns
 // of the values, or from the unit matrix and without values for VT columns of the part's map; nothing is kept but where the
@@ -1792,7 +1794,9 @@ bool pieces(const void* x, int64_t D) {
 // Of the cuts into up to 64 segments and 1, 2, 3 or 4 parts each the one whose generations of workgroups take the fewest chunks
 // one after the other: a chunk of the pass before counts 3/4 of one of the sweep (measured: bf16, D128, 2.9 and 3.7 us), a step
 // of the chain 1/3 or, above 64 elements of the keys, one (it is shorter, but with 1/5 and 2/5 b1 L2048 H32 D128 took 128 us, so 107),
-// the launches 3.
+// the launches 3.  Float takes the same counts.  Forward / backward in us, cut and uncut: float b1 L8192 H4 D64 90 / 206 and
+// 673 / 1260, b1 L2048 H32 D128 200 / 601 and 288 / 706, b1 L32768 H40 D128 2914 / 9669 and 4534 / 11971, but b4 L1024 H24
+// D64, where the counts are nearly even, 103 / 298 and 102 / 270; bf16 b1 L8192 H8 D128 140 / 383 and 480 / 1016.
 constexpr int64_t kAtOnce = 256;
 struct Cut {
   int n_segs = 1, parts = 1, part_chunks = 1, n_parts = 0;
